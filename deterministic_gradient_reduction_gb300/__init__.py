@@ -23,6 +23,9 @@ __all__ = [
     "grouped_wgrad_accumulate", "colsum_workspace_bytes", "rowdot_workspace_bytes",
     "index_add_workspace_bytes", "wgrad_workspace_bytes", "workspace", "read_device_status",
     "ordered_colsum_noalloc", "colsum_noalloc_read_status",
+    "router_balance", "router_balance_backward", "router_balance_workspace_bytes", "block_norm",
+    "block_norm_backward", "block_norm_workspace_bytes", "topk_distill", "topk_distill_backward",
+    "topk_distill_workspace_bytes",
 ]
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
@@ -48,6 +51,7 @@ def lib() -> ctypes.CDLL:
                               "(deterministic_gradient_reduction_gb300.build())")
         L = ctypes.CDLL(_LIB_PATH)
         P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+        F32 = ctypes.c_float
         sig = {
             "dgr_status_string": ([I32], ctypes.c_char_p),
             "dgr_version": ([], I32),
@@ -69,6 +73,17 @@ def lib() -> ctypes.CDLL:
             "dgr_aux_loss": ([P, I64, I32, I64, P, ctypes.c_float, P, P, SZ, P], I32),
             "dgr_dsrelu_dprob_workspace_bytes": ([I64, I64], SZ),
             "dgr_dsrelu_dprob": ([P, P, P, I32, I64, I64, I64, P, P, I32, P, SZ, P], I32),
+            "dgr_router_balance_workspace_bytes": ([I64, I32, I32], SZ),
+            "dgr_router_balance": ([P, I32, I64, I32, I64, P, I32, I64, P, P, I32, I32, F32, P, P, P, P, SZ, P], I32),
+            "dgr_router_balance_backward": ([P, I32, I64, I32, I64, P, P, I32, I32, I32, F32, P, P, P, P, I64, I32,
+                                             P], I32),
+            "dgr_block_norm_workspace_bytes": ([I64, I64], SZ),
+            "dgr_block_norm": ([P, I64, P, I64, I32, I64, I64, P, P, I32, P, I32, F32, F32, P, I64, P, I64, P], I32),
+            "dgr_block_norm_backward": ([P, I64, P, I64, P, I64, P, I64, I32, I64, I64, P, P, I32, P, I32, F32, F32,
+                                         P, I64, P, I64, P, P, P, I32, P, SZ, P], I32),
+            "dgr_topk_distill_workspace_bytes": ([I64], SZ),
+            "dgr_topk_distill": ([P, I32, I64, I64, I64, P, I64, P, I64, I32, F32, P, P, F32, P, P, P, P, I64, P, SZ,
+                                  P], I32),
             "dgr_diag_wait_timeout": ([I32, I32, P, SZ, P], I32),
             "dgr_diag_wgrad_stall": ([P, P, P, I32, I64, I64, I64, P, P, SZ, I32, I32, I32, P], I32),
             "dgr_diag_packed_ops": ([P, P, I64, P, P, P], I32),
@@ -332,3 +347,227 @@ def dsrelu_dprob(A: torch.Tensor, B: torch.Tensor, offs: torch.Tensor, dY: torch
         _ptr(A), _ptr(B), _ptr(offs), E, T, K, N, _ptr(dY), _ptr(dprob), int(accumulate), _ptr(ws), ws.numel(),
         _stream(stream)))
     return dprob
+
+
+def _on(stream):
+    """The context in which a call allocates: the call's stream (torch's current one when None)."""
+    return torch.cuda.stream(stream) if stream is not None else _nullcontext()
+
+
+def _rows(t: torch.Tensor, shape, dtype, name: str) -> int:
+    """Row stride of a 2-D tensor of the given shape and type with contiguous rows."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+    if t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0:
+        raise ValueError(f"{name}: contiguous rows expected")
+    return t.stride(0) if shape[0] > 1 else shape[1]  # a single row's stride says nothing
+
+
+def _vec(t: torch.Tensor | None, n: int, dtype, name: str) -> int | None:
+    """Address of an optional contiguous vector of n elements."""
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} of {n} elements expected, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def router_balance_workspace_bytes(N: int, E: int, G: int = 1) -> int:
+    return int(lib().dgr_router_balance_workspace_bytes(N, E, G))
+
+
+def _balance_args(logits, mask, offs, score):
+    if logits.dim() != 2 or score not in _SCORES:
+        raise ValueError("logits [N, E] and score 'softmax' or 'sigmoid' expected")
+    N, E = logits.shape
+    G = 1 if offs is None else offs.numel() - 1
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    return N, E, G, _rows(logits, (N, E), logits.dtype, "logits"), _vec(mask, N, torch.uint8, "mask"), \
+        _vec(offs, G + 1, torch.int64, "offs")
+
+
+def router_balance(logits: torch.Tensor, ids: torch.Tensor, coeff: float, *, offs: torch.Tensor | None = None,
+                   mask: torch.Tensor | None = None, score: str = "softmax", loss: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None, stream=None):
+    """The router's balance loss with its counts: (loss [1], counts int32 [G, E], tokens int32 [G]).
+
+    logits bf16/fp32 [N, E]; ids int32 [N, K] (id < 0: no expert); offs int64 device [G+1] cuts the
+    tokens into groups with a loss of their own; tokens with mask 0 take no part."""
+    N, E, G, ld, pm, po = _balance_args(logits, mask, offs, score)
+    if ids.dim() != 2:
+        raise ValueError("ids int32 [N, K] expected")
+    K = ids.shape[1]
+    ld_ids = _rows(ids, (N, K), torch.int32, "ids")
+    if loss is None or counts is None or tokens is None:
+        with _on(stream):
+            loss = torch.empty(1, dtype=torch.float32, device=logits.device) if loss is None else loss
+            counts = torch.empty(G, E, dtype=torch.int32, device=logits.device) if counts is None else counts
+            tokens = torch.empty(G, dtype=torch.int32, device=logits.device) if tokens is None else tokens
+    if ws is None:
+        ws = workspace(router_balance_workspace_bytes(N, E, G), logits.device, stream)
+    _check("dgr_router_balance", lib().dgr_router_balance(
+        logits.data_ptr(), _dtype(logits), N, E, ld, ids.data_ptr(), K, ld_ids, pm, po, G, _SCORES[score], coeff,
+        _vec(counts, G * E, torch.int32, "counts"), _vec(tokens, G, torch.int32, "tokens"),
+        _vec(loss, 1, torch.float32, "loss"), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return loss, counts, tokens
+
+
+def router_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, topk: int, coeff: float,
+                            *, offs: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                            score: str = "softmax", dloss: torch.Tensor | None = None,
+                            dlogits: torch.Tensor | None = None, accumulate: bool = False,
+                            stream=None) -> torch.Tensor:
+    """Gradient of router_balance's loss to the logits, from the counts and tokens that it gave
+    (topk: the width K of its ids; dloss: fp32 [1] on the device, 1 when None)."""
+    N, E, G, ld, pm, po = _balance_args(logits, mask, offs, score)
+    if dlogits is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dlogits to add to")
+        with _on(stream):
+            dlogits = torch.empty(N, E, dtype=logits.dtype, device=logits.device)
+    _check("dgr_router_balance_backward", lib().dgr_router_balance_backward(
+        logits.data_ptr(), _dtype(logits), N, E, ld, pm, po, G, _SCORES[score], topk, coeff,
+        _vec(counts, G * E, torch.int32, "counts"), _vec(tokens, G, torch.int32, "tokens"),
+        _vec(dloss, 1, torch.float32, "dloss"), dlogits.data_ptr(), _rows(dlogits, (N, E), logits.dtype, "dlogits"),
+        int(accumulate), _stream(stream)))
+    return dlogits
+
+
+def block_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().dgr_block_norm_workspace_bytes(T, H))
+
+
+def _norm_weights(T, H, w_post, gate, w_pre):
+    """(w_post, gate, gate_mode, w_pre, dtype) as the library takes them; the three share one type."""
+    given = [w for w in (w_post, gate, w_pre) if w is not None]
+    dt = given[0].dtype if given else torch.float32
+    mode = 0
+    if gate is not None:
+        if gate.shape == (H,):
+            mode = 1
+        elif gate.shape == (T, 1):
+            mode = 2
+        else:
+            raise ValueError(f"gate [H] or [T, 1] expected, got {list(gate.shape)}")
+    return (_vec(w_post, H, dt, "w_post"), _vec(gate, H if mode == 1 else T, dt, "gate"), mode,
+            _vec(w_pre, H, dt, "w_pre"), _dtype(given[0]) if given else DTYPE_F32)
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, w_post: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, res_scale: float = 1.0, w_pre: torch.Tensor | None = None,
+               eps: float = 1e-6, h: torch.Tensor | None = None, u: torch.Tensor | None = None, stream=None):
+    """The boundary between two blocks: h = res_scale x + gate norm(y; w_post), u = norm(h; w_pre).
+
+    x (residual stream) and y (block output) bf16/fp32 [T, H]; gate [H] or [T, 1]. w_post None: no
+    norm after the block; w_pre None: no u; y None: u = norm(x; w_pre). Returns (h, u); h may be x."""
+    if x.dim() != 2:
+        raise ValueError("x [T, H] expected")
+    T, H = x.shape
+    pw, pg, mode, pp, wdt = _norm_weights(T, H, w_post, gate, w_pre)
+    if (y is not None and h is None) or (w_pre is not None and u is None):
+        with _on(stream):
+            h = torch.empty(T, H, dtype=x.dtype, device=x.device) if y is not None and h is None else h
+            u = torch.empty(T, H, dtype=x.dtype, device=x.device) if w_pre is not None and u is None else u
+    S, dt = (T, H), x.dtype
+    _check("dgr_block_norm", lib().dgr_block_norm(
+        x.data_ptr(), _rows(x, S, dt, "x"), _ptr(y), _rows(y, S, dt, "y") if y is not None else 0, _dtype(x), T, H,
+        pw, pg, mode, pp, wdt, res_scale, eps, _ptr(h), _rows(h, S, dt, "h") if h is not None else 0, _ptr(u),
+        _rows(u, S, dt, "u") if u is not None else 0, _stream(stream)))
+    return (x if y is None else h), u
+
+
+def block_norm_backward(h: torch.Tensor | None, y: torch.Tensor | None, dh: torch.Tensor | None,
+                        du: torch.Tensor | None, *, w_post: torch.Tensor | None = None,
+                        gate: torch.Tensor | None = None, res_scale: float = 1.0, w_pre: torch.Tensor | None = None,
+                        eps: float = 1e-6, dx: torch.Tensor | None = None, dy: torch.Tensor | None = None,
+                        dw_post: torch.Tensor | None = None, dgate: torch.Tensor | None = None,
+                        dw_pre: torch.Tensor | None = None, accumulate: bool = False, ws: torch.Tensor | None = None,
+                        stream=None) -> dict:
+    """Gradients of block_norm from those of h (dh, or None) and u (du): a dict of dx, dy, dw_post,
+    dgate and dw_pre (those that the call has). dx and dy have x's type, the others are fp32;
+    accumulate adds the weights' and the gate's to what dw_post, dgate and dw_pre hold."""
+    like = du if du is not None else dh
+    if like is None or like.dim() != 2:
+        raise ValueError("du [T, H] or dh [T, H] expected")
+    T, H = like.shape
+    S, dt, dev = (T, H), like.dtype, like.device
+    pw, pg, mode, pp, wdt = _norm_weights(T, H, w_post, gate, w_pre)
+    if accumulate and any(w is not None and d is None for w, d in ((w_post, dw_post), (gate, dgate), (w_pre, dw_pre))):
+        raise ValueError("accumulate needs dw_post, dgate and dw_pre to add to")
+    if dx is None or (y is not None and dy is None) or (w_post is not None and dw_post is None) or \
+            (gate is not None and dgate is None) or (w_pre is not None and dw_pre is None):
+        with _on(stream):
+            dx = torch.empty(T, H, dtype=dt, device=dev) if dx is None else dx
+            dy = torch.empty(T, H, dtype=dt, device=dev) if y is not None and dy is None else dy
+            f32 = dict(dtype=torch.float32, device=dev)
+            dw_post = torch.empty(H, **f32) if w_post is not None and dw_post is None else dw_post
+            dgate = torch.empty(gate.shape, **f32) if gate is not None and dgate is None else dgate
+            dw_pre = torch.empty(H, **f32) if w_pre is not None and dw_pre is None else dw_pre
+    if ws is None:
+        ws = workspace(block_norm_workspace_bytes(T, H), dev, stream)
+    ld = lambda t, name: _rows(t, S, dt, name) if t is not None else 0  # noqa: E731
+    _check("dgr_block_norm_backward", lib().dgr_block_norm_backward(
+        _ptr(h), ld(h, "h"), _ptr(y), ld(y, "y"), _ptr(dh), ld(dh, "dh"), _ptr(du), ld(du, "du"), _dtype(like), T, H,
+        pw, pg, mode, pp, wdt, res_scale, eps, _ptr(dx), ld(dx, "dx"), _ptr(dy), ld(dy, "dy"),
+        _vec(dw_post, H, torch.float32, "dw_post"), _vec(dgate, H if mode == 1 else T, torch.float32, "dgate"),
+        _vec(dw_pre, H, torch.float32, "dw_pre"), int(accumulate), ws.data_ptr(), ws.numel(), _stream(stream)))
+    out = {"dx": dx, "dy": dy, "dw_post": dw_post, "dgate": dgate, "dw_pre": dw_pre}
+    return {k: v for k, v in out.items() if v is not None}
+
+
+def topk_distill_workspace_bytes(T: int) -> int:
+    return int(lib().dgr_topk_distill_workspace_bytes(T))
+
+
+def _distill(logits, ids, teacher, tau, teacher_lse, weights, scale, dloss, row_loss, loss, dlogits, ws, stream):
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits [T, V] and ids [T, K] expected")
+    T, V = logits.shape
+    K = ids.shape[1]
+    if ws is None:
+        ws = workspace(topk_distill_workspace_bytes(T), logits.device, stream)
+    f32 = torch.float32
+    _check("dgr_topk_distill", lib().dgr_topk_distill(
+        logits.data_ptr(), _dtype(logits), T, V, _rows(logits, (T, V), logits.dtype, "logits"), ids.data_ptr(),
+        _rows(ids, (T, K), torch.int32, "ids"), teacher.data_ptr(), _rows(teacher, (T, K), f32, "teacher"), K, tau,
+        _vec(teacher_lse, T, f32, "teacher_lse"), _vec(weights, T, f32, "weights"), scale,
+        _vec(dloss, 1, f32, "dloss"), _vec(row_loss, T, f32, "row_loss"), _vec(loss, 1, f32, "loss"), _ptr(dlogits),
+        _rows(dlogits, (T, V), logits.dtype, "dlogits") if dlogits is not None else 0, ws.data_ptr(), ws.numel(),
+        _stream(stream)))
+
+
+def topk_distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *, tau: float = 1.0,
+                 teacher_lse: torch.Tensor | None = None, weights: torch.Tensor | None = None, scale: float = 1.0,
+                 loss: torch.Tensor | None = None, row_loss: torch.Tensor | None = None,
+                 dlogits: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Distillation loss against the teacher's top logits: (loss [1], row_loss [T]), loss = scale
+    sum_t weights[t] row_loss[t].
+
+    logits bf16/fp32 [T, V]; ids int32 [T, K] (id < 0: none) with the teacher's logits fp32 [T, K];
+    teacher_lse: logsumexp of all the teacher's logits / tau, for its mass outside the list. Given
+    dlogits ([T, V]; may be logits itself), the same pass writes loss's gradient there."""
+    T = logits.shape[0]
+    if loss is None or row_loss is None:
+        with _on(stream):
+            loss = torch.empty(1, dtype=torch.float32, device=logits.device) if loss is None else loss
+            row_loss = torch.empty(T, dtype=torch.float32, device=logits.device) if row_loss is None else row_loss
+    _distill(logits, ids, teacher, tau, teacher_lse, weights, scale, None, row_loss, loss, dlogits, ws, stream)
+    return loss, row_loss
+
+
+def topk_distill_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *, tau: float = 1.0,
+                          teacher_lse: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                          scale: float = 1.0, dloss: torch.Tensor | None = None, dlogits: torch.Tensor | None = None,
+                          ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dloss (fp32 [1] on the device, 1 when None) times the gradient of topk_distill's loss to the
+    logits; dlogits may be logits itself."""
+    if dlogits is None:
+        with _on(stream):
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _distill(logits, ids, teacher, tau, teacher_lse, weights, scale, dloss, None, None, dlogits, ws, stream)
+    return dlogits

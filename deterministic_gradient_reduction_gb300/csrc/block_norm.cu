@@ -1,0 +1,486 @@
+// Norms before and after a block, fused with its gate and residual scale.
+//
+// For every token (row) of the residual stream x and the block's output y:
+//   r1 = (mean(y^2) + eps)^(-1/2),  n = y r1 w_post          (norm after the block)
+//   h  = a x + g n                                            (gate g, residual scale a)
+//   r2 = (mean(h^2) + eps)^(-1/2),  u = h r2 w_pre           (norm before the next block)
+// and backwards, from dh and du (gradients of h and u):
+//   v  = du w_pre,  D = dh + r2 v - (r2^3 / H) (v . h) h,  dx = a D
+//   q  = g w_post D,  dy = r1 q - (r1^3 / H) (q . y) y
+//   dw_pre = sum_t du h r2,  C = sum_t [g_t] D y r1,
+//   dw_post = [g] C,  dgate = w_post C (a gate a channel) or D . n (a gate a token).
+// All in binary32 from the stored rows; h and u are rounded once, u from the
+// unrounded h (a second rounding in between would add its error to u's).
+//
+// Deterministic: a row's sums are made by one team of threads in a fixed
+// order; the sums over tokens go through a fixed number of slots (set by T and
+// H alone): slot s takes the rows s, s + P, s + 2P, ... in ascending order,
+// and a second launch adds the slots in a fixed tree.
+#include "row_common.cuh"
+
+namespace dgr {
+namespace {
+
+using namespace row;
+
+constexpr int kWarpTeams = 8;     // rows side by side in a CTA where a warp takes a row
+constexpr int kFoldCols = 32;     // columns of a fold CTA
+constexpr int kFoldWays = 16;     // threads that share a column's slots
+constexpr int64_t kMaxWidth = 16384;
+
+enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
+
+struct NormParams {
+    const void *x, *y;          // forward
+    const void *h, *dh, *du;    // backward (h: the forward's output)
+    int64_t ld_x, ld_y, ld_h, ld_dh, ld_du;
+    void *out_h, *out_u;        // forward: h, u; backward: dx, dy
+    int64_t ld_oh, ld_ou;
+    const void *w_post, *gate, *w_pre;
+    int32_t w_bf16, gate_mode;
+    int32_t T, H;
+    float alpha, eps;
+    float *dw_post, *dgate, *dw_pre;
+    float *slots;               // [n_slots, 2H]: C, then dw_pre
+    int32_t n_slots, accumulate;
+    Sched sched;
+};
+
+// The row's elements of this thread: vector i of its NV is number i * team + tl.
+template <typename T, int VEC, int NV>
+struct Cols {
+    int team, tl, n_vec;
+    __device__ __forceinline__ bool has(int i) const { return i * team + tl < n_vec; }
+    __device__ __forceinline__ int at(int i) const { return (i * team + tl) * VEC; }
+};
+
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_row(float *f, const void *base, int64_t ld, int32_t row, const Cols<T, VEC, NV> &c) {
+    const T *src = static_cast<const T *>(base) + static_cast<int64_t>(row) * ld;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        raw_t<T, VEC> v{};
+        if (c.has(i)) v = *reinterpret_cast<const raw_t<T, VEC> *>(src + c.at(i));
+        unpack<T, VEC>(v, f + i * VEC);
+    }
+}
+
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row(const float *f, void *base, int64_t ld, int32_t row, const Cols<T, VEC, NV> &c) {
+    T *dst = static_cast<T *>(base) + static_cast<int64_t>(row) * ld;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (c.has(i)) *reinterpret_cast<raw_t<T, VEC> *>(dst + c.at(i)) = pack<T, VEC>(f + i * VEC);
+}
+
+// gw = w_post times the channel gate (1 where there is none), w2 = w_pre.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_weights(float *gw, float *w2, const NormParams &p, const Cols<T, VEC, NV> &c) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            float a = 1.0f, b = 0.0f;
+            if (c.has(i)) {
+                const int e = c.at(i) + j;
+                if (p.w_post) a = param(p.w_post, p.w_bf16, e);
+                if (p.gate_mode == kGateChannel) a = __fmul_rn(a, param(p.gate, p.w_bf16, e));
+                if (p.w_pre) b = param(p.w_pre, p.w_bf16, e);
+            }
+            gw[i * VEC + j] = a;
+            w2[i * VEC + j] = b;
+        }
+}
+
+// Sums over the team that has a row: a warp, or the whole block (two buffers
+// in turn, so that one barrier a sum is enough).
+template <bool WARP, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], float *buf, int &turn) {
+    if constexpr (WARP) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    } else {
+        block_sum<N>(v, buf + turn * 32 * 8, blockDim.x >> 5);
+        turn ^= 1;
+    }
+}
+
+template <typename T, int VEC, int NV, int MAXT, bool WARP>
+__global__ void __launch_bounds__(MAXT) norm_forward(const NormParams p) {
+    __shared__ float buf[2 * 32 * 8];
+    constexpr int E = NV * VEC;
+    const int teams = WARP ? kWarpTeams : 1;
+    const Cols<T, VEC, NV> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
+    float gw[E], w2[E];
+    load_weights(gw, w2, p, c);
+    const float inv_h = 1.0f / static_cast<float>(p.H);
+    int turn = 0;
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0); it < p.T;
+         it += static_cast<int64_t>(gridDim.x) * teams) {
+        const int32_t row = static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(it)));
+        float h[E];
+        load_row<T, VEC, NV>(h, p.x, p.ld_x, row, c);
+        if (p.y) {
+            float y[E];
+            load_row<T, VEC, NV>(y, p.y, p.ld_y, row, c);
+            float f = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
+            if (p.w_post) {
+                float s[1] = {0.0f};
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[0] = __fmaf_rn(y[e], y[e], s[0]);
+                team_sum<WARP>(s, buf, turn);
+                f = __fmul_rn(f, rsqrtf(__fmaf_rn(s[0], inv_h, p.eps)));
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = __fmaf_rn(p.alpha, h[e], __fmul_rn(__fmul_rn(y[e], f), gw[e]));
+            store_row<T, VEC, NV>(h, p.out_h, p.ld_oh, row, c);
+        }
+        if (p.out_u) {
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[0] = __fmaf_rn(h[e], h[e], s[0]);
+            team_sum<WARP>(s, buf, turn);
+            const float r = rsqrtf(__fmaf_rn(s[0], inv_h, p.eps));
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = __fmul_rn(__fmul_rn(h[e], r), w2[e]);
+            store_row<T, VEC, NV>(h, p.out_u, p.ld_ou, row, c);
+        }
+    }
+}
+
+// One round of sums a row: with gy = gw y,
+//   q . y = dh . gy + r2 v . gy - (r2^3 / H) (v . h) h . gy,
+// so D need not be known before the second norm's sum is made.
+template <typename T, int VEC, int NV, int MAXT, bool WARP>
+__global__ void __launch_bounds__(MAXT) norm_backward(const NormParams p) {
+    __shared__ float buf[2 * 32 * 8];
+    extern __shared__ float team_cols[];  // WARP: [kWarpTeams][2H]
+    constexpr int E = NV * VEC;
+    const int teams = WARP ? kWarpTeams : 1;
+    const int team = WARP ? threadIdx.x >> 5 : 0;
+    const Cols<T, VEC, NV> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
+    float gw[E], w2[E];
+    load_weights(gw, w2, p, c);
+    const float inv_h = 1.0f / static_cast<float>(p.H);
+    int turn = 0;
+    for (int32_t is = blockIdx.x; is < p.n_slots; is += gridDim.x) {
+        const int32_t slot = static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(is)));
+        float accC[E], accW[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) accC[e] = accW[e] = 0.0f;
+        for (int64_t r64 = static_cast<int64_t>(slot) * teams + team; r64 < p.T; r64 += static_cast<int64_t>(p.n_slots) * teams) {
+            const int32_t row = static_cast<int32_t>(r64);
+            float h[E], dh[E], du[E], y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = dh[e] = du[e] = y[e] = 0.0f;
+            if (p.w_pre) {
+                load_row<T, VEC, NV>(h, p.h, p.ld_h, row, c);
+                load_row<T, VEC, NV>(du, p.du, p.ld_du, row, c);
+            }
+            if (p.dh) load_row<T, VEC, NV>(dh, p.dh, p.ld_dh, row, c);
+            if (p.y) load_row<T, VEC, NV>(y, p.y, p.ld_y, row, c);
+            float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // h.h, v.h, y.y, dh.gy, v.gy, h.gy
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float v = __fmul_rn(du[e], w2[e]), gy = __fmul_rn(gw[e], y[e]);
+                s[0] = __fmaf_rn(h[e], h[e], s[0]);
+                s[1] = __fmaf_rn(v, h[e], s[1]);
+                s[2] = __fmaf_rn(y[e], y[e], s[2]);
+                s[3] = __fmaf_rn(dh[e], gy, s[3]);
+                s[4] = __fmaf_rn(v, gy, s[4]);
+                s[5] = __fmaf_rn(h[e], gy, s[5]);
+            }
+            team_sum<WARP>(s, buf, turn);
+            float r2 = 0.0f, k2 = 0.0f;  // D = dh + r2 v - k2 h
+            if (p.w_pre) {
+                r2 = rsqrtf(__fmaf_rn(s[0], inv_h, p.eps));
+                k2 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(s[1], inv_h), r2), r2), r2);  // r2^3 alone may underflow
+            }
+            const float dot = __fmaf_rn(-k2, s[5], __fmaf_rn(r2, s[4], s[3]));  // D . gy
+            const float gt = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
+            float r1 = 1.0f, k1 = 0.0f;  // dy = gt (r1 gw D - k1 y)
+            if (p.w_post) {
+                r1 = rsqrtf(__fmaf_rn(s[2], inv_h, p.eps));
+                k1 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(dot, inv_h), r1), r1), r1);
+            }
+            if (p.gate_mode == kGateToken && p.dgate && c.tl == 0) {
+                const float g = __fmul_rn(r1, dot);
+                p.dgate[row] = p.accumulate ? __fadd_rn(p.dgate[row], g) : g;
+            }
+            const float yr = __fmul_rn(r1, gt), kg = __fmul_rn(k1, gt);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float v = __fmul_rn(du[e], w2[e]);
+                const float D = __fmaf_rn(-k2, h[e], __fmaf_rn(r2, v, dh[e]));
+                accW[e] = __fmaf_rn(du[e], __fmul_rn(h[e], r2), accW[e]);
+                accC[e] = __fmaf_rn(D, __fmul_rn(y[e], yr), accC[e]);
+                y[e] = __fmaf_rn(-kg, y[e], __fmul_rn(__fmul_rn(gw[e], yr), D));
+                h[e] = __fmul_rn(p.alpha, D);
+            }
+            store_row<T, VEC, NV>(h, p.out_h, p.ld_oh, row, c);
+            if (p.y) store_row<T, VEC, NV>(y, p.out_u, p.ld_ou, row, c);
+        }
+        float *dst = p.slots + static_cast<int64_t>(slot) * 2 * p.H;
+        if constexpr (WARP) {  // the warps' sums, in ascending order
+            float *mine = team_cols + static_cast<int64_t>(team) * 2 * p.H;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (c.has(i))
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        mine[c.at(i) + j] = accC[i * VEC + j];
+                        mine[p.H + c.at(i) + j] = accW[i * VEC + j];
+                    }
+            __syncthreads();
+            for (int e = threadIdx.x; e < 2 * p.H; e += blockDim.x) {
+                float v = team_cols[e];
+                for (int k = 1; k < kWarpTeams; ++k) v = __fadd_rn(v, team_cols[k * 2 * p.H + e]);
+                dst[e] = v;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (c.has(i))
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        dst[c.at(i) + j] = accC[i * VEC + j];
+                        dst[p.H + c.at(i) + j] = accW[i * VEC + j];
+                    }
+        }
+    }
+}
+
+// The slots of a column: way w of 16 takes the slots w, w + 16, ... in order,
+// the ways meet in a fixed pairwise tree.
+__global__ void __launch_bounds__(kFoldCols *kFoldWays) norm_fold(const NormParams p) {
+    __shared__ float part[kFoldWays][kFoldCols + 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int w = threadIdx.y;
+    const int e = blockIdx.x * kFoldCols + threadIdx.x, n = 2 * p.H;
+    float v = 0.0f;
+    if (e < n)
+#pragma unroll 8
+        for (int s = w; s < p.n_slots; s += kFoldWays) v = __fadd_rn(v, __ldcg(p.slots + static_cast<int64_t>(s) * n + e));
+    part[w][threadIdx.x] = v;
+    __syncthreads();
+    for (int s = 1; s < kFoldWays; s <<= 1) {
+        if ((w & (2 * s - 1)) == 0) part[w][threadIdx.x] = __fadd_rn(part[w][threadIdx.x], part[w + s][threadIdx.x]);
+        __syncthreads();
+    }
+    if (w != 0 || e >= n) return;
+    v = part[0][threadIdx.x];
+    auto put = [&](float *dst, int i, float g) {
+        if (dst) dst[i] = p.accumulate ? __fadd_rn(dst[i], g) : g;
+    };
+    if (e >= p.H) {
+        put(p.dw_pre, e - p.H, v);
+    } else {
+        const bool channel = p.gate_mode == kGateChannel;
+        put(p.dw_post, e, channel ? __fmul_rn(param(p.gate, p.w_bf16, e), v) : v);
+        if (channel) put(p.dgate, e, p.w_post ? __fmul_rn(param(p.w_post, p.w_bf16, e), v) : v);
+    }
+}
+
+// Host side -------------------------------------------------------------------
+
+// Elements a thread: 16 from 2048 columns on (or where a warp takes the row),
+// 8 below.
+struct NormPlan {
+    bool warp;
+    int ept, threads;
+    int slots;
+};
+
+NormPlan norm_plan(int64_t T, int64_t H) {
+    NormPlan pl{};
+    pl.warp = H <= 512;
+    pl.ept = (pl.warp ? H > 256 : H > 1024) ? 16 : 8;
+    pl.threads = pl.warp ? 32 * kWarpTeams : static_cast<int>(((H + pl.ept - 1) / pl.ept + 31) / 32 * 32);
+    const int64_t teams = pl.warp ? kWarpTeams : 1;
+    const int64_t most = (!pl.warp && pl.threads <= 128) ? 608 : 304;
+    const int64_t want = (T + teams - 1) / teams;
+    pl.slots = static_cast<int>(want < most ? want : most);
+    return pl;
+}
+
+template <typename T, int VEC, int EPT, int MAXT, bool WARP>
+dgr_status launch_norm(bool backward, const NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
+    constexpr int NV = EPT / VEC;
+    if (!backward) {
+        const int64_t teams = WARP ? kWarpTeams : 1;
+        const int64_t want = (p.T + teams - 1) / teams;
+        const int64_t most = static_cast<int64_t>(sms) * (768 / pl.threads > 0 ? 768 / pl.threads : 1);
+        norm_forward<T, VEC, NV, MAXT, WARP><<<sched_grid(static_cast<unsigned>(want < most ? want : most)), pl.threads, 0, s>>>(p);
+        return launch_status();
+    }
+    const size_t smem = WARP ? static_cast<size_t>(kWarpTeams) * 2 * p.H * 4 : 0;  // at most 32 KB
+    norm_backward<T, VEC, NV, MAXT, WARP><<<sched_grid(static_cast<unsigned>(pl.slots)), pl.threads, smem, s>>>(p);
+    return launch_status();
+}
+
+template <typename T, int VEC>
+dgr_status launch_width(bool backward, const NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
+    if (pl.warp)
+        return pl.ept == 8 ? launch_norm<T, VEC, 8, 256, true>(backward, p, pl, sms, s)
+                           : launch_norm<T, VEC, 16, 256, true>(backward, p, pl, sms, s);
+    if (pl.ept == 8) return launch_norm<T, VEC, 8, 128, false>(backward, p, pl, sms, s);
+    if (pl.threads <= 512) return launch_norm<T, VEC, 16, 512, false>(backward, p, pl, sms, s);
+    return launch_norm<T, VEC, 16, 1024, false>(backward, p, pl, sms, s);
+}
+
+// The widest vector that every row's start allows.
+template <typename T>
+dgr_status launch_type(bool backward, const NormParams &p, const NormPlan &pl, int sms, cudaStream_t s, size_t align) {
+    constexpr int full = 16 / static_cast<int>(sizeof(T));
+    if (align >= 16 && p.H % full == 0) return launch_width<T, full>(backward, p, pl, sms, s);
+    return launch_width<T, 1>(backward, p, pl, sms, s);
+}
+
+// The power of two (at most 16) that divides every row's address.
+size_t row_align(size_t a, const void *base, int64_t ld, int es) {
+    if (!base) return a;
+    const uintptr_t v = reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(ld * es);
+    while (a > 1 && v % a) a >>= 1;
+    return a;
+}
+
+size_t extent(int64_t T, int64_t H, int64_t ld, int es) { return T > 0 && H > 0 ? static_cast<size_t>(((T - 1) * ld + H) * es) : 0; }
+
+}  // namespace
+}  // namespace dgr
+
+using namespace dgr;
+
+extern "C" size_t dgr_block_norm_workspace_bytes(int64_t T, int64_t H) {
+    if (T < 0 || T > INT32_MAX || H < 1 || H > kMaxWidth) return 0;
+    return sizeof(WsHeader) + align_up(static_cast<size_t>(norm_plan(T, H).slots) * 2 * H * 4);
+}
+
+extern "C" dgr_status dgr_block_norm(const void *x, int64_t ld_x, const void *y, int64_t ld_y, int32_t dtype, int64_t T,
+                                     int64_t H, const void *w_post, const void *gate, int32_t gate_mode,
+                                     const void *w_pre, int32_t w_dtype, float res_scale, float eps, void *h,
+                                     int64_t ld_h, void *u, int64_t ld_u, void *stream) {
+    if ((dtype != DGR_DTYPE_BF16 && dtype != DGR_DTYPE_F32) || (w_dtype != DGR_DTYPE_BF16 && w_dtype != DGR_DTYPE_F32))
+        return DGR_ERR_INVALID_ARG;
+    if (T < 0 || H < 1 || !(eps >= 0.0f) || gate_mode < kGateNone || gate_mode > kGateToken) return DGR_ERR_INVALID_ARG;
+    if (T == 0) return check_device();  // no rows: row pointers may be null
+    if ((gate_mode != kGateNone) != (gate != nullptr) || (w_pre != nullptr) != (u != nullptr)) return DGR_ERR_INVALID_ARG;
+    if (!y && (w_post || gate || h || res_scale != 1.0f || !w_pre)) return DGR_ERR_INVALID_ARG;
+    if (y && !h) return DGR_ERR_INVALID_ARG;
+    if (ld_x < H || (y && (ld_y < H || ld_h < H)) || (u && ld_u < H)) return DGR_ERR_INVALID_ARG;
+    if (T > INT32_MAX || H > kMaxWidth) return DGR_ERR_UNSUPPORTED;
+    if (!x) return DGR_ERR_INVALID_ARG;
+    const int es = dtype == DGR_DTYPE_BF16 ? 2 : 4, ws = w_dtype == DGR_DTYPE_BF16 ? 2 : 4;
+    for (const void *q : {x, y, static_cast<const void *>(h), static_cast<const void *>(u)})
+        if (!aligned(q, es)) return DGR_ERR_MISALIGNED;
+    for (const void *q : {w_post, gate, w_pre})
+        if (!aligned(q, ws)) return DGR_ERR_MISALIGNED;
+    const size_t bx = extent(T, H, ld_x, es), by = extent(T, H, ld_y, es), bh = extent(T, H, ld_h, es), bu = extent(T, H, ld_u, es);
+    const size_t bg = static_cast<size_t>(gate_mode == kGateToken ? T : H) * ws;
+    if (ranges_overlap(h, bh, x, bx) && !(h == x && ld_h == ld_x)) return DGR_ERR_ALIAS;
+    if (ranges_overlap(h, bh, y, by) || ranges_overlap(h, bh, u, bu) || ranges_overlap(u, bu, x, bx) || ranges_overlap(u, bu, y, by))
+        return DGR_ERR_ALIAS;
+    const struct { const void *q; size_t n; } params[3] = {{w_post, H * static_cast<size_t>(ws)}, {gate, bg}, {w_pre, H * static_cast<size_t>(ws)}};
+    for (const auto &a : params)
+        if (ranges_overlap(h, bh, a.q, a.n) || ranges_overlap(u, bu, a.q, a.n)) return DGR_ERR_ALIAS;
+    dgr_status st = check_device();
+    if (st != DGR_OK) return st;
+    NormParams p{};
+    p.x = x, p.y = y, p.ld_x = ld_x, p.ld_y = ld_y;
+    p.out_h = h, p.out_u = u, p.ld_oh = ld_h, p.ld_ou = ld_u;
+    p.w_post = w_post, p.gate = gate, p.w_pre = w_pre, p.w_bf16 = ws == 2, p.gate_mode = gate_mode;
+    p.T = static_cast<int32_t>(T), p.H = static_cast<int32_t>(H), p.alpha = res_scale, p.eps = eps;
+    p.sched = sched_for(static_cast<uint32_t>(T));
+    size_t al = row_align(16, x, ld_x, es);
+    al = row_align(al, y, ld_y, es);
+    al = row_align(al, h, ld_h, es);
+    al = row_align(al, u, ld_u, es);
+    int sms = 0;
+    if ((st = usable_sms(&sms)) != DGR_OK) return st;
+    const NormPlan pl = norm_plan(T, H);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return es == 2 ? launch_type<bf16>(false, p, pl, sms, s, al) : launch_type<float>(false, p, pl, sms, s, al);
+}
+
+extern "C" dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const void *y, int64_t ld_y, const void *dh,
+                                              int64_t ld_dh, const void *du, int64_t ld_du, int32_t dtype, int64_t T,
+                                              int64_t H, const void *w_post, const void *gate, int32_t gate_mode,
+                                              const void *w_pre, int32_t w_dtype, float res_scale, float eps, void *dx,
+                                              int64_t ld_dx, void *dy, int64_t ld_dy, float *dw_post, float *dgate,
+                                              float *dw_pre, int32_t accumulate, void *ws, size_t ws_bytes, void *stream) {
+    if ((dtype != DGR_DTYPE_BF16 && dtype != DGR_DTYPE_F32) || (w_dtype != DGR_DTYPE_BF16 && w_dtype != DGR_DTYPE_F32))
+        return DGR_ERR_INVALID_ARG;
+    if (T < 0 || H < 1 || !(eps >= 0.0f) || gate_mode < kGateNone || gate_mode > kGateToken) return DGR_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {  // no rows (their pointers may be null): sums of nothing are +0.0 on overwrite, untouched on accumulate
+        const dgr_status st = check_device();
+        if (st != DGR_OK || accumulate) return st;
+        for (float *w : {dw_post, gate_mode == kGateChannel ? dgate : nullptr, dw_pre})
+            if (w && cudaMemsetAsync(w, 0, static_cast<size_t>(H) * 4, s) != cudaSuccess) return DGR_ERR_CUDA;
+        return DGR_OK;
+    }
+    if ((gate_mode != kGateNone) != (gate != nullptr)) return DGR_ERR_INVALID_ARG;
+    if ((w_pre != nullptr) != (du != nullptr) || (w_pre && !h) || (!w_pre && !dh) || (!w_pre && dw_pre)) return DGR_ERR_INVALID_ARG;
+    if (!y && (w_post || gate || dy || res_scale != 1.0f || !w_pre)) return DGR_ERR_INVALID_ARG;
+    if ((y && !dy) || !dx || (dw_post && !w_post) || (dgate && !gate)) return DGR_ERR_INVALID_ARG;
+    if ((w_pre && (ld_h < H || ld_du < H)) || (y && (ld_y < H || ld_dy < H)) || (dh && ld_dh < H) || ld_dx < H)
+        return DGR_ERR_INVALID_ARG;
+    if (T > INT32_MAX || H > kMaxWidth) return DGR_ERR_UNSUPPORTED;
+    const int es = dtype == DGR_DTYPE_BF16 ? 2 : 4, wes = w_dtype == DGR_DTYPE_BF16 ? 2 : 4;
+    for (const void *q : {w_pre ? h : nullptr, y, dh, du, static_cast<const void *>(dx), static_cast<const void *>(dy)})
+        if (!aligned(q, es)) return DGR_ERR_MISALIGNED;
+    for (const void *q : {w_post, gate, w_pre})
+        if (!aligned(q, wes)) return DGR_ERR_MISALIGNED;
+    for (const void *q : {dw_post, dgate, dw_pre})
+        if (!aligned(q, 4)) return DGR_ERR_MISALIGNED;
+    const size_t need = dgr_block_norm_workspace_bytes(T, H);
+    if (!ws) return DGR_ERR_INVALID_ARG;
+    if (ws_bytes < need) return DGR_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(ws, kAlign)) return DGR_ERR_MISALIGNED;
+    struct Range { const void *q; size_t n; };
+    const size_t hb = static_cast<size_t>(H);
+    const size_t gn = gate_mode == kGateToken ? static_cast<size_t>(T) : hb;
+    const Range ins[] = {{w_pre ? h : nullptr, extent(T, H, ld_h, es)}, {y, extent(T, H, ld_y, es)}, {dh, extent(T, H, ld_dh, es)},
+                         {du, extent(T, H, ld_du, es)}, {w_post, hb * wes}, {gate, gn * wes}, {w_pre, hb * wes}};
+    const Range outs[] = {{dx, extent(T, H, ld_dx, es)}, {dy, extent(T, H, ld_dy, es)}, {dw_post, hb * 4}, {dgate, gn * 4},
+                          {dw_pre, hb * 4}, {ws, need}};
+    for (const Range &o : outs) {
+        for (const Range &i : ins)
+            if (ranges_overlap(o.q, o.n, i.q, i.n) && !(o.q == dx && i.q == dh && dx == dh && ld_dx == ld_dh)) return DGR_ERR_ALIAS;
+        for (const Range &b : outs)
+            if (&o < &b && ranges_overlap(o.q, o.n, b.q, b.n)) return DGR_ERR_ALIAS;
+    }
+    dgr_status st = check_device();
+    if (st != DGR_OK) return st;
+    NormParams p{};
+    p.h = w_pre ? h : nullptr, p.y = y, p.dh = dh, p.du = du;
+    p.ld_h = ld_h, p.ld_y = ld_y, p.ld_dh = ld_dh, p.ld_du = ld_du;
+    p.out_h = dx, p.out_u = dy, p.ld_oh = ld_dx, p.ld_ou = ld_dy;
+    p.w_post = w_post, p.gate = gate, p.w_pre = w_pre, p.w_bf16 = wes == 2, p.gate_mode = gate_mode;
+    p.T = static_cast<int32_t>(T), p.H = static_cast<int32_t>(H), p.alpha = res_scale, p.eps = eps;
+    p.dw_post = dw_post, p.dgate = dgate, p.dw_pre = dw_pre, p.accumulate = accumulate ? 1 : 0;
+    const NormPlan pl = norm_plan(T, H);
+    p.n_slots = pl.slots;
+    p.slots = reinterpret_cast<float *>(static_cast<char *>(ws) + sizeof(WsHeader));
+    p.sched = sched_for(static_cast<uint32_t>(pl.slots));
+    size_t al = 16;
+    if (w_pre) al = row_align(al, h, ld_h, es);
+    al = row_align(al, y, ld_y, es);
+    al = row_align(al, dh, ld_dh, es);
+    al = row_align(al, du, ld_du, es);
+    al = row_align(al, dx, ld_dx, es);
+    al = row_align(al, dy, ld_dy, es);
+    st = es == 2 ? launch_type<bf16>(true, p, pl, 0, s, al) : launch_type<float>(true, p, pl, 0, s, al);
+    if (st != DGR_OK || (!dw_post && !dw_pre && !(dgate && gate_mode == kGateChannel))) return st;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((2 * H + kFoldCols - 1) / kFoldCols));
+    cfg.blockDim = dim3(kFoldCols, kFoldWays);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_fold, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
+}

@@ -1,0 +1,138 @@
+// Helpers of the row-wise kernels (norms, softmaxes): vectors of bf16 or fp32
+// elements, fixed-order sums over a warp and a block.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "dgr_common.cuh"
+
+namespace dgr {
+namespace row {
+
+using bf16 = __nv_bfloat16;
+
+// VEC elements of T as one load or store (2, 4, 8 or 16 bytes).
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<2> {
+    using type = uint16_t;
+};
+template <>
+struct Raw<4> {
+    using type = uint32_t;
+};
+template <>
+struct Raw<8> {
+    using type = uint2;
+};
+template <>
+struct Raw<16> {
+    using type = uint4;
+};
+template <typename T, int VEC>
+using raw_t = typename Raw<static_cast<int>(sizeof(T)) * VEC>::type;
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const raw_t<T, VEC> &v, float *f) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (VEC == 1) {
+            f[0] = __uint_as_float(v);
+        } else if constexpr (VEC == 2) {
+            f[0] = __uint_as_float(v.x);
+            f[1] = __uint_as_float(v.y);
+        } else {
+            f[0] = __uint_as_float(v.x);
+            f[1] = __uint_as_float(v.y);
+            f[2] = __uint_as_float(v.z);
+            f[3] = __uint_as_float(v.w);
+        }
+    } else {
+        auto two = [](uint32_t w, float *g) {
+            g[0] = __uint_as_float(w << 16);
+            g[1] = __uint_as_float(w & 0xffff0000u);
+        };
+        if constexpr (VEC == 1) {
+            f[0] = bf16_bits_to_f32(v);
+        } else if constexpr (VEC == 2) {
+            two(v, f);
+        } else if constexpr (VEC == 4) {
+            two(v.x, f);
+            two(v.y, f + 2);
+        } else {
+            two(v.x, f);
+            two(v.y, f + 2);
+            two(v.z, f + 4);
+            two(v.w, f + 6);
+        }
+    }
+}
+
+// Rounded to nearest even, once.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ raw_t<T, VEC> pack(const float *f) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (VEC == 1) return __float_as_uint(f[0]);
+        else if constexpr (VEC == 2) return make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
+        else return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+        if constexpr (VEC == 1) return __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+        else if constexpr (VEC == 2) return pack2(f[0], f[1]);
+        else if constexpr (VEC == 4) return make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+        else return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return __bfloat162float(v);
+}
+
+// A 32-bit or bf16 parameter read as binary32.
+__device__ __forceinline__ float param(const void *p, int bf, int64_t i) {
+    return bf ? bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p) + i)) : __ldg(static_cast<const float *>(p) + i);
+}
+
+// Sum over the warp, the same bits in every lane (each step adds the same
+// pair in both lanes of it).
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, s));
+    return v;
+}
+
+// N sums over the block, the same bits in every thread; `buf` holds
+// N * 32 floats and must not be reused before the next barrier of the caller.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float *buf, int n_warps) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = warp_sum(v[i]);
+        if (lane == 0) buf[i * 32 + w] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float s = buf[i * 32];
+        for (int k = 1; k < n_warps; ++k) s = __fadd_rn(s, buf[i * 32 + k]);
+        v[i] = s;
+    }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace row
+}  // namespace dgr

@@ -395,6 +395,148 @@ dgr_status dgr_dsrelu_dprob(const void *A, const void *B, const int64_t *d_offs,
                             int64_t N, const void *dY, float *dprob, int32_t accumulate, void *ws, size_t ws_bytes,
                             void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* 9. Router balance loss with per-expert counts, and its gradient           */
+/* ------------------------------------------------------------------------ */
+/*
+ * The router's load-balance loss from its logits (dgr_aux_loss takes given
+ * probabilities and counts), for one group of tokens or for packed sequences
+ * that each have a loss of their own:
+ *
+ *   p_t       = softmax(l_t)                              (score 0)
+ *             = sigmoid(l_t) / sum_e sigmoid(l_t[e])      (score 1);
+ *   counts[g][e] = slots (t, k) of group g's valid tokens with ids[t][k] = e;
+ *   tokens[g] = valid tokens of group g (mask[t] != 0, or all without a mask);
+ *   *loss     = sum_g a_g sum_e counts[g][e] sum_{t in g} p_t[e],
+ *   a_g       = coeff * E / (G * K * tokens[g]^2)         (0 without tokens);
+ *   dl_t[e]   = *dloss * a_g * p_t[e] (counts[g][e] - sum_j counts[g][j] p_t[j])
+ *               [* (1 - sigmoid(l_t[e]))], 0 for a token that is not valid.
+ *
+ * Sums are binary32 in a fixed order that depends on N, E and G alone: the
+ * bits do not depend on the launch. Logits of -inf have probability 0 (a row
+ * of them only: 0 everywhere); a NaN or +inf makes its row NaN. Masked tokens
+ * are not read, whatever they hold.
+ *
+ * logits:   [N, E] bf16 or fp32 (dtype), row stride ld.
+ * ids:      [N, K] int32, row stride ld_ids; an id < 0 is no expert; an id >= E
+ *           is left out too and records DGR_ERR_INVALID_ARG in the status word.
+ * mask:     [N] bytes or null.
+ * d_offs:   [G+1] int64 DEVICE array, non-decreasing, d_offs[0] = 0, d_offs[G] = N,
+ *           or null with G = 1. Offsets outside this contract: the forward call
+ *           writes nothing and records DGR_ERR_INVALID_ARG; the backward call
+ *           gives tokens outside [d_offs[0], d_offs[G]) no gradient.
+ * counts:   [G, E] int32; tokens: [G] int32; loss: one fp32 (overwritten).
+ * dloss:    one DEVICE fp32 or null (1). dlogits: [N, E] of dtype, row stride
+ *           ld_d; accumulate != 0 adds to it (rounded once more).
+ * Limits:   1 <= E <= 1024, 1 <= K <= 1024, 1 <= G <= 1024, N < 2^31.
+ * ws:       dgr_router_balance_workspace_bytes(N, E, G) bytes, zeroed once. The
+ *           backward call needs none.
+ * No output may overlap an input, another output or ws.
+ */
+size_t dgr_router_balance_workspace_bytes(int64_t N, int32_t E, int32_t G);
+dgr_status dgr_router_balance(const void *logits, int32_t dtype, int64_t N, int32_t E, int64_t ld,
+                              const int32_t *ids, int32_t K, int64_t ld_ids, const uint8_t *mask,
+                              const int64_t *d_offs, int32_t G, int32_t score, float coeff, int32_t *counts,
+                              int32_t *tokens, float *loss, void *ws, size_t ws_bytes, void *stream);
+dgr_status dgr_router_balance_backward(const void *logits, int32_t dtype, int64_t N, int32_t E, int64_t ld,
+                                       const uint8_t *mask, const int64_t *d_offs, int32_t G, int32_t score,
+                                       int32_t K, float coeff, const int32_t *counts, const int32_t *tokens,
+                                       const float *dloss, void *dlogits, int64_t ld_d, int32_t accumulate,
+                                       void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* 10. Norms before and after a block, with its gate and residual scale      */
+/* ------------------------------------------------------------------------ */
+/*
+ * The boundary between two blocks: the norm after a block, its gate, the
+ * residual sum and the norm before the next block, in one pass over the rows.
+ *
+ *   n = y * r1 * w_post,              r1 = (mean(y^2) + eps)^(-1/2);
+ *   h = res_scale * x + gate * n;
+ *   u = h * r2 * w_pre,               r2 = (mean(h^2) + eps)^(-1/2)
+ *
+ * w_post null: n = y (no norm after the block). w_pre null: no norm before the
+ * next one, u must be null. y null: u = norm(x) alone (then w_post, gate and h
+ * must be null and res_scale 1). gate_mode: 0 none (gate null), 1 one value a
+ * channel [H], 2 one value a token [T].
+ *
+ * Backward, from dh and du (dh null: 0; du null exactly when w_pre is):
+ *   v = du * w_pre,  D = dh + r2 v - (r2^3 / H) (v . h) h,  dx = res_scale * D;
+ *   q = gate * w_post * D,  dy = r1 q - (r1^3 / H) (q . y) y;
+ *   dw_pre = sum_t du h r2,  dw_post = sum_t gate D y r1,
+ *   dgate[e] = sum_t D n (mode 1), dgate[t] = sum_e D n (mode 2).
+ * dw_post, dgate and dw_pre may be null; they are written, or added to with one
+ * rounding (accumulate != 0). h is the forward's output (x where y is null; not
+ * read without w_pre); x is not needed.
+ *
+ * Binary32 throughout, each output rounded once (u from the unrounded h). The
+ * order of every sum depends on T, H and the rows' alignment alone; a row's
+ * sums are its own, the sums over tokens go through a number of slots set by T
+ * and H.
+ *
+ * x, y, h, u, dh, du, dx, dy: [T, H] bf16 or fp32 (dtype), each with its row
+ *           stride; w_post, gate, w_pre: bf16 or fp32 (w_dtype);
+ *           dw_post [H], dgate [H] or [T], dw_pre [H]: fp32.
+ * Limits:   1 <= H <= 16384, T < 2^31.
+ * ws:       dgr_block_norm_workspace_bytes(T, H) bytes for the backward call.
+ * h may be x and dx may be dh (same pointer and stride); nothing else may overlap.
+ */
+size_t dgr_block_norm_workspace_bytes(int64_t T, int64_t H);
+dgr_status dgr_block_norm(const void *x, int64_t ld_x, const void *y, int64_t ld_y, int32_t dtype, int64_t T,
+                          int64_t H, const void *w_post, const void *gate, int32_t gate_mode, const void *w_pre,
+                          int32_t w_dtype, float res_scale, float eps, void *h, int64_t ld_h, void *u,
+                          int64_t ld_u, void *stream);
+dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const void *y, int64_t ld_y, const void *dh,
+                                   int64_t ld_dh, const void *du, int64_t ld_du, int32_t dtype, int64_t T,
+                                   int64_t H, const void *w_post, const void *gate, int32_t gate_mode,
+                                   const void *w_pre, int32_t w_dtype, float res_scale, float eps, void *dx,
+                                   int64_t ld_dx, void *dy, int64_t ld_dy, float *dw_post, float *dgate,
+                                   float *dw_pre, int32_t accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* 11. Distillation from a teacher's top logits                              */
+/* ------------------------------------------------------------------------ */
+/*
+ * For each row, the student's logits z [V] against the teacher's list
+ * (ids, teacher) [K] at temperature tau:
+ *
+ *   p   = softmax(z / tau);
+ *   q_k = softmax(teacher / tau) over the list's valid entries, or, with
+ *         teacher_lse[t] = logsumexp of all the teacher's logits / tau:
+ *         q_k = exp(teacher_k / tau - teacher_lse), q_r = max(0, 1 - sum_k q_k);
+ *   L   = sum_k q_k (ln q_k - ln p_k)  [+ q_r (ln q_r - ln p_r)],
+ *         p_r = sum of p outside the list; the bracket is left out where no
+ *         logit outside the list is above -inf;
+ *   row_loss[t] = L, *loss = scale * sum_t weights[t] L_t;
+ *   dz_j = *dloss * scale * weights[t] / tau *
+ *          (S p_j - sum of q_k with ids_k = j   for j in the list,
+ *           p_j (S - q_r / p_r)                 otherwise),
+ *          S = the q that L counts: 1, but where the bracket is left out or the
+ *          list's q exceed 1.
+ *
+ * An entry with ids < 0 is none (the lists of dgr_topk_canonicalize may be
+ * passed as they are); an id >= V is left out and records DGR_ERR_INVALID_ARG
+ * in the status word. An id that comes twice adds both its q. A row of weight
+ * 0, or without a valid entry, has loss 0 and gradient 0, and its logits are not read.
+ * Sums are binary32 in an order that depends on T, V, K and alignment alone.
+ *
+ * logits:   [T, V] bf16 or fp32 (dtype), row stride ld; ids int32 and teacher
+ *           fp32 [T, K], strides ld_ids, ld_teacher; teacher_lse, weights [T]
+ *           fp32 or null; dloss one DEVICE fp32 or null (1).
+ * row_loss: [T] fp32 or null; loss: one fp32 or null (needs row_loss);
+ *           dlogits: [T, V] of dtype, row stride ld_d, or null; one at least.
+ *           loss and dlogits of one call cost one reading of the logits.
+ * Limits:   1 <= V <= 2^20, 1 <= K <= 1024, T < 2^31, tau > 0.
+ * ws:       dgr_topk_distill_workspace_bytes(T) bytes, zeroed once.
+ * dlogits may be logits (same pointer and stride); nothing else may overlap.
+ */
+size_t dgr_topk_distill_workspace_bytes(int64_t T);
+dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t *ids,
+                            int64_t ld_ids, const float *teacher, int64_t ld_teacher, int32_t K, float tau,
+                            const float *teacher_lse, const float *weights, float scale, const float *dloss,
+                            float *row_loss, float *loss, void *dlogits, int64_t ld_d, void *ws, size_t ws_bytes,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif
