@@ -10,13 +10,14 @@
 // atomicAdd; here every sum has one writer and a fixed order.
 //
 // Forward, one launch: a CTA per tile of consecutive tokens of one group. A row
-// is held by the fewest lanes that cover it with 4 experts each (several rows
-// a warp where there are few experts); a lane keeps the running sums of its
-// own experts' probabilities over the tile, which lanes, then warps, then
-// tiles add in ascending order. The counts are integer sums (shared-memory
-// integer atomics: any order, the same value). The CTA that finishes a group
-// last folds the group's tiles, and the one that finishes the last group adds
-// the groups.
+// is held by the fewest lanes that cover it with 16 logits each, so a softmax's
+// maximum and sum cost log2(E / 16) shuffles for several rows at a time; the
+// next rows' logits are loaded before the present ones are worked on. A lane
+// keeps the running sums of its own experts' probabilities over the tile, which
+// lanes, then warps, then tiles add in ascending order. The counts are integer
+// sums (shared-memory integer atomics: any order, the same value). The CTA that
+// finishes a group last folds the group's tiles, and the one that finishes the
+// last group adds the groups.
 #include "row_common.cuh"
 
 namespace dgr {
@@ -24,8 +25,10 @@ namespace {
 
 using namespace row;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBackThreads = 256;
+constexpr int kBackTile = 128;  // tokens a backward tile
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxTile = 16384;  // tokens: a lane's running sums stay short
@@ -43,6 +46,7 @@ struct BalParams {
     int32_t sigmoid;
     int32_t tile;         // tokens a tile
     int32_t lanes;        // lanes a row
+    uint64_t k_magic;     // ceil(2^40 / K): i / K for i < 2^24
     float coef;           // coeff E / (G K)
     int32_t *counts, *tokens;
     float *loss;
@@ -51,7 +55,8 @@ struct BalParams {
     int32_t *done;        // [G] tiles done
     float *group_loss;    // [G]
     float *mass;          // [tiles][E]
-    int32_t *part;        // [tiles][E + 1]: counts, valid tokens
+    int32_t *part;        // [tiles][E]: counts
+    int32_t *live;        // [tiles]: valid tokens
     // backward
     const float *dloss;
     void *dlogits;
@@ -107,18 +112,31 @@ __device__ __forceinline__ void scores(float (&x)[E], int lanes, int sigmoid) {
 
 // A lane's experts: vector i of NV starts at expert (i * lanes + sub) * VEC.
 template <typename T, int VEC, int NV>
-__device__ __forceinline__ void load_logits(float *x, const T *row, int sub, int lanes, int E, bool live) {
+struct Logits {
+    raw_t<T, VEC> v[NV];
+    uint32_t there;  // vectors with experts
+
+    __device__ __forceinline__ void load(const T *row, int sub, int lanes, int E, bool live) {
+        there = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = (i * lanes + sub) * VEC;
-        if (live && e < E) {
-            unpack<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(row + e), x + i * VEC);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) x[i * VEC + j] = -INFINITY;
+        for (int i = 0; i < NV; ++i) {
+            const int e = (i * lanes + sub) * VEC;
+            if (live && e < E) {
+                v[i] = *reinterpret_cast<const raw_t<T, VEC> *>(row + e);
+                there |= 1u << i;
+            }
         }
     }
-}
+    __device__ __forceinline__ void get(float *x) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack<T, VEC>(v[i], x + i * VEC);
+            if (!(there >> i & 1))
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) x[i * VEC + j] = -INFINITY;
+        }
+    }
+};
 
 // tbase[g] = first tile of group g, offsets into so[]; false when the offsets
 // break their contract. Every block computes the same.
@@ -177,6 +195,59 @@ __device__ __forceinline__ int group_of(const I *table, int n, I v) {
     return lo;
 }
 
+// Adds a group's tiles, CV experts a thread: `ways` threads share an expert's
+// tiles (way w takes w, w + ways, ...), their sums are added in ascending
+// order. Writes the group's counts; returns this thread's part of their dot
+// product with the probabilities.
+template <int CV>
+__device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *buf) {
+    const int tid = threadIdx.x, n_col = p.E / CV;
+    int span = 1;
+    while (span < n_col && span < kThreads) span <<= 1;
+    const int ways = kThreads / span, way = tid / span;
+    float dot = 0.0f;
+    int32_t *ibuf = reinterpret_cast<int32_t *>(buf) + CV * kThreads;
+    for (int c0 = 0; c0 < n_col; c0 += span) {
+        const int col = c0 + (tid & (span - 1));
+        float m[CV];
+        int32_t c[CV];
+#pragma unroll
+        for (int j = 0; j < CV; ++j) m[j] = 0.0f, c[j] = 0;
+        if (col < n_col)
+#pragma unroll 8
+            for (int t = way; t < n; t += ways) {
+                const int64_t at = static_cast<int64_t>(first + t) * p.E + col * CV;
+                if constexpr (CV == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.mass + at));
+                    const int4 k = __ldcg(reinterpret_cast<const int4 *>(p.part + at));
+                    m[0] = __fadd_rn(m[0], v.x), m[1] = __fadd_rn(m[1], v.y), m[2] = __fadd_rn(m[2], v.z), m[3] = __fadd_rn(m[3], v.w);
+                    c[0] += k.x, c[1] += k.y, c[2] += k.z, c[3] += k.w;
+                } else {
+                    m[0] = __fadd_rn(m[0], __ldcg(p.mass + at));
+                    c[0] += __ldcg(p.part + at);
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < CV; ++j) buf[j * kThreads + tid] = m[j], ibuf[j * kThreads + tid] = c[j];
+        __syncthreads();
+        // one thread an expert
+        for (int e = tid; e < span * CV; e += kThreads) {
+            const int j = e & (CV - 1), k0 = e / CV;
+            if (c0 + k0 >= n_col) continue;
+            float v = buf[j * kThreads + k0];
+            int32_t k = ibuf[j * kThreads + k0];
+            for (int q = 1; q < ways; ++q) {
+                v = __fadd_rn(v, buf[j * kThreads + q * span + k0]);
+                k += ibuf[j * kThreads + q * span + k0];
+            }
+            p.counts[static_cast<int64_t>(g) * p.E + (c0 + k0) * CV + j] = k;
+            dot = __fmaf_rn(static_cast<float>(k), v, dot);
+        }
+    }
+    return dot;
+}
+
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
     extern __shared__ char smem[];
@@ -217,17 +288,33 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
         for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
         if (tid == 0) valid = 0;
         __syncthreads();
-        // counts
-        for (int i = tid; i < count * p.K; i += kThreads) {
-            const int r = i / p.K, k = i - r * p.K;
-            const int32_t id = p.ids[(t0 + r) * p.ld_ids + k];
-            if (id < 0 || (p.mask && !p.mask[t0 + r])) continue;
-            if (id >= p.E) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereExpertId);
-            else atomicAdd(&hist[id], 1);
+        // the first rows' logits are on their way while the counts are made
+        const T *base = static_cast<const T *>(p.logits) + t0 * p.ld;
+        auto is_live = [&](int r) { return r < count && (!p.mask || p.mask[t0 + r]); };
+        Logits<T, VEC, NV> cur, nxt;
+        bool live = is_live(w * rows_warp + my_row), live_next = false;
+        cur.load(base + static_cast<int64_t>(w * rows_warp + my_row) * p.ld, sub, p.lanes, p.E, live);
+        const int n_ids = count * p.K;
+        for (int i0 = tid; i0 < n_ids; i0 += 4 * kThreads) {
+            int32_t id[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * kThreads;
+                id[j] = -1;
+                if (i < n_ids) {
+                    const int r = static_cast<int>((static_cast<uint64_t>(i) * p.k_magic) >> 40);
+                    if (!p.mask || p.mask[t0 + r]) id[j] = __ldg(p.ids + (t0 + r) * p.ld_ids + (i - r * p.K));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (id[j] < 0) continue;
+                if (id[j] >= p.E) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereExpertId);
+                else atomicAdd(&hist[id[j]], 1);
+            }
         }
-        int mine = count;
         if (p.mask) {
-            mine = 0;
+            int mine = 0;
             for (int r = tid; r < count; r += kThreads) mine += p.mask[t0 + r] != 0;
             mine = __reduce_add_sync(0xffffffffu, mine);
             if (lane == 0 && mine) atomicAdd(&valid, mine);
@@ -239,13 +326,16 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
 #pragma unroll
         for (int e = 0; e < EL; ++e) acc[e] = 0.0f;
         for (int b = w * rows_warp; b < count; b += kWarps * rows_warp) {
-            const int r = b + my_row;
-            const bool live = r < count && (!p.mask || p.mask[t0 + r]);
+            const int r = b + kWarps * rows_warp + my_row;
+            live_next = is_live(r);
+            nxt.load(base + static_cast<int64_t>(r) * p.ld, sub, p.lanes, p.E, live_next);
             float x[EL];
-            load_logits<T, VEC, NV>(x, static_cast<const T *>(p.logits) + (t0 + r) * p.ld, sub, p.lanes, p.E, live);
+            cur.get(x);
             scores(x, p.lanes, p.sigmoid);
 #pragma unroll
             for (int e = 0; e < EL; ++e) acc[e] = __fadd_rn(acc[e], live ? x[e] : 0.0f);
+            cur = nxt;
+            live = live_next;
         }
 #pragma unroll
         for (int e = 0; e < EL; ++e)
@@ -261,14 +351,15 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
         }
         __syncthreads();
         float *mass = p.mass + static_cast<int64_t>(tile) * p.E;
-        int32_t *part = p.part + static_cast<int64_t>(tile) * (p.E + 1);
+        int32_t *part = p.part + static_cast<int64_t>(tile) * p.E;
         for (int e = tid; e < p.E; e += kThreads) {
             float v = cols[e];
+#pragma unroll
             for (int k = 1; k < kWarps; ++k) v = __fadd_rn(v, cols[k * p.E + e]);
             mass[e] = v;
             part[e] = hist[e];
         }
-        if (tid == 0) part[p.E] = valid;
+        if (tid == 0) p.live[tile] = valid;
         __threadfence();
         __syncthreads();
         if (tid == 0) last = atomicAdd(&p.done[g], 1) == tbase[g + 1] - tbase[g] - 1;
@@ -278,39 +369,12 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
         __threadfence();
         const int first = tbase[g], n = tbase[g + 1] - first;
         int32_t tokens = 0;
-        for (int j = tid; j < n; j += kThreads) tokens += __ldcg(p.part + static_cast<int64_t>(first + j) * (p.E + 1) + p.E);
-        tokens = __reduce_add_sync(0xffffffffu, tokens);
+        for (int j = tid; j < n; j += kThreads) tokens += __ldcg(p.live + first + j);
         if (tid == 0) valid = 0;
         __syncthreads();
-        if (lane == 0) atomicAdd(&valid, tokens);
-        int span = 1;  // threads side by side over the experts
-        while (span < p.E && span < kThreads) span <<= 1;
-        const int ways = kThreads / span, way = tid / span;
-        float dot = 0.0f;
-        for (int e0 = 0; e0 < p.E; e0 += span) {
-            const int e = e0 + (tid & (span - 1));
-            float m = 0.0f;
-            int32_t c = 0;
-            if (e < p.E)
-#pragma unroll 4
-                for (int j = way; j < n; j += ways) {
-                    m = __fadd_rn(m, __ldcg(p.mass + static_cast<int64_t>(first + j) * p.E + e));
-                    c += __ldcg(p.part + static_cast<int64_t>(first + j) * (p.E + 1) + e);
-                }
-            __syncthreads();
-            cols[tid] = m;
-            int32_t *csum = reinterpret_cast<int32_t *>(cols) + kThreads;
-            csum[tid] = c;
-            __syncthreads();
-            if (way == 0 && e < p.E) {
-                for (int k = 1; k < ways; ++k) {
-                    m = __fadd_rn(m, cols[k * span + tid]);
-                    c += csum[k * span + tid];
-                }
-                p.counts[static_cast<int64_t>(g) * p.E + e] = c;
-                dot = __fmaf_rn(static_cast<float>(c), m, dot);
-            }
-        }
+        tokens = __reduce_add_sync(0xffffffffu, tokens);
+        if (lane == 0 && tokens) atomicAdd(&valid, tokens);
+        const float dot = p.E % 4 == 0 ? fold_tiles<4>(p, first, n, g, cols) : fold_tiles<1>(p, first, n, g, cols);
         float s[1] = {dot};
         block_sum<1>(s, red, kWarps);
         if (tid == 0) {
@@ -336,77 +400,87 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
     }
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads) balance_backward(const BalParams p) {
+template <typename T, int VEC, int NV, bool SIGMOID>
+__global__ void __launch_bounds__(kBackThreads) balance_backward(const BalParams p) {
     extern __shared__ char smem[];
     int64_t *so = reinterpret_cast<int64_t *>(smem);  // [G + 1] when there are offsets
-    constexpr int EL = NV * VEC;
+    constexpr int EL = NV * VEC, kBackWarps = kBackThreads / 32;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     if (p.offs) {
-        for (int g = tid; g <= p.G; g += kThreads) so[g] = p.offs[g];
+        for (int g = tid; g <= p.G; g += kBackThreads) so[g] = p.offs[g];
         __syncthreads();
     }
     const int sub = lane & (p.lanes - 1), rows_warp = 32 / p.lanes, my_row = lane / p.lanes;
+    const int step = kBackWarps * rows_warp;
     const float up = p.dloss ? __fmul_rn(__ldg(p.dloss), p.coef) : p.coef;
-    const int n_tiles = (p.N + p.tile - 1) / p.tile;
+    const int n_tiles = (p.N + kBackTile - 1) / kBackTile;
     for (int it = blockIdx.x; it < n_tiles; it += gridDim.x) {
-        const int64_t t0 = static_cast<int64_t>(sched_item(p.sched, static_cast<uint32_t>(it))) * p.tile;
-        const int count = static_cast<int>(min(static_cast<int64_t>(p.tile), p.N - t0));
+        const int64_t t0 = static_cast<int64_t>(sched_item(p.sched, static_cast<uint32_t>(it))) * kBackTile;
+        const int count = static_cast<int>(min(static_cast<int64_t>(kBackTile), p.N - t0));
+        const T *base = static_cast<const T *>(p.logits) + t0 * p.ld;
+        // offsets outside their contract leave tokens without a group: no gradient
+        auto is_live = [&](int r) {
+            return r < count && (!p.mask || p.mask[t0 + r]) && (!p.offs || (t0 + r >= so[0] && t0 + r < so[p.G]));
+        };
         int have = -1;
         float a[EL];  // the group's counts times its factor
-        for (int b = w * rows_warp; b < count; b += kWarps * rows_warp) {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) a[e] = 0.0f;
+        Logits<T, VEC, NV> cur, nxt;
+        bool live = is_live(w * rows_warp + my_row), live_next = false;
+        cur.load(base + static_cast<int64_t>(w * rows_warp + my_row) * p.ld, sub, p.lanes, p.E, live);
+        for (int b = w * rows_warp; b < count; b += step) {
             const int r = b + my_row;
-            const int64_t t = t0 + r;
-            bool live = r < count && (!p.mask || p.mask[t]);
-            int g = 0;
-            if (p.offs) {
-                // offsets outside their contract leave tokens without a group: no gradient
-                live = live && t >= so[0] && t < so[p.G];
-                if (live) g = group_of(so, p.G, t);
-            }
+            live_next = is_live(r + step);
+            nxt.load(base + static_cast<int64_t>(r + step) * p.ld, sub, p.lanes, p.E, live_next);
+            const int g = live && p.offs ? group_of(so, p.G, t0 + r) : 0;
             if (live && g != have) {
                 have = g;
-                const float nt = static_cast<float>(max(p.tokens[g], 1));
+                const float nt = static_cast<float>(max(__ldg(p.tokens + g), 1));
                 const float f = up / (nt * nt);
+                const int32_t *counts = p.counts + static_cast<int64_t>(g) * p.E;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
                         const int e = (i * p.lanes + sub) * VEC + j;
-                        a[i * VEC + j] = e < p.E ? __fmul_rn(f, static_cast<float>(__ldg(p.counts + static_cast<int64_t>(g) * p.E + e))) : 0.0f;
+                        a[i * VEC + j] = e < p.E ? __fmul_rn(f, static_cast<float>(__ldg(counts + e))) : 0.0f;
                     }
             }
-            float x[EL], q[EL];
-            load_logits<T, VEC, NV>(x, static_cast<const T *>(p.logits) + t * p.ld, sub, p.lanes, p.E, live);
-#pragma unroll
-            for (int e = 0; e < EL; ++e) q[e] = x[e];
-            scores(q, p.lanes, p.sigmoid);
+            float q[EL];
+            cur.get(q);
+            scores(q, p.lanes, SIGMOID);
             float inner = 0.0f;
 #pragma unroll
-            for (int e = 0; e < EL; ++e) inner = __fmaf_rn(live ? a[e] : 0.0f, q[e], inner);
+            for (int e = 0; e < EL; ++e) inner = __fmaf_rn(a[e], live ? q[e] : 0.0f, inner);
             inner = lanes_sum(inner, p.lanes);
-            if (r >= count) continue;
-            T *dst = static_cast<T *>(p.dlogits) + t * p.ld_d;
+            if (r < count) {
+                T *dst = static_cast<T *>(p.dlogits) + (t0 + r) * p.ld_d;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = (i * p.lanes + sub) * VEC;
-                if (e >= p.E) continue;
-                float d[VEC];
+                for (int i = 0; i < NV; ++i) {
+                    const int e = (i * p.lanes + sub) * VEC;
+                    if (e >= p.E) continue;
+                    float d[VEC], x[VEC];
+                    if (SIGMOID) unpack<T, VEC>(cur.v[i], x);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const int k = i * VEC + j;
-                    d[j] = live ? __fmul_rn(q[k], __fadd_rn(a[k], -inner)) : 0.0f;
-                    if (live && p.sigmoid) d[j] = __fdividef(d[j], __fadd_rn(1.0f, ex2(__fmul_rn(x[k], kLog2e))));
+                    for (int j = 0; j < VEC; ++j) {
+                        const int k = i * VEC + j;
+                        d[j] = __fmul_rn(q[k], __fadd_rn(a[k], -inner));
+                        if (SIGMOID) d[j] = __fdividef(d[j], __fadd_rn(1.0f, ex2(__fmul_rn(x[j], kLog2e))));
+                        if (!live) d[j] = 0.0f;
+                    }
+                    raw_t<T, VEC> *to = reinterpret_cast<raw_t<T, VEC> *>(dst + e);
+                    if (p.accumulate) {
+                        float old[VEC];
+                        unpack<T, VEC>(*to, old);
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) d[j] = live ? __fadd_rn(old[j], d[j]) : old[j];
+                    }
+                    *to = pack<T, VEC>(d);
                 }
-                raw_t<T, VEC> *to = reinterpret_cast<raw_t<T, VEC> *>(dst + e);
-                if (p.accumulate) {
-                    float old[VEC];
-                    unpack<T, VEC>(*to, old);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) d[j] = live ? __fadd_rn(old[j], d[j]) : old[j];
-                }
-                *to = pack<T, VEC>(d);
             }
+            cur = nxt;
+            live = live_next;
         }
     }
 }
@@ -423,7 +497,7 @@ int32_t balance_tile(int64_t N, int64_t E) {
 
 struct BalLayout {
     int64_t tiles;
-    size_t done, group_loss, mass, part, total;
+    size_t done, group_loss, mass, part, live, total;
 };
 
 BalLayout balance_layout(int64_t N, int64_t E, int64_t G) {
@@ -434,16 +508,19 @@ BalLayout balance_layout(int64_t N, int64_t E, int64_t G) {
     L.group_loss = L.done + align_up(static_cast<size_t>(G) * 4);
     L.mass = L.group_loss + align_up(static_cast<size_t>(G) * 4);
     L.part = L.mass + align_up(static_cast<size_t>(L.tiles) * E * 4);
-    L.total = L.part + align_up(static_cast<size_t>(L.tiles) * (E + 1) * 4);
+    L.live = L.part + align_up(static_cast<size_t>(L.tiles) * E * 4);
+    L.total = L.live + align_up(static_cast<size_t>(L.tiles) * 4);
     return L;
 }
 
 template <typename T, int VEC, int NV>
 dgr_status launch_nv(bool backward, const BalParams &p, unsigned grid, cudaStream_t s) {
     if (backward) {
-        balance_backward<T, VEC, NV><<<grid, kThreads, p.offs ? (p.G + 1) * 8 : 0, s>>>(p);
+        const size_t smem = p.offs ? (p.G + 1) * 8 : 0;
+        if (p.sigmoid) balance_backward<T, VEC, NV, true><<<grid, kBackThreads, smem, s>>>(p);
+        else balance_backward<T, VEC, NV, false><<<grid, kBackThreads, smem, s>>>(p);
     } else {
-        const size_t cols = static_cast<size_t>(kWarps) * p.E * 4, fold = kThreads * 8;  // the fold reuses the columns' place
+        const size_t cols = static_cast<size_t>(kWarps) * p.E * 4, fold = kThreads * (p.E % 4 == 0 ? 32 : 8);  // the fold reuses the columns' place
         const size_t smem = (p.G + 1) * 12 + p.E * 4 + (cols > fold ? cols : fold);
         if (smem > 47 * 1024 && cudaFuncSetAttribute(balance_forward<T, VEC, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
             return DGR_ERR_CUDA;
@@ -454,19 +531,20 @@ dgr_status launch_nv(bool backward, const BalParams &p, unsigned grid, cudaStrea
 
 template <typename T, int VEC>
 dgr_status launch_vec(bool backward, BalParams &p, unsigned grid, cudaStream_t s) {
+    // 16 logits a lane (fewer lanes, fewer shuffles) until a row takes the whole warp
     const int n_vec = (p.E + VEC - 1) / VEC;
     p.lanes = 1;
-    while (p.lanes < 32 && p.lanes < n_vec) p.lanes <<= 1;
-    const int nv = (n_vec + 31) / 32;
-    if (nv <= 1) return launch_nv<T, VEC, 1>(backward, p, grid, s);
-    if (nv <= 2) return launch_nv<T, VEC, 2>(backward, p, grid, s);
-    if (nv <= 4) return launch_nv<T, VEC, 4>(backward, p, grid, s);
-    if (nv <= 8) return launch_nv<T, VEC, 8>(backward, p, grid, s);
-    if constexpr (VEC == 1) {
+    while (p.lanes < 32 && p.lanes * 16 < n_vec * VEC) p.lanes <<= 1;
+    const int nv = (n_vec + p.lanes - 1) / p.lanes;
+    if constexpr (VEC == 4) {
+        if (nv <= 2) return launch_nv<T, VEC, 2>(backward, p, grid, s);
+        if (nv <= 4) return launch_nv<T, VEC, 4>(backward, p, grid, s);
+        return launch_nv<T, VEC, 8>(backward, p, grid, s);
+    } else {
+        if (nv <= 8) return launch_nv<T, VEC, 8>(backward, p, grid, s);
         if (nv <= 16) return launch_nv<T, VEC, 16>(backward, p, grid, s);
         return launch_nv<T, VEC, 32>(backward, p, grid, s);
     }
-    return DGR_ERR_UNSUPPORTED;
 }
 
 // Vectors of 4 experts where every row starts at a multiple of them.
@@ -527,6 +605,8 @@ extern "C" dgr_status dgr_router_balance(const void *logits, int32_t dtype, int6
     p.group_loss = reinterpret_cast<float *>(b + L.group_loss);
     p.mass = reinterpret_cast<float *>(b + L.mass);
     p.part = reinterpret_cast<int32_t *>(b + L.part);
+    p.live = reinterpret_cast<int32_t *>(b + L.live);
+    p.k_magic = ((1ull << 40) + K - 1) / K;
     p.sched = sched_setting();
     const unsigned grid = sched_grid(static_cast<unsigned>(L.tiles > 0 ? L.tiles : 1));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -555,13 +635,12 @@ extern "C" dgr_status dgr_router_balance_backward(const void *logits, int32_t dt
     BalParams p{};
     p.logits = logits, p.ld = ld, p.mask = mask, p.offs = d_offs;
     p.N = static_cast<int32_t>(N), p.E = E, p.K = K, p.G = G, p.sigmoid = score;
-    p.tile = 64;
     p.coef = static_cast<float>(static_cast<double>(coeff) * E / (static_cast<double>(G) * K));
     p.counts = const_cast<int32_t *>(counts), p.tokens = const_cast<int32_t *>(tokens), p.dloss = dloss;
     p.dlogits = dlogits, p.ld_d = ld_d, p.accumulate = accumulate ? 1 : 0;
-    const uint32_t tiles = static_cast<uint32_t>((N + p.tile - 1) / p.tile);
+    const uint32_t tiles = static_cast<uint32_t>((N + kBackTile - 1) / kBackTile);
     p.sched = sched_for(tiles);
-    const unsigned most = 152 * 8;
+    const unsigned most = 152 * 16;
     const unsigned grid = sched_grid(tiles < most ? tiles : most);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return es == 2 ? launch_type<bf16>(true, p, grid, s) : launch_type<float>(true, p, grid, s);
