@@ -111,8 +111,9 @@ def _check(fn: str, rc: int) -> None:
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:  # the handle of torch's current stream, without building a Stream object (2.8 us) around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -358,6 +359,8 @@ def _rows(t: torch.Tensor, shape, dtype, name: str) -> int:
     """Row stride of a 2-D tensor of the given shape and type with contiguous rows."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+    if t.is_contiguous():
+        return shape[1]
     if t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name}: contiguous rows expected")
     return t.stride(0) if shape[0] > 1 else shape[1]  # a single row's stride says nothing

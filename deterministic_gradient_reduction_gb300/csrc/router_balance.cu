@@ -11,8 +11,7 @@
 //
 // Forward, one launch: a CTA per tile of consecutive tokens of one group. A row
 // is held by the fewest lanes that cover it with 16 logits each, so a softmax's
-// maximum and sum cost log2(E / 16) shuffles for several rows at a time; the
-// next rows' logits are loaded before the present ones are worked on. A lane
+// maximum and sum cost log2(E / 16) shuffles for several rows at a time. A lane
 // keeps the running sums of its own experts' probabilities over the tile, which
 // lanes, then warps, then tiles add in ascending order. The counts are integer
 // sums (shared-memory integer atomics: any order, the same value). The CTA that
@@ -25,10 +24,10 @@ namespace {
 
 using namespace row;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+// Forward threads: 1024 while a lane holds up to 16 logits (64 registers a thread), 512 beyond.
+template <int EL>
+constexpr int kThreadsFor = EL <= 16 ? 1024 : 512;
 constexpr int kBackThreads = 256;
-constexpr int kBackTile = 128;  // tokens a backward tile
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxTile = 16384;  // tokens: a lane's running sums stay short
@@ -75,72 +74,69 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
     return v;
 }
 
-// The row's probabilities in place of its logits (lanes without an expert
-// hold -inf and get 0; a row of -inf only gets 0 everywhere). A NaN or +inf
-// logit makes the row NaN, as the formula does.
-template <int E>
-__device__ __forceinline__ void scores(float (&x)[E], int lanes, int sigmoid) {
+// The row's probabilities in place of its logits (-inf where a lane has no
+// expert); 0 for a row that is not live, whose logits must be finite, and for
+// a row of -inf only. A NaN or +inf logit makes the row NaN, as the formula does.
+template <int E, bool SIGMOID>
+__device__ __forceinline__ void scores(float (&x)[E], int lanes, bool live) {
     float m = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
     m = lanes_max(m, lanes);
     const bool empty = m == -INFINITY;
-    float s = 0.0f;
-    if (!sigmoid) {
-        const float c = empty ? 0.0f : m;
+    if constexpr (!SIGMOID) {
+        if (fabsf(m) > 1e38f && !empty) {  // m log2(e) may be beyond the type's range: subtract first
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            x[e] = ex2(__fmul_rn(__fadd_rn(x[e], -c), kLog2e));
-            s = __fadd_rn(s, x[e]);
+            for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], -m);
+            m = 0.0f;
         }
+        vec_fma(x, kLog2e, empty ? 0.0f : -__fmul_rn(m, kLog2e));
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = ex2(x[e]);
     } else {
         // all logits below 0: each sigmoid divided by exp(m), so that rows far
         // below 0 keep their shares
         const bool low = m < 0.0f && !empty;
+        const float c = low ? m : 0.0f, k = low ? kLog2e : -kLog2e;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float a = low ? ex2(__fmul_rn(__fadd_rn(x[e], -m), kLog2e)) : 1.0f;
-            x[e] = __fdividef(a, __fadd_rn(1.0f, ex2(__fmul_rn(low ? x[e] : -x[e], kLog2e))));
-            s = __fadd_rn(s, x[e]);
+            const float a = low ? ex2(__fmul_rn(__fadd_rn(x[e], -c), kLog2e)) : 1.0f;
+            x[e] = __fdividef(a, __fadd_rn(1.0f, ex2(__fmul_rn(x[e], k))));
         }
     }
-    s = lanes_sum(s, lanes);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], inv);
+    const float s = lanes_sum(vec_sum(x), lanes);
+    vec_scale(x, live && s != 0.0f ? 1.0f / s : 0.0f);
 }
 
 // A lane's experts: vector i of NV starts at expert (i * lanes + sub) * VEC.
-template <typename T, int VEC, int NV>
-struct Logits {
-    raw_t<T, VEC> v[NV];
-    uint32_t there;  // vectors with experts
+// FULL: the lanes' vectors cover exactly the E experts. Rows that are not live
+// are not read (zeros).
+template <typename T, int VEC, int NV, bool FULL>
+__device__ __forceinline__ void load_raw(raw_t<T, VEC> (&v)[NV], const T *row, int sub, int lanes, int E, bool live) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = (i * lanes + sub) * VEC;
+        v[i] = raw_t<T, VEC>{};
+        if (live && (FULL || e < E)) v[i] = *reinterpret_cast<const raw_t<T, VEC> *>(row + e);
+    }
+}
 
-    __device__ __forceinline__ void load(const T *row, int sub, int lanes, int E, bool live) {
-        there = 0;
+template <typename T, int VEC, int NV, bool FULL>
+__device__ __forceinline__ void to_logits(float (&x)[NV * VEC], const raw_t<T, VEC> (&v)[NV], int sub, int lanes, int E) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (i * lanes + sub) * VEC;
-            if (live && e < E) {
-                v[i] = *reinterpret_cast<const raw_t<T, VEC> *>(row + e);
-                there |= 1u << i;
-            }
-        }
+    for (int i = 0; i < NV; ++i) {
+        unpack<T, VEC>(v[i], x + i * VEC);
+        if (!FULL && (i * lanes + sub) * VEC >= E)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) x[i * VEC + j] = -INFINITY;
     }
-    __device__ __forceinline__ void get(float *x) const {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack<T, VEC>(v[i], x + i * VEC);
-            if (!(there >> i & 1))
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) x[i * VEC + j] = -INFINITY;
-        }
-    }
-};
+}
 
 // tbase[g] = first tile of group g, offsets into so[]; false when the offsets
 // break their contract. Every block computes the same.
+template <int kThreads>
 __device__ bool group_tiles(const BalParams &p, int32_t *tbase, int64_t *so, int32_t *wsum, int32_t *bad) {
+    constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (!p.offs) {
         if (tid == 0) {
@@ -199,7 +195,7 @@ __device__ __forceinline__ int group_of(const I *table, int n, I v) {
 // tiles (way w takes w, w + ways, ...), their sums are added in ascending
 // order. Writes the group's counts; returns this thread's part of their dot
 // product with the probabilities.
-template <int CV>
+template <int CV, int kThreads>
 __device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *buf) {
     const int tid = threadIdx.x, n_col = p.E / CV;
     int span = 1;
@@ -248,8 +244,9 @@ __device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *
     return dot;
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
+template <typename T, int VEC, int NV, bool FULL, bool SIGMOID>
+__global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const BalParams p) {
+    constexpr int kThreads = kThreadsFor<NV * VEC>, kWarps = kThreads / 32;
     extern __shared__ char smem[];
     int64_t *so = reinterpret_cast<int64_t *>(smem);                        // [G + 1]
     int32_t *tbase = reinterpret_cast<int32_t *>(so + p.G + 1);             // [G + 1]
@@ -259,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
     __shared__ float red[32];
     constexpr int EL = NV * VEC;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    if (!group_tiles(p, tbase, so, wsum, &bad)) {
+    if (!group_tiles<kThreads>(p, tbase, so, wsum, &bad)) {
         if (blockIdx.x == 0 && tid == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereOffsets);
         return;
     }
@@ -274,10 +271,14 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
         if (blockIdx.x == 0 && tid == 0) *p.loss = 0.0f;
         return;
     }
-    if (tid == 0) n_groups = 0;
-    __syncthreads();
-    for (int g = tid; g < p.G; g += kThreads)
-        if (tbase[g + 1] > tbase[g]) atomicAdd(&n_groups, 1);
+    if (p.G > 1) {
+        if (tid == 0) n_groups = 0;
+        __syncthreads();
+        for (int g = tid; g < p.G; g += kThreads)
+            if (tbase[g + 1] > tbase[g]) atomicAdd(&n_groups, 1);
+    } else if (tid == 0) {
+        n_groups = 1;
+    }
     const int sub = lane & (p.lanes - 1), rows_warp = 32 / p.lanes, my_row = lane / p.lanes;
     const Sched sched = sched_over(p.sched, static_cast<uint32_t>(n_tiles));
     for (int it = blockIdx.x; it < n_tiles; it += gridDim.x) {
@@ -291,9 +292,9 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
         // the first rows' logits are on their way while the counts are made
         const T *base = static_cast<const T *>(p.logits) + t0 * p.ld;
         auto is_live = [&](int r) { return r < count && (!p.mask || p.mask[t0 + r]); };
-        Logits<T, VEC, NV> cur, nxt;
-        bool live = is_live(w * rows_warp + my_row), live_next = false;
-        cur.load(base + static_cast<int64_t>(w * rows_warp + my_row) * p.ld, sub, p.lanes, p.E, live);
+        raw_t<T, VEC> v[NV];
+        bool live = is_live(w * rows_warp + my_row);
+        load_raw<T, VEC, NV, FULL>(v, base + static_cast<int64_t>(w * rows_warp + my_row) * p.ld, sub, p.lanes, p.E, live);
         const int n_ids = count * p.K;
         for (int i0 = tid; i0 < n_ids; i0 += 4 * kThreads) {
             int32_t id[4];
@@ -326,16 +327,14 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
 #pragma unroll
         for (int e = 0; e < EL; ++e) acc[e] = 0.0f;
         for (int b = w * rows_warp; b < count; b += kWarps * rows_warp) {
-            const int r = b + kWarps * rows_warp + my_row;
-            live_next = is_live(r);
-            nxt.load(base + static_cast<int64_t>(r) * p.ld, sub, p.lanes, p.E, live_next);
             float x[EL];
-            cur.get(x);
-            scores(x, p.lanes, p.sigmoid);
-#pragma unroll
-            for (int e = 0; e < EL; ++e) acc[e] = __fadd_rn(acc[e], live ? x[e] : 0.0f);
-            cur = nxt;
-            live = live_next;
+            to_logits<T, VEC, NV, FULL>(x, v, sub, p.lanes, p.E);
+            const bool was = live;
+            const int r = b + kWarps * rows_warp + my_row;
+            live = is_live(r);
+            load_raw<T, VEC, NV, FULL>(v, base + static_cast<int64_t>(r) * p.ld, sub, p.lanes, p.E, live);
+            scores<EL, SIGMOID>(x, p.lanes, was);
+            vec_add(acc, x);
         }
 #pragma unroll
         for (int e = 0; e < EL; ++e)
@@ -350,40 +349,55 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
                 }
         }
         __syncthreads();
-        float *mass = p.mass + static_cast<int64_t>(tile) * p.E;
-        int32_t *part = p.part + static_cast<int64_t>(tile) * p.E;
-        for (int e = tid; e < p.E; e += kThreads) {
-            float v = cols[e];
-#pragma unroll
-            for (int k = 1; k < kWarps; ++k) v = __fadd_rn(v, cols[k * p.E + e]);
-            mass[e] = v;
-            part[e] = hist[e];
-        }
-        if (tid == 0) p.live[tile] = valid;
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) last = atomicAdd(&p.done[g], 1) == tbase[g + 1] - tbase[g] - 1;
-        __syncthreads();
-        if (!last) continue;
-        // this group's tiles are all in: fold them
-        __threadfence();
         const int first = tbase[g], n = tbase[g + 1] - first;
-        int32_t tokens = 0;
-        for (int j = tid; j < n; j += kThreads) tokens += __ldcg(p.live + first + j);
-        if (tid == 0) valid = 0;
-        __syncthreads();
-        tokens = __reduce_add_sync(0xffffffffu, tokens);
-        if (lane == 0 && tokens) atomicAdd(&valid, tokens);
-        const float dot = p.E % 4 == 0 ? fold_tiles<4>(p, first, n, g, cols) : fold_tiles<1>(p, first, n, g, cols);
+        auto column = [&](int e) {
+            float v = cols[e];
+#pragma unroll 8
+            for (int k = 1; k < kWarps; ++k) v = __fadd_rn(v, cols[k * p.E + e]);
+            return v;
+        };
+        float dot = 0.0f;
+        if (n == 1) {  // the group's only tile
+            for (int e = tid; e < p.E; e += kThreads) {
+                p.counts[static_cast<int64_t>(g) * p.E + e] = hist[e];
+                dot = __fmaf_rn(static_cast<float>(hist[e]), column(e), dot);
+            }
+        } else {
+            for (int e = tid; e < p.E; e += kThreads) {
+                p.mass[static_cast<int64_t>(tile) * p.E + e] = column(e);
+                p.part[static_cast<int64_t>(tile) * p.E + e] = hist[e];
+            }
+            if (tid == 0) p.live[tile] = valid;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) last = atomicAdd(&p.done[g], 1) == n - 1;
+            __syncthreads();
+            if (!last) continue;
+            // this group's tiles are all in: fold them
+            __threadfence();
+            int32_t tokens = 0;
+            for (int j = tid; j < n; j += kThreads) tokens += __ldcg(p.live + first + j);
+            if (tid == 0) valid = 0;
+            __syncthreads();
+            tokens = __reduce_add_sync(0xffffffffu, tokens);
+            if (lane == 0 && tokens) atomicAdd(&valid, tokens);
+            dot = p.E % 4 == 0 ? fold_tiles<4, kThreads>(p, first, n, g, cols) : fold_tiles<1, kThreads>(p, first, n, g, cols);
+        }
         float s[1] = {dot};
         block_sum<1>(s, red, kWarps);
         if (tid == 0) {
             const float nt = static_cast<float>(max(valid, 1));
+            const float loss = p.coef * s[0] / (nt * nt);
             p.tokens[g] = valid;
-            p.group_loss[g] = p.coef * s[0] / (nt * nt);
-            p.done[g] = 0;  // ready for the next call
-            __threadfence();
-            last = atomicAdd(&p.hdr->pad[0], 1) == n_groups - 1;
+            if (n > 1) p.done[g] = 0;  // ready for the next call
+            if (n_groups == 1) {
+                *p.loss = loss;
+                last = 0;
+            } else {
+                p.group_loss[g] = loss;
+                __threadfence();
+                last = atomicAdd(&p.hdr->pad[0], 1) == n_groups - 1;
+            }
         }
         __syncthreads();
         if (!last) continue;
@@ -400,88 +414,93 @@ __global__ void __launch_bounds__(kThreads) balance_forward(const BalParams p) {
     }
 }
 
-template <typename T, int VEC, int NV, bool SIGMOID>
+// A warp takes rows_warp consecutive rows at a time; the next ones are on
+// their way while it works. Rows are independent: no order to keep.
+template <typename T, int VEC, int NV, bool FULL, bool SIGMOID>
 __global__ void __launch_bounds__(kBackThreads) balance_backward(const BalParams p) {
     extern __shared__ char smem[];
     int64_t *so = reinterpret_cast<int64_t *>(smem);  // [G + 1] when there are offsets
     constexpr int EL = NV * VEC, kBackWarps = kBackThreads / 32;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     if (p.offs) {
         for (int g = tid; g <= p.G; g += kBackThreads) so[g] = p.offs[g];
         __syncthreads();
     }
     const int sub = lane & (p.lanes - 1), rows_warp = 32 / p.lanes, my_row = lane / p.lanes;
-    const int step = kBackWarps * rows_warp;
     const float up = p.dloss ? __fmul_rn(__ldg(p.dloss), p.coef) : p.coef;
-    const int n_tiles = (p.N + kBackTile - 1) / kBackTile;
-    for (int it = blockIdx.x; it < n_tiles; it += gridDim.x) {
-        const int64_t t0 = static_cast<int64_t>(sched_item(p.sched, static_cast<uint32_t>(it))) * kBackTile;
-        const int count = static_cast<int>(min(static_cast<int64_t>(kBackTile), p.N - t0));
-        const T *base = static_cast<const T *>(p.logits) + t0 * p.ld;
-        // offsets outside their contract leave tokens without a group: no gradient
-        auto is_live = [&](int r) {
-            return r < count && (!p.mask || p.mask[t0 + r]) && (!p.offs || (t0 + r >= so[0] && t0 + r < so[p.G]));
-        };
-        int have = -1;
-        float a[EL];  // the group's counts times its factor
+    // offsets outside their contract leave tokens without a group: no gradient
+    auto is_live = [&](int64_t t) {
+        return t < p.N && (!p.mask || p.mask[t]) && (!p.offs || (t >= so[0] && t < so[p.G]));
+    };
+    const T *logits = static_cast<const T *>(p.logits);
+    uint32_t item = blockIdx.x * kBackWarps + (tid >> 5);
+    const uint32_t n_items = p.sched.n, step = gridDim.x * kBackWarps;
+    if (item >= n_items) return;
+    auto row_of = [&](uint32_t i) { return static_cast<int64_t>(sched_item(p.sched, i)) * rows_warp + my_row; };
+    int have = -1;
+    float a[EL];  // the group's counts times its factor
 #pragma unroll
-        for (int e = 0; e < EL; ++e) a[e] = 0.0f;
-        Logits<T, VEC, NV> cur, nxt;
-        bool live = is_live(w * rows_warp + my_row), live_next = false;
-        cur.load(base + static_cast<int64_t>(w * rows_warp + my_row) * p.ld, sub, p.lanes, p.E, live);
-        for (int b = w * rows_warp; b < count; b += step) {
-            const int r = b + my_row;
-            live_next = is_live(r + step);
-            nxt.load(base + static_cast<int64_t>(r + step) * p.ld, sub, p.lanes, p.E, live_next);
-            const int g = live && p.offs ? group_of(so, p.G, t0 + r) : 0;
-            if (live && g != have) {
-                have = g;
-                const float nt = static_cast<float>(max(__ldg(p.tokens + g), 1));
-                const float f = up / (nt * nt);
-                const int32_t *counts = p.counts + static_cast<int64_t>(g) * p.E;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const int e = (i * p.lanes + sub) * VEC + j;
-                        a[i * VEC + j] = e < p.E ? __fmul_rn(f, static_cast<float>(__ldg(counts + e))) : 0.0f;
-                    }
-            }
-            float q[EL];
-            cur.get(q);
-            scores(q, p.lanes, SIGMOID);
-            float inner = 0.0f;
-#pragma unroll
-            for (int e = 0; e < EL; ++e) inner = __fmaf_rn(a[e], live ? q[e] : 0.0f, inner);
-            inner = lanes_sum(inner, p.lanes);
-            if (r < count) {
-                T *dst = static_cast<T *>(p.dlogits) + (t0 + r) * p.ld_d;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int e = (i * p.lanes + sub) * VEC;
-                    if (e >= p.E) continue;
-                    float d[VEC], x[VEC];
-                    if (SIGMOID) unpack<T, VEC>(cur.v[i], x);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const int k = i * VEC + j;
-                        d[j] = __fmul_rn(q[k], __fadd_rn(a[k], -inner));
-                        if (SIGMOID) d[j] = __fdividef(d[j], __fadd_rn(1.0f, ex2(__fmul_rn(x[j], kLog2e))));
-                        if (!live) d[j] = 0.0f;
-                    }
-                    raw_t<T, VEC> *to = reinterpret_cast<raw_t<T, VEC> *>(dst + e);
-                    if (p.accumulate) {
-                        float old[VEC];
-                        unpack<T, VEC>(*to, old);
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) d[j] = live ? __fadd_rn(old[j], d[j]) : old[j];
-                    }
-                    *to = pack<T, VEC>(d);
-                }
-            }
-            cur = nxt;
-            live = live_next;
+    for (int e = 0; e < EL; ++e) a[e] = 0.0f;
+    raw_t<T, VEC> v[NV], next[NV];
+    int64_t t = row_of(item);
+    bool live = is_live(t);
+    load_raw<T, VEC, NV, FULL>(v, logits + t * p.ld, sub, p.lanes, p.E, live);
+    for (;;) {
+        const bool more = item + step < n_items;
+        int64_t t_next = 0;
+        bool live_next = false;
+        if (more) {
+            t_next = row_of(item + step);
+            live_next = is_live(t_next);
+            load_raw<T, VEC, NV, FULL>(next, logits + t_next * p.ld, sub, p.lanes, p.E, live_next);
         }
+        const int g = live && p.offs ? group_of(so, p.G, t) : 0;
+        if (live && g != have) {
+            have = g;
+            const float nt = static_cast<float>(max(__ldg(p.tokens + g), 1));
+            const float f = up / (nt * nt);
+            const int32_t *counts = p.counts + static_cast<int64_t>(g) * p.E;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = (i * p.lanes + sub) * VEC + j;
+                    a[i * VEC + j] = FULL || e < p.E ? __fmul_rn(f, static_cast<float>(__ldg(counts + e))) : 0.0f;
+                }
+        }
+        float q[EL];
+        to_logits<T, VEC, NV, FULL>(q, v, sub, p.lanes, p.E);
+        scores<EL, SIGMOID>(q, p.lanes, live);
+        const float inner = lanes_sum(vec_dot(a, q), p.lanes);
+        if (t < p.N) {
+            T *dst = static_cast<T *>(p.dlogits) + t * p.ld_d;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = (i * p.lanes + sub) * VEC;
+                if (!FULL && e >= p.E) continue;
+                float d[VEC], x[VEC];
+                if (SIGMOID) unpack<T, VEC>(v[i], x);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    d[j] = __fmul_rn(q[i * VEC + j], __fadd_rn(a[i * VEC + j], -inner));  // 0 where not live: q is
+                    if (SIGMOID) d[j] = __fdividef(d[j], __fadd_rn(1.0f, ex2(__fmul_rn(x[j], kLog2e))));
+                }
+                raw_t<T, VEC> *to = reinterpret_cast<raw_t<T, VEC> *>(dst + e);
+                if (p.accumulate) {
+                    float old[VEC];
+                    unpack<T, VEC>(*to, old);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) d[j] = live ? __fadd_rn(old[j], d[j]) : old[j];
+                }
+                *to = pack<T, VEC>(d);
+            }
+        }
+        if (!more) break;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = next[i];
+        t = t_next;
+        live = live_next;
+        item += step;
     }
 }
 
@@ -513,20 +532,33 @@ BalLayout balance_layout(int64_t N, int64_t E, int64_t G) {
     return L;
 }
 
-template <typename T, int VEC, int NV>
-dgr_status launch_nv(bool backward, const BalParams &p, unsigned grid, cudaStream_t s) {
+template <typename T, int VEC, int NV, bool FULL, bool SIGMOID>
+dgr_status launch_one(bool backward, BalParams &p, unsigned grid, cudaStream_t s) {
     if (backward) {
-        const size_t smem = p.offs ? (p.G + 1) * 8 : 0;
-        if (p.sigmoid) balance_backward<T, VEC, NV, true><<<grid, kBackThreads, smem, s>>>(p);
-        else balance_backward<T, VEC, NV, false><<<grid, kBackThreads, smem, s>>>(p);
+        const int64_t rows_warp = 32 / p.lanes;
+        p.sched = sched_for(static_cast<uint32_t>((p.N + rows_warp - 1) / rows_warp));
+        // 3 to 4 CTAs an SM are resident; each warp then has its share of the rows
+        const unsigned want = (p.sched.n + kBackThreads / 32 - 1) / (kBackThreads / 32), most = 152 * 4;
+        balance_backward<T, VEC, NV, FULL, SIGMOID><<<sched_grid(want < most ? want : most), kBackThreads, p.offs ? (p.G + 1) * 8 : 0, s>>>(p);
     } else {
-        const size_t cols = static_cast<size_t>(kWarps) * p.E * 4, fold = kThreads * (p.E % 4 == 0 ? 32 : 8);  // the fold reuses the columns' place
+        constexpr int threads = kThreadsFor<NV * VEC>;
+        const size_t cols = static_cast<size_t>(threads / 32) * p.E * 4, fold = threads * (p.E % 4 == 0 ? 32 : 8);  // the fold reuses the columns' place
         const size_t smem = (p.G + 1) * 12 + p.E * 4 + (cols > fold ? cols : fold);
-        if (smem > 47 * 1024 && cudaFuncSetAttribute(balance_forward<T, VEC, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        auto *k = balance_forward<T, VEC, NV, FULL, SIGMOID>;
+        if (smem > 47 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
             return DGR_ERR_CUDA;
-        balance_forward<T, VEC, NV><<<grid, kThreads, smem, s>>>(p);
+        k<<<grid, threads, smem, s>>>(p);
     }
     return launch_status();
+}
+
+template <typename T, int VEC, int NV>
+dgr_status launch_nv(bool backward, BalParams &p, unsigned grid, cudaStream_t s) {
+    const bool full = p.E == p.lanes * NV * VEC;
+    if constexpr (VEC > 1) {
+        if (full) return p.sigmoid ? launch_one<T, VEC, NV, true, true>(backward, p, grid, s) : launch_one<T, VEC, NV, true, false>(backward, p, grid, s);
+    }
+    return p.sigmoid ? launch_one<T, VEC, NV, false, true>(backward, p, grid, s) : launch_one<T, VEC, NV, false, false>(backward, p, grid, s);
 }
 
 template <typename T, int VEC>
@@ -638,10 +670,6 @@ extern "C" dgr_status dgr_router_balance_backward(const void *logits, int32_t dt
     p.coef = static_cast<float>(static_cast<double>(coeff) * E / (static_cast<double>(G) * K));
     p.counts = const_cast<int32_t *>(counts), p.tokens = const_cast<int32_t *>(tokens), p.dloss = dloss;
     p.dlogits = dlogits, p.ld_d = ld_d, p.accumulate = accumulate ? 1 : 0;
-    const uint32_t tiles = static_cast<uint32_t>((N + kBackTile - 1) / kBackTile);
-    p.sched = sched_for(tiles);
-    const unsigned most = 152 * 16;
-    const unsigned grid = sched_grid(tiles < most ? tiles : most);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return es == 2 ? launch_type<bf16>(true, p, grid, s) : launch_type<float>(true, p, grid, s);
+    return es == 2 ? launch_type<bf16>(true, p, 0, s) : launch_type<float>(true, p, 0, s);
 }

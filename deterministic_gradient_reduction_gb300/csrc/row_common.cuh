@@ -132,6 +132,66 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// a b + c, two at a time, each rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// v[e] = v[e] * k + c, v[e] = v[e] * k, r[e] = a[e] * b[e] + r[e], in pairs (N even, or 1).
+template <int N>
+__device__ __forceinline__ void vec_fma(float (&v)[N], float k, float c) {
+    if constexpr (N == 1) v[0] = __fmaf_rn(v[0], k, c);
+#pragma unroll
+    for (int e = 0; e + 1 < N; e += 2) {
+        const float2 r = fma2(make_float2(v[e], v[e + 1]), make_float2(k, k), make_float2(c, c));
+        v[e] = r.x, v[e + 1] = r.y;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void vec_scale(float (&v)[N], float k) {
+    if constexpr (N == 1) v[0] = __fmul_rn(v[0], k);
+#pragma unroll
+    for (int e = 0; e + 1 < N; e += 2) {
+        const float2 r = mul2(make_float2(v[e], v[e + 1]), make_float2(k, k));
+        v[e] = r.x, v[e + 1] = r.y;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void vec_add(float (&r)[N], const float (&a)[N]) {
+    if constexpr (N == 1) r[0] = __fadd_rn(r[0], a[0]);
+#pragma unroll
+    for (int e = 0; e + 1 < N; e += 2) {
+        const float2 s = add2(make_float2(r[e], r[e + 1]), make_float2(a[e], a[e + 1]));
+        r[e] = s.x, r[e + 1] = s.y;
+    }
+}
+
+// Sum of v and dot product of a and b: even and odd elements apart, then together.
+template <int N>
+__device__ __forceinline__ float vec_sum(const float (&v)[N]) {
+    if constexpr (N == 1) return v[0];
+    float2 s = make_float2(v[0], v[1]);
+#pragma unroll
+    for (int e = 2; e + 1 < N; e += 2) s = add2(s, make_float2(v[e], v[e + 1]));
+    return __fadd_rn(s.x, s.y);
+}
+
+template <int N>
+__device__ __forceinline__ float vec_dot(const float (&a)[N], const float (&b)[N]) {
+    if constexpr (N == 1) return __fmul_rn(a[0], b[0]);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int e = 0; e + 1 < N; e += 2) s = fma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), s);
+    return __fadd_rn(s.x, s.y);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace row
