@@ -130,7 +130,7 @@ __device__ __forceinline__ void load_raw(raw_t<T, VEC> (&v)[NV], const T *row, i
     for (int i = 0; i < NV; ++i) {
         const int e = (i * lanes + sub) * VEC;
         v[i] = raw_t<T, VEC>{};
-        if (live && (LANES > 0 || e < E)) v[i] = *reinterpret_cast<const raw_t<T, VEC> *>(row + e);
+        load_if<true>(v[i], row + e, live && (LANES > 0 || e < E));
     }
 }
 
@@ -145,23 +145,23 @@ __device__ __forceinline__ void to_logits(float (&x)[NV * VEC], const raw_t<T, V
     }
 }
 
-// tbase[g] = first tile of group g, offsets into so[]; false when the offsets
-// break their contract. Every block computes the same.
+// tbase[g] = first tile of group g, offsets into so[], the groups with tiles;
+// false when the offsets break their contract. Every block computes the same.
 template <int kThreads>
-__device__ bool group_tiles(const BalParams &p, int32_t *tbase, int64_t *so, int32_t *wsum, int32_t *bad) {
+__device__ bool group_tiles(const BalParams &p, int32_t *tbase, int64_t *so, int32_t *wsum, int32_t *n_groups) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (!p.offs) {
         if (tid == 0) {
             so[0] = 0, so[1] = p.N;
             tbase[0] = 0, tbase[1] = (p.N + p.tile - 1) / p.tile;
+            *n_groups = 1;
         }
         __syncthreads();
         return true;
     }
-    if (tid == 0) *bad = 0;
-    __syncthreads();
-    int32_t run = 0;
+    bool broken = false;
+    int32_t run = 0, filled = 0;
     for (int g0 = 0; g0 < p.G; g0 += kThreads) {
         const int g = g0 + tid;
         int32_t c = 0;
@@ -169,7 +169,7 @@ __device__ bool group_tiles(const BalParams &p, int32_t *tbase, int64_t *so, int
             const int64_t a = p.offs[g], b = p.offs[g + 1];
             so[g] = a;
             if (g == p.G - 1) so[p.G] = b;
-            if (b < a || a < 0 || b > p.N || (g == 0 && a != 0) || (g == p.G - 1 && b != p.N)) *bad = 1;
+            if (b < a || a < 0 || b > p.N || (g == 0 && a != 0) || (g == p.G - 1 && b != p.N)) broken = true;
             else c = static_cast<int32_t>((b - a + p.tile - 1) / p.tile);
         }
         int32_t incl = c;
@@ -179,16 +179,15 @@ __device__ bool group_tiles(const BalParams &p, int32_t *tbase, int64_t *so, int
             if (lane >= s) incl += o;
         }
         if (lane == 31) wsum[w] = incl;
-        __syncthreads();
-        int32_t before = run;
-        for (int v = 0; v < w; ++v) before += wsum[v];
-        if (g < p.G) tbase[g] = before + incl - c;
-        for (int v = 0; v < kWarps; ++v) run += wsum[v];
-        __syncthreads();
+        filled += __syncthreads_count(c > 0);
+        const int32_t v = lane < kWarps ? wsum[lane] : 0;
+        if (g < p.G) tbase[g] = run + incl - c;
+        const int32_t before = __reduce_add_sync(0xffffffffu, lane < w ? v : 0);
+        if (g < p.G) tbase[g] += before;
+        run += __reduce_add_sync(0xffffffffu, v);
     }
-    if (tid == 0) tbase[p.G] = run;
-    __syncthreads();
-    return *bad == 0;
+    if (tid == 0) tbase[p.G] = run, *n_groups = filled;
+    return !__syncthreads_or(broken);
 }
 
 // The last g with table[g] <= v (table ascending, table[0] <= v < table[n]):
@@ -204,6 +203,21 @@ __device__ __forceinline__ int group_of(const I *table, int n, I v) {
     return lo;
 }
 
+// The fold's shape: threads that add one expert's ways, and a way's distance in
+// shared memory, such that neighbouring helpers meet different banks.
+struct FoldShape {
+    int ways, helpers, stride;
+};
+template <int CV>
+__host__ __device__ inline FoldShape fold_shape(int E, int threads) {
+    int span = 1;
+    while (span < E / CV && span < threads) span <<= 1;
+    FoldShape f{threads / span, threads / span / CV, 0};
+    f.helpers = f.helpers < 1 ? 1 : f.helpers > 32 ? 32 : f.helpers;
+    f.stride = span + 32 / f.helpers;
+    return f;
+}
+
 // Adds a group's tiles, CV experts a thread: `ways` threads share an expert's
 // tiles (way w takes w, w + ways, ... in ascending order, up to 8 of them in
 // flight), then neighbouring threads add the ways in a fixed order. Writes the
@@ -216,9 +230,10 @@ __device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *
     int span = 1;
     while (span < n_col && span < kThreads) span <<= 1;
     const int ways = kThreads / span, way = tid / span;
-    const int helpers = min(32, max(1, ways / CV));  // threads that add one expert's ways
+    const FoldShape f = fold_shape<CV>(p.E, kThreads);
+    const int log_span = __ffs(span) - 1, log_help = __ffs(f.helpers) - 1, plane = ways * f.stride;
     float dot = 0.0f;
-    int32_t *ibuf = reinterpret_cast<int32_t *>(buf) + CV * kThreads;
+    int32_t *ibuf = reinterpret_cast<int32_t *>(buf) + CV * plane;
     for (int c0 = 0; c0 < n_col; c0 += span) {
         const int col = c0 + (tid & (span - 1));
         float m[CV];
@@ -231,15 +246,14 @@ __device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *
             for (int i = 0; i < kFlight; ++i) {
                 const int t = t0 + i * ways;
                 v[i] = k[i] = make_uint4(0, 0, 0, 0);
-                if (t < n && col < n_col) {
-                    const int64_t at = static_cast<int64_t>(first + t) * p.E + col * CV;
-                    if constexpr (CV == 4) {
-                        v[i] = __ldcg(reinterpret_cast<const uint4 *>(p.mass + at));
-                        k[i] = __ldcg(reinterpret_cast<const uint4 *>(p.part + at));
-                    } else {
-                        v[i].x = __float_as_uint(__ldcg(p.mass + at));
-                        k[i].x = __ldcg(p.part + at);
-                    }
+                const bool on = t < n && col < n_col;
+                const int64_t at = static_cast<int64_t>(first + t) * p.E + col * CV;
+                if constexpr (CV == 4) {  // written by other CTAs of this launch, never read before: no stale line in L1
+                    load_if<false>(v[i], p.mass + at, on);
+                    load_if<false>(k[i], p.part + at, on);
+                } else {
+                    load_if<false>(v[i].x, p.mass + at, on);
+                    load_if<false>(k[i].x, p.part + at, on);
                 }
             }
 #pragma unroll
@@ -251,20 +265,24 @@ __device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < CV; ++j) buf[j * kThreads + tid] = m[j], ibuf[j * kThreads + tid] = c[j];
+        for (int j = 0; j < CV; ++j) {
+            buf[j * plane + way * f.stride + (tid & (span - 1))] = m[j];
+            ibuf[j * plane + way * f.stride + (tid & (span - 1))] = c[j];
+        }
         __syncthreads();
         // `helpers` neighbouring threads an expert (whole warps go round together)
-        const int n_out = span * CV * helpers;
+        const int n_out = span * CV * f.helpers;
         for (int i = tid; i < ((n_out + 31) & ~31); i += kThreads) {
-            const int h = i & (helpers - 1), e = i / helpers, j = e / span, k0 = e - j * span;
+            const int h = i & (f.helpers - 1), e = i >> log_help, j = e >> log_span, k0 = e & (span - 1);
             float v = 0.0f;
             int32_t k = 0;
             if (i < n_out)
-                for (int q = h; q < ways; q += helpers) {
-                    v = __fadd_rn(v, buf[j * kThreads + q * span + k0]);
-                    k += ibuf[j * kThreads + q * span + k0];
+#pragma unroll 4
+                for (int q = h; q < ways; q += f.helpers) {
+                    v = __fadd_rn(v, buf[j * plane + q * f.stride + k0]);
+                    k += ibuf[j * plane + q * f.stride + k0];
                 }
-            for (int s = 1; s < helpers; s <<= 1) {
+            for (int s = 1; s < f.helpers; s <<= 1) {
                 v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, s));
                 k += __shfl_xor_sync(0xffffffffu, k, s);
             }
@@ -277,6 +295,29 @@ __device__ float fold_tiles(const BalParams &p, int first, int n, int g, float *
     return dot;
 }
 
+// Adds EL columns over the row groups of a warp (LANES lanes a row): at each
+// step a lane hands half of its columns to its partner and adds the other half,
+// then put(column, sum) for those that it is left with.
+template <int EL, int LANES, int VEC, int S = 16, typename Put>
+__device__ __forceinline__ void scatter_columns(const float (&acc)[EL], int lane, Put put, int first = 0) {
+    if constexpr (S < LANES) {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) put(first + e, acc[e]);
+    } else if constexpr (EL == 1) {
+        const float v[1] = {__fadd_rn(acc[0], __shfl_xor_sync(0xffffffffu, acc[0], S))};
+        scatter_columns<1, LANES, VEC, S / 2>(v, lane, put, first);  // both lanes hold it
+    } else {
+        const bool up = (lane & S) != 0;
+        float half[EL / 2];
+#pragma unroll
+        for (int e = 0; e < EL / 2; ++e) {
+            const float give = up ? acc[e] : acc[e + EL / 2], keep = up ? acc[e + EL / 2] : acc[e];
+            half[e] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, S));
+        }
+        scatter_columns<EL / 2, LANES, VEC, S / 2>(half, lane, put, first + (up ? EL / 2 : 0));
+    }
+}
+
 template <typename T, int VEC, int NV, int LANES, bool SIGMOID>
 __global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const BalParams p) {
     constexpr int kThreads = kThreadsFor<NV * VEC>, kWarps = kThreads / 32;
@@ -284,12 +325,12 @@ __global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const B
     int64_t *so = reinterpret_cast<int64_t *>(smem);                        // [G + 1]
     int32_t *tbase = reinterpret_cast<int32_t *>(so + p.G + 1);             // [G + 1]
     int32_t *hist = tbase + p.G + 1;                                        // [E]
-    float *cols = reinterpret_cast<float *>(hist + p.E);                    // [kWarps][E], later [kThreads]
-    __shared__ int32_t wsum[kWarps], bad, valid, last, n_groups;
+    float *cols = reinterpret_cast<float *>(hist + p.E);                    // [kWarps][stride], later the fold's
+    __shared__ int32_t wsum[kWarps], valid, last, n_groups;
     __shared__ float red[32];
     constexpr int EL = NV * VEC;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    if (!group_tiles<kThreads>(p, tbase, so, wsum, &bad)) {
+    if (!group_tiles<kThreads>(p, tbase, so, wsum, &n_groups)) {
         if (blockIdx.x == 0 && tid == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereOffsets);
         return;
     }
@@ -304,16 +345,12 @@ __global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const B
         if (blockIdx.x == 0 && tid == 0) *p.loss = 0.0f;
         return;
     }
-    if (p.G > 1) {
-        if (tid == 0) n_groups = 0;
-        __syncthreads();
-        for (int g = tid; g < p.G; g += kThreads)
-            if (tbase[g + 1] > tbase[g]) atomicAdd(&n_groups, 1);
-    } else if (tid == 0) {
-        n_groups = 1;
-    }
     const int lanes = LANES > 0 ? LANES : p.lanes;
     const int sub = lane & (lanes - 1), rows_warp = 32 / lanes, my_row = lane / lanes;
+    int helpers = 32;
+    while (helpers > 1 && p.E * helpers > kThreads) helpers >>= 1;
+    const int log_help = __ffs(helpers) - 1;
+    const int stride = p.E + (32 >> log_help);  // of a warp's columns: its helpers meet different banks
     const Sched sched = sched_over(p.sched, static_cast<uint32_t>(n_tiles));
     for (int it = blockIdx.x; it < n_tiles; it += gridDim.x) {
         const int tile = static_cast<int>(sched_item(sched, static_cast<uint32_t>(it)));
@@ -335,11 +372,10 @@ __global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const B
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = i0 + j * kThreads;
-                id[j] = -1;
-                if (i < n_ids) {
-                    const int r = static_cast<int>((static_cast<uint64_t>(i) * p.k_magic) >> 40);
-                    if (!p.mask || p.mask[t0 + r]) id[j] = __ldg(p.ids + (t0 + r) * p.ld_ids + (i - r * p.K));
-                }
+                const int r = static_cast<int>((static_cast<uint64_t>(i) * p.k_magic) >> 40);
+                uint32_t got = 0xffffffffu;
+                load_if<true>(got, p.ids + (t0 + r) * p.ld_ids + (i - r * p.K), i < n_ids && (!p.mask || p.mask[t0 + r]));
+                id[j] = static_cast<int32_t>(got);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -370,52 +406,65 @@ __global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const B
             scores<EL, LANES, SIGMOID>(x, lanes, was);
             vec_add(acc, x);
         }
+        // rows side by side in the warp: halves of the columns are exchanged, so
+        // that each lane ends with its share of them; without known lanes every
+        // lane adds all
+        float *mine = cols + w * stride;
+        if constexpr (LANES > 0) {
+            scatter_columns<EL, LANES, VEC>(acc, lane, [&](int k, float v) {
+                mine[((k / VEC) * LANES + sub) * VEC + k % VEC] = v;
+            });
+        } else {
+            for (int s = lanes; s < 32; s <<= 1)
 #pragma unroll
-        for (int e = 0; e < EL; ++e)
-            for (int s = lanes; s < 32; s <<= 1) acc[e] = __fadd_rn(acc[e], __shfl_xor_sync(0xffffffffu, acc[e], s));
-        if (lane < lanes) {
+                for (int e = 0; e < EL; ++e) acc[e] = __fadd_rn(acc[e], __shfl_xor_sync(0xffffffffu, acc[e], s));
+            if (lane < lanes) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const int e = (i * lanes + sub) * VEC + j;
-                    if (e < p.E) cols[w * p.E + e] = acc[i * VEC + j];
-                }
+                    for (int j = 0; j < VEC; ++j) {
+                        const int e = (i * lanes + sub) * VEC + j;
+                        if (e < p.E) mine[e] = acc[i * VEC + j];
+                    }
+            }
         }
         __syncthreads();
         const int first = tbase[g], n = tbase[g + 1] - first;
-        auto column = [&](int e) {
-            float v = cols[e];
-#pragma unroll 8
-            for (int k = 1; k < kWarps; ++k) v = __fadd_rn(v, cols[k * p.E + e]);
-            return v;
-        };
         float dot = 0.0f;
-        if (n == 1) {  // the group's only tile
-            for (int e = tid; e < p.E; e += kThreads) {
+        // `helpers` neighbouring threads add a column's warps
+        for (int i = tid; i < ((p.E * helpers + 31) & ~31); i += kThreads) {
+            const int e = i >> log_help, h = i & (helpers - 1);
+            float v = 0.0f;
+            if (e < p.E)
+#pragma unroll 4
+                for (int k = h; k < kWarps; k += helpers) v = __fadd_rn(v, cols[k * stride + e]);
+            for (int s = 1; s < helpers; s <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, s));
+            if (h != 0 || e >= p.E) continue;
+            if (n == 1) {  // the group's only tile
                 p.counts[static_cast<int64_t>(g) * p.E + e] = hist[e];
-                dot = __fmaf_rn(static_cast<float>(hist[e]), column(e), dot);
-            }
-        } else {
-            for (int e = tid; e < p.E; e += kThreads) {
-                p.mass[static_cast<int64_t>(tile) * p.E + e] = column(e);
+                dot = __fmaf_rn(static_cast<float>(hist[e]), v, dot);
+            } else {
+                p.mass[static_cast<int64_t>(tile) * p.E + e] = v;
                 p.part[static_cast<int64_t>(tile) * p.E + e] = hist[e];
             }
+        }
+        if (n > 1) {
             if (tid == 0) p.live[tile] = valid;
-            __threadfence();
             __syncthreads();
-            if (tid == 0) last = atomicAdd(&p.done[g], 1) == n - 1;
+            if (tid == 0) {  // the block's writes before the ticket, the others' before what is read after it
+                __threadfence();
+                last = atomicAdd(&p.done[g], 1) == n - 1;
+                __threadfence();
+                valid = 0;
+            }
             __syncthreads();
             if (!last) continue;
             // this group's tiles are all in: fold them
-            __threadfence();
             int32_t tokens = 0;
             for (int j = tid; j < n; j += kThreads) tokens += __ldcg(p.live + first + j);
-            if (tid == 0) valid = 0;
-            __syncthreads();
+            dot = p.E % 4 == 0 ? fold_tiles<4, kThreads>(p, first, n, g, cols) : fold_tiles<1, kThreads>(p, first, n, g, cols);
             tokens = __reduce_add_sync(0xffffffffu, tokens);
             if (lane == 0 && tokens) atomicAdd(&valid, tokens);
-            dot = p.E % 4 == 0 ? fold_tiles<4, kThreads>(p, first, n, g, cols) : fold_tiles<1, kThreads>(p, first, n, g, cols);
         }
         float s[1] = {dot};
         block_sum<1>(s, red, kWarps);
@@ -431,11 +480,11 @@ __global__ void __launch_bounds__(kThreadsFor<NV * VEC>) balance_forward(const B
                 p.group_loss[g] = loss;
                 __threadfence();
                 last = atomicAdd(&p.hdr->pad[0], 1) == n_groups - 1;
+                __threadfence();
             }
         }
         __syncthreads();
         if (!last) continue;
-        __threadfence();
         float t[1] = {0.0f};
         for (int k = tid; k < p.G; k += kThreads)
             if (tbase[k + 1] > tbase[k]) t[0] = __fadd_rn(t[0], __ldcg(p.group_loss + k));
@@ -579,6 +628,11 @@ BalLayout balance_layout(int64_t N, int64_t E, int64_t G) {
     return L;
 }
 
+size_t fold_bytes(int E, int threads) {
+    const FoldShape f = E % 4 == 0 ? fold_shape<4>(E, threads) : fold_shape<1>(E, threads);
+    return static_cast<size_t>(E % 4 == 0 ? 4 : 1) * f.ways * f.stride * 8;
+}
+
 template <typename T, int VEC, int NV, int LANES, bool SIGMOID>
 dgr_status launch_one(bool backward, BalParams &p, unsigned grid, cudaStream_t s) {
     if (backward) {
@@ -589,7 +643,7 @@ dgr_status launch_one(bool backward, BalParams &p, unsigned grid, cudaStream_t s
         balance_backward<T, VEC, NV, LANES, SIGMOID><<<sched_grid(want < most ? want : most), kBackThreads, p.offs ? (p.G + 1) * 8 : 0, s>>>(p);
     } else {
         constexpr int threads = kThreadsFor<NV * VEC>;
-        const size_t cols = static_cast<size_t>(threads / 32) * p.E * 4, fold = threads * (p.E % 4 == 0 ? 32 : 8);  // the fold reuses the columns' place
+        const size_t cols = static_cast<size_t>(threads / 32) * (p.E + 32) * 4, fold = fold_bytes(p.E, threads);  // the fold takes the columns' place
         const size_t smem = (p.G + 1) * 12 + p.E * 4 + (cols > fold ? cols : fold);
         auto *k = balance_forward<T, VEC, NV, LANES, SIGMOID>;
         if (smem > 47 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)

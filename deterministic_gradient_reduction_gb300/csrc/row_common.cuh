@@ -68,6 +68,38 @@ __device__ __forceinline__ void unpack(const raw_t<T, VEC> &v, float *f) {
     }
 }
 
+// Loads under a predicate: the destination keeps its value where it is off.
+// NC: data that nothing writes during the launch; otherwise a plain load.
+template <bool NC>
+__device__ __forceinline__ void load_if(uint16_t &v, const void *p, bool on) {
+    if constexpr (NC) asm volatile("{ .reg .pred q; setp.ne.b32 q, %2, 0; @q ld.global.nc.b16 %0, [%1]; }" : "+h"(v) : "l"(p), "r"(static_cast<int>(on)));
+    else asm volatile("{ .reg .pred q; setp.ne.b32 q, %2, 0; @q ld.global.b16 %0, [%1]; }" : "+h"(v) : "l"(p), "r"(static_cast<int>(on)) : "memory");
+}
+
+template <bool NC>
+__device__ __forceinline__ void load_if(uint32_t &v, const void *p, bool on) {
+    if constexpr (NC) asm volatile("{ .reg .pred q; setp.ne.b32 q, %2, 0; @q ld.global.nc.b32 %0, [%1]; }" : "+r"(v) : "l"(p), "r"(static_cast<int>(on)));
+    else asm volatile("{ .reg .pred q; setp.ne.b32 q, %2, 0; @q ld.global.b32 %0, [%1]; }" : "+r"(v) : "l"(p), "r"(static_cast<int>(on)) : "memory");
+}
+
+template <bool NC>
+__device__ __forceinline__ void load_if(uint2 &v, const void *p, bool on) {
+    if constexpr (NC)
+        asm volatile("{ .reg .pred q; setp.ne.b32 q, %3, 0; @q ld.global.nc.v2.b32 {%0, %1}, [%2]; }" : "+r"(v.x), "+r"(v.y) : "l"(p), "r"(static_cast<int>(on)));
+    else
+        asm volatile("{ .reg .pred q; setp.ne.b32 q, %3, 0; @q ld.global.v2.b32 {%0, %1}, [%2]; }" : "+r"(v.x), "+r"(v.y) : "l"(p), "r"(static_cast<int>(on)) : "memory");
+}
+
+template <bool NC>
+__device__ __forceinline__ void load_if(uint4 &v, const void *p, bool on) {
+    if constexpr (NC)
+        asm volatile("{ .reg .pred q; setp.ne.b32 q, %5, 0; @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4]; }"
+                     : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(static_cast<int>(on)));
+    else
+        asm volatile("{ .reg .pred q; setp.ne.b32 q, %5, 0; @q ld.global.v4.b32 {%0, %1, %2, %3}, [%4]; }"
+                     : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(static_cast<int>(on)) : "memory");
+}
+
 // Rounded to nearest even, once.
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
