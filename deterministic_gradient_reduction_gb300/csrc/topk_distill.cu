@@ -12,20 +12,30 @@
 //                               p_j (S - q_r / p_r)                   outside),
 //   S the sum of all q that L counts: 1, but where q_r is left out (no logit
 //   outside the list above -inf) or the list's q exceed 1.
-// A row of weight 0, and one whose list is empty, is not read and has loss 0
+// A row of weight 0 is not read; it and one whose list is empty have loss 0
 // and gradient 0.
 //
-// The softmax's maximum and sum are carried along in one pass. With q_r the
-// list's tokens are left out of that pass (a bit a token in shared memory) and
-// added back afterwards, so that p_r is a sum of its own and not a difference
-// from 1; the gradient outside is then
+// A row is read twice: once for maximum and sum, once (out of L2) for the
+// gradient. It lies across a cluster of CTAs, few enough rows at a time that
+// they stay in L2 between the two (below), and few CTAs a row, as each has to
+// do what there is to do for the list. The CTAs of a row exchange a (maximum,
+// sum) pair a warp through shared memory of the cluster.
+//
+// With q_r the list's tokens (a bit an element in shared memory) are left out
+// of that maximum and sum and have their own, so that p_r is a sum and not a
+// difference from 1; the gradient outside is then
 //   exp(z_j / tau - m) (S exp(m - lse) - q_r / s),  m, s: maximum and sum outside,
 // which stays finite however small p_r is. Exponentials are taken to base 2
-// (k = log2(e) / tau): every one of a row is ex2(z k - fl(m k)) with the same
-// rounded product fl(m k), so its rounding cancels between numerator and sum.
+// (k = log2(e) / tau): with m a running maximum every one is ex2(z k - fl(m k)),
+// sums meet by ex2(fl(m k) - fl(m' k)), so the roundings of these products
+// cancel between numerator and sum. Where even the row's maximum times k is
+// beyond 1e38 the row is done again with its maximum subtracted first.
 //
-// Deterministic: a row's sums go over threads, warps and the block in a fixed
-// order, the rows' losses over one CTA in a fixed order.
+// Deterministic: a row's sums go over threads, warps, CTAs of the cluster in a
+// fixed order set by V, T and the alignment; the rows' losses over one CTA in a
+// fixed order.
+#include <atomic>
+
 #include "row_common.cuh"
 
 namespace dgr {
@@ -35,8 +45,10 @@ using namespace row;
 
 constexpr int kMaxList = 1024;
 constexpr int kMaxVocab = 1 << 20;
+constexpr int kMaxCluster = 8;
 constexpr int kWhereId = 311;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kFar = 1e38f;  // products with k beyond this are not relied on
 
 struct DistillParams {
     const void *z;
@@ -52,245 +64,496 @@ struct DistillParams {
     void *dz;
     int64_t ld_dz;
     int32_t same_align;  // z's and dz's rows start at the same place of a 16-byte vector
-    WsHeader *hdr;       // pad[0]: CTAs done
+    WsHeader *hdr;       // pad[0]: clusters done
     Sched sched;
 };
 
-// A row as whole 16-byte vectors between a few single elements.
+// ---- cluster and copy instructions ---------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster's CTAs; what was written before is seen after.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void remote_store(uint32_t a, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void remote_store(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// ---- a row's parts -------------------------------------------------------------
+
+// A row as whole 16-byte vectors between a few single elements; CTA `rank` of a
+// cluster of `size` has vectors [first, first + count), CTA 0 the singles too.
 template <typename T>
 struct RowView {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-    int head, n_vec, n_single;
-    __device__ __forceinline__ RowView(const T *z, int V) {
+    int head, n_vec, n_single, per, first, count;
+    __device__ __forceinline__ RowView(const T *z, int V, int rank, int size) {
         const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / static_cast<int>(sizeof(T));
         head = min(V, off ? VEC - off : 0);
         n_vec = (V - head) / VEC;
         n_single = V - n_vec * VEC;
+        per = (n_vec + size - 1) / size;
+        first = min(n_vec, rank * per);
+        count = min(per, n_vec - first);
+        if (rank != 0) n_single = 0;
     }
     // element of single i: before the vectors, then behind them
     __device__ __forceinline__ int single(int i) const { return i < head ? i : n_vec * VEC + i; }
-    // the bit of element j in the list's mask: a vector's bits lie together
-    __device__ __forceinline__ int bit(int j) const { return j - head + VEC; }
+    // where element j lies in this CTA: an element of its vectors, kSingle + i, or -1
+    static constexpr int kSingle = 1 << 24;
+    __device__ __forceinline__ int place(int j) const {
+        const int e = j - head;
+        if (e >= 0 && e < n_vec * VEC) {
+            const int mine = e - first * VEC;
+            return mine >= 0 && mine < count * VEC ? mine : -1;
+        }
+        return n_single ? kSingle + (e < 0 ? j : j - n_vec * VEC) : -1;
+    }
 };
 
-__device__ __forceinline__ float block_max(float v, float *buf, int n_warps) {
+// fl(m k), at least -1e38: elements that far below give 0 and never inf - inf.
+__device__ __forceinline__ float scaled_max(float m, float k) { return fmaxf(__fmul_rn(m, k), -kFar); }
+
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = buf[0];
-    for (int k = 1; k < n_warps; ++k) v = fmaxf(v, buf[k]);
     return v;
 }
 
-// Running maximum and sum of exp2(x k - m k).
-struct Running {
-    float m = -INFINITY, c = 0.0f, s = 0.0f;  // c = fl(m k), 0 while m is -inf
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], float k) {
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
-        if (top > m) {
-            const float to = __fmul_rn(top, k);
-            s = m == -INFINITY ? s : __fmul_rn(s, ex2(__fadd_rn(c, -to)));
-            m = top;
-            c = to;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) s = __fadd_rn(s, ex2(__fmaf_rn(x[i], k, -c)));
+// A maximum and the sum of exp2(x k - fl(m k)); the warp's from the lanes'.
+struct Pair {
+    float m, s;
+    __device__ __forceinline__ void over_warp(float k) {
+        const float top = warp_max(m);
+        s = warp_sum(__fmul_rn(s, ex2(__fadd_rn(scaled_max(m, k), -scaled_max(top, k)))));
+        m = top;
     }
 };
 
-template <typename T, int NT, bool TAIL>
-__global__ void __launch_bounds__(NT) distill_rows(const DistillParams p) {
-    constexpr int VEC = RowView<T>::VEC, W = NT / 32;
-    extern __shared__ char smem[];
-    int32_t *s_id = reinterpret_cast<int32_t *>(smem);        // [K], -1: none
-    float *s_q = reinterpret_cast<float *>(s_id + p.K);       // [K]
-    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_q + p.K);  // TAIL: a bit a token
-    __shared__ float buf[6][32 * 4];
-    __shared__ int last;
-    const int tid = threadIdx.x;
-    if constexpr (TAIL) {
-        for (int i = tid; i < (p.V + 2 * VEC) / 32 + 1; i += NT) s_mask[i] = 0;
-        __syncthreads();
+// Maximum of a vector's elements (a NaN is passed over: it shows in the sum).
+template <typename T, int U>
+__device__ __forceinline__ float max_of(const uint4 (&r)[U]) {
+    if constexpr (sizeof(T) == 2) {
+        auto h = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+        __nv_bfloat162 m = h(r[0].x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) m = __hmax2(m, __hmax2(__hmax2(h(r[u].x), h(r[u].y)), __hmax2(h(r[u].z), h(r[u].w))));
+        return fmaxf(__low2float(m), __high2float(m));
+    } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[u].x), __uint_as_float(r[u].y)), fmaxf(__uint_as_float(r[u].z), __uint_as_float(r[u].w))));
+        return m;
     }
-    for (int32_t it = blockIdx.x; it < p.T; it += gridDim.x) {
-        const int32_t row = static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(it)));
-        const float weight = p.weights ? __ldg(p.weights + row) : 1.0f;
+}
+
+// Running maximum m, c = fl(m k) and sum of exp2(x k - c) of a thread's elements.
+struct Running {
+    float m = -INFINITY, c = -kFar;
+    float2 s = make_float2(0.0f, 0.0f);
+    __device__ __forceinline__ void raise(float top, float k) {
+        if (top > m) {
+            m = top;
+            const float to = scaled_max(top, k), down = ex2(__fadd_rn(c, -to));
+            s = mul2(s, make_float2(down, down));
+            c = to;
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void add(float (&x)[N], float k) {
+        vec_fma(x, k, -c);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            s.x = __fadd_rn(s.x, ex2(x[i]));
+            s.y = __fadd_rn(s.y, ex2(x[i + 1]));
+        }
+    }
+};
+
+// The list's bytes: ids, then teacher logits.
+__host__ __device__ inline size_t list_bytes(int K) { return (static_cast<size_t>(K) * 8 + 15) / 16 * 16; }
+
+// 32-element batches of a thread in a CTA's part of a row of V, and the words
+// of the list's bits: one for each.
+__host__ __device__ inline int batches(int V, int threads, int size, int es) {
+    const int n_vec = V / (16 / es), per = (n_vec + size - 1) / size, flight = 32 * es / 16;
+    return (per + threads * flight - 1) / (threads * flight);
+}
+
+// Dynamic shared memory: the lists of this row and the next, the student's
+// logits at the entries, copy flags [K], and with q_r the list's bits.
+size_t distill_smem(int K, int V, int threads, int size, int es) {
+    return 2 * list_bytes(K) + static_cast<size_t>(K) * 8 + static_cast<size_t>(batches(V, threads, size, es)) * threads * 4;
+}
+
+template <typename T, int NT, bool TAIL>
+__global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParams p) {
+    using View = RowView<T>;
+    constexpr int VEC = View::VEC, W = NT / 32, U = 32 / VEC;  // U vectors of a thread in flight: 32 elements, one word of bits
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float4 s_pair[2][kMaxCluster * W];  // the cluster's warps, by row parity: outside the list, in it
+    __shared__ float s_loss[2][kMaxCluster * W];   // likewise their parts of a row's loss
+    __shared__ float2 s_list;                      // ln of the list's normaliser, sum of its q
+    __shared__ int s_any, last;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    const uint32_t n_clusters = gridDim.x / size, T_rows = static_cast<uint32_t>(p.T);
+    const int K = p.K;
+    auto ids_of = [&](uint32_t n) { return reinterpret_cast<int32_t *>(smem + (n & 1) * list_bytes(K)); };
+    float *s_z = reinterpret_cast<float *>(smem + 2 * list_bytes(K));      // [K]
+    int32_t *s_copy = reinterpret_cast<int32_t *>(s_z + K);                // [K]: place, with kCopy where the id came before
+    uint32_t *s_bits = reinterpret_cast<uint32_t *>(s_copy + K);           // [batches][NT]
+    constexpr int kCopy = 1 << 30;
+
+    auto row_of = [&](uint32_t i) { return static_cast<int64_t>(sched_item(p.sched, i)); };
+    auto weight_of = [&](uint32_t i) { return i < T_rows ? (p.weights ? __ldg(p.weights + row_of(i)) : 1.0f) : 0.0f; };
+    // the list of item i, the n-th of this cluster, on its way
+    auto fetch_list = [&](uint32_t i, uint32_t n, float weight) {
+        if (i < T_rows && weight != 0.0f) {
+            const int64_t row = row_of(i);
+            int32_t *ids = ids_of(n);
+            for (int k = tid; k < K; k += NT) {
+                copy_async<4>(ids + k, p.ids + row * p.ld_ids + k);
+                copy_async<4>(ids + K + k, p.teacher + row * p.ld_t + k);
+            }
+        }
+        copy_commit();
+    };
+    const int list_warps = min(W, (K + 31) / 32);  // warps that hold entries
+    int64_t loss_row = -1;      // CTA 0, warp 0: a row whose loss waits for the other CTAs' parts
+    float loss_tail = 0.0f;
+    uint32_t live_n = 0;        // rows worked on: the exchange's parity
+    auto finish_loss = [&]() {  // their parts have come with the last cluster barrier
+        if (loss_row < 0) return;
+        float L = 0.0f;
+        for (int j = lane; j < size * list_warps; j += 32) L = __fadd_rn(L, s_loss[(live_n & 1) ^ 1][j]);
+        L = __fadd_rn(loss_tail, warp_sum(L));
+        if (lane == 0) p.row_loss[loss_row] = L;
+        loss_row = -1;
+    };
+
+    uint32_t item = blockIdx.x / size;
+    float weight = weight_of(item), weight_next = weight_of(item + n_clusters);
+    if (TAIL)
+        for (int j = tid; j < batches(p.V, NT, size, sizeof(T)) * NT; j += NT) s_bits[j] = 0;
+    fetch_list(item, 0, weight);
+    __syncthreads();
+    for (uint32_t n = 0; item < T_rows; ++n, item += n_clusters) {
+        const int64_t row = row_of(item);
         const T *z = static_cast<const T *>(p.z) + row * p.ld;
         T *dz = static_cast<T *>(p.dz) + row * p.ld_dz;
-        const RowView<T> view(z, p.V);
-        const float lse_t = TAIL ? __ldg(p.teacher_lse + row) : 0.0f;
-        // the list: each thread keeps entries tid, tid + NT, ...
-        float top = -INFINITY;
-        int any = 0;
-        if (weight != 0.0f)
-            for (int i = tid; i < p.K; i += NT) {
-                int id = p.ids[row * p.ld_ids + i];
-                if (id >= p.V) {
-                    if (p.hdr) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereId);
-                    id = -1;
+        const View view(z, p.V, rank, size);
+        const char *first = reinterpret_cast<const char *>(z + view.head) + static_cast<int64_t>(view.first) * 16;
+        int32_t *ids = ids_of(n);
+        const float *teacher = reinterpret_cast<const float *>(ids + K);
+        copy_wait();  // each thread's own part of the list
+        const float weight_2 = weight_of(item + 2 * n_clusters);
+        float a = 0.0f, c_rest = 0.0f, f = 0.0f, c_all = 0.0f, inv_mass = 0.0f, total = 1.0f, shift = 0.0f;
+        bool live = false;
+        if (weight != 0.0f) {
+            // the list's entries in this CTA: where they lie, their student's
+            // logits (on their way during the pass), their bits. An entry whose
+            // bit is set already is a copy; which of the two does not matter,
+            // the other writes the sum of both.
+            for (int k = tid; k < K; k += NT) {
+                const int id = ids[k];
+                int at = id >= 0 && id < p.V ? view.place(id) : -1;
+                if (at >= 0) s_z[k] = to_f32(z[id]);
+                if (TAIL && at >= 0 && at < View::kSingle) {
+                    const int v = at / VEC, j = v / NT;  // vector j of its thread
+                    const uint32_t bit = 1u << (j % U * VEC + at % VEC);
+                    if (atomicOr(&s_bits[j / U * NT + v % NT], bit) & bit) at |= kCopy;
                 }
-                const float t = id < 0 ? -INFINITY : __fmul_rn(p.teacher[row * p.ld_t + i], p.inv_tau);
-                s_id[i] = id < 0 ? -1 : id;
-                s_q[i] = t;
-                top = fmaxf(top, t);
-                any |= id >= 0 && (TAIL || !(t == -INFINITY));
-                if (TAIL && id >= 0) atomicOr(&s_mask[view.bit(id) >> 5], 1u << (view.bit(id) & 31));
-            }
-        if (!__syncthreads_or(any)) {  // nothing taught here
-            if (p.row_loss && tid == 0) p.row_loss[row] = 0.0f;
-            if (p.dz) {
-                T zero{};
-                for (int j = tid; j < p.V; j += NT) dz[j] = zero;
+                s_copy[k] = at;
             }
             __syncthreads();
-            continue;
-        }
-        top = block_max(top, buf[0], W);
-        float part[2] = {0.0f, 0.0f};  // sum of q, sum of q ln q
-        // student logits at the list's entries; an id that comes twice counts once in the student's sum
-        float m_list = -INFINITY;
-        {
-            float sum[1] = {0.0f};
-            for (int i = tid; i < p.K; i += NT)
-                if (!TAIL) sum[0] = __fadd_rn(sum[0], expf(__fadd_rn(s_q[i], -top)));
-            if (!TAIL) block_sum<1>(sum, buf[1], W);
-            const float base = TAIL ? lse_t : __fadd_rn(top, logf(sum[0]));
-            for (int i = tid; i < p.K; i += NT) {
-                const float lq = TAIL ? __fadd_rn(s_q[i], -base) : __fadd_rn(__fadd_rn(s_q[i], -top), -logf(sum[0]));
-                const float q = s_id[i] < 0 ? 0.0f : expf(lq);
-                part[0] = __fadd_rn(part[0], q);
-                if (q != 0.0f) part[1] = __fmaf_rn(q, lq, part[1]);
-                s_q[i] = q;
-                if (s_id[i] >= 0) m_list = fmaxf(m_list, to_f32(z[s_id[i]]));
-            }
-        }
-        // the row, once
-        Running run;
-        for (int v = tid; v < view.n_vec; v += NT) {
-            float x[VEC];
-            unpack<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(z + view.head + v * VEC), x);
-            if constexpr (TAIL) {
-                const int b = (v + 1) * VEC;
-                const uint32_t bits = (s_mask[b >> 5] >> (b & 31)) & ((1u << VEC) - 1);
-                if (bits)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (bits >> i & 1) x[i] = -INFINITY;
-            }
-            run.add(x, p.k2);
-        }
-        if (tid < view.n_single) {
-            const int j = view.single(tid);
-            float x[1] = {to_f32(z[j])};
-            if (TAIL && (s_mask[view.bit(j) >> 5] >> (view.bit(j) & 31) & 1)) x[0] = -INFINITY;
-            run.add(x, p.k2);
-        }
-        const float m = block_max(run.m, buf[2], W);          // outside the list (TAIL), else of all
-        const float c = m == -INFINITY ? 0.0f : __fmul_rn(m, p.k2);
-        float m_all = m, c_all = c;
-        if (TAIL) {
-            m_all = fmaxf(m, block_max(m_list, buf[3], W));
-            c_all = m_all == -INFINITY ? 0.0f : __fmul_rn(m_all, p.k2);
-        }
-        // sums: outside, in the list, q, q ln q
-        float sums[4] = {run.m == -INFINITY ? run.s : __fmul_rn(run.s, ex2(__fadd_rn(run.c, -c))), 0.0f, part[0], part[1]};
-        if (TAIL)
-            for (int i = tid; i < p.K; i += NT) {
-                const int id = s_id[i];
-                bool first = id >= 0;
-                for (int j = 0; j < i && first; ++j) first = s_id[j] != id;
-                if (first) sums[1] = __fadd_rn(sums[1], ex2(__fmaf_rn(to_f32(z[id]), p.k2, -c_all)));
-            }
-        block_sum<4>(sums, buf[4], W);
-        const float rest = sums[0];
-        const float shift = m == -INFINITY ? 0.0f : ex2(__fadd_rn(c, -c_all));
-        const float total = TAIL ? __fmaf_rn(rest, shift, sums[1]) : rest;
-        const float inv = 1.0f / total, ln_total = logf(total);
-        const float q_rest = TAIL && m != -INFINITY ? fmaxf(__fadd_rn(1.0f, -sums[2]), 0.0f) : 0.0f;
-        const float mass = !TAIL || q_rest > 0.0f ? 1.0f : sums[2];
-        // loss: sum of q ln q less sum of q ln p, entry by entry
-        float lp[1] = {0.0f};
-        if (p.row_loss)
-            for (int i = tid; i < p.K; i += NT)
-                if (s_q[i] != 0.0f)
-                    lp[0] = __fmaf_rn(s_q[i], __fmaf_rn(__fmaf_rn(to_f32(z[s_id[i]]), p.k2, -c_all), kLn2, -ln_total), lp[0]);
-        // what the gradient writes into: the list's student logits have to be read before
-        const float inv_mass = __fmul_rn(inv, mass);
-        const float f = __fmul_rn(__fmul_rn(__fmul_rn(p.scale, weight), p.inv_tau), p.dloss ? __ldg(p.dloss) : 1.0f);
-        float fix[(kMaxList + NT - 1) / NT];
-        if (p.dz) {
-#pragma unroll
-            for (int n = 0; n < (kMaxList + NT - 1) / NT; ++n) {
-                const int i = tid + n * NT;
-                fix[n] = 0.0f;
-                if (i < p.K && s_id[i] >= 0) {
-                    const int id = s_id[i];
-                    float q = 0.0f;
-                    for (int j = 0; j < p.K; ++j)
-                        if (s_id[j] == id) q = __fadd_rn(q, s_q[j]);
-                    fix[n] = __fmul_rn(__fadd_rn(__fmul_rn(ex2(__fmaf_rn(to_f32(z[id]), p.k2, -c_all)), inv_mass), -q), f);
+            fetch_list(item + n_clusters, n + 1, weight_next);
+            if (w == W - 1) {  // the list's sums
+                float top = -INFINITY, sum = 0.0f;
+                const float lse_t = TAIL ? __ldg(p.teacher_lse + row) : 0.0f;
+                bool any = false, bad = false;
+                for (int k = lane; k < K; k += 32) {
+                    const int id = ids[k];
+                    bad |= id >= p.V;
+                    if (id < 0 || id >= p.V) continue;
+                    const float t = __fmul_rn(teacher[k], p.inv_tau);
+                    any |= TAIL || !(t == -INFINITY);
+                    if (TAIL) sum = __fadd_rn(sum, expf(__fadd_rn(t, -lse_t)));
+                    else top = fmaxf(top, t);
+                }
+                if (!TAIL) {
+                    top = warp_max(top);
+                    if (!(top > -INFINITY)) top = 0.0f;
+                    for (int k = lane; k < K; k += 32)
+                        if (ids[k] >= 0 && ids[k] < p.V) sum = __fadd_rn(sum, expf(__fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -top)));
+                }
+                sum = warp_sum(sum);
+                any = __any_sync(0xffffffffu, any);
+                if (__any_sync(0xffffffffu, bad) && rank == 0 && lane == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereId);
+                if (lane == 0) {
+                    s_any = any;
+                    s_list = make_float2(TAIL ? lse_t : __fadd_rn(top, logf(sum)), TAIL ? sum : 1.0f);
                 }
             }
-        }
-        block_sum<1>(lp, buf[5], W);
-        if (p.row_loss && tid == 0) {
-            float L = __fadd_rn(sums[3], -lp[0]);
-            if (q_rest > 0.0f)
-                L = __fadd_rn(L, __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -__fadd_rn(__fmaf_rn(__fadd_rn(c, -c_all), kLn2, logf(rest)), -ln_total))));
-            p.row_loss[row] = L;
+            // copies among the single elements, and without bits: entry by entry
+            // (neighbouring threads share an entry's comparisons)
+            {
+                int log_help = 0;
+                while (log_help < 5 && K << (log_help + 1) <= NT) ++log_help;
+                for (int i = tid; i < (((K << log_help) + 31) & ~31); i += NT) {
+                    const int k = i >> log_help, h = i & ((1 << log_help) - 1);
+                    bool copy = false;
+                    if (k < K && s_copy[k] >= 0 && (!TAIL || (s_copy[k] & ~kCopy) >= View::kSingle))
+                        for (int j = h; j < k; j += 1 << log_help) copy |= ids[j] == ids[k];
+                    for (int s = 1; s < 1 << log_help; s <<= 1) copy |= __shfl_xor_sync(0xffffffffu, copy, s) != 0;
+                    if (copy && h == 0) s_copy[k] |= kCopy;
+                }
+            }
+            __syncthreads();
+            for (;;) {  // a second time only where k times the maximum is out of range; `shift` is subtracted then
+                Running run;
+                const char *src = first + tid * 16;
+                int b = tid;
+                for (int v = tid; v < view.count; v += U * NT, src += static_cast<size_t>(U) * NT * 16, b += NT) {
+                    uint4 r[U];
+                    constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        r[u] = make_uint4(low, low, low, low);
+                        load_if<false>(r[u], src + u * NT * 16, v + u * NT < view.count);
+                    }
+                    uint32_t bits = TAIL ? s_bits[b] : 0;
+                    if (bits) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            uint32_t q[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (sizeof(T) == 4) {
+                                    if (bits >> (u * 4 + i) & 1) q[i] = low;
+                                } else {
+                                    const uint32_t two = bits >> (u * 8 + 2 * i) & 3;
+                                    if (two & 1) q[i] = (q[i] & 0xffff0000u) | 0xff80u;
+                                    if (two & 2) q[i] = (q[i] & 0xffffu) | 0xff800000u;
+                                }
+                            }
+                            r[u] = make_uint4(q[0], q[1], q[2], q[3]);
+                        }
+                    }
+                    run.raise(__fadd_rn(max_of<T, U>(r), -shift), p.k2);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float x[VEC];
+                        unpack<T, VEC>(r[u], x);
+                        if (shift != 0.0f)
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) x[i] = __fadd_rn(x[i], -shift);
+                        run.add(x, p.k2);
+                    }
+                }
+                if (tid < view.n_single) {
+                    const int j = view.single(tid);
+                    bool listed = false;
+                    if (TAIL)
+                        for (int k = 0; k < K; ++k) listed |= ids[k] == j;
+                    if (!listed) {
+                        const float x = __fadd_rn(to_f32(z[j]), -shift);
+                        run.raise(x, p.k2);
+                        run.s.x = __fadd_rn(run.s.x, ex2(__fmaf_rn(x, p.k2, -run.c)));
+                    }
+                }
+                Pair rest{run.m, __fadd_rn(run.s.x, run.s.y)}, in{-INFINITY, 0.0f};
+                rest.over_warp(p.k2);
+                if (TAIL && w < list_warps) {  // the list's tokens in this CTA, each once
+                    for (int k = tid; k < K; k += NT)
+                        if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.m = fmaxf(in.m, __fadd_rn(s_z[k], -shift));
+                    const float ci = scaled_max(in.m, p.k2);
+                    for (int k = tid; k < K; k += NT)
+                        if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.s = __fadd_rn(in.s, ex2(__fmaf_rn(__fadd_rn(s_z[k], -shift), p.k2, -ci)));
+                    in.over_warp(p.k2);
+                }
+                __syncwarp();
+                if (lane < size) remote_store(remote(&s_pair[live_n & 1][rank * W + w], lane), make_float4(rest.m, rest.s, in.m, in.s));
+                __syncwarp();
+                if (size > 1) cluster_barrier();
+                else __syncthreads();
+                rest = Pair{-INFINITY, 0.0f};
+                in = Pair{-INFINITY, 0.0f};
+                for (int j = lane; j < size * W; j += 32) {
+                    const float4 got = s_pair[live_n & 1][j];
+                    rest.m = fmaxf(rest.m, got.x);
+                    in.m = fmaxf(in.m, got.z);
+                }
+                rest.m = warp_max(rest.m);
+                if (TAIL) in.m = warp_max(in.m);
+                c_rest = scaled_max(rest.m, p.k2);
+                const float c_in = scaled_max(in.m, p.k2);
+                for (int j = lane; j < size * W; j += 32) {
+                    const float4 got = s_pair[live_n & 1][j];
+                    rest.s = __fadd_rn(rest.s, __fmul_rn(got.y, ex2(__fadd_rn(scaled_max(got.x, p.k2), -c_rest))));
+                    if (TAIL) in.s = __fadd_rn(in.s, __fmul_rn(got.w, ex2(__fadd_rn(scaled_max(got.z, p.k2), -c_in))));
+                }
+                rest.s = warp_sum(rest.s);
+                if (TAIL) in.s = warp_sum(in.s);
+                const float m_all = TAIL ? fmaxf(rest.m, in.m) : rest.m;
+                if (shift == 0.0f && fabsf(m_all) < INFINITY && fabsf(__fmul_rn(m_all, p.k2)) >= kFar) {
+                    shift = m_all;  // the same in every warp of the cluster
+                    if (size > 1) cluster_barrier();  // before the pairs are written over
+                    else __syncthreads();
+                    continue;
+                }
+                live = s_any != 0;
+                const float sum_q = s_list.y;
+                c_all = scaled_max(m_all, p.k2);
+                const float down = ex2(__fadd_rn(c_rest, -c_all));
+                total = TAIL ? __fmaf_rn(rest.s, down, __fmul_rn(in.s, ex2(__fadd_rn(c_in, -c_all)))) : rest.s;
+                const float inv = 1.0f / total;
+                const float q_rest = TAIL && rest.m != -INFINITY ? fmaxf(__fadd_rn(1.0f, -sum_q), 0.0f) : 0.0f;
+                inv_mass = __fmul_rn(inv, !TAIL || q_rest > 0.0f ? 1.0f : sum_q);
+                f = __fmul_rn(__fmul_rn(__fmul_rn(p.scale, weight), p.inv_tau), p.dloss ? __ldg(p.dloss) : 1.0f);
+                a = __fmul_rn(TAIL ? __fadd_rn(__fmul_rn(down, inv_mass), q_rest > 0.0f ? -q_rest / rest.s : 0.0f) : inv, f);
+                if (p.row_loss && rank == 0 && w == 0) {
+                    finish_loss();
+                    loss_row = row;
+                    loss_tail = 0.0f;
+                    if (q_rest > 0.0f && live)
+                        loss_tail = __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -__fadd_rn(__fmaf_rn(__fadd_rn(c_rest, -c_all), kLn2, logf(rest.s)), -logf(total))));
+                }
+                break;
+            }
+        } else {
+            fetch_list(item + n_clusters, n + 1, weight_next);
         }
         if (p.dz) {
-            const float a = __fmul_rn(TAIL ? __fadd_rn(__fmul_rn(shift, inv_mass), q_rest > 0.0f ? -q_rest / rest : 0.0f) : inv, f);
-            for (int v = tid; v < view.n_vec; v += NT) {
-                const int j = view.head + v * VEC;
-                float x[VEC];
-                unpack<T, VEC>(*reinterpret_cast<const raw_t<T, VEC> *>(z + j), x);
+            const char *src = first + tid * 16;
+            T *dst = dz + view.head + static_cast<int64_t>(view.first) * VEC + tid * VEC;
+            for (int v = tid; v < view.count; v += U * NT, src += static_cast<size_t>(U) * NT * 16, dst += U * NT * VEC) {
+                uint4 r[U];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) x[i] = __fmul_rn(ex2(__fmaf_rn(x[i], p.k2, -c)), a);
-                if (p.same_align) {
-                    *reinterpret_cast<raw_t<T, VEC> *>(dz + j) = pack<T, VEC>(x);
-                } else {
+                for (int u = 0; u < U; ++u) {
+                    r[u] = make_uint4(0, 0, 0, 0);
+                    load_if<false>(r[u], src + u * NT * 16, live && v + u * NT < view.count);
+                }
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) *reinterpret_cast<raw_t<T, 1> *>(dz + j + i) = pack<T, 1>(x + i);
+                for (int u = 0; u < U; ++u) {
+                    float x[VEC];
+                    unpack<T, VEC>(r[u], x);
+                    if (shift != 0.0f)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) x[i] = __fadd_rn(x[i], -shift);
+                    vec_fma(x, p.k2, -c_rest);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) x[i] = ex2(x[i]);
+                    vec_scale(x, a);
+                    r[u] = pack<T, VEC>(x);
+                    if (!live) r[u] = make_uint4(0, 0, 0, 0);  // whatever the row holds
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (v + u * NT >= view.count) continue;
+                    if (p.same_align) {
+                        *reinterpret_cast<uint4 *>(dst + u * NT * VEC) = r[u];
+                    } else {
+                        const T *e = reinterpret_cast<const T *>(&r[u]);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) dst[u * NT * VEC + i] = e[i];
+                    }
                 }
             }
             if (tid < view.n_single) {
                 const int j = view.single(tid);
-                const float x = __fmul_rn(ex2(__fmaf_rn(to_f32(z[j]), p.k2, -c)), a);
+                const float x = live ? __fmul_rn(ex2(__fmaf_rn(__fadd_rn(to_f32(z[j]), -shift), p.k2, -c_rest)), a) : 0.0f;
                 *reinterpret_cast<raw_t<T, 1> *>(dz + j) = pack<T, 1>(&x);
             }
-            __syncthreads();  // the list's tokens are written over
-#pragma unroll
-            for (int n = 0; n < (kMaxList + NT - 1) / NT; ++n) {
-                const int i = tid + n * NT;
-                if (i < p.K && s_id[i] >= 0) *reinterpret_cast<raw_t<T, 1> *>(dz + s_id[i]) = pack<T, 1>(&fix[n]);
+        }
+        if (weight != 0.0f) {
+            __syncthreads();
+            // the list's entries: their part of the loss, their tokens' gradient
+            if (w < list_warps) {
+                float part = 0.0f;
+                const float base = s_list.x, ln_total = logf(total);
+                for (int k = tid; k < K; k += NT) {
+                    const int at = s_copy[k] & ~kCopy;
+                    if (s_copy[k] < 0) continue;
+                    if (TAIL && at < View::kSingle) s_bits[at / VEC / NT / U * NT + at / VEC % NT] = 0;  // free again
+                    if (!live) continue;
+                    const float lq = __fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -base);
+                    float q = expf(lq);
+                    const float x = __fmaf_rn(__fadd_rn(s_z[k], -shift), p.k2, -c_all);  // log2 of p times the total
+                    if (q != 0.0f) part = __fmaf_rn(q, __fadd_rn(lq, -__fmaf_rn(x, kLn2, -ln_total)), part);
+                    if (!p.dz || (s_copy[k] & kCopy)) continue;
+                    const int id = ids[k];
+                    q = 0.0f;
+                    for (int j = 0; j < K; ++j)
+                        if (ids[j] == id) q = __fadd_rn(q, expf(__fadd_rn(__fmul_rn(teacher[j], p.inv_tau), -base)));
+                    const float g = __fmul_rn(__fmaf_rn(ex2(x), inv_mass, -q), f);
+                    *reinterpret_cast<raw_t<T, 1> *>(dz + id) = pack<T, 1>(&g);
+                }
+                if (p.row_loss) {
+                    part = warp_sum(part);
+                    // read behind the next cluster barrier
+                    if (lane == 0) remote_store(remote(&s_loss[live_n & 1][rank * list_warps + w], 0), part);
+                }
             }
+            ++live_n;
         }
         __syncthreads();
-        if constexpr (TAIL) {
-            for (int i = tid; i < p.K; i += NT)
-                if (s_id[i] >= 0) s_mask[view.bit(s_id[i]) >> 5] = 0;
-            __syncthreads();
-        }
+        weight = weight_next;
+        weight_next = weight_2;
     }
+    copy_wait();
+    __syncwarp();
+    if (size > 1) cluster_barrier();  // the last row's parts; no CTA leaves before its shared memory is read
+    else __syncthreads();
+    if (rank != 0) return;
+    if (w == 0) finish_loss();
+    // rows without weight: no loss
+    if (p.row_loss && p.weights)
+        for (uint32_t i = blockIdx.x / size + tid * n_clusters; i < T_rows; i += NT * n_clusters)
+            if (weight_of(i) == 0.0f) p.row_loss[row_of(i)] = 0.0f;
     if (!p.loss) return;
-    // the CTA that ends last adds the rows' losses
-    __threadfence();
+    // the cluster that ends last adds the rows' losses
     __syncthreads();
-    if (tid == 0) last = atomicAdd(&p.hdr->pad[0], 1) == static_cast<int>(gridDim.x) - 1;
+    if (tid == 0) {
+        __threadfence();
+        last = atomicAdd(&p.hdr->pad[0], 1) == static_cast<int>(n_clusters) - 1;
+        __threadfence();
+    }
     __syncthreads();
     if (!last) return;
-    __threadfence();
     float s[1] = {0.0f};
     for (int t = tid; t < p.T; t += NT) {
-        const float w = p.weights ? __ldg(p.weights + t) : 1.0f;
-        if (w != 0.0f) s[0] = __fmaf_rn(w, __ldcg(p.row_loss + t), s[0]);
+        const float wt = p.weights ? __ldg(p.weights + t) : 1.0f;
+        if (wt != 0.0f) s[0] = __fmaf_rn(wt, __ldcg(p.row_loss + t), s[0]);
     }
-    block_sum<1>(s, buf[0], W);
+    float *buf = reinterpret_cast<float *>(s_pair);  // free by now
+    block_sum<1>(s, buf, W);
     if (tid == 0) {
         *p.loss = __fmul_rn(p.scale, s[0]);
         p.hdr->pad[0] = 0;  // ready for the next call
@@ -300,21 +563,43 @@ __global__ void __launch_bounds__(NT) distill_rows(const DistillParams p) {
 // Host side -------------------------------------------------------------------
 
 template <typename T, int NT, bool TAIL>
-dgr_status launch_rows(const DistillParams &p, int sms, cudaStream_t s) {
-    constexpr int VEC = RowView<T>::VEC;
-    size_t smem = static_cast<size_t>(p.K) * 8;
-    if (TAIL) smem += (static_cast<size_t>(p.V + 2 * VEC) / 32 + 1) * 4;
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(distill_rows<T, NT, TAIL>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return DGR_ERR_CUDA;
-    const int64_t most = static_cast<int64_t>(sms) * (1536 / NT), want = p.T > 0 ? p.T : 1;
-    distill_rows<T, NT, TAIL><<<sched_grid(static_cast<unsigned>(want < most ? want : most)), NT, smem, s>>>(p);
-    return launch_status();
+dgr_status launch_rows(const DistillParams &p, int cluster, int sms, cudaStream_t s) {
+    auto *k = distill_rows<T, NT, TAIL>;
+    const size_t smem = distill_smem(p.K, p.V, NT, cluster, sizeof(T));
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DGR_ERR_CUDA;
+    static std::atomic<int> granted[64];  // the largest size asked for so far
+    if (smem > 32 * 1024 && static_cast<int>(smem) > granted[dev].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return DGR_ERR_CUDA;
+        granted[dev].store(static_cast<int>(smem), std::memory_order_relaxed);
+    }
+    int64_t clusters = static_cast<int64_t>(sms) * (1024 / NT) / cluster;
+    if (clusters < 1) clusters = 1;
+    if (clusters > p.T) clusters = p.T > 0 ? p.T : 1;
+    const unsigned capped = sched_grid(static_cast<unsigned>(clusters * cluster)) / cluster;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((capped > 0 ? capped : 1) * cluster);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
-template <typename T>
-dgr_status launch_type(const DistillParams &p, int sms, cudaStream_t s) {
-    if (p.teacher_lse) return p.V >= 16384 ? launch_rows<T, 512, true>(p, sms, s) : launch_rows<T, 128, true>(p, sms, s);
-    return p.V >= 16384 ? launch_rows<T, 512, false>(p, sms, s) : launch_rows<T, 128, false>(p, sms, s);
+template <typename T, bool TAIL>
+dgr_status launch_size(const DistillParams &p, int sms, cudaStream_t s) {
+    if (p.V < 8192) return launch_rows<T, 128, TAIL>(p, 1, sms, s);
+    int cluster = 1;
+    // with a gradient: the rows that 304 CTAs hold at a time stay within about 40 MB of L2
+    while (p.dz && cluster < kMaxCluster && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10) * cluster) cluster <<= 1;
+    // few rows: a row over more CTAs, down to 4096 elements each
+    while (cluster < kMaxCluster && static_cast<int64_t>(p.T) * cluster * 2 <= 304 && p.V >= 4096 * cluster * 2) cluster <<= 1;
+    return launch_rows<T, 512, TAIL>(p, cluster, sms, s);
 }
 
 size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? static_cast<size_t>(((T - 1) * ld + W) * es) : 0; }
@@ -372,5 +657,6 @@ extern "C" dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_
     int sms = 0;
     if ((st = usable_sms(&sms)) != DGR_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return es == 2 ? launch_type<bf16>(p, sms, s) : launch_type<float>(p, sms, s);
+    if (es == 2) return teacher_lse ? launch_size<bf16, true>(p, sms, s) : launch_size<bf16, false>(p, sms, s);
+    return teacher_lse ? launch_size<float, true>(p, sms, s) : launch_size<float, false>(p, sms, s);
 }

@@ -516,8 +516,8 @@ dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const void *y, i
  *
  * An entry with ids < 0 is none (the lists of dgr_topk_canonicalize may be
  * passed as they are); an id >= V is left out and records DGR_ERR_INVALID_ARG
- * in the status word. An id that comes twice adds both its q. A row of weight
- * 0, or without a valid entry, has loss 0 and gradient 0, and its logits are not read.
+ * in the status word. An id that comes twice adds both its q. A row of weight 0,
+ * or without a valid entry, has loss 0 and gradient 0, whatever its logits hold.
  * Sums are binary32 in an order that depends on T, V, K and alignment alone.
  *
  * logits:   [T, V] bf16 or fp32 (dtype), row stride ld; ids int32 and teacher
