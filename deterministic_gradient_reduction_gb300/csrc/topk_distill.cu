@@ -35,6 +35,7 @@
 // fixed order set by V, T and the alignment; the rows' losses over one CTA in a
 // fixed order.
 #include <atomic>
+#include <type_traits>
 
 #include "row_common.cuh"
 
@@ -63,7 +64,6 @@ struct DistillParams {
     float *row_loss, *loss;
     void *dz;
     int64_t ld_dz;
-    int32_t same_align;  // z's and dz's rows start at the same place of a 16-byte vector
     WsHeader *hdr;       // pad[0]: clusters done
     Sched sched;
 };
@@ -338,45 +338,50 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             __syncthreads();
             for (;;) {  // a second time only where k times the maximum is out of range; `shift` is subtracted then
                 Running run;
-                const char *src = first + tid * 16;
-                int b = tid;
-                for (int v = tid; v < view.count; v += U * NT, src += static_cast<size_t>(U) * NT * 16, b += NT) {
-                    uint4 r[U];
-                    constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        r[u] = make_uint4(low, low, low, low);
-                        load_if<false>(r[u], src + u * NT * 16, v + u * NT < view.count);
-                    }
-                    uint32_t bits = TAIL ? s_bits[b] : 0;
-                    if (bits) {
+                auto pass = [&](auto shifted) {
+                    const char *src = first + tid * 16;
+                    int b = tid;
+                    for (int v = tid; v < view.count; v += U * NT, src += static_cast<size_t>(U) * NT * 16, b += NT) {
+                        uint4 r[U];
+                        constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            uint32_t q[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+                            r[u] = make_uint4(low, low, low, low);
+                            load_if<false>(r[u], src + u * NT * 16, v + u * NT < view.count);
+                        }
+                        const uint32_t bits = TAIL ? s_bits[b] : 0;
+                        if (bits) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if constexpr (sizeof(T) == 4) {
-                                    if (bits >> (u * 4 + i) & 1) q[i] = low;
-                                } else {
-                                    const uint32_t two = bits >> (u * 8 + 2 * i) & 3;
-                                    if (two & 1) q[i] = (q[i] & 0xffff0000u) | 0xff80u;
-                                    if (two & 2) q[i] = (q[i] & 0xffffu) | 0xff800000u;
+                            for (int u = 0; u < U; ++u) {
+                                uint32_t q[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    if constexpr (sizeof(T) == 4) {
+                                        if (bits >> (u * 4 + i) & 1) q[i] = low;
+                                    } else {
+                                        const uint32_t two = bits >> (u * 8 + 2 * i) & 3;
+                                        if (two & 1) q[i] = (q[i] & 0xffff0000u) | 0xff80u;
+                                        if (two & 2) q[i] = (q[i] & 0xffffu) | 0xff800000u;
+                                    }
                                 }
+                                r[u] = make_uint4(q[0], q[1], q[2], q[3]);
                             }
-                            r[u] = make_uint4(q[0], q[1], q[2], q[3]);
+                        }
+                        const float top = max_of<T, U>(r);
+                        run.raise(shifted.value ? __fadd_rn(top, -shift) : top, p.k2);
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            float x[VEC];
+                            unpack<T, VEC>(r[u], x);
+                            if constexpr (shifted.value)
+#pragma unroll
+                                for (int i = 0; i < VEC; ++i) x[i] = __fadd_rn(x[i], -shift);
+                            run.add(x, p.k2);
                         }
                     }
-                    run.raise(__fadd_rn(max_of<T, U>(r), -shift), p.k2);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        float x[VEC];
-                        unpack<T, VEC>(r[u], x);
-                        if (shift != 0.0f)
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) x[i] = __fadd_rn(x[i], -shift);
-                        run.add(x, p.k2);
-                    }
-                }
+                };
+                if (shift == 0.0f) pass(std::false_type{});
+                else pass(std::true_type{});
                 if (tid < view.n_single) {
                     const int j = view.single(tid);
                     bool listed = false;
@@ -451,40 +456,68 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             fetch_list(item + n_clusters, n + 1, weight_next);
         }
         if (p.dz) {
-            const char *src = first + tid * 16;
-            T *dst = dz + view.head + static_cast<int64_t>(view.first) * VEC + tid * VEC;
-            for (int v = tid; v < view.count; v += U * NT, src += static_cast<size_t>(U) * NT * 16, dst += U * NT * VEC) {
-                uint4 r[U];
+            // the gradient of four words' elements
+            auto gradient = [&](uint4 r, auto shifted) {
+                float x[VEC];
+                unpack<T, VEC>(r, x);
+                if constexpr (shifted.value)
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    r[u] = make_uint4(0, 0, 0, 0);
-                    load_if<false>(r[u], src + u * NT * 16, live && v + u * NT < view.count);
-                }
+                    for (int i = 0; i < VEC; ++i) x[i] = __fadd_rn(x[i], -shift);
+                vec_fma(x, p.k2, -c_rest);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float x[VEC];
-                    unpack<T, VEC>(r[u], x);
-                    if (shift != 0.0f)
+                for (int i = 0; i < VEC; ++i) x[i] = ex2(x[i]);
+                vec_scale(x, a);
+                return pack<T, VEC>(x);
+            };
+            T *own = dz + view.head + static_cast<int64_t>(view.first) * VEC;  // this CTA's part of the gradient's row
+            // elements before its first 16-byte boundary: its vectors are then
+            // made of two neighbouring ones of the logits
+            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(own) & 15) / static_cast<int>(sizeof(T));
+            const int lead = off ? min(VEC - off, view.count * VEC) : 0, n_out = (view.count * VEC - lead) / VEC;
+            auto pass = [&](auto shifted, auto aligned_too) {
+                constexpr int F = aligned_too.value ? U : 2;
+                for (int v = tid; v < n_out; v += F * NT) {
+                    const char *src = first + static_cast<int64_t>(v) * 16;
+                    uint4 r[F], next[F];
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) x[i] = __fadd_rn(x[i], -shift);
-                    vec_fma(x, p.k2, -c_rest);
+                    for (int u = 0; u < F; ++u) {
+                        const bool on = v + u * NT < n_out;
+                        r[u] = next[u] = make_uint4(0, 0, 0, 0);
+                        load_if<false>(r[u], src + u * NT * 16, on);
+                        if constexpr (!aligned_too.value) load_if<false>(next[u], src + u * NT * 16 + 16, on);
+                    }
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) x[i] = ex2(x[i]);
-                    vec_scale(x, a);
-                    r[u] = pack<T, VEC>(x);
-                    if (!live) r[u] = make_uint4(0, 0, 0, 0);  // whatever the row holds
-                }
+                    for (int u = 0; u < F; ++u) {
+                        if constexpr (!aligned_too.value) {
+                            const int by = lead * static_cast<int>(sizeof(T)) * 8;
+                            uint32_t q[8] = {r[u].x, r[u].y, r[u].z, r[u].w, next[u].x, next[u].y, next[u].z, next[u].w};
+                            if (by & 64)
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (v + u * NT >= view.count) continue;
-                    if (p.same_align) {
-                        *reinterpret_cast<uint4 *>(dst + u * NT * VEC) = r[u];
-                    } else {
-                        const T *e = reinterpret_cast<const T *>(&r[u]);
+                                for (int i = 0; i < 6; ++i) q[i] = q[i + 2];
+                            if (by & 32)
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) dst[u * NT * VEC + i] = e[i];
+                                for (int i = 0; i < 5; ++i) q[i] = q[i + 1];
+                            r[u] = make_uint4(__funnelshift_r(q[0], q[1], by & 31), __funnelshift_r(q[1], q[2], by & 31),
+                                              __funnelshift_r(q[2], q[3], by & 31), __funnelshift_r(q[3], q[4], by & 31));
+                        }
+                        if (v + u * NT < n_out) reinterpret_cast<uint4 *>(own + lead)[v + u * NT] = gradient(r[u], shifted);
                     }
                 }
+            };
+            if (!live) {  // zeros, whatever the row holds
+                for (int v = tid; v < n_out; v += NT) reinterpret_cast<uint4 *>(own + lead)[v] = make_uint4(0, 0, 0, 0);
+            } else if (shift != 0.0f) {
+                pass(std::true_type{}, std::false_type{});
+            } else if (lead == 0) {
+                pass(std::false_type{}, std::true_type{});
+            } else {
+                pass(std::false_type{}, std::false_type{});
+            }
+            if (tid < view.count * VEC - n_out * VEC) {  // elements around the vectors
+                const int j = tid < lead ? tid : n_out * VEC + tid;
+                const float in = to_f32(reinterpret_cast<const T *>(first)[j]);
+                const float x = live ? __fmul_rn(ex2(__fmaf_rn(__fadd_rn(in, -shift), p.k2, -c_rest)), a) : 0.0f;
+                *reinterpret_cast<raw_t<T, 1> *>(own + j) = pack<T, 1>(&x);
             }
             if (tid < view.n_single) {
                 const int j = view.single(tid);
@@ -650,8 +683,6 @@ extern "C" dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_
     p.teacher_lse = teacher_lse, p.weights = weights, p.dloss = dloss;
     p.inv_tau = inv_tau, p.k2 = static_cast<float>(1.4426950408889634 / static_cast<double>(tau)), p.scale = scale;
     p.row_loss = row_loss, p.loss = loss, p.dz = dlogits, p.ld_dz = ld_d;
-    const intptr_t apart = reinterpret_cast<intptr_t>(dlogits) - reinterpret_cast<intptr_t>(logits);
-    p.same_align = dlogits && apart % 16 == 0 && ((ld_d - ld) * es) % 16 == 0;
     p.hdr = static_cast<WsHeader *>(ws);
     p.sched = sched_for(static_cast<uint32_t>(T));
     int sms = 0;
