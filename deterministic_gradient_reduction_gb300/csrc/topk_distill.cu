@@ -207,7 +207,7 @@ __host__ __device__ inline int batches(int V, int threads, int size, int es) {
 }
 
 // Dynamic shared memory: the lists of this row and the next, the student's
-// logits at the entries, copy flags [K], and with q_r the list's bits.
+// logits at the entries, their places [K], and the list's bits.
 size_t distill_smem(int K, int V, int threads, int size, int es) {
     return 2 * list_bytes(K) + static_cast<size_t>(K) * 8 + static_cast<size_t>(batches(V, threads, size, es)) * threads * 4;
 }
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     __shared__ float s_loss[2][kMaxCluster * W];   // likewise their parts of a row's loss
     __shared__ float2 s_list;                      // ln of the list's normaliser, sum of its q
     __shared__ int s_any, last;
+    __shared__ uint32_t s_twice;                   // the row (item + 1) in whose list an id came twice
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     const uint32_t n_clusters = gridDim.x / size, T_rows = static_cast<uint32_t>(p.T);
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         copy_commit();
     };
     const int list_warps = min(W, (K + 31) / 32);  // warps that hold entries
-    int64_t loss_row = -1;      // CTA 0, warp 0: a row whose loss waits for the other CTAs' parts
+    int64_t loss_row = -1;      // CTA 0, last warp: a row whose loss waits for the other CTAs' parts
     float loss_tail = 0.0f;
     uint32_t live_n = 0;        // rows worked on: the exchange's parity
     auto finish_loss = [&]() {  // their parts have come with the last cluster barrier
@@ -260,8 +261,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
 
     uint32_t item = blockIdx.x / size;
     float weight = weight_of(item), weight_next = weight_of(item + n_clusters);
-    if (TAIL)
-        for (int j = tid; j < batches(p.V, NT, size, sizeof(T)) * NT; j += NT) s_bits[j] = 0;
+    if (tid == 0) s_twice = 0;
+    for (int j = tid; j < batches(p.V, NT, size, sizeof(T)) * NT; j += NT) s_bits[j] = 0;
     fetch_list(item, 0, weight);
     __syncthreads();
     for (uint32_t n = 0; item < T_rows; ++n, item += n_clusters) {
@@ -275,26 +276,33 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         copy_wait();  // each thread's own part of the list
         const float weight_2 = weight_of(item + 2 * n_clusters);
         float a = 0.0f, c_rest = 0.0f, f = 0.0f, c_all = 0.0f, inv_mass = 0.0f, total = 1.0f, shift = 0.0f;
+        float rest_s = 0.0f, left = 0.0f;  // sum outside the list, q left for it
         bool live = false;
         if (weight != 0.0f) {
-            // the list's entries in this CTA: where they lie, their student's
-            // logits (on their way during the pass), their bits. An entry whose
-            // bit is set already is a copy; which of the two does not matter,
-            // the other writes the sum of both.
+            // the list's entries in this CTA: where they lie, their bits. An
+            // entry whose bit is set already is a copy; which of the two does
+            // not matter, the other writes the sum of both.
             for (int k = tid; k < K; k += NT) {
                 const int id = ids[k];
                 int at = id >= 0 && id < p.V ? view.place(id) : -1;
-                if (at >= 0) s_z[k] = to_f32(z[id]);
-                if (TAIL && at >= 0 && at < View::kSingle) {
+                if (at >= View::kSingle) {
+                    for (int j = 0; j < k; ++j)
+                        if (__ldg(p.ids + row * p.ld_ids + j) == id) at |= kCopy;
+                } else if (at >= 0) {
                     const int v = at / VEC, j = v / NT;  // vector j of its thread
                     const uint32_t bit = 1u << (j % U * VEC + at % VEC);
                     if (atomicOr(&s_bits[j / U * NT + v % NT], bit) & bit) at |= kCopy;
                 }
+                if (at >= 0 && (at & kCopy)) s_twice = item + 1;
                 s_copy[k] = at;
+                if (k >= NT && at >= 0) s_z[k] = to_f32(z[id]);
             }
+            // the student's logit at this thread's first entry, on its way during the pass
+            raw_t<T, 1> z_raw = 0;
+            if (tid < K) load_if<false>(z_raw, z + max(ids[tid], 0), s_copy[tid] >= 0);
             __syncthreads();
             fetch_list(item + n_clusters, n + 1, weight_next);
-            if (w == W - 1) {  // the list's sums
+            if (w == W - 1) {  // the list's sums (read behind the cluster barrier)
                 float top = -INFINITY, sum = 0.0f;
                 const float lse_t = TAIL ? __ldg(p.teacher_lse + row) : 0.0f;
                 bool any = false, bad = false;
@@ -321,21 +329,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     s_list = make_float2(TAIL ? lse_t : __fadd_rn(top, logf(sum)), TAIL ? sum : 1.0f);
                 }
             }
-            // copies among the single elements, and without bits: entry by entry
-            // (neighbouring threads share an entry's comparisons)
-            {
-                int log_help = 0;
-                while (log_help < 5 && K << (log_help + 1) <= NT) ++log_help;
-                for (int i = tid; i < (((K << log_help) + 31) & ~31); i += NT) {
-                    const int k = i >> log_help, h = i & ((1 << log_help) - 1);
-                    bool copy = false;
-                    if (k < K && s_copy[k] >= 0 && (!TAIL || (s_copy[k] & ~kCopy) >= View::kSingle))
-                        for (int j = h; j < k; j += 1 << log_help) copy |= ids[j] == ids[k];
-                    for (int s = 1; s < 1 << log_help; s <<= 1) copy |= __shfl_xor_sync(0xffffffffu, copy, s) != 0;
-                    if (copy && h == 0) s_copy[k] |= kCopy;
-                }
-            }
-            __syncthreads();
             for (;;) {  // a second time only where k times the maximum is out of range; `shift` is subtracted then
                 Running run;
                 auto pass = [&](auto shifted) {
@@ -395,6 +388,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 }
                 Pair rest{run.m, __fadd_rn(run.s.x, run.s.y)}, in{-INFINITY, 0.0f};
                 rest.over_warp(p.k2);
+                if (tid < K) {
+                    float one[1];
+                    unpack<T, 1>(z_raw, one);
+                    s_z[tid] = one[0];
+                }
                 if (TAIL && w < list_warps) {  // the list's tokens in this CTA, each once
                     for (int k = tid; k < K; k += NT)
                         if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.m = fmaxf(in.m, __fadd_rn(s_z[k], -shift));
@@ -443,13 +441,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 inv_mass = __fmul_rn(inv, !TAIL || q_rest > 0.0f ? 1.0f : sum_q);
                 f = __fmul_rn(__fmul_rn(__fmul_rn(p.scale, weight), p.inv_tau), p.dloss ? __ldg(p.dloss) : 1.0f);
                 a = __fmul_rn(TAIL ? __fadd_rn(__fmul_rn(down, inv_mass), q_rest > 0.0f ? -q_rest / rest.s : 0.0f) : inv, f);
-                if (p.row_loss && rank == 0 && w == 0) {
-                    finish_loss();
-                    loss_row = row;
-                    loss_tail = 0.0f;
-                    if (q_rest > 0.0f && live)
-                        loss_tail = __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -__fadd_rn(__fmaf_rn(__fadd_rn(c_rest, -c_all), kLn2, logf(rest.s)), -logf(total))));
-                }
+                rest_s = rest.s;
+                left = q_rest;
                 break;
             }
         } else {
@@ -527,6 +520,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         }
         if (weight != 0.0f) {
             __syncthreads();
+            if (p.row_loss && rank == 0 && w == W - 1) {
+                finish_loss();
+                loss_row = row;
+                loss_tail = 0.0f;
+                if (left > 0.0f && live)
+                    loss_tail = __fmul_rn(left, __fadd_rn(logf(left), -__fadd_rn(__fmaf_rn(__fadd_rn(c_rest, -c_all), kLn2, logf(rest_s)), -logf(total))));
+            }
             // the list's entries: their part of the loss, their tokens' gradient
             if (w < list_warps) {
                 float part = 0.0f;
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 for (int k = tid; k < K; k += NT) {
                     const int at = s_copy[k] & ~kCopy;
                     if (s_copy[k] < 0) continue;
-                    if (TAIL && at < View::kSingle) s_bits[at / VEC / NT / U * NT + at / VEC % NT] = 0;  // free again
+                    if (at < View::kSingle) s_bits[at / VEC / NT / U * NT + at / VEC % NT] = 0;  // free again
                     if (!live) continue;
                     const float lq = __fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -base);
                     float q = expf(lq);
@@ -542,9 +542,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     if (q != 0.0f) part = __fmaf_rn(q, __fadd_rn(lq, -__fmaf_rn(x, kLn2, -ln_total)), part);
                     if (!p.dz || (s_copy[k] & kCopy)) continue;
                     const int id = ids[k];
-                    q = 0.0f;
-                    for (int j = 0; j < K; ++j)
-                        if (ids[j] == id) q = __fadd_rn(q, expf(__fadd_rn(__fmul_rn(teacher[j], p.inv_tau), -base)));
+                    if (s_twice == item + 1) {
+                        q = 0.0f;
+                        for (int j = 0; j < K; ++j)
+                            if (ids[j] == id) q = __fadd_rn(q, expf(__fadd_rn(__fmul_rn(teacher[j], p.inv_tau), -base)));
+                    }
                     const float g = __fmul_rn(__fmaf_rn(ex2(x), inv_mass, -q), f);
                     *reinterpret_cast<raw_t<T, 1> *>(dz + id) = pack<T, 1>(&g);
                 }
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     if (size > 1) cluster_barrier();  // the last row's parts; no CTA leaves before its shared memory is read
     else __syncthreads();
     if (rank != 0) return;
-    if (w == 0) finish_loss();
+    if (w == W - 1) finish_loss();
     // rows without weight: no loss
     if (p.row_loss && p.weights)
         for (uint32_t i = blockIdx.x / size + tid * n_clusters; i < T_rows; i += NT * n_clusters)
