@@ -608,12 +608,8 @@ dgr_status launch_rows(const DistillParams &p, int cluster, int sms, cudaStream_
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return DGR_ERR_CUDA;
         granted[dev].store(static_cast<int>(smem), std::memory_order_relaxed);
     }
-    int64_t clusters = static_cast<int64_t>(sms) * (1024 / NT) / cluster;
-    if (clusters < 1) clusters = 1;
-    if (clusters > p.T) clusters = p.T > 0 ? p.T : 1;
-    const unsigned capped = sched_grid(static_cast<unsigned>(clusters * cluster)) / cluster;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((capped > 0 ? capped : 1) * cluster);
+    cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -623,6 +619,22 @@ dgr_status launch_rows(const DistillParams &p, int cluster, int sms, cudaStream_
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    // one wave: as many clusters as the device holds at once (a cluster's CTAs
+    // share a part of the SMs, so this is less than the SMs over its size; a
+    // few clusters more would each take their share of the rows afterwards)
+    static std::atomic<uint64_t> held[64][4];  // by device and cluster size: shared memory << 32 | clusters
+    std::atomic<uint64_t> &h = held[dev][cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3];
+    const uint64_t known = h.load(std::memory_order_relaxed);
+    int clusters = static_cast<int>(known & 0xffffffffu);
+    if (known == 0 || known >> 32 != smem) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) != cudaSuccess || clusters < 1) return DGR_ERR_CUDA;
+        h.store(static_cast<uint64_t>(smem) << 32 | static_cast<uint32_t>(clusters), std::memory_order_relaxed);
+    }
+    const int within = sms * (1024 / NT) / cluster;  // a green context's, or the test's cap
+    if (clusters > within) clusters = within > 0 ? within : 1;
+    if (clusters > p.T) clusters = p.T > 0 ? p.T : 1;
+    const unsigned capped = sched_grid(static_cast<unsigned>(clusters * cluster)) / cluster;
+    cfg.gridDim = dim3((capped > 0 ? capped : 1) * cluster);
     return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
