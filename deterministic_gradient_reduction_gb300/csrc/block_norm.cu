@@ -43,39 +43,21 @@ struct NormParams {
     float *dw_post, *dgate, *dw_pre;
     float *slots;               // [n_slots, 2H]: C, then dw_pre
     int32_t n_slots, accumulate;
+    int32_t depth;              // rows in shared memory
     Sched sched;
 };
 
 // The row's elements of this thread: vector i of its NV is number i * team + tl.
-template <typename T, int VEC, int NV>
+template <int VEC>
 struct Cols {
     int team, tl, n_vec;
     __device__ __forceinline__ bool has(int i) const { return i * team + tl < n_vec; }
     __device__ __forceinline__ int at(int i) const { return (i * team + tl) * VEC; }
 };
 
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void load_row(float *f, const void *base, int64_t ld, int32_t row, const Cols<T, VEC, NV> &c) {
-    const T *src = static_cast<const T *>(base) + static_cast<int64_t>(row) * ld;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        raw_t<T, VEC> v{};
-        if (c.has(i)) v = *reinterpret_cast<const raw_t<T, VEC> *>(src + c.at(i));
-        unpack<T, VEC>(v, f + i * VEC);
-    }
-}
-
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void store_row(const float *f, void *base, int64_t ld, int32_t row, const Cols<T, VEC, NV> &c) {
-    T *dst = static_cast<T *>(base) + static_cast<int64_t>(row) * ld;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (c.has(i)) *reinterpret_cast<raw_t<T, VEC> *>(dst + c.at(i)) = pack<T, VEC>(f + i * VEC);
-}
-
 // gw = w_post times the channel gate (1 where there is none), w2 = w_pre.
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void load_weights(float *gw, float *w2, const NormParams &p, const Cols<T, VEC, NV> &c) {
+template <int VEC, int NV>
+__device__ __forceinline__ void load_weights(float *gw, float *w2, const NormParams &p, const Cols<VEC> &c) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -92,112 +74,216 @@ __device__ __forceinline__ void load_weights(float *gw, float *w2, const NormPar
         }
 }
 
-// Sums over the team that has a row: a warp, or the whole block (two buffers
-// in turn, so that one barrier a sum is enough).
-template <bool WARP, int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], float *buf, int &turn) {
-    if constexpr (WARP) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    } else {
-        block_sum<N>(v, buf + turn * 32 * 8, blockDim.x >> 5);
-        turn ^= 1;
+// The rows' elements on their way: `depth` rows of S streams in shared memory,
+// every element fetched and read by the same thread, so no barrier is needed
+// for it. Elements of 2 bytes (rows that start at odd ones) are too small for
+// such copies, and rows too wide for shared memory (depth 0) do not fit: they
+// are loaded where they are used.
+template <typename T, int VEC, int NV, int S>
+struct Feed {
+    using raw = raw_t<T, VEC>;
+    static constexpr bool kRing = sizeof(raw) >= 4;
+    raw *ring;
+    const T *rows[S];
+    int64_t ld[S];
+    const Cols<VEC> &c;
+    int in = 0, out = 0, depth;
+
+    __device__ __forceinline__ raw *slot(int d, int s, int i) const {
+        return ring + ((d * S + s) * NV + i) * static_cast<int>(blockDim.x) + threadIdx.x;
     }
+    __device__ __forceinline__ void fetch(int64_t row, bool on) {
+        if constexpr (kRing) {
+            if (on && depth)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (rows[s]) {
+                        const T *src = rows[s] + row * ld[s];
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            if (c.has(i)) copy_async<sizeof(raw)>(slot(in, s, i), src + c.at(i));
+                    }
+            copy_commit();
+            in = in + 1 >= depth ? 0 : in + 1;
+        }
+    }
+    // vector i of stream s of the row in use (zeros where the thread has none)
+    __device__ __forceinline__ void get(float *f, int64_t row, int s, int i) const {
+        raw v{};
+        if (rows[s] && c.has(i)) {
+            if (kRing && depth) v = *slot(out, s, i);
+            else v = *reinterpret_cast<const raw *>(rows[s] + row * ld[s] + c.at(i));
+        }
+        unpack<T, VEC>(v, f);
+    }
+    __device__ __forceinline__ void next() {
+        if constexpr (kRing) out = out + 1 >= depth ? 0 : out + 1;
+    }
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void put(const float *f, void *base, int64_t at) {
+    *reinterpret_cast<raw_t<T, VEC> *>(static_cast<T *>(base) + at) = pack<T, VEC>(f);
 }
 
-template <typename T, int VEC, int NV, int MAXT, bool WARP>
-__global__ void __launch_bounds__(MAXT) norm_forward(const NormParams p) {
-    __shared__ float buf[2 * 32 * 8];
+// The sum of v over the team that has a row: a warp, or the whole block (two
+// buffers in turn, so that one barrier a sum is enough).
+template <bool WARP>
+__device__ __forceinline__ float team_sum(float v, float *buf, int &turn) {
+    v = warp_sum(v);
+    if constexpr (!WARP) {
+        float *b = buf + turn * 32;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int n = blockDim.x >> 5;
+        v = (threadIdx.x & 31) < n ? b[threadIdx.x & 31] : 0.0f;
+        for (int s = 1; s < n; s <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, s));
+        v = __shfl_sync(0xffffffffu, v, 0);
+    }
+    return v;
+}
+
+template <typename T, int VEC, int NV, int MAXT, int MINB, bool WARP>
+__global__ void __launch_bounds__(MAXT, MINB) norm_forward(const NormParams p) {
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float buf[2 * 32];
     constexpr int E = NV * VEC;
     const int teams = WARP ? kWarpTeams : 1;
-    const Cols<T, VEC, NV> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
+    const Cols<VEC> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
+    Feed<T, VEC, NV, 2> feed{reinterpret_cast<raw_t<T, VEC> *>(smem), {static_cast<const T *>(p.x), static_cast<const T *>(p.y)}, {p.ld_x, p.ld_y}, c, 0, 0, p.depth};
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t it = static_cast<int64_t>(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0);
+    auto row_of = [&](int64_t i) { return static_cast<int64_t>(sched_item(p.sched, static_cast<uint32_t>(i < p.T ? i : 0))); };
+    for (int d = 0; d + 1 < p.depth; ++d) feed.fetch(row_of(it + d * step), it + d * step < p.T);
     float gw[E], w2[E];
-    load_weights(gw, w2, p, c);
+    load_weights<VEC, NV>(gw, w2, p, c);
     const float inv_h = 1.0f / static_cast<float>(p.H);
     int turn = 0;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0); it < p.T;
-         it += static_cast<int64_t>(gridDim.x) * teams) {
-        const int32_t row = static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(it)));
+    for (; it < p.T; it += step) {
+        const int64_t row = row_of(it), ahead = it + (p.depth > 0 ? p.depth - 1 : 0) * step;
+        feed.fetch(row_of(ahead), ahead < p.T);
+        float f = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
+        copy_wait_for(p.depth);
         float h[E];
-        load_row<T, VEC, NV>(h, p.x, p.ld_x, row, c);
         if (p.y) {
-            float y[E];
-            load_row<T, VEC, NV>(y, p.y, p.ld_y, row, c);
-            float f = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
             if (p.w_post) {
-                float s[1] = {0.0f};
+                float s = 0.0f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[0] = __fmaf_rn(y[e], y[e], s[0]);
-                team_sum<WARP>(s, buf, turn);
-                f = __fmul_rn(f, rsqrtf(__fmaf_rn(s[0], inv_h, p.eps)));
+                for (int i = 0; i < NV; ++i) {
+                    float y[VEC];
+                    feed.get(y, row, 1, i);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) s = __fmaf_rn(y[j], y[j], s);
+                }
+                s = team_sum<WARP>(s, buf, turn);
+                f = __fmul_rn(f, rsqrtf(__fmaf_rn(s, inv_h, p.eps)));
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = __fmaf_rn(p.alpha, h[e], __fmul_rn(__fmul_rn(y[e], f), gw[e]));
-            store_row<T, VEC, NV>(h, p.out_h, p.ld_oh, row, c);
+            for (int i = 0; i < NV; ++i) {
+                float x[VEC], y[VEC];
+                feed.get(x, row, 0, i);
+                feed.get(y, row, 1, i);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    h[i * VEC + j] = __fmaf_rn(p.alpha, x[j], __fmul_rn(__fmul_rn(y[j], f), gw[i * VEC + j]));
+                if (c.has(i)) put<T, VEC>(h + i * VEC, p.out_h, row * p.ld_oh + c.at(i));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) feed.get(h + i * VEC, row, 0, i);
         }
         if (p.out_u) {
-            float s[1] = {0.0f};
+            float s = 0.0f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[0] = __fmaf_rn(h[e], h[e], s[0]);
-            team_sum<WARP>(s, buf, turn);
-            const float r = rsqrtf(__fmaf_rn(s[0], inv_h, p.eps));
+            for (int e = 0; e < E; ++e) s = __fmaf_rn(h[e], h[e], s);
+            s = team_sum<WARP>(s, buf, turn);
+            const float r = rsqrtf(__fmaf_rn(s, inv_h, p.eps));
 #pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = __fmul_rn(__fmul_rn(h[e], r), w2[e]);
-            store_row<T, VEC, NV>(h, p.out_u, p.ld_ou, row, c);
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) h[i * VEC + j] = __fmul_rn(__fmul_rn(h[i * VEC + j], r), w2[i * VEC + j]);
+                if (c.has(i)) put<T, VEC>(h + i * VEC, p.out_u, row * p.ld_ou + c.at(i));
+            }
         }
+        feed.next();
     }
+    copy_wait();
 }
 
 // One round of sums a row: with gy = gw y,
 //   q . y = dh . gy + r2 v . gy - (r2^3 / H) (v . h) h . gy,
 // so D need not be known before the second norm's sum is made.
-template <typename T, int VEC, int NV, int MAXT, bool WARP>
-__global__ void __launch_bounds__(MAXT) norm_backward(const NormParams p) {
-    __shared__ float buf[2 * 32 * 8];
-    extern __shared__ float team_cols[];  // WARP: [kWarpTeams][2H]
+template <typename T, int VEC, int NV, int MAXT, int MINB, bool WARP>
+__global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) {
+    extern __shared__ __align__(16) char smem[];  // the rows on their way; at the end WARP: the teams' columns [kWarpTeams][2H]
+    __shared__ float buf[2][32][8];
     constexpr int E = NV * VEC;
-    const int teams = WARP ? kWarpTeams : 1;
+    enum { kH, kDh, kDu, kY };
+    const int teams = WARP ? kWarpTeams : 1, lane = threadIdx.x & 31;
     const int team = WARP ? threadIdx.x >> 5 : 0;
-    const Cols<T, VEC, NV> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
+    const Cols<VEC> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
+    Feed<T, VEC, NV, 4> feed{reinterpret_cast<raw_t<T, VEC> *>(smem),
+                             {static_cast<const T *>(p.h), static_cast<const T *>(p.dh), static_cast<const T *>(p.du), static_cast<const T *>(p.y)},
+                             {p.ld_h, p.ld_dh, p.ld_du, p.ld_y}, c, 0, 0, p.depth};
+    const int64_t step = static_cast<int64_t>(p.n_slots) * teams;
     float gw[E], w2[E];
-    load_weights(gw, w2, p, c);
     const float inv_h = 1.0f / static_cast<float>(p.H);
     int turn = 0;
+    bool first = true;
     for (int32_t is = blockIdx.x; is < p.n_slots; is += gridDim.x) {
         const int32_t slot = static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(is)));
+        const int64_t row0 = static_cast<int64_t>(slot) * teams + team;
+        for (int d = 0; d + 1 < p.depth; ++d) feed.fetch(row0 + d * step, row0 + d * step < p.T);
+        if (first) load_weights<VEC, NV>(gw, w2, p, c);
+        first = false;
         float accC[E], accW[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) accC[e] = accW[e] = 0.0f;
-        for (int64_t r64 = static_cast<int64_t>(slot) * teams + team; r64 < p.T; r64 += static_cast<int64_t>(p.n_slots) * teams) {
-            const int32_t row = static_cast<int32_t>(r64);
-            float h[E], dh[E], du[E], y[E];
+        for (int64_t row = row0; row < p.T; row += step) {
+            const int64_t ahead = row + (p.depth > 0 ? p.depth - 1 : 0) * step;
+            feed.fetch(ahead, ahead < p.T);
+            const float gt = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
+            copy_wait_for(p.depth);
+            float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // h.h, v.h, y.y, dh.gy, v.gy, h.gy
 #pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = dh[e] = du[e] = y[e] = 0.0f;
-            if (p.w_pre) {
-                load_row<T, VEC, NV>(h, p.h, p.ld_h, row, c);
-                load_row<T, VEC, NV>(du, p.du, p.ld_du, row, c);
-            }
-            if (p.dh) load_row<T, VEC, NV>(dh, p.dh, p.ld_dh, row, c);
-            if (p.y) load_row<T, VEC, NV>(y, p.y, p.ld_y, row, c);
-            float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // h.h, v.h, y.y, dh.gy, v.gy, h.gy
+            for (int i = 0; i < NV; ++i) {
+                float h[VEC], dh[VEC], du[VEC], y[VEC];
+                feed.get(h, row, kH, i);
+                feed.get(dh, row, kDh, i);
+                feed.get(du, row, kDu, i);
+                feed.get(y, row, kY, i);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float v = __fmul_rn(du[e], w2[e]), gy = __fmul_rn(gw[e], y[e]);
-                s[0] = __fmaf_rn(h[e], h[e], s[0]);
-                s[1] = __fmaf_rn(v, h[e], s[1]);
-                s[2] = __fmaf_rn(y[e], y[e], s[2]);
-                s[3] = __fmaf_rn(dh[e], gy, s[3]);
-                s[4] = __fmaf_rn(v, gy, s[4]);
-                s[5] = __fmaf_rn(h[e], gy, s[5]);
+                for (int j = 0; j < VEC; ++j) {
+                    const float v = __fmul_rn(du[j], w2[i * VEC + j]), gy = __fmul_rn(gw[i * VEC + j], y[j]);
+                    s[0] = __fmaf_rn(h[j], h[j], s[0]);
+                    s[1] = __fmaf_rn(v, h[j], s[1]);
+                    s[2] = __fmaf_rn(y[j], y[j], s[2]);
+                    s[3] = __fmaf_rn(dh[j], gy, s[3]);
+                    s[4] = __fmaf_rn(v, gy, s[4]);
+                    s[5] = __fmaf_rn(h[j], gy, s[5]);
+                }
             }
-            team_sum<WARP>(s, buf, turn);
+            float t = warp_sum8(s, lane);  // of sum lane / 4
+            if constexpr (!WARP) {
+                if ((lane & 3) == 0) buf[turn][threadIdx.x >> 5][lane >> 2] = t;
+                __syncthreads();
+                // lane: sum lane % 8 of the warps lane / 8, lane / 8 + 4, ...
+                const int n = blockDim.x >> 5;
+                t = 0.0f;
+                for (int w = lane >> 3; w < n; w += 4) t = __fadd_rn(t, buf[turn][w][lane & 7]);
+                t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                turn ^= 1;
+            }
+#pragma unroll
+            for (int k = 0; k < 6; ++k) s[k] = __shfl_sync(0xffffffffu, t, WARP ? 4 * k : k);
             float r2 = 0.0f, k2 = 0.0f;  // D = dh + r2 v - k2 h
             if (p.w_pre) {
                 r2 = rsqrtf(__fmaf_rn(s[0], inv_h, p.eps));
                 k2 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(s[1], inv_h), r2), r2), r2);  // r2^3 alone may underflow
             }
             const float dot = __fmaf_rn(-k2, s[5], __fmaf_rn(r2, s[4], s[3]));  // D . gy
-            const float gt = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
             float r1 = 1.0f, k1 = 0.0f;  // dy = gt (r1 gw D - k1 y)
             if (p.w_post) {
                 r1 = rsqrtf(__fmaf_rn(s[2], inv_h, p.eps));
@@ -209,19 +295,34 @@ __global__ void __launch_bounds__(MAXT) norm_backward(const NormParams p) {
             }
             const float yr = __fmul_rn(r1, gt), kg = __fmul_rn(k1, gt);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float v = __fmul_rn(du[e], w2[e]);
-                const float D = __fmaf_rn(-k2, h[e], __fmaf_rn(r2, v, dh[e]));
-                accW[e] = __fmaf_rn(du[e], __fmul_rn(h[e], r2), accW[e]);
-                accC[e] = __fmaf_rn(D, __fmul_rn(y[e], yr), accC[e]);
-                y[e] = __fmaf_rn(-kg, y[e], __fmul_rn(__fmul_rn(gw[e], yr), D));
-                h[e] = __fmul_rn(p.alpha, D);
+            for (int i = 0; i < NV; ++i) {
+                float h[VEC], dh[VEC], du[VEC], y[VEC];
+                feed.get(h, row, kH, i);
+                feed.get(dh, row, kDh, i);
+                feed.get(du, row, kDu, i);
+                feed.get(y, row, kY, i);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = i * VEC + j;
+                    const float v = __fmul_rn(du[j], w2[e]);
+                    const float D = __fmaf_rn(-k2, h[j], __fmaf_rn(r2, v, dh[j]));
+                    accW[e] = __fmaf_rn(du[j], __fmul_rn(h[j], r2), accW[e]);
+                    accC[e] = __fmaf_rn(D, __fmul_rn(y[j], yr), accC[e]);
+                    y[j] = __fmaf_rn(-kg, y[j], __fmul_rn(__fmul_rn(gw[e], yr), D));
+                    h[j] = __fmul_rn(p.alpha, D);
+                }
+                if (c.has(i)) {
+                    put<T, VEC>(h, p.out_h, row * p.ld_oh + c.at(i));
+                    if (p.y) put<T, VEC>(y, p.out_u, row * p.ld_ou + c.at(i));
+                }
             }
-            store_row<T, VEC, NV>(h, p.out_h, p.ld_oh, row, c);
-            if (p.y) store_row<T, VEC, NV>(y, p.out_u, p.ld_ou, row, c);
+            feed.next();
         }
+        copy_wait();  // (nothing but empty groups)
+        feed.in = feed.out = 0;
         float *dst = p.slots + static_cast<int64_t>(slot) * 2 * p.H;
         if constexpr (WARP) {  // the warps' sums, in ascending order
+            float *team_cols = reinterpret_cast<float *>(smem);
             float *mine = team_cols + static_cast<int64_t>(team) * 2 * p.H;
             __syncthreads();
 #pragma unroll
@@ -238,6 +339,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward(const NormParams p) {
                 for (int k = 1; k < kWarpTeams; ++k) v = __fadd_rn(v, team_cols[k * 2 * p.H + e]);
                 dst[e] = v;
             }
+            __syncthreads();
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -304,37 +406,61 @@ NormPlan norm_plan(int64_t T, int64_t H) {
     return pl;
 }
 
-template <typename T, int VEC, int EPT, int MAXT, bool WARP>
-dgr_status launch_norm(bool backward, const NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
+template <typename K>
+dgr_status grant(K *k, size_t smem) {
+    if (smem <= 40 * 1024) return DGR_OK;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
+}
+
+// FB, BB: CTAs that an SM is to hold, forward and backward (registers and, by
+// the ring's depth, shared memory).
+template <typename T, int VEC, int EPT, int MAXT, int FB, int BB, bool WARP>
+dgr_status launch_norm(bool backward, NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
     constexpr int NV = EPT / VEC;
+    constexpr bool ring = VEC * sizeof(T) >= 4;
+    const size_t row = ring ? static_cast<size_t>(pl.threads) * EPT * sizeof(T) * (backward ? 4 : 2) : 0;
+    const size_t room = (224 * 1024) / (backward ? BB : FB);
+    p.depth = 0;
+    if constexpr (ring) p.depth = row * 3 <= room ? 3 : row * 2 <= room ? 2 : row <= room ? 1 : 0;
+    size_t smem = row * p.depth;
     if (!backward) {
+        auto *k = norm_forward<T, VEC, NV, MAXT, FB, WARP>;
+        const dgr_status st = grant(k, smem);
+        if (st != DGR_OK) return st;
         const int64_t teams = WARP ? kWarpTeams : 1;
-        const int64_t want = (p.T + teams - 1) / teams;
-        const int64_t most = static_cast<int64_t>(sms) * (768 / pl.threads > 0 ? 768 / pl.threads : 1);
-        norm_forward<T, VEC, NV, MAXT, WARP><<<sched_grid(static_cast<unsigned>(want < most ? want : most)), pl.threads, 0, s>>>(p);
+        const int64_t want = (p.T + teams - 1) / teams, most = static_cast<int64_t>(sms) * FB;
+        k<<<sched_grid(static_cast<unsigned>(want < most ? want : most)), pl.threads, smem, s>>>(p);
         return launch_status();
     }
-    const size_t smem = WARP ? static_cast<size_t>(kWarpTeams) * 2 * p.H * 4 : 0;  // at most 32 KB
-    norm_backward<T, VEC, NV, MAXT, WARP><<<sched_grid(static_cast<unsigned>(pl.slots)), pl.threads, smem, s>>>(p);
+    const size_t cols = WARP ? static_cast<size_t>(kWarpTeams) * 2 * p.H * 4 : 0;  // at most 32 KB
+    if (smem < cols) smem = cols;
+    auto *k = norm_backward<T, VEC, NV, MAXT, BB, WARP>;
+    const dgr_status st = grant(k, smem);
+    if (st != DGR_OK) return st;
+    k<<<sched_grid(static_cast<unsigned>(pl.slots)), pl.threads, smem, s>>>(p);
     return launch_status();
 }
 
 template <typename T, int VEC>
-dgr_status launch_width(bool backward, const NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
+dgr_status launch_width(bool backward, NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
     if (pl.warp)
-        return pl.ept == 8 ? launch_norm<T, VEC, 8, 256, true>(backward, p, pl, sms, s)
-                           : launch_norm<T, VEC, 16, 256, true>(backward, p, pl, sms, s);
-    if (pl.ept == 8) return launch_norm<T, VEC, 8, 128, false>(backward, p, pl, sms, s);
-    if (pl.threads <= 512) return launch_norm<T, VEC, 16, 512, false>(backward, p, pl, sms, s);
-    return launch_norm<T, VEC, 16, 1024, false>(backward, p, pl, sms, s);
+        return pl.ept == 8 ? launch_norm<T, VEC, 8, 256, 4, 2, true>(backward, p, pl, sms, s)
+                           : launch_norm<T, VEC, 16, 256, 3, 2, true>(backward, p, pl, sms, s);
+    if (pl.ept == 8) return launch_norm<T, VEC, 8, 128, 6, 4, false>(backward, p, pl, sms, s);
+    if (pl.threads <= 128) return launch_norm<T, VEC, 16, 128, 6, 4, false>(backward, p, pl, sms, s);
+    if (pl.threads <= 256) return launch_norm<T, VEC, 16, 256, 3, 2, false>(backward, p, pl, sms, s);
+    if (pl.threads <= 512) return launch_norm<T, VEC, 16, 512, 1, 1, false>(backward, p, pl, sms, s);
+    return launch_norm<T, VEC, 16, 1024, 1, 1, false>(backward, p, pl, sms, s);
 }
 
-// The widest vector that every row's start allows.
+// The widest vector that every row's start allows: 16 bytes, 4, or one bf16.
 template <typename T>
-dgr_status launch_type(bool backward, const NormParams &p, const NormPlan &pl, int sms, cudaStream_t s, size_t align) {
-    constexpr int full = 16 / static_cast<int>(sizeof(T));
+dgr_status launch_type(bool backward, NormParams &p, const NormPlan &pl, int sms, cudaStream_t s, size_t align) {
+    constexpr int full = 16 / static_cast<int>(sizeof(T)), word = 4 / static_cast<int>(sizeof(T));
     if (align >= 16 && p.H % full == 0) return launch_width<T, full>(backward, p, pl, sms, s);
-    return launch_width<T, 1>(backward, p, pl, sms, s);
+    if (align >= 4 && p.H % word == 0) return launch_width<T, word>(backward, p, pl, sms, s);
+    if constexpr (sizeof(T) == 2) return launch_width<T, 1>(backward, p, pl, sms, s);
+    return DGR_ERR_MISALIGNED;
 }
 
 // The power of two (at most 16) that divides every row's address.

@@ -158,6 +158,38 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *buf, int n_warps
     }
 }
 
+// Eight sums over the warp at once: lanes 4 j .. 4 j + 3 end with the sum of
+// v[j] (halves of the values are exchanged at each step: 9 shuffles, not 40).
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
+    float a[4], b[2];
+    const bool up16 = (lane & 16) != 0, up8 = (lane & 8) != 0, up4 = (lane & 4) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a[i] = __fadd_rn(up16 ? v[i + 4] : v[i], __shfl_xor_sync(0xffffffffu, up16 ? v[i] : v[i + 4], 16));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b[i] = __fadd_rn(up8 ? a[i + 2] : a[i], __shfl_xor_sync(0xffffffffu, up8 ? a[i] : a[i + 2], 8));
+    float c = __fadd_rn(up4 ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, up4 ? b[0] : b[1], 4));
+    c = __fadd_rn(c, __shfl_xor_sync(0xffffffffu, c, 2));
+    return __fadd_rn(c, __shfl_xor_sync(0xffffffffu, c, 1));
+}
+
+// Copies of 4 or 16 bytes from global to shared memory, in groups.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// Until all but the newest `depth` - 1 groups have come (depth 1 to 3).
+__device__ __forceinline__ void copy_wait_for(int depth) {
+    if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else copy_wait();
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -97,21 +97,6 @@ __device__ __forceinline__ void remote_store(uint32_t a, float4 v) {
 __device__ __forceinline__ void remote_store(uint32_t a, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-// Until all but the newest `depth` - 1 groups have come (depth 1 to 3).
-__device__ __forceinline__ void copy_wait_for(int depth) {
-    if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else copy_wait();
-}
-
 // ---- a row's parts -------------------------------------------------------------
 
 // A row as whole 16-byte vectors between a few single elements; CTA `rank` of a
