@@ -48,29 +48,38 @@ struct NormParams {
 };
 
 // The row's elements of this thread: vector i of its NV is number i * team + tl.
+// They are worked on in pairs (two at a time by the packed instructions): unit
+// u is vector u, or vectors 2 u and 2 u + 1 where a vector is one element.
 template <int VEC>
 struct Cols {
+    static constexpr int kPer = VEC == 1 ? 2 : 1;     // vectors a unit
+    static constexpr int kPairs = VEC * kPer / 2;     // pairs a unit
     int team, tl, n_vec;
     __device__ __forceinline__ bool has(int i) const { return i * team + tl < n_vec; }
     __device__ __forceinline__ int at(int i) const { return (i * team + tl) * VEC; }
+    // element j of unit u: its vector and its column
+    __device__ __forceinline__ int vec(int u, int j) const { return VEC == 1 ? 2 * u + j : u; }
+    __device__ __forceinline__ int col(int u, int j) const { return VEC == 1 ? at(2 * u + j) : at(u) + j; }
 };
 
-// gw = w_post times the channel gate (1 where there is none), w2 = w_pre.
-template <int VEC, int NV>
-__device__ __forceinline__ void load_weights(float *gw, float *w2, const NormParams &p, const Cols<VEC> &c) {
+// gw = w_post times the channel gate (1 where there is none), w2 = w_pre; 0
+// where the thread has no element.
+template <int VEC, int NU>
+__device__ __forceinline__ void load_weights(float2 *gw, float2 *w2, const NormParams &p, const Cols<VEC> &c) {
+    constexpr int P = Cols<VEC>::kPairs;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            float a = 1.0f, b = 0.0f;
-            if (c.has(i)) {
-                const int e = c.at(i) + j;
-                if (p.w_post) a = param(p.w_post, p.w_bf16, e);
+        for (int j = 0; j < 2 * P; ++j) {
+            float a = 0.0f, b = 0.0f;
+            if (c.has(c.vec(u, j))) {
+                const int e = c.col(u, j);
+                a = p.w_post ? param(p.w_post, p.w_bf16, e) : 1.0f;
                 if (p.gate_mode == kGateChannel) a = __fmul_rn(a, param(p.gate, p.w_bf16, e));
                 if (p.w_pre) b = param(p.w_pre, p.w_bf16, e);
             }
-            gw[i * VEC + j] = a;
-            w2[i * VEC + j] = b;
+            (j & 1 ? gw[u * P + j / 2].y : gw[u * P + j / 2].x) = a;
+            (j & 1 ? w2[u * P + j / 2].y : w2[u * P + j / 2].x) = b;
         }
 }
 
@@ -79,18 +88,32 @@ __device__ __forceinline__ void load_weights(float *gw, float *w2, const NormPar
 // for it. Elements of 2 bytes (rows that start at odd ones) are too small for
 // such copies, and rows too wide for shared memory (depth 0) do not fit: they
 // are loaded where they are used.
-template <typename T, int VEC, int NV, int S>
+// Places that a thread never fetches are zeroed once and stay so.
+template <typename T, int VEC, int NV, int S, int MAXT>
 struct Feed {
     using raw = raw_t<T, VEC>;
     static constexpr bool kRing = sizeof(raw) >= 4;
-    raw *ring;
+    static constexpr int kStage = S * NV * MAXT;
+    raw *mine;
     const T *rows[S];
     int64_t ld[S];
     const Cols<VEC> &c;
-    int in = 0, out = 0, depth;
+    int in = 0, out = 0, end, depth;  // offsets of stages
 
-    __device__ __forceinline__ raw *slot(int d, int s, int i) const {
-        return ring + ((d * S + s) * NV + i) * static_cast<int>(blockDim.x) + threadIdx.x;
+    __device__ __forceinline__ Feed(char *smem, const void *const (&src)[S], const int64_t (&strides)[S], const Cols<VEC> &cols, int d)
+        : mine(reinterpret_cast<raw *>(smem) + threadIdx.x), c(cols), end(d * kStage), depth(d) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) rows[s] = static_cast<const T *>(src[s]), ld[s] = strides[s];
+        clear();
+    }
+    __device__ __forceinline__ void clear() {
+        if constexpr (kRing)
+            for (int k = 0; k < depth; ++k)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        if (!rows[s] || !c.has(i)) mine[k * kStage + (s * NV + i) * MAXT] = raw{};
     }
     __device__ __forceinline__ void fetch(int64_t row, bool on) {
         if constexpr (kRing) {
@@ -98,32 +121,45 @@ struct Feed {
 #pragma unroll
                 for (int s = 0; s < S; ++s)
                     if (rows[s]) {
-                        const T *src = rows[s] + row * ld[s];
+                        const T *src = rows[s] + row * ld[s] + c.tl * VEC;
 #pragma unroll
                         for (int i = 0; i < NV; ++i)
-                            if (c.has(i)) copy_async<sizeof(raw)>(slot(in, s, i), src + c.at(i));
+                            if (c.has(i)) copy_async<sizeof(raw)>(mine + in + (s * NV + i) * MAXT, src + i * c.team * VEC);
                     }
             copy_commit();
-            in = in + 1 >= depth ? 0 : in + 1;
+            in = in + kStage >= end ? 0 : in + kStage;
         }
     }
-    // vector i of stream s of the row in use (zeros where the thread has none)
-    __device__ __forceinline__ void get(float *f, int64_t row, int s, int i) const {
+    __device__ __forceinline__ raw vector(int64_t row, int s, int i) const {
         raw v{};
-        if (rows[s] && c.has(i)) {
-            if (kRing && depth) v = *slot(out, s, i);
-            else v = *reinterpret_cast<const raw *>(rows[s] + row * ld[s] + c.at(i));
-        }
-        unpack<T, VEC>(v, f);
+        if (kRing && depth) v = mine[out + (s * NV + i) * MAXT];
+        else if (rows[s] && c.has(i)) v = *reinterpret_cast<const raw *>(rows[s] + row * ld[s] + c.at(i));
+        return v;
+    }
+    // unit u of stream s of the row in use (zeros where the thread has none)
+    __device__ __forceinline__ void get(float2 *f, int64_t row, int s, int u) const {
+        float e[VEC * Cols<VEC>::kPer];
+#pragma unroll
+        for (int k = 0; k < Cols<VEC>::kPer; ++k) unpack<T, VEC>(vector(row, s, u * Cols<VEC>::kPer + k), e + k * VEC);
+#pragma unroll
+        for (int j = 0; j < Cols<VEC>::kPairs; ++j) f[j] = make_float2(e[2 * j], e[2 * j + 1]);
     }
     __device__ __forceinline__ void next() {
-        if constexpr (kRing) out = out + 1 >= depth ? 0 : out + 1;
+        if constexpr (kRing) out = out + kStage >= end ? 0 : out + kStage;
     }
+    __device__ __forceinline__ void restart() { in = out = 0; }
 };
 
 template <typename T, int VEC>
-__device__ __forceinline__ void put(const float *f, void *base, int64_t at) {
-    *reinterpret_cast<raw_t<T, VEC> *>(static_cast<T *>(base) + at) = pack<T, VEC>(f);
+__device__ __forceinline__ void put(const float2 *f, void *base, int64_t row_at, const Cols<VEC> &c, int u) {
+    float e[VEC * Cols<VEC>::kPer];
+#pragma unroll
+    for (int j = 0; j < Cols<VEC>::kPairs; ++j) e[2 * j] = f[j].x, e[2 * j + 1] = f[j].y;
+#pragma unroll
+    for (int k = 0; k < Cols<VEC>::kPer; ++k) {
+        const int i = u * Cols<VEC>::kPer + k;
+        if (c.has(i)) *reinterpret_cast<raw_t<T, VEC> *>(static_cast<T *>(base) + row_at + c.at(i)) = pack<T, VEC>(e + k * VEC);
+    }
 }
 
 // The sum of v over the team that has a row: a warp, or the whole block (two
@@ -148,16 +184,16 @@ template <typename T, int VEC, int NV, int MAXT, int MINB, bool WARP>
 __global__ void __launch_bounds__(MAXT, MINB) norm_forward(const NormParams p) {
     extern __shared__ __align__(16) char smem[];
     __shared__ float buf[2 * 32];
-    constexpr int E = NV * VEC;
+    constexpr int P = Cols<VEC>::kPairs, NU = NV / Cols<VEC>::kPer;
     const int teams = WARP ? kWarpTeams : 1;
     const Cols<VEC> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
-    Feed<T, VEC, NV, 2> feed{reinterpret_cast<raw_t<T, VEC> *>(smem), {static_cast<const T *>(p.x), static_cast<const T *>(p.y)}, {p.ld_x, p.ld_y}, c, 0, 0, p.depth};
+    Feed<T, VEC, NV, 2, MAXT> feed(smem, {p.x, p.y}, {p.ld_x, p.ld_y}, c, p.depth);
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
     int64_t it = static_cast<int64_t>(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0);
     auto row_of = [&](int64_t i) { return static_cast<int64_t>(sched_item(p.sched, static_cast<uint32_t>(i < p.T ? i : 0))); };
     for (int d = 0; d + 1 < p.depth; ++d) feed.fetch(row_of(it + d * step), it + d * step < p.T);
-    float gw[E], w2[E];
-    load_weights<VEC, NV>(gw, w2, p, c);
+    float2 gw[NU * P], w2[NU * P];
+    load_weights<VEC, NU>(gw, w2, p, c);
     const float inv_h = 1.0f / static_cast<float>(p.H);
     int turn = 0;
     for (; it < p.T; it += step) {
@@ -165,45 +201,42 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward(const NormParams p) {
         feed.fetch(row_of(ahead), ahead < p.T);
         float f = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
         copy_wait_for(p.depth);
-        float h[E];
+        float2 h[NU * P];
         if (p.y) {
             if (p.w_post) {
-                float s = 0.0f;
+                float2 s = both(0.0f);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    float y[VEC];
+                for (int i = 0; i < NU; ++i) {
+                    float2 y[P];
                     feed.get(y, row, 1, i);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) s = __fmaf_rn(y[j], y[j], s);
+                    for (int j = 0; j < P; ++j) s = fma2(y[j], y[j], s);
                 }
-                s = team_sum<WARP>(s, buf, turn);
-                f = __fmul_rn(f, rsqrtf(__fmaf_rn(s, inv_h, p.eps)));
+                f = __fmul_rn(f, rsqrtf(__fmaf_rn(team_sum<WARP>(across(s), buf, turn), inv_h, p.eps)));
             }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float x[VEC], y[VEC];
+            for (int i = 0; i < NU; ++i) {
+                float2 x[P], y[P];
                 feed.get(x, row, 0, i);
                 feed.get(y, row, 1, i);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    h[i * VEC + j] = __fmaf_rn(p.alpha, x[j], __fmul_rn(__fmul_rn(y[j], f), gw[i * VEC + j]));
-                if (c.has(i)) put<T, VEC>(h + i * VEC, p.out_h, row * p.ld_oh + c.at(i));
+                for (int j = 0; j < P; ++j) h[i * P + j] = fma2(both(p.alpha), x[j], mul2(mul2(y[j], both(f)), gw[i * P + j]));
+                put<T, VEC>(h + i * P, p.out_h, row * p.ld_oh, c, i);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) feed.get(h + i * VEC, row, 0, i);
+            for (int i = 0; i < NU; ++i) feed.get(h + i * P, row, 0, i);
         }
         if (p.out_u) {
-            float s = 0.0f;
+            float2 s = both(0.0f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) s = __fmaf_rn(h[e], h[e], s);
-            s = team_sum<WARP>(s, buf, turn);
-            const float r = rsqrtf(__fmaf_rn(s, inv_h, p.eps));
+            for (int e = 0; e < NU * P; ++e) s = fma2(h[e], h[e], s);
+            const float r = rsqrtf(__fmaf_rn(team_sum<WARP>(across(s), buf, turn), inv_h, p.eps));
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
+            for (int i = 0; i < NU; ++i) {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) h[i * VEC + j] = __fmul_rn(__fmul_rn(h[i * VEC + j], r), w2[i * VEC + j]);
-                if (c.has(i)) put<T, VEC>(h + i * VEC, p.out_u, row * p.ld_ou + c.at(i));
+                for (int j = 0; j < P; ++j) h[i * P + j] = mul2(mul2(h[i * P + j], both(r)), w2[i * P + j]);
+                put<T, VEC>(h + i * P, p.out_u, row * p.ld_ou, c, i);
             }
         }
         feed.next();
@@ -218,16 +251,14 @@ template <typename T, int VEC, int NV, int MAXT, int MINB, bool WARP>
 __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) {
     extern __shared__ __align__(16) char smem[];  // the rows on their way; at the end WARP: the teams' columns [kWarpTeams][2H]
     __shared__ float buf[2][32][8];
-    constexpr int E = NV * VEC;
+    constexpr int P = Cols<VEC>::kPairs, NU = NV / Cols<VEC>::kPer;
     enum { kH, kDh, kDu, kY };
     const int teams = WARP ? kWarpTeams : 1, lane = threadIdx.x & 31;
     const int team = WARP ? threadIdx.x >> 5 : 0;
     const Cols<VEC> c{WARP ? 32 : static_cast<int>(blockDim.x), static_cast<int>(WARP ? threadIdx.x & 31 : threadIdx.x), p.H / VEC};
-    Feed<T, VEC, NV, 4> feed{reinterpret_cast<raw_t<T, VEC> *>(smem),
-                             {static_cast<const T *>(p.h), static_cast<const T *>(p.dh), static_cast<const T *>(p.du), static_cast<const T *>(p.y)},
-                             {p.ld_h, p.ld_dh, p.ld_du, p.ld_y}, c, 0, 0, p.depth};
+    Feed<T, VEC, NV, 4, MAXT> feed(smem, {p.h, p.dh, p.du, p.y}, {p.ld_h, p.ld_dh, p.ld_du, p.ld_y}, c, p.depth);
     const int64_t step = static_cast<int64_t>(p.n_slots) * teams;
-    float gw[E], w2[E];
+    float2 gw[NU * P], w2[NU * P];
     const float inv_h = 1.0f / static_cast<float>(p.H);
     int turn = 0;
     bool first = true;
@@ -235,35 +266,38 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) 
         const int32_t slot = static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(is)));
         const int64_t row0 = static_cast<int64_t>(slot) * teams + team;
         for (int d = 0; d + 1 < p.depth; ++d) feed.fetch(row0 + d * step, row0 + d * step < p.T);
-        if (first) load_weights<VEC, NV>(gw, w2, p, c);
+        if (first) load_weights<VEC, NU>(gw, w2, p, c);
         first = false;
-        float accC[E], accW[E];
+        float2 accC[NU * P], accW[NU * P];
 #pragma unroll
-        for (int e = 0; e < E; ++e) accC[e] = accW[e] = 0.0f;
+        for (int e = 0; e < NU * P; ++e) accC[e] = accW[e] = both(0.0f);
         for (int64_t row = row0; row < p.T; row += step) {
             const int64_t ahead = row + (p.depth > 0 ? p.depth - 1 : 0) * step;
             feed.fetch(ahead, ahead < p.T);
             const float gt = p.gate_mode == kGateToken ? param(p.gate, p.w_bf16, row) : 1.0f;
             copy_wait_for(p.depth);
-            float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // h.h, v.h, y.y, dh.gy, v.gy, h.gy
+            float2 q[6];  // h.h, v.h, y.y, dh.gy, v.gy, h.gy
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float h[VEC], dh[VEC], du[VEC], y[VEC];
+            for (int k = 0; k < 6; ++k) q[k] = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                float2 h[P], dh[P], du[P], y[P];
                 feed.get(h, row, kH, i);
                 feed.get(dh, row, kDh, i);
                 feed.get(du, row, kDu, i);
                 feed.get(y, row, kY, i);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float v = __fmul_rn(du[j], w2[i * VEC + j]), gy = __fmul_rn(gw[i * VEC + j], y[j]);
-                    s[0] = __fmaf_rn(h[j], h[j], s[0]);
-                    s[1] = __fmaf_rn(v, h[j], s[1]);
-                    s[2] = __fmaf_rn(y[j], y[j], s[2]);
-                    s[3] = __fmaf_rn(dh[j], gy, s[3]);
-                    s[4] = __fmaf_rn(v, gy, s[4]);
-                    s[5] = __fmaf_rn(h[j], gy, s[5]);
+                for (int j = 0; j < P; ++j) {
+                    const float2 v = mul2(du[j], w2[i * P + j]), gy = mul2(gw[i * P + j], y[j]);
+                    q[0] = fma2(h[j], h[j], q[0]);
+                    q[1] = fma2(v, h[j], q[1]);
+                    q[2] = fma2(y[j], y[j], q[2]);
+                    q[3] = fma2(dh[j], gy, q[3]);
+                    q[4] = fma2(v, gy, q[4]);
+                    q[5] = fma2(h[j], gy, q[5]);
                 }
             }
+            float s[8] = {across(q[0]), across(q[1]), across(q[2]), across(q[3]), across(q[4]), across(q[5]), 0.0f, 0.0f};
             float t = warp_sum8(s, lane);  // of sum lane / 4
             if constexpr (!WARP) {
                 if ((lane & 3) == 0) buf[turn][threadIdx.x >> 5][lane >> 2] = t;
@@ -295,43 +329,40 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) 
             }
             const float yr = __fmul_rn(r1, gt), kg = __fmul_rn(k1, gt);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float h[VEC], dh[VEC], du[VEC], y[VEC];
+            for (int i = 0; i < NU; ++i) {
+                float2 h[P], dh[P], du[P], y[P];
                 feed.get(h, row, kH, i);
                 feed.get(dh, row, kDh, i);
                 feed.get(du, row, kDu, i);
                 feed.get(y, row, kY, i);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const int e = i * VEC + j;
-                    const float v = __fmul_rn(du[j], w2[e]);
-                    const float D = __fmaf_rn(-k2, h[j], __fmaf_rn(r2, v, dh[j]));
-                    accW[e] = __fmaf_rn(du[j], __fmul_rn(h[j], r2), accW[e]);
-                    accC[e] = __fmaf_rn(D, __fmul_rn(y[j], yr), accC[e]);
-                    y[j] = __fmaf_rn(-kg, y[j], __fmul_rn(__fmul_rn(gw[e], yr), D));
-                    h[j] = __fmul_rn(p.alpha, D);
+                for (int j = 0; j < P; ++j) {
+                    const int e = i * P + j;
+                    const float2 D = fma2(both(-k2), h[j], fma2(both(r2), mul2(du[j], w2[e]), dh[j]));
+                    accW[e] = fma2(du[j], mul2(h[j], both(r2)), accW[e]);
+                    accC[e] = fma2(D, mul2(y[j], both(yr)), accC[e]);
+                    y[j] = fma2(both(-kg), y[j], mul2(mul2(gw[e], both(yr)), D));
+                    h[j] = mul2(both(p.alpha), D);
                 }
-                if (c.has(i)) {
-                    put<T, VEC>(h, p.out_h, row * p.ld_oh + c.at(i));
-                    if (p.y) put<T, VEC>(y, p.out_u, row * p.ld_ou + c.at(i));
-                }
+                put<T, VEC>(h, p.out_h, row * p.ld_oh, c, i);
+                if (p.y) put<T, VEC>(y, p.out_u, row * p.ld_ou, c, i);
             }
             feed.next();
         }
         copy_wait();  // (nothing but empty groups)
-        feed.in = feed.out = 0;
+        feed.restart();
         float *dst = p.slots + static_cast<int64_t>(slot) * 2 * p.H;
         if constexpr (WARP) {  // the warps' sums, in ascending order
             float *team_cols = reinterpret_cast<float *>(smem);
             float *mine = team_cols + static_cast<int64_t>(team) * 2 * p.H;
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (c.has(i))
+            for (int i = 0; i < NU; ++i)
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        mine[c.at(i) + j] = accC[i * VEC + j];
-                        mine[p.H + c.at(i) + j] = accW[i * VEC + j];
+                for (int j = 0; j < 2 * P; ++j)
+                    if (c.has(c.vec(i, j))) {
+                        mine[c.col(i, j)] = j & 1 ? accC[i * P + j / 2].y : accC[i * P + j / 2].x;
+                        mine[p.H + c.col(i, j)] = j & 1 ? accW[i * P + j / 2].y : accW[i * P + j / 2].x;
                     }
             __syncthreads();
             for (int e = threadIdx.x; e < 2 * p.H; e += blockDim.x) {
@@ -340,14 +371,15 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) 
                 dst[e] = v;
             }
             __syncthreads();
+            feed.clear();  // the columns lay where the rows go
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (c.has(i))
+            for (int i = 0; i < NU; ++i)
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        dst[c.at(i) + j] = accC[i * VEC + j];
-                        dst[p.H + c.at(i) + j] = accW[i * VEC + j];
+                for (int j = 0; j < 2 * P; ++j)
+                    if (c.has(c.vec(i, j))) {
+                        dst[c.col(i, j)] = j & 1 ? accC[i * P + j / 2].y : accC[i * P + j / 2].x;
+                        dst[p.H + c.col(i, j)] = j & 1 ? accW[i * P + j / 2].y : accW[i * P + j / 2].x;
                     }
         }
     }
@@ -418,10 +450,10 @@ template <typename T, int VEC, int EPT, int MAXT, int FB, int BB, bool WARP>
 dgr_status launch_norm(bool backward, NormParams &p, const NormPlan &pl, int sms, cudaStream_t s) {
     constexpr int NV = EPT / VEC;
     constexpr bool ring = VEC * sizeof(T) >= 4;
-    const size_t row = ring ? static_cast<size_t>(pl.threads) * EPT * sizeof(T) * (backward ? 4 : 2) : 0;
+    const size_t row = ring ? static_cast<size_t>(MAXT) * EPT * sizeof(T) * (backward ? 4 : 2) : 0;
     const size_t room = (224 * 1024) / (backward ? BB : FB);
     p.depth = 0;
-    if constexpr (ring) p.depth = row * 3 <= room ? 3 : row * 2 <= room ? 2 : row <= room ? 1 : 0;
+    if (ring) p.depth = static_cast<int>(room / (row + 1 - ring) < 3 ? room / (row + 1 - ring) : 3);  // 0 where one does not fit
     size_t smem = row * p.depth;
     if (!backward) {
         auto *k = norm_forward<T, VEC, NV, MAXT, FB, WARP>;
@@ -458,9 +490,10 @@ template <typename T>
 dgr_status launch_type(bool backward, NormParams &p, const NormPlan &pl, int sms, cudaStream_t s, size_t align) {
     constexpr int full = 16 / static_cast<int>(sizeof(T)), word = 4 / static_cast<int>(sizeof(T));
     if (align >= 16 && p.H % full == 0) return launch_width<T, full>(backward, p, pl, sms, s);
-    if (align >= 4 && p.H % word == 0) return launch_width<T, word>(backward, p, pl, sms, s);
-    if constexpr (sizeof(T) == 2) return launch_width<T, 1>(backward, p, pl, sms, s);
-    return DGR_ERR_MISALIGNED;
+    if constexpr (sizeof(T) == 2) {
+        if (align < 4 || p.H % word != 0) return launch_width<T, 1>(backward, p, pl, sms, s);
+    }
+    return launch_width<T, word>(backward, p, pl, sms, s);
 }
 
 // The power of two (at most 16) that divides every row's address.

@@ -256,6 +256,9 @@ __device__ __forceinline__ float vec_dot(const float (&a)[N], const float (&b)[N
     return __fadd_rn(s.x, s.y);
 }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float across(float2 v) { return __fadd_rn(v.x, v.y); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace row
