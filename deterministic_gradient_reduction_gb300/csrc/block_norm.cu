@@ -24,8 +24,8 @@ namespace {
 using namespace row;
 
 constexpr int kWarpTeams = 8;     // rows side by side in a CTA where a warp takes a row
-constexpr int kFoldCols = 32;     // columns of a fold CTA
-constexpr int kFoldWays = 16;     // threads that share a column's slots
+constexpr int kFoldCols = 16;     // columns of a fold CTA (64 bytes of a slot)
+constexpr int kFoldWays = 32;     // threads that share a column's slots
 constexpr int64_t kMaxWidth = 16384;
 
 enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
@@ -38,6 +38,7 @@ struct NormParams {
     int64_t ld_oh, ld_ou;
     const void *w_post, *gate, *w_pre;
     int32_t w_bf16, gate_mode;
+    int32_t w_vec;              // the weights start at multiples of 16 bytes
     int32_t T, H;
     float alpha, eps;
     float *dw_post, *dgate, *dw_pre;
@@ -67,20 +68,38 @@ struct Cols {
 template <int VEC, int NU>
 __device__ __forceinline__ void load_weights(float2 *gw, float2 *w2, const NormParams &p, const Cols<VEC> &c) {
     constexpr int P = Cols<VEC>::kPairs;
+    const void *gate = p.gate_mode == kGateChannel ? p.gate : nullptr;
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int u = 0; u < NU; ++u) {
+        float a[2 * P], g[2 * P], b[2 * P];
+        auto unit = [&](const void *w, float *f, float without) {
 #pragma unroll
-        for (int j = 0; j < 2 * P; ++j) {
-            float a = 0.0f, b = 0.0f;
-            if (c.has(c.vec(u, j))) {
-                const int e = c.col(u, j);
-                a = p.w_post ? param(p.w_post, p.w_bf16, e) : 1.0f;
-                if (p.gate_mode == kGateChannel) a = __fmul_rn(a, param(p.gate, p.w_bf16, e));
-                if (p.w_pre) b = param(p.w_pre, p.w_bf16, e);
+            for (int j = 0; j < 2 * P; ++j) f[j] = c.has(c.vec(u, j)) ? without : 0.0f;
+            if (!w) return;
+            if constexpr (VEC >= 4) {
+                if (p.w_vec && c.has(u)) {  // VEC columns from a multiple of VEC on
+                    if (p.w_bf16) {
+                        unpack<bf16, VEC>(__ldg(reinterpret_cast<const raw_t<bf16, VEC> *>(static_cast<const bf16 *>(w) + c.at(u))), f);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < VEC; j += 4) unpack<float, 4>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(w) + c.at(u) + j)), f + j);
+                    }
+                    return;
+                }
             }
-            (j & 1 ? gw[u * P + j / 2].y : gw[u * P + j / 2].x) = a;
-            (j & 1 ? w2[u * P + j / 2].y : w2[u * P + j / 2].x) = b;
+#pragma unroll
+            for (int j = 0; j < 2 * P; ++j)
+                if (c.has(c.vec(u, j))) f[j] = param(w, p.w_bf16, c.col(u, j));
+        };
+        unit(p.w_post, a, 1.0f);
+        unit(gate, g, 1.0f);
+        unit(p.w_pre, b, 0.0f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            gw[u * P + j] = mul2(make_float2(a[2 * j], a[2 * j + 1]), make_float2(g[2 * j], g[2 * j + 1]));
+            w2[u * P + j] = make_float2(b[2 * j], b[2 * j + 1]);
         }
+    }
 }
 
 // The rows' elements on their way: `depth` rows of S streams in shared memory,
@@ -249,6 +268,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward(const NormParams p) {
 // so D need not be known before the second norm's sum is made.
 template <typename T, int VEC, int NV, int MAXT, int MINB, bool WARP>
 __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) {
+    // the fold's CTAs may come as soon as this kernel's leave room; they wait for all of it
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) char smem[];  // the rows on their way; at the end WARP: the teams' columns [kWarpTeams][2H]
     __shared__ float buf[2][32][8];
     constexpr int P = Cols<VEC>::kPairs, NU = NV / Cols<VEC>::kPer;
@@ -385,19 +406,27 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) 
     }
 }
 
-// The slots of a column: way w of 16 takes the slots w, w + 16, ... in order,
-// the ways meet in a fixed pairwise tree.
+// The slots of a column: way w of 32 takes the slots w, w + 32, ... in order (8
+// of them in flight), the ways meet in a fixed pairwise tree.
 __global__ void __launch_bounds__(kFoldCols *kFoldWays) norm_fold(const NormParams p) {
     __shared__ float part[kFoldWays][kFoldCols + 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int w = threadIdx.y;
     const int e = blockIdx.x * kFoldCols + threadIdx.x, n = 2 * p.H;
     float v = 0.0f;
-    if (e < n)
-#pragma unroll 8
-        for (int s = w; s < p.n_slots; s += kFoldWays) v = __fadd_rn(v, __ldcg(p.slots + static_cast<int64_t>(s) * n + e));
+    for (int s = w; s < p.n_slots; s += 8 * kFoldWays) {
+        uint32_t r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            r[k] = 0;
+            load_if<false>(r[k], p.slots + static_cast<int64_t>(s + k * kFoldWays) * n + e, e < n && s + k * kFoldWays < p.n_slots);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v = __fadd_rn(v, __uint_as_float(r[k]));
+    }
     part[w][threadIdx.x] = v;
     __syncthreads();
+#pragma unroll
     for (int s = 1; s < kFoldWays; s <<= 1) {
         if ((w & (2 * s - 1)) == 0) part[w][threadIdx.x] = __fadd_rn(part[w][threadIdx.x], part[w + s][threadIdx.x]);
         __syncthreads();
@@ -549,6 +578,7 @@ extern "C" dgr_status dgr_block_norm(const void *x, int64_t ld_x, const void *y,
     p.x = x, p.y = y, p.ld_x = ld_x, p.ld_y = ld_y;
     p.out_h = h, p.out_u = u, p.ld_oh = ld_h, p.ld_ou = ld_u;
     p.w_post = w_post, p.gate = gate, p.w_pre = w_pre, p.w_bf16 = ws == 2, p.gate_mode = gate_mode;
+    p.w_vec = aligned(w_post, 16) && aligned(gate, 16) && aligned(w_pre, 16);
     p.T = static_cast<int32_t>(T), p.H = static_cast<int32_t>(H), p.alpha = res_scale, p.eps = eps;
     p.sched = sched_for(static_cast<uint32_t>(T));
     size_t al = row_align(16, x, ld_x, es);
@@ -617,6 +647,7 @@ extern "C" dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const
     p.ld_h = ld_h, p.ld_y = ld_y, p.ld_dh = ld_dh, p.ld_du = ld_du;
     p.out_h = dx, p.out_u = dy, p.ld_oh = ld_dx, p.ld_ou = ld_dy;
     p.w_post = w_post, p.gate = gate, p.w_pre = w_pre, p.w_bf16 = wes == 2, p.gate_mode = gate_mode;
+    p.w_vec = aligned(w_post, 16) && aligned(gate, 16) && aligned(w_pre, 16);
     p.T = static_cast<int32_t>(T), p.H = static_cast<int32_t>(H), p.alpha = res_scale, p.eps = eps;
     p.dw_post = dw_post, p.dgate = dgate, p.dw_pre = dw_pre, p.accumulate = accumulate ? 1 : 0;
     const NormPlan pl = norm_plan(T, H);
