@@ -64,8 +64,7 @@ struct DistillParams {
     float *row_loss, *loss;
     void *dz;
     int64_t ld_dz;
-    int32_t same_align;  // z's and dz's rows start at the same place of a 16-byte vector
-    int32_t depth;       // batches of a thread in shared memory: 2 or 3
+    int32_t per;         // vectors of a row a CTA
     WsHeader *hdr;       // pad[0]: clusters done
     Sched sched;
 };
@@ -99,18 +98,18 @@ __device__ __forceinline__ void remote_store(uint32_t a, float v) {
 }
 // ---- a row's parts -------------------------------------------------------------
 
-// A row as whole 16-byte vectors between a few single elements; CTA `rank` of a
-// cluster of `size` has vectors [first, first + count), CTA 0 the singles too.
+// A row as whole 16-byte vectors between a few single elements; CTA `rank` of
+// its cluster has `per` vectors from rank * per on (fewer at the row's end),
+// CTA 0 the singles too.
 template <typename T>
 struct RowView {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-    int head, n_vec, n_single, per, first, count;
-    __device__ __forceinline__ RowView(const T *z, int V, int rank, int size) {
+    int head, n_vec, n_single, first, count;
+    __device__ __forceinline__ RowView(const T *z, int V, int rank, int per) {
         const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / static_cast<int>(sizeof(T));
         head = min(V, off ? VEC - off : 0);
         n_vec = (V - head) / VEC;
         n_single = V - n_vec * VEC;
-        per = (n_vec + size - 1) / size;
         first = min(n_vec, rank * per);
         count = min(per, n_vec - first);
         if (rank != 0) n_single = 0;
@@ -192,25 +191,22 @@ struct Running {
 // The list's bytes: ids, then teacher logits.
 __host__ __device__ inline size_t list_bytes(int K) { return (static_cast<size_t>(K) * 8 + 15) / 16 * 16; }
 
-// Batches of 4 vectors of a thread in a CTA's part of a row of V (a word of the
-// list's bits for each).
-__host__ __device__ inline int batches(int V, int threads, int size, int es) {
-    const int n_vec = V / (16 / es), per = (n_vec + size - 1) / size;
-    return (per + threads * 4 - 1) / (threads * 4);
-}
+// Vectors of a row a CTA, batches of 4 of a thread's in them (2 or 8 in flight
+// are slower: 544 us instead of 461 for 4096 x 131072 bf16; 60 instead of 56 for
+// 2048 x 32768 fp32); the list's bits have a word for each batch.
+inline int vectors(int V, int size, int es) { return (V / (16 / es) + size - 1) / size; }
+__host__ __device__ inline int batches(int per, int threads) { return (per + threads * 4 - 1) / (threads * 4); }
 
-// Dynamic shared memory: the batches on their way [depth], the lists of this
-// row and the next, the student's logits at the entries, their places [K], and
-// the list's bits.
-size_t distill_smem(int K, int V, int threads, int size, int es, int depth) {
-    return static_cast<size_t>(depth) * threads * 64 + 2 * list_bytes(K) + static_cast<size_t>(K) * 8 +
-           static_cast<size_t>(batches(V, threads, size, es)) * threads * 4;
+// Dynamic shared memory: the lists of this row and the next, the student's
+// logits at the entries, their places [K], and the list's bits.
+size_t distill_smem(int K, int V, int threads, int size, int es) {
+    return 2 * list_bytes(K) + static_cast<size_t>(K) * 8 + static_cast<size_t>(batches(vectors(V, size, es), threads)) * threads * 4;
 }
 
 template <typename T, int NT, bool TAIL>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParams p) {
     using View = RowView<T>;
-    constexpr int VEC = View::VEC, W = NT / 32, U = 4;  // U vectors a batch
+    constexpr int VEC = View::VEC, W = NT / 32, U = 4;  // U vectors of a thread in flight, one word of bits
     extern __shared__ __align__(16) char smem[];
     __shared__ float4 s_pair[2][kMaxCluster * W];  // the cluster's warps, by row parity: outside the list, in it
     __shared__ float s_loss[2][kMaxCluster * W];   // likewise their parts of a row's loss
@@ -221,13 +217,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     const uint32_t n_clusters = gridDim.x / size, T_rows = static_cast<uint32_t>(p.T);
     const int K = p.K;
-    const int depth = p.depth, B = batches(p.V, NT, size, sizeof(T));      // of every row: some of the last may be empty
-    const bool second = p.dz && p.same_align;                              // the second reading comes the same way
-    const int Q = second ? 2 * B : B;
-    uint4 *ring = reinterpret_cast<uint4 *>(smem);                         // [depth][U][NT]
-    char *lists = smem + static_cast<size_t>(depth) * NT * U * 16;
-    auto ids_of = [&](uint32_t n) { return reinterpret_cast<int32_t *>(lists + (n & 1) * list_bytes(K)); };
-    float *s_z = reinterpret_cast<float *>(lists + 2 * list_bytes(K));     // [K]
+    auto ids_of = [&](uint32_t n) { return reinterpret_cast<int32_t *>(smem + (n & 1) * list_bytes(K)); };
+    float *s_z = reinterpret_cast<float *>(smem + 2 * list_bytes(K));      // [K]
     int32_t *s_copy = reinterpret_cast<int32_t *>(s_z + K);                // [K]: place, with kCopy where the id came before
     uint32_t *s_bits = reinterpret_cast<uint32_t *>(s_copy + K);           // [batches][NT]
     constexpr int kCopy = 1 << 30;
@@ -244,23 +235,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 copy_async<4>(ids + K + k, p.teacher + row * p.ld_t + k);
             }
         }
-    };
-    // A thread's batches come through its own places of the ring, `depth` - 1
-    // of them ahead of the one in use: first a row's, then the same again for
-    // the gradient, then the next row's, so that barriers and the list's work
-    // do not empty the path to memory. Each is a group of copies; the next
-    // row's list comes with the first.
-    int in_slot = 0, out_slot = 0;
-    auto issue = [&](const char *first, int count, int batch, bool on) {
-        uint4 *to = ring + in_slot * (U * NT) + tid;
-        if (on)
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = (batch * U + u) * NT + tid;
-                if (v < count) copy_async<16>(to + u * NT, first + static_cast<int64_t>(v) * 16);
-            }
         copy_commit();
-        in_slot = in_slot + 1 == depth ? 0 : in_slot + 1;
     };
     const int list_warps = min(W, (K + 31) / 32);  // warps that hold entries
     int64_t loss_row = -1;      // CTA 0, last warp: a row whose loss waits for the other CTAs' parts
@@ -278,48 +253,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     uint32_t item = blockIdx.x / size;
     float weight = weight_of(item), weight_next = weight_of(item + n_clusters);
     if (tid == 0) s_twice = 0;
-    for (int j = tid; j < batches(p.V, NT, size, sizeof(T)) * NT; j += NT) s_bits[j] = 0;
+    for (int j = tid; j < batches(p.per, NT) * NT; j += NT) s_bits[j] = 0;
     fetch_list(item, 0, weight);
-    bool ready = false;  // the row's first batches are on their way
     __syncthreads();
     for (uint32_t n = 0; item < T_rows; ++n, item += n_clusters) {
         const int64_t row = row_of(item);
         const T *z = static_cast<const T *>(p.z) + row * p.ld;
         T *dz = static_cast<T *>(p.dz) + row * p.ld_dz;
-        const View view(z, p.V, rank, size);
+        const View view(z, p.V, rank, p.per);
         const char *first = reinterpret_cast<const char *>(z + view.head) + static_cast<int64_t>(view.first) * 16;
         int32_t *ids = ids_of(n);
         const float *teacher = reinterpret_cast<const float *>(ids + K);
-        auto batch_of = [&](int q) { return q < B ? q : q - B; };
-        if (weight != 0.0f && !ready) {
-            out_slot = in_slot;
-            for (int q = 0; q + 1 < depth; ++q) issue(first, view.count, batch_of(q), true);
-        }
-        // the next row's part, and its first batches when this row's have all been asked for
-        const bool next_on = item + n_clusters < T_rows && weight_next != 0.0f;
-        const View next_view(static_cast<const T *>(p.z) + row_of(next_on ? item + n_clusters : item) * p.ld, p.V, rank, size);
-        const char *next_first = reinterpret_cast<const char *>(static_cast<const T *>(p.z) + row_of(next_on ? item + n_clusters : item) * p.ld + next_view.head) +
-                                 static_cast<int64_t>(next_view.first) * 16;
-        auto ahead = [&](int q) {  // with batch q (of Q) in use
-            const int a = q + depth - 1;
-            if (a < Q) issue(first, view.count, batch_of(a), true);
-            else issue(next_first, next_view.count, batch_of(a - Q), next_on);
-            copy_wait_for(depth);
-        };
-        auto take = [&](uint4 (&r)[U], int batch, uint32_t absent) {
-            const uint4 *from = ring + out_slot * (U * NT) + tid;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                r[u] = make_uint4(absent, absent, absent, absent);
-                if ((batch * U + u) * NT + tid < view.count) r[u] = from[u * NT];
-            }
-            out_slot = out_slot + 1 == depth ? 0 : out_slot + 1;
-        };
-        if (weight != 0.0f) {  // each thread's own part of the list, which came before this row's first batch
-            if (ready) copy_wait_for(depth - 1);
-            else copy_wait();
-        }
-        ready = next_on && weight != 0.0f;
+        copy_wait();  // each thread's own part of the list
         const float weight_2 = weight_of(item + 2 * n_clusters);
         float a = 0.0f, c_rest = 0.0f, f = 0.0f, c_all = 0.0f, inv_mass = 0.0f, total = 1.0f, shift = 0.0f;
         float rest_s = 0.0f, left = 0.0f;  // sum outside the list, q left for it
@@ -377,22 +322,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             }
             for (;;) {  // a second time only where k times the maximum is out of range; `shift` is subtracted then
                 Running run;
-                constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
                 auto pass = [&](auto shifted) {
-                    for (int b = 0; b < B; ++b) {
+                    const char *src = first + tid * 16;
+                    int b = tid;
+                    for (int v = tid; v < view.count; v += U * NT, src += static_cast<size_t>(U) * NT * 16, b += NT) {
                         uint4 r[U];
-                        if constexpr (!shifted.value) {
-                            ahead(b);
-                            take(r, b, low);
-                        } else {  // the ring has gone on
+                        constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
 #pragma unroll
-                            for (int u = 0; u < U; ++u) {
-                                const int v = (b * U + u) * NT + tid;
-                                r[u] = make_uint4(low, low, low, low);
-                                load_if<false>(r[u], first + static_cast<int64_t>(v) * 16, v < view.count);
-                            }
+                        for (int u = 0; u < U; ++u) {
+                            r[u] = make_uint4(low, low, low, low);
+                            load_if<false>(r[u], src + u * NT * 16, v + u * NT < view.count);
                         }
-                        const uint32_t bits = TAIL ? s_bits[b * NT + tid] : 0;
+                        const uint32_t bits = TAIL ? s_bits[b] : 0;
                         if (bits) {
 #pragma unroll
                             for (int u = 0; u < U; ++u) {
@@ -497,8 +438,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             }
         } else {
             fetch_list(item + n_clusters, n + 1, weight_next);
-            copy_commit();
-            copy_wait();
         }
         if (p.dz) {
             // the gradient of four words' elements
@@ -519,54 +458,44 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             // made of two neighbouring ones of the logits
             const int off = static_cast<int>(reinterpret_cast<uintptr_t>(own) & 15) / static_cast<int>(sizeof(T));
             const int lead = off ? min(VEC - off, view.count * VEC) : 0, n_out = (view.count * VEC - lead) / VEC;
-            auto from_ring = [&](auto shifted) {
-                for (int b = 0; b < B; ++b) {
-                    uint4 r[U];
-                    ahead(B + b);
-                    take(r, b, 0);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int v = (b * U + u) * NT + tid;
-                        r[u] = live ? gradient(r[u], shifted) : make_uint4(0, 0, 0, 0);  // 0 whatever the row holds
-                        if (v < view.count) reinterpret_cast<uint4 *>(own)[v] = r[u];
-                    }
-                }
-            };
-            auto shifted_by = [&](auto shifted) {
-                for (int v = tid; v < n_out; v += 2 * NT) {
+            auto pass = [&](auto shifted, auto aligned_too) {
+                constexpr int F = aligned_too.value ? U : 2;
+                for (int v = tid; v < n_out; v += F * NT) {
                     const char *src = first + static_cast<int64_t>(v) * 16;
-                    uint4 r[2], next[2];
+                    uint4 r[F], next[F];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < F; ++u) {
+                        const bool on = v + u * NT < n_out;
                         r[u] = next[u] = make_uint4(0, 0, 0, 0);
-                        load_if<false>(r[u], src + u * NT * 16, v + u * NT < n_out);
-                        load_if<false>(next[u], src + u * NT * 16 + 16, lead && v + u * NT < n_out);
+                        load_if<false>(r[u], src + u * NT * 16, on);
+                        if constexpr (!aligned_too.value) load_if<false>(next[u], src + u * NT * 16 + 16, on);
                     }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int by = lead * static_cast<int>(sizeof(T)) * 8;
-                        uint32_t q[8] = {r[u].x, r[u].y, r[u].z, r[u].w, next[u].x, next[u].y, next[u].z, next[u].w};
-                        if (by & 64)
+                    for (int u = 0; u < F; ++u) {
+                        if constexpr (!aligned_too.value) {
+                            const int by = lead * static_cast<int>(sizeof(T)) * 8;
+                            uint32_t q[8] = {r[u].x, r[u].y, r[u].z, r[u].w, next[u].x, next[u].y, next[u].z, next[u].w};
+                            if (by & 64)
 #pragma unroll
-                            for (int i = 0; i < 6; ++i) q[i] = q[i + 2];
-                        if (by & 32)
+                                for (int i = 0; i < 6; ++i) q[i] = q[i + 2];
+                            if (by & 32)
 #pragma unroll
-                            for (int i = 0; i < 5; ++i) q[i] = q[i + 1];
-                        r[u] = make_uint4(__funnelshift_r(q[0], q[1], by & 31), __funnelshift_r(q[1], q[2], by & 31),
-                                          __funnelshift_r(q[2], q[3], by & 31), __funnelshift_r(q[3], q[4], by & 31));
+                                for (int i = 0; i < 5; ++i) q[i] = q[i + 1];
+                            r[u] = make_uint4(__funnelshift_r(q[0], q[1], by & 31), __funnelshift_r(q[1], q[2], by & 31),
+                                              __funnelshift_r(q[2], q[3], by & 31), __funnelshift_r(q[3], q[4], by & 31));
+                        }
                         if (v + u * NT < n_out) reinterpret_cast<uint4 *>(own + lead)[v + u * NT] = gradient(r[u], shifted);
                     }
                 }
             };
-            if (second && weight != 0.0f) {
-                if (shift == 0.0f) from_ring(std::false_type{});
-                else from_ring(std::true_type{});
-            } else if (!live) {
+            if (!live) {  // zeros, whatever the row holds
                 for (int v = tid; v < n_out; v += NT) reinterpret_cast<uint4 *>(own + lead)[v] = make_uint4(0, 0, 0, 0);
-            } else if (shift == 0.0f) {
-                shifted_by(std::false_type{});
+            } else if (shift != 0.0f) {
+                pass(std::true_type{}, std::false_type{});
+            } else if (lead == 0) {
+                pass(std::false_type{}, std::true_type{});
             } else {
-                shifted_by(std::true_type{});
+                pass(std::false_type{}, std::false_type{});
             }
             if (tid < view.count * VEC - n_out * VEC) {  // elements around the vectors
                 const int j = tid < lead ? tid : n_out * VEC + tid;
@@ -662,10 +591,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
 template <typename T, int NT, bool TAIL>
 dgr_status launch_rows(DistillParams &p, int cluster, int sms, cudaStream_t s) {
     auto *k = distill_rows<T, NT, TAIL>;
-    // 3 batches where the CTAs of an SM have room for them, and a row has 2 at least
-    const int Q = batches(p.V, NT, cluster, sizeof(T)) * (p.dz && p.same_align ? 2 : 1);
-    p.depth = Q >= 2 && distill_smem(p.K, p.V, NT, cluster, sizeof(T), 3) <= 216 * 1024 / (1024 / NT) ? 3 : 2;
-    const size_t smem = distill_smem(p.K, p.V, NT, cluster, sizeof(T), p.depth);
+    p.per = vectors(p.V, cluster, sizeof(T));
+    const size_t smem = distill_smem(p.K, p.V, NT, cluster, sizeof(T));
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DGR_ERR_CUDA;
     static std::atomic<int> granted[64];  // the largest size asked for so far
@@ -706,14 +633,20 @@ dgr_status launch_rows(DistillParams &p, int cluster, int sms, cudaStream_t s) {
 template <typename T, bool TAIL>
 dgr_status launch_size(DistillParams &p, int sms, cudaStream_t s) {
     if (p.V < 8192) return launch_rows<T, 128, TAIL>(p, 1, sms, s);
+    // A CTA does a list's work for every row it has a part of, so few CTAs a
+    // row. With a gradient a row of up to 128 KB has one, a longer one more, so
+    // that the 608 CTAs hold no more than about 80 MB at a time and the second
+    // reading finds most of it in L2: 4096 x 131072 bf16 462 us with 2 CTAs a
+    // row, 477 with 1; 1021 x 50001 bf16 (100 KB) 53 us with 1, 58 with 2.
+    // (512 threads a CTA instead of 256: 449 and 57 us, 2048 x 32768 fp32
+    // forward 66 instead of 60.)
     int cluster = 1;
-    // with a gradient: the rows that 304 CTAs hold at a time stay within about 40 MB of L2
     while (p.dz && cluster < kMaxCluster && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10) * cluster) cluster <<= 1;
     // few rows: a row over more CTAs, down to 4096 elements each
     while (cluster < kMaxCluster && static_cast<int64_t>(p.T) * cluster * 2 <= 304 && p.V >= 4096 * cluster * 2) cluster <<= 1;
-    // long rows: the list's bits leave room for two CTAs an SM
-    while (cluster < kMaxCluster && distill_smem(p.K, p.V, 512, cluster, sizeof(T), 2) > 108 * 1024) cluster <<= 1;
-    return launch_rows<T, 512, TAIL>(p, cluster, sms, s);
+    // long rows: the list's bits leave room for four CTAs an SM
+    while (cluster < kMaxCluster && distill_smem(p.K, p.V, 256, cluster, sizeof(T)) > 48 * 1024) cluster <<= 1;
+    return launch_rows<T, 256, TAIL>(p, cluster, sms, s);
 }
 
 size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? static_cast<size_t>(((T - 1) * ld + W) * es) : 0; }
@@ -764,8 +697,6 @@ extern "C" dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_
     p.teacher_lse = teacher_lse, p.weights = weights, p.dloss = dloss;
     p.inv_tau = inv_tau, p.k2 = static_cast<float>(1.4426950408889634 / static_cast<double>(tau)), p.scale = scale;
     p.row_loss = row_loss, p.loss = loss, p.dz = dlogits, p.ld_dz = ld_d;
-    const intptr_t apart = reinterpret_cast<intptr_t>(dlogits) - reinterpret_cast<intptr_t>(logits);
-    p.same_align = dlogits && apart % 16 == 0 && ((ld_d - ld) * es) % 16 == 0;
     p.hdr = static_cast<WsHeader *>(ws);
     p.sched = sched_for(static_cast<uint32_t>(T));
     int sms = 0;

@@ -136,6 +136,39 @@ def test_infinities(tail):
     assert bool(torch.isfinite(out["dz"]).all())
 
 
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [900, 20000])
+def test_lowest_and_largest_values(V, dtype, tail):
+    t = make(6, V, 8, dtype, tau=0.7, tail=tail, weights=False)
+    low = torch.finfo(DT[dtype]).min
+    t["ids"][:, 0] = 3
+    closed = torch.arange(V, device="cuda") >= V // 2  # a mask of the type's lowest value
+    closed[t["ids"][t["ids"] >= 0].long()] = False
+    t["z"][0][closed] = low
+    t["z"][1][:] = low                  # a row that the mask leaves nothing of
+    t["z"][2][:] = 2.5e38               # k times the maximum is out of range
+    t["z"][2][3] = 2.5e38
+    t["z"][3][:] = -2.0e38
+    t["z"][3][closed] = low
+    t["z"][4] += 1000.0
+    z = ref.d(t["z"])
+    if not tail:
+        # p is uniform over the largest logits; the bound's exponents would be those of the values themselves
+        same = dict(tau=t["tau"], scale=t["scale"])
+        dz = torch.empty_like(t["z"])
+        loss, rows = dgr.topk_distill(t["z"], t["ids"], t["t"], dlogits=dz, **same)
+        _, want_rows, want = ref.distill(z, t["ids"].cpu(), ref.d(t["t"]), t["tau"], None, None, t["scale"])
+        eps = 2 * ref.half_ulp(t["z"].dtype) + 1e-5
+        for r in (0, 1, 2, 3):
+            assert bool(torch.isfinite(dz[r]).all()) and abs(float(rows[r]) - float(want_rows[r])) <= 1e-5 * (1 + abs(float(want_rows[r]))), r
+            assert float((ref.d(dz[r]) - want[r]).norm()) <= eps * float(want[r].norm()), r
+    else:
+        dz = torch.empty_like(t["z"])
+        loss, rows = dgr.topk_distill(t["z"], t["ids"], t["t"], tau=t["tau"], teacher_lse=t["lse"], scale=t["scale"], dlogits=dz)
+        assert bool(torch.isfinite(dz).all()) and bool(torch.isfinite(rows[[0, 1, 2, 3]]).all())
+
+
 def test_little_mass_outside_the_list():
     t = make(3, 5000, 4, "fp32", tail=True, weights=False)
     t["ids"] = torch.tensor([[1, 2, 3, 4]] * 3, dtype=torch.int32, device="cuda")
