@@ -263,13 +263,25 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward(const NormParams p) {
     copy_wait();
 }
 
+// The sum of column e of [C, dw_pre] to where it goes.
+__device__ __forceinline__ void put_column(const NormParams &p, int e, float v) {
+    auto put = [&](float *dst, int i, float g) {
+        if (dst) dst[i] = p.accumulate ? __fadd_rn(dst[i], g) : g;
+    };
+    if (e >= p.H) {
+        put(p.dw_pre, e - p.H, v);
+    } else {
+        const bool channel = p.gate_mode == kGateChannel;
+        put(p.dw_post, e, channel ? __fmul_rn(param(p.gate, p.w_bf16, e), v) : v);
+        if (channel) put(p.dgate, e, p.w_post ? __fmul_rn(param(p.w_post, p.w_bf16, e), v) : v);
+    }
+}
+
 // One round of sums a row: with gy = gw y,
 //   q . y = dh . gy + r2 v . gy - (r2^3 / H) (v . h) h . gy,
 // so D need not be known before the second norm's sum is made.
 template <typename T, int VEC, int NV, int MAXT, int MINB, bool WARP>
 __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) {
-    // the fold's CTAs may come as soon as this kernel's leave room; they wait for all of it
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) char smem[];  // the rows on their way; at the end WARP: the teams' columns [kWarpTeams][2H]
     __shared__ float buf[2][32][8];
     constexpr int P = Cols<VEC>::kPairs, NU = NV / Cols<VEC>::kPer;
@@ -372,6 +384,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) 
         }
         copy_wait();  // (nothing but empty groups)
         feed.restart();
+        // the fold's CTAs may come as this kernel's leave; they wait for all of them
+        if (is + gridDim.x >= p.n_slots) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         float *dst = p.slots + static_cast<int64_t>(slot) * 2 * p.H;
         if constexpr (WARP) {  // the warps' sums, in ascending order
             float *team_cols = reinterpret_cast<float *>(smem);
@@ -389,19 +403,39 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward(const NormParams p) 
             for (int e = threadIdx.x; e < 2 * p.H; e += blockDim.x) {
                 float v = team_cols[e];
                 for (int k = 1; k < kWarpTeams; ++k) v = __fadd_rn(v, team_cols[k * 2 * p.H + e]);
-                dst[e] = v;
+                if (p.n_slots == 1) put_column(p, e, v);
+                else dst[e] = v;
             }
             __syncthreads();
             feed.clear();  // the columns lay where the rows go
-        } else {
+        } else if (p.n_slots == 1) {  // nothing to fold
 #pragma unroll
             for (int i = 0; i < NU; ++i)
 #pragma unroll
                 for (int j = 0; j < 2 * P; ++j)
                     if (c.has(c.vec(i, j))) {
-                        dst[c.col(i, j)] = j & 1 ? accC[i * P + j / 2].y : accC[i * P + j / 2].x;
-                        dst[p.H + c.col(i, j)] = j & 1 ? accW[i * P + j / 2].y : accW[i * P + j / 2].x;
+                        put_column(p, c.col(i, j), j & 1 ? accC[i * P + j / 2].y : accC[i * P + j / 2].x);
+                        put_column(p, p.H + c.col(i, j), j & 1 ? accW[i * P + j / 2].y : accW[i * P + j / 2].x);
                     }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if constexpr (VEC >= 4) {  // H is a multiple of 4
+                    if (!c.has(i)) continue;
+#pragma unroll
+                    for (int j = 0; j < P; j += 2) {
+                        *reinterpret_cast<float4 *>(dst + c.at(i) + 2 * j) = make_float4(accC[i * P + j].x, accC[i * P + j].y, accC[i * P + j + 1].x, accC[i * P + j + 1].y);
+                        *reinterpret_cast<float4 *>(dst + p.H + c.at(i) + 2 * j) = make_float4(accW[i * P + j].x, accW[i * P + j].y, accW[i * P + j + 1].x, accW[i * P + j + 1].y);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2 * P; ++j)
+                        if (c.has(c.vec(i, j))) {
+                            dst[c.col(i, j)] = j & 1 ? accC[i * P + j / 2].y : accC[i * P + j / 2].x;
+                            dst[p.H + c.col(i, j)] = j & 1 ? accW[i * P + j / 2].y : accW[i * P + j / 2].x;
+                        }
+                }
+            }
         }
     }
 }
@@ -432,17 +466,7 @@ __global__ void __launch_bounds__(kFoldCols *kFoldWays) norm_fold(const NormPara
         __syncthreads();
     }
     if (w != 0 || e >= n) return;
-    v = part[0][threadIdx.x];
-    auto put = [&](float *dst, int i, float g) {
-        if (dst) dst[i] = p.accumulate ? __fadd_rn(dst[i], g) : g;
-    };
-    if (e >= p.H) {
-        put(p.dw_pre, e - p.H, v);
-    } else {
-        const bool channel = p.gate_mode == kGateChannel;
-        put(p.dw_post, e, channel ? __fmul_rn(param(p.gate, p.w_bf16, e), v) : v);
-        if (channel) put(p.dgate, e, p.w_post ? __fmul_rn(param(p.w_post, p.w_bf16, e), v) : v);
-    }
+    put_column(p, e, part[0][threadIdx.x]);
 }
 
 // Host side -------------------------------------------------------------------
@@ -463,7 +487,8 @@ NormPlan norm_plan(int64_t T, int64_t H) {
     const int64_t teams = pl.warp ? kWarpTeams : 1;
     const int64_t most = (!pl.warp && pl.threads <= 128) ? 608 : 304;
     const int64_t want = (T + teams - 1) / teams;
-    pl.slots = static_cast<int>(want < most ? want : most);
+    // up to 4 rows a team: one CTA, whose sums need no second launch
+    pl.slots = static_cast<int>(want <= 4 ? 1 : want < most ? want : most);
     return pl;
 }
 
@@ -483,12 +508,15 @@ dgr_status launch_norm(bool backward, NormParams &p, const NormPlan &pl, int sms
     const size_t room = (224 * 1024) / (backward ? BB : FB);
     p.depth = 0;
     if (ring) p.depth = static_cast<int>(room / (row + 1 - ring) < 3 ? room / (row + 1 - ring) : 3);  // 0 where one does not fit
+    // no more than the rows that a CTA has
+    const int64_t teams = WARP ? kWarpTeams : 1, ctas = backward ? pl.slots : static_cast<int64_t>(sms) * FB;
+    const int64_t rows = (p.T + teams * ctas - 1) / (teams * ctas);
+    if (rows < p.depth) p.depth = static_cast<int>(rows);
     size_t smem = row * p.depth;
     if (!backward) {
         auto *k = norm_forward<T, VEC, NV, MAXT, FB, WARP>;
         const dgr_status st = grant(k, smem);
         if (st != DGR_OK) return st;
-        const int64_t teams = WARP ? kWarpTeams : 1;
         const int64_t want = (p.T + teams - 1) / teams, most = static_cast<int64_t>(sms) * FB;
         k<<<sched_grid(static_cast<unsigned>(want < most ? want : most)), pl.threads, smem, s>>>(p);
         return launch_status();
@@ -662,7 +690,7 @@ extern "C" dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const
     al = row_align(al, dx, ld_dx, es);
     al = row_align(al, dy, ld_dy, es);
     st = es == 2 ? launch_type<bf16>(true, p, pl, 0, s, al) : launch_type<float>(true, p, pl, 0, s, al);
-    if (st != DGR_OK || (!dw_post && !dw_pre && !(dgate && gate_mode == kGateChannel))) return st;
+    if (st != DGR_OK || pl.slots == 1 || (!dw_post && !dw_pre && !(dgate && gate_mode == kGateChannel))) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((2 * H + kFoldCols - 1) / kFoldCols));
     cfg.blockDim = dim3(kFoldCols, kFoldWays);
