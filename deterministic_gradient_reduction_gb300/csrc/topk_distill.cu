@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     extern __shared__ __align__(16) char smem[];
     __shared__ float4 s_pair[2][kMaxCluster * W];  // the cluster's warps, by row parity: outside the list, in it
     __shared__ float s_loss[2][kMaxCluster * W];   // likewise their parts of a row's loss
-    __shared__ float2 s_list;                      // ln of the list's normaliser, sum of its q
+    __shared__ float3 s_list;                      // ln of the list's normaliser in two parts (one sum of them
+                                                   // would be rounded at its own size), sum of its q
     __shared__ int s_any, last;
     __shared__ uint32_t s_twice;                   // the row (item + 1) in whose list an id came twice
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 if (__any_sync(0xffffffffu, bad) && rank == 0 && lane == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereId);
                 if (lane == 0) {
                     s_any = any;
-                    s_list = make_float2(TAIL ? lse_t : __fadd_rn(top, logf(sum)), TAIL ? sum : 1.0f);
+                    s_list = TAIL ? make_float3(lse_t, 0.0f, sum) : make_float3(top, logf(sum), 1.0f);
                 }
             }
             for (;;) {  // a second time only where k times the maximum is out of range; `shift` is subtracted then
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     continue;
                 }
                 live = s_any != 0;
-                const float sum_q = s_list.y;
+                const float sum_q = s_list.z;
                 c_all = scaled_max(m_all, p.k2);
                 const float down = ex2(__fadd_rn(c_rest, -c_all));
                 total = TAIL ? __fmaf_rn(rest.s, down, __fmul_rn(in.s, ex2(__fadd_rn(c_in, -c_all)))) : rest.s;
@@ -521,13 +522,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             // the list's entries: their part of the loss, their tokens' gradient
             if (w < list_warps) {
                 float part = 0.0f;
-                const float base = s_list.x, ln_total = logf(total);
+                const float2 base = make_float2(s_list.x, s_list.y);
+                const float ln_total = logf(total);
                 for (int k = tid; k < K; k += NT) {
                     const int at = s_copy[k] & ~kCopy;
                     if (s_copy[k] < 0) continue;
                     if (at < View::kSingle) s_bits[at / VEC / NT / U * NT + at / VEC % NT] = 0;  // free again
                     if (!live) continue;
-                    const float lq = __fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -base);
+                    const float lq = __fadd_rn(__fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -base.x), -base.y);
                     float q = expf(lq);
                     const float x = __fmaf_rn(__fadd_rn(s_z[k], -shift), p.k2, -c_all);  // log2 of p times the total
                     if (q != 0.0f) part = __fmaf_rn(q, __fadd_rn(lq, -__fmaf_rn(x, kLn2, -ln_total)), part);
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     if (s_twice == item + 1) {
                         q = 0.0f;
                         for (int j = 0; j < K; ++j)
-                            if (ids[j] == id) q = __fadd_rn(q, expf(__fadd_rn(__fmul_rn(teacher[j], p.inv_tau), -base)));
+                            if (ids[j] == id) q = __fadd_rn(q, expf(__fadd_rn(__fadd_rn(__fmul_rn(teacher[j], p.inv_tau), -base.x), -base.y)));
                     }
                     const float g = __fmul_rn(__fmaf_rn(ex2(x), inv_mass, -q), f);
                     *reinterpret_cast<raw_t<T, 1> *>(dz + id) = pack<T, 1>(&g);
