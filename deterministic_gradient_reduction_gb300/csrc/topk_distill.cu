@@ -637,18 +637,19 @@ dgr_status launch_size(DistillParams &p, int sms, cudaStream_t s) {
     if (p.V < 8192) return launch_rows<T, 128, TAIL>(p, 1, sms, s);
     // A CTA does a list's work for every row it has a part of, so few CTAs a
     // row. With a gradient a row of up to 128 KB has one, a longer one more, so
-    // that the 608 CTAs hold no more than about 80 MB at a time and the second
-    // reading finds most of it in L2: 4096 x 131072 bf16 462 us with 2 CTAs a
-    // row, 477 with 1; 1021 x 50001 bf16 (100 KB) 53 us with 1, 58 with 2.
-    // (512 threads a CTA instead of 256: 449 and 57 us, 2048 x 32768 fp32
-    // forward 66 instead of 60.)
+    // that the CTAs of the device hold no more than about 80 MB at a time and
+    // the second reading finds most of it in L2: 1021 x 50001 bf16 (100 KB) 53
+    // us with 1, 58 with 2. Longer rows have CTAs of 512 threads (4096 x 131072
+    // bf16, 2 CTAs a row: 449 us with 512, 461 with 256), others of 256 (2048 x
+    // 32768 fp32 forward 56 us with 256, 66 with 512).
+    const bool is_long = p.dz && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10);
     int cluster = 1;
-    while (p.dz && cluster < kMaxCluster && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10) * cluster) cluster <<= 1;
+    while (is_long && cluster < kMaxCluster && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10) * cluster) cluster <<= 1;
     // few rows: a row over more CTAs, down to 4096 elements each
     while (cluster < kMaxCluster && static_cast<int64_t>(p.T) * cluster * 2 <= 304 && p.V >= 4096 * cluster * 2) cluster <<= 1;
-    // long rows: the list's bits leave room for four CTAs an SM
+    // the list's bits leave room for four CTAs an SM
     while (cluster < kMaxCluster && distill_smem(p.K, p.V, 256, cluster, sizeof(T)) > 48 * 1024) cluster <<= 1;
-    return launch_rows<T, 256, TAIL>(p, cluster, sms, s);
+    return is_long ? launch_rows<T, 512, TAIL>(p, cluster, sms, s) : launch_rows<T, 256, TAIL>(p, cluster, sms, s);
 }
 
 size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? static_cast<size_t>(((T - 1) * ld + W) * es) : 0; }
