@@ -525,7 +525,8 @@ dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const void *y, i
  *           fp32 or null; dloss one DEVICE fp32 or null (1).
  * row_loss: [T] fp32 or null; loss: one fp32 or null (needs row_loss);
  *           dlogits: [T, V] of dtype, row stride ld_d, or null; one at least.
- *           loss and dlogits of one call cost one reading of the logits.
+ *           loss and dlogits of one call share the reading of the logits from
+ *           memory (the gradient reads them again out of L2).
  * Limits:   1 <= V <= 2^20, 1 <= K <= 1024, T < 2^31, tau > 0.
  * ws:       dgr_topk_distill_workspace_bytes(T) bytes, zeroed once.
  * dlogits may be logits (same pointer and stride); nothing else may overlap.
