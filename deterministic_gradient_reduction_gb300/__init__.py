@@ -94,6 +94,7 @@ def lib() -> ctypes.CDLL:
             "dgr_diag_noalloc_wait_timeout": ([I32, I32, P], I32),
             "dgr_diag_set_schedule": ([I32, ctypes.c_uint32, I32], I32),
             "dgr_diag_colsum_plan": ([I64, I64, I32, I32, I32, I32, I32, I32, P], I32),
+            "dgr_diag_distill_reads": ([I32, I64, I32, I32, I32, P], I32),
             "dgr_diag_atomic_colsum": ([P, I64, I32, P, P], I32),
             "dgr_diag_atomic_rowdot": ([P, P, I64, I32, P, P], I32),
         }

@@ -41,6 +41,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "dgr_diag.h"
 #include "row_common.cuh"
 
 namespace dgr {
@@ -109,13 +110,14 @@ template <typename T>
 struct RowView {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     int head, n_vec, n_single, first, count;
-    __device__ __forceinline__ RowView(const T *z, int V, int rank, int per) {
+    __host__ __device__ __forceinline__ RowView(const T *z, int V, int rank, int per) {
         const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / static_cast<int>(sizeof(T));
-        head = min(V, off ? VEC - off : 0);
+        head = off ? VEC - off : 0;
+        head = head < V ? head : V;
         n_vec = (V - head) / VEC;
         n_single = V - n_vec * VEC;
-        first = min(n_vec, rank * per);
-        count = min(per, n_vec - first);
+        first = rank * per < n_vec ? rank * per : n_vec;
+        count = per < n_vec - first ? per : n_vec - first;
         if (rank != 0) n_single = 0;
     }
     // element of single i: before the vectors, then behind them
@@ -130,6 +132,25 @@ struct RowView {
         }
         return n_single ? kSingle + (e < 0 ? j : j - n_vec * VEC) : -1;
     }
+};
+
+// A CTA's part of the gradient's row, `elements` long from `own` on: `lead`
+// elements before its first 16-byte boundary, then n_out whole vectors. With a
+// lead they lie across the logits' vectors, and vector v is made of the logits'
+// vectors v and v + 1; without one of v alone, and v + 1 is not read: behind the
+// last vector of the last row there may be no memory.
+template <typename T>
+struct GradView {
+    static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    int lead, n_out;
+    __host__ __device__ __forceinline__ GradView(const T *own, int elements) {
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(own) & 15) / static_cast<int>(sizeof(T));
+        lead = off ? VEC - off : 0;
+        lead = lead < elements ? lead : elements;
+        n_out = (elements - lead) / VEC;
+    }
+    __host__ __device__ __forceinline__ bool has(int v) const { return v < n_out; }
+    __host__ __device__ __forceinline__ bool takes_next(int v) const { return v < n_out && lead != 0; }
 };
 
 // fl(m k), at least -1e38: elements that far below give 0 and never inf - inf.
@@ -461,8 +482,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             T *own = dz + view.head + static_cast<int64_t>(view.first) * VEC;  // this CTA's part of the gradient's row
             // elements before its first 16-byte boundary: its vectors are then
             // made of two neighbouring ones of the logits
-            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(own) & 15) / static_cast<int>(sizeof(T));
-            const int lead = off ? min(VEC - off, view.count * VEC) : 0, n_out = (view.count * VEC - lead) / VEC;
+            const GradView<T> out(own, view.count * VEC);
+            const int lead = out.lead, n_out = out.n_out;
             auto pass = [&](auto shifted, auto aligned_too) {
                 constexpr int F = aligned_too.value ? U : 2;
                 for (int v = tid; v < n_out; v += F * NT) {
@@ -470,10 +491,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     uint4 r[F], next[F];
 #pragma unroll
                     for (int u = 0; u < F; ++u) {
-                        const bool on = v + u * NT < n_out;
                         r[u] = next[u] = make_uint4(0, 0, 0, 0);
-                        load_if<false>(r[u], src + u * NT * 16, on);
-                        if constexpr (!aligned_too.value) load_if<false>(next[u], src + u * NT * 16 + 16, on);
+                        load_if<false>(r[u], src + u * NT * 16, out.has(v + u * NT));
+                        if constexpr (!aligned_too.value) load_if<false>(next[u], src + u * NT * 16 + 16, out.takes_next(v + u * NT));
                     }
 #pragma unroll
                     for (int u = 0; u < F; ++u) {
@@ -489,7 +509,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                             r[u] = make_uint4(__funnelshift_r(q[0], q[1], by & 31), __funnelshift_r(q[1], q[2], by & 31),
                                               __funnelshift_r(q[2], q[3], by & 31), __funnelshift_r(q[3], q[4], by & 31));
                         }
-                        if (v + u * NT < n_out) reinterpret_cast<uint4 *>(own + lead)[v + u * NT] = gradient(r[u], shifted);
+                        if (out.has(v + u * NT)) reinterpret_cast<uint4 *>(own + lead)[v + u * NT] = gradient(r[u], shifted);
                     }
                 }
             };
@@ -656,6 +676,25 @@ dgr_status launch_size(DistillParams &p, int sms, cudaStream_t s) {
     return is_long ? launch_rows<T, 512, TAIL>(p, cluster, sms, s) : launch_rows<T, 256, TAIL>(p, cluster, sms, s);
 }
 
+// The end, in elements from the row's start, of the vectors that the gradient
+// pass reads in a row of V elements at z with its gradient at dz, over `ctas`
+// CTAs (the walk of distill_rows, by the same RowView and GradView).
+template <typename T>
+int64_t gradient_reads(int V, const T *z, const T *dz, int ctas) {
+    constexpr int VEC = RowView<T>::VEC;
+    int64_t end = 0;
+    for (int rank = 0; rank < ctas; ++rank) {
+        const RowView<T> view(z, V, rank, vectors(V, ctas, sizeof(T)));
+        const int64_t first = view.head + static_cast<int64_t>(view.first) * VEC;
+        const GradView<T> out(dz + first, view.count * VEC);
+        for (int v = 0; out.has(v); ++v) {
+            const int64_t e = first + static_cast<int64_t>(v + (out.takes_next(v) ? 2 : 1)) * VEC;
+            if (e > end) end = e;
+        }
+    }
+    return end;
+}
+
 size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? static_cast<size_t>(((T - 1) * ld + W) * es) : 0; }
 
 }  // namespace
@@ -664,6 +703,17 @@ size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? sta
 using namespace dgr;
 
 extern "C" size_t dgr_topk_distill_workspace_bytes(int64_t T) { return T < 0 || T > INT32_MAX ? 0 : sizeof(WsHeader); }
+
+extern "C" dgr_status dgr_diag_distill_reads(int32_t dtype, int64_t V, int32_t z_at, int32_t dz_at, int32_t ctas, int64_t *end) {
+    if ((dtype != DGR_DTYPE_BF16 && dtype != DGR_DTYPE_F32) || V < 1 || V > kMaxVocab || ctas < 1 || ctas > kMaxCluster || !end)
+        return DGR_ERR_INVALID_ARG;
+    const int vec = dtype == DGR_DTYPE_BF16 ? 8 : 4;
+    if (z_at < 0 || z_at >= vec || dz_at < 0 || dz_at >= vec) return DGR_ERR_INVALID_ARG;
+    auto walk = [&](auto *base) { return gradient_reads(static_cast<int>(V), base + z_at, base + dz_at, ctas); };
+    // addresses only, never read; both 16-byte boundaries
+    *end = vec == 8 ? walk(reinterpret_cast<const bf16 *>(uintptr_t{4096})) : walk(reinterpret_cast<const float *>(uintptr_t{4096}));
+    return DGR_OK;
+}
 
 extern "C" dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t *ids,
                                        int64_t ld_ids, const float *teacher, int64_t ld_teacher, int32_t K, float tau,

@@ -128,6 +128,15 @@ dgr_status dgr_diag_colsum_plan(int64_t T, int64_t H, int32_t tile_rows, int32_t
                                 int32_t cta_occupancy, int32_t grid_cap, int32_t *plan);
 
 /*
+ * What the gradient pass of dgr_topk_distill() reads of a row, computed on the
+ * host alone with the kernel's own index arithmetic: *end = the end of its
+ * vector loads in elements from the row's start, for a row of V elements whose
+ * logits start z_at elements and whose gradient starts dz_at elements behind a
+ * 16-byte boundary, spread over `ctas` CTAs (1 .. 8). It must not pass V.
+ */
+dgr_status dgr_diag_distill_reads(int32_t dtype, int64_t V, int32_t z_at, int32_t dz_at, int32_t ctas, int64_t *end);
+
+/*
  * Test-only: how every later launch of this process hands out its work. The
  * kernels take work items (tiles, rows, token chunks, warp shares) in
  * ascending order over as many CTAs as they need; here a test can ask for
