@@ -189,6 +189,7 @@ __device__ bool group_tiles(const BalParams &p, int32_t *tbase, int64_t *so, int
         const int32_t before = __reduce_add_sync(0xffffffffu, lane < w ? v : 0);
         if (g < p.G) tbase[g] += before;
         run += __reduce_add_sync(0xffffffffu, v);
+        if (g0 + kThreads < p.G) __syncthreads();  // all have read wsum before the next round writes it
     }
     if (tid == 0) tbase[p.G] = run, *n_groups = filled;
     return !__syncthreads_or(broken);
