@@ -36,6 +36,12 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxTile = 16384;  // tokens: a lane's running sums stay short
 
+// x log2(e) - fl(m log2(e)) carries the rounding of the product, up to half a
+// unit of its size: 1/4 below this maximum, where it cancels between an
+// exponential and its row's sum; at 1e10 it is in the hundreds, and ex2 would
+// give infinity or 0. Beyond, the maximum is subtracted before scaling.
+constexpr float kFarLogit = 4194304.0f;
+
 enum { kWhereOffsets = 301, kWhereExpertId = 302 };
 
 struct BalParams {
@@ -101,7 +107,7 @@ __device__ __forceinline__ void scores(float (&x)[E], int lanes, bool live) {
     m = lanes_max<LANES>(m, lanes);
     const bool empty = m == -INFINITY;
     if constexpr (!SIGMOID) {
-        if (fabsf(m) > 1e38f && !empty) {  // m log2(e) may be beyond the type's range: subtract first
+        if (fabsf(m) > kFarLogit && !empty) {
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], -m);
             m = 0.0f;

@@ -1,4 +1,4 @@
-"""The router balance loss with more groups than a CTA has threads."""
+"""The router balance loss with more groups than a CTA has threads, and of rows of logits far from zero."""
 import numpy as np
 import pytest
 import torch
@@ -29,3 +29,39 @@ def test_more_groups_than_a_cta_has_threads(dtype, E, G):
     base = bits(_call(t))
     for _ in range(30):
         assert (bits(_call(t)) == base).all()
+
+
+def near_range(x):
+    """Largest distance of a logit that counts from its row's maximum (in powers of two): beyond 200 a
+    probability is 0 in both."""
+    d = x.amax(1, keepdim=True) - x
+    d = d[torch.isfinite(d) & (d < 200)]
+    return 1.4427 * float(d.max())
+
+
+@pytest.mark.parametrize("value", [-5.0e7, -1.0e10, -1.0e20, -1.0e30, 5.0e7, 1.0e10, 1.0e20, 1.0e30])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [16, 60, 128, 33])
+def test_rows_far_from_zero(E, dtype, score, value):
+    t = make(40, E, 2, dtype)
+    t["x"][1] = value
+    t["x"][2, : E // 2] = value
+    t["x"][3] = value
+    t["x"][3, 5] = value + abs(value) / 2
+    t["x"][39] = value
+    if dtype == "fp32" and abs(value) < 1e8:
+        t["x"][4] = value + 4.0 * torch.round(t["x"][4])
+    loss, counts, tokens = dgr.router_balance(t["x"], t["ids"], COEFF, score=score)
+    got = dgr.router_balance_backward(t["x"], counts, tokens, 2, COEFF, score=score)
+    v = ref.d(t["x"]).requires_grad_()
+    wl, wc, _ = ref.balance(v, t["ids"].cpu(), COEFF, score=score)
+    want = torch.autograd.grad(wl, v)[0]
+    x = v.detach() if score == "softmax" else torch.nn.functional.logsigmoid(v.detach())
+    rel = (64 + 4 * near_range(x) + 16 + E // 32) * ref.U  # as in test_gpu_router_balance.check, for N < 256
+    assert abs(float(loss) - float(wl)) <= rel * float(wl)
+    p, c = ref.balance_scores(v.detach(), score), wc[0].double()
+    a = COEFF * E / (2 * 40 ** 2)
+    bound = a * rel * p * (c + (p * c).sum(1, keepdim=True)) + ref.half_ulp(t["x"].dtype) * want.abs() + 1e-38
+    err = (ref.d(got) - want).abs()
+    assert (err <= bound).all(), (float((err / bound).max()), torch.isnan(got).any(1).nonzero())
