@@ -626,12 +626,15 @@ struct BalLayout {
     size_t done, group_loss, mass, part, live, total;
 };
 
+// The counters come first and have room for the most groups, so that they lie
+// at the same place whatever the sizes: what one call leaves in its sums is never
+// another's counter, and a workspace serves calls of any sizes that fit it.
 BalLayout balance_layout(int64_t N, int64_t E, int64_t G) {
     BalLayout L{};
     const int64_t tile = balance_tile(N, E);
     L.tiles = (N + tile - 1) / tile + (G > 1 ? G : 0);
     L.done = sizeof(WsHeader);
-    L.group_loss = L.done + align_up(static_cast<size_t>(G) * 4);
+    L.group_loss = L.done + align_up(static_cast<size_t>(kMaxGroups) * 4);
     L.mass = L.group_loss + align_up(static_cast<size_t>(G) * 4);
     L.part = L.mass + align_up(static_cast<size_t>(L.tiles) * E * 4);
     L.live = L.part + align_up(static_cast<size_t>(L.tiles) * E * 4);

@@ -429,8 +429,9 @@ dgr_status dgr_dsrelu_dprob(const void *A, const void *B, const int64_t *d_offs,
  * dloss:    one DEVICE fp32 or null (1). dlogits: [N, E] of dtype, row stride
  *           ld_d; accumulate != 0 adds to it (rounded once more).
  * Limits:   1 <= E <= 1024, 1 <= K <= 1024, 1 <= G <= 1024, N < 2^31.
- * ws:       dgr_router_balance_workspace_bytes(N, E, G) bytes, zeroed once. The
- *           backward call needs none.
+ * ws:       dgr_router_balance_workspace_bytes(N, E, G) bytes, zeroed once; one
+ *           that is large enough may go on to calls with other sizes as it is.
+ *           The backward call needs none.
  * No output may overlap an input, another output or ws.
  */
 size_t dgr_router_balance_workspace_bytes(int64_t N, int32_t E, int32_t G);
@@ -478,7 +479,8 @@ dgr_status dgr_router_balance_backward(const void *logits, int32_t dtype, int64_
  *           stride; w_post, gate, w_pre: bf16 or fp32 (w_dtype);
  *           dw_post [H], dgate [H] or [T], dw_pre [H]: fp32.
  * Limits:   1 <= H <= 16384, T < 2^31.
- * ws:       dgr_block_norm_workspace_bytes(T, H) bytes for the backward call.
+ * ws:       dgr_block_norm_workspace_bytes(T, H) bytes for the backward call; it
+ *           may go on to calls with other sizes as it is.
  * h may be x and dx may be dh (same pointer and stride); nothing else may overlap.
  */
 size_t dgr_block_norm_workspace_bytes(int64_t T, int64_t H);
@@ -528,7 +530,8 @@ dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const void *y, i
  *           loss and dlogits of one call share the reading of the logits from
  *           memory (the gradient reads them again out of L2).
  * Limits:   1 <= V <= 2^20, 1 <= K <= 1024, T < 2^31, tau > 0.
- * ws:       dgr_topk_distill_workspace_bytes(T) bytes, zeroed once.
+ * ws:       dgr_topk_distill_workspace_bytes(T) bytes, zeroed once; it may go on
+ *           to calls with other sizes as it is.
  * dlogits may be logits (same pointer and stride); nothing else may overlap.
  */
 size_t dgr_topk_distill_workspace_bytes(int64_t T);

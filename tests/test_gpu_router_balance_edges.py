@@ -1,4 +1,5 @@
-"""The router balance loss with more groups than a CTA has threads, and of rows of logits far from zero."""
+"""The router balance loss with more groups than a CTA has threads, of rows of logits far from zero, and with one
+workspace for calls of other sizes."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +66,20 @@ def test_rows_far_from_zero(E, dtype, score, value):
     bound = a * rel * p * (c + (p * c).sum(1, keepdim=True)) + ref.half_ulp(t["x"].dtype) * want.abs() + 1e-38
     err = (ref.d(got) - want).abs()
     assert (err <= bound).all(), (float((err / bound).max()), torch.isnan(got).any(1).nonzero())
+
+
+def test_one_workspace_for_calls_of_other_sizes():
+    """The workspace is zeroed once and then serves calls of any sizes that fit it."""
+    # groups of one tile and of several, more than 64 groups after fewer and fewer after more
+    sizes = [(3000, 64, 1), (30000, 128, 200), (900, 16, 300), (60000, 64, 90), (64, 4, 1), (2000, 8, 1024), (20000, 64, 33),
+             (40000, 32, 130), (700, 520, 600), (3000, 64, 1)]
+    ws = dgr.workspace(max(dgr.router_balance_workspace_bytes(*s) for s in sizes))
+    for N, E, G in sizes:
+        t = make(N, E, 4, "fp32", offs=None if G == 1 else cuts_of(G, N, G), masked=True)
+        same = dict(offs=t["offs"], mask=t["mask"])
+        want = dgr.router_balance(t["x"], t["ids"], COEFF, **same)
+        out = dict(loss=torch.full((1,), -3.0, device="cuda"), counts=torch.full((G, E), -3, dtype=torch.int32, device="cuda"),
+                   tokens=torch.full((G,), -3, dtype=torch.int32, device="cuda"))
+        for _ in range(2):
+            got = dgr.router_balance(t["x"], t["ids"], COEFF, ws=ws, **same, **out)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (N, E, G)
