@@ -28,8 +28,10 @@
 // which stays finite however small p_r is. Exponentials are taken to base 2
 // (k = log2(e) / tau): with m a running maximum every one is ex2(z k - fl(m k)),
 // sums meet by ex2(fl(m k) - fl(m' k)), so the roundings of these products
-// cancel between numerator and sum. Where even the row's maximum times k is
-// beyond 1e38 the row is done again with its maximum subtracted first.
+// cancel between numerator and sum. A maximum times k below -2^24 counts as -2^24
+// there, so that a thread that meets nothing but a mask's values has a sum that
+// is small and not infinite; where the row's own maximum times k is beyond 2^24
+// the row is done again with its maximum subtracted first.
 //
 // Deterministic: a row's sums go over threads, warps, CTAs of the cluster in a
 // fixed order set by V, T and the alignment; the rows' losses over one CTA in a
@@ -54,7 +56,10 @@ constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxCluster = 8;
 constexpr int kWhereId = 311;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kFar = 1e38f;  // products with k beyond this are not relied on
+// x k - fl(m k) carries the rounding of m k, up to half a unit of its size: up
+// to 1/2 below this bound, where it cancels between an exponential and its sum;
+// at 1e10 it is in the hundreds, and ex2 would give infinity or 0.
+constexpr float kFar = 16777216.0f;
 
 struct DistillParams {
     const void *z;
@@ -153,7 +158,7 @@ struct GradView {
     __host__ __device__ __forceinline__ bool takes_next(int v) const { return v < n_out && lead != 0; }
 };
 
-// fl(m k), at least -1e38: elements that far below give 0 and never inf - inf.
+// fl(m k), at least -kFar: elements further below give little or 0, never inf - inf.
 __device__ __forceinline__ float scaled_max(float m, float k) { return fmaxf(__fmul_rn(m, k), -kFar); }
 
 __device__ __forceinline__ float warp_max(float v) {

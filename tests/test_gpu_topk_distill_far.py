@@ -1,0 +1,105 @@
+"""The distillation loss and gradient of rows with logits far from zero, by value against the 64-bit
+form: finite masks over part of a row, whole rows far below or above, in place and not.
+
+Bounds as in operator_ref.distill_bounds, with the exponents that count: distances from the maximum
+outside the list and from the row's maximum, up to 200 (beyond, a probability is 0 in both)."""
+import pytest
+import torch
+
+import deterministic_gradient_reduction_gb300 as dgr
+import operator_ref as ref
+from test_gpu_topk_distill import DT, make
+
+pytestmark = pytest.mark.gpu
+
+FAR = [-5.0e7, -1.0e10, -1.0e20, -1.0e30, -1.0e38, 5.0e7, 1.0e10, 1.0e20, 1.0e30]
+MASKS = [-1.0e8, -1.0e10, -3.0e12, -1.0e20, -1.0e30, -1.0e38, "lowest"]
+
+
+def softmax_to(z, keep):
+    """(softmax over the kept elements, largest exponent that counts)."""
+    z = torch.where(keep, z, torch.full_like(z, float("-inf")))
+    d = z - z.amax(1, keepdim=True)
+    near = d[torch.isfinite(d) & (d > -200)]
+    return torch.softmax(z, 1), float(near.abs().max())
+
+
+def check(t, in_place=False):
+    z, ids, teacher, lse = ref.d(t["z"]), t["ids"].cpu(), ref.d(t["t"]), ref.d(t["lse"])
+    tau, scale, dtype = t["tau"], t["scale"], t["z"].dtype
+    T, V = z.shape
+    loss, rows, grad = ref.distill(z, ids, teacher, tau, lse, None, scale)
+    outside = torch.ones(T, V + 1, dtype=torch.bool)
+    outside.scatter_(1, torch.where((ids < 0) | (ids >= V), V, ids).long(), False)
+    outside = outside[:, :V]
+    p, reach = softmax_to(z / tau, torch.ones_like(outside))
+    share, reach_out = softmax_to(z / tau, outside)
+    R = 1.4427 * max(2 * reach, 2 * reach_out, 2 * float(teacher.abs().max()) / tau, 0.0 if lse is None else float(lse.abs().max())) + 32
+    f = scale / tau
+    size = f * (p + (share if lse is not None else 0)) + grad.abs()
+    bound = (64 + 4 * R) * ref.U * size + ref.half_ulp(dtype) * grad.abs() + 1e-38
+    lp = torch.log_softmax(z / tau, 1)
+    listed = torch.where(outside, torch.zeros_like(lp), lp).abs().amax(1)
+    rest = torch.logsumexp(torch.where(outside, lp, torch.full_like(lp, float("-inf"))), 1).abs() if lse is not None else 0.0
+    row_bound = (64 + 8 * R) * ref.U * (listed + rest + 2 * teacher.abs().amax(1) / tau + 16)
+    dz = t["z"].clone() if in_place else torch.empty(T, V, dtype=dtype, device="cuda")
+    got, got_rows = dgr.topk_distill(dz if in_place else t["z"], t["ids"], t["t"], tau=tau, teacher_lse=t["lse"], scale=scale, dlogits=dz)
+    err = (ref.d(got_rows) - rows).abs()
+    assert (err <= row_bound).all(), (got_rows, rows, row_bound)
+    assert abs(float(got) - float(loss)) <= scale * float(row_bound.sum()) + 64 * ref.U * scale * float(rows.abs().sum())
+    err = (ref.d(dz) - grad).abs()
+    assert (err <= bound).all(), (float((err / bound).max()), torch.isnan(dz).any(1), (err > bound).sum(1))
+    return got, got_rows, dz
+
+
+def masks(value, dtype):
+    return torch.finfo(DT[dtype]).min if value == "lowest" else value
+
+
+def unlisted(t):
+    T, V = t["z"].shape
+    keep = torch.ones(T, V + 1, dtype=torch.bool, device="cuda")
+    keep.scatter_(1, torch.where(t["ids"] < 0, V, t["ids"]).long(), False)
+    return keep[:, :V]
+
+
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [900, 40000])
+def test_masked_parts(V, dtype, tail, value):
+    t = make(6, V, 8, dtype, tau=0.9, tail=tail, weights=False)
+    at = torch.arange(V, device="cuda")
+    for r, closed in enumerate([at >= V // 2, at < V // 2, at % 2 == 1, (at > V // 3) & (at < V - 50), at < V - 20]):
+        t["z"][r][closed & unlisted(t)[r]] = masks(value, dtype)
+    check(t)
+
+
+@pytest.mark.parametrize("value", FAR)
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [900, 40000])
+def test_whole_rows(V, dtype, tail, value):
+    t = make(5, V, 8, dtype, tail=tail, weights=False)
+    t["z"][0] = value
+    t["z"][4] = value                        # the last row too
+    if dtype == "fp32" and abs(value) < 1e8:  # a spread that the type still holds: multiples of 4
+        t["z"][1] = value + 4.0 * torch.round(t["z"][1])
+    else:
+        t["z"][1] = value
+        t["z"][1, ::3] = value - abs(value) / 2  # a third of it much lower
+    t["z"][2, V // 2:] = value               # two levels: one of them far away
+    check(t)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V", [904, 32768, 40001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_in_place(dtype, V, tail):
+    t = make(3, V, 8, dtype, tail=tail, weights=False)
+    t["z"][0] = -1.0e30
+    t["z"][1, V // 2:] = 1.0e20
+    t["z"][2] = torch.finfo(DT[dtype]).min
+    out = check(t)
+    there = check(t, in_place=True)
+    assert all(torch.equal(a, b) for a, b in zip(out, there))
