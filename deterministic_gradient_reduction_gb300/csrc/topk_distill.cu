@@ -607,12 +607,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     float s[1] = {0.0f};
     for (int t = tid; t < p.T; t += NT) {
         const float wt = p.weights ? __ldg(p.weights + t) : 1.0f;
-        if (wt != 0.0f) s[0] = __fmaf_rn(wt, __ldcg(p.row_loss + t), s[0]);
+        // scaled first: the sum is out of range only where the loss is
+        if (wt != 0.0f) s[0] = __fmaf_rn(__fmul_rn(p.scale, wt), __ldcg(p.row_loss + t), s[0]);
     }
     float *buf = reinterpret_cast<float *>(s_pair);  // free by now
     block_sum<1>(s, buf, W);
     if (tid == 0) {
-        *p.loss = __fmul_rn(p.scale, s[0]);
+        *p.loss = s[0];
         p.hdr->pad[0] = 0;  // ready for the next call
     }
 }

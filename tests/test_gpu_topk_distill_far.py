@@ -24,11 +24,22 @@ def softmax_to(z, keep):
     return torch.softmax(z, 1), float(near.abs().max())
 
 
+def gradient(p, share, outside, ids, teacher, tau, lse, f):
+    """From the formula (autograd's logsumexp does not resolve shares of exponents beyond 1e12, even in 64 bits)."""
+    valid = ids >= 0
+    tl = (teacher / tau).masked_fill(~valid, float("-inf"))
+    q = torch.exp(tl - (torch.logsumexp(tl, 1, keepdim=True) if lse is None else lse[:, None]))
+    left = (1 - q.sum(1, keepdim=True)).clamp(min=0) if lse is not None else torch.zeros(len(q), 1, dtype=torch.float64)
+    S = torch.where(left > 0, torch.ones_like(left), q.sum(1, keepdim=True))
+    target = torch.zeros_like(p).scatter_add_(1, ids.clamp(min=0).long(), q)
+    return f * (S * p - target - torch.where(outside, left * share, torch.zeros_like(p)))
+
+
 def check(t, in_place=False):
     z, ids, teacher, lse = ref.d(t["z"]), t["ids"].cpu(), ref.d(t["t"]), ref.d(t["lse"])
     tau, scale, dtype = t["tau"], t["scale"], t["z"].dtype
     T, V = z.shape
-    loss, rows, grad = ref.distill(z, ids, teacher, tau, lse, None, scale)
+    loss, rows, _ = ref.distill(z, ids, teacher, tau, lse, None, scale)
     outside = torch.ones(T, V + 1, dtype=torch.bool)
     outside.scatter_(1, torch.where((ids < 0) | (ids >= V), V, ids).long(), False)
     outside = outside[:, :V]
@@ -36,6 +47,7 @@ def check(t, in_place=False):
     share, reach_out = softmax_to(z / tau, outside)
     R = 1.4427 * max(2 * reach, 2 * reach_out, 2 * float(teacher.abs().max()) / tau, 0.0 if lse is None else float(lse.abs().max())) + 32
     f = scale / tau
+    grad = gradient(p, share, outside, ids, teacher, tau, lse, f)
     size = f * (p + (share if lse is not None else 0)) + grad.abs()
     bound = (64 + 4 * R) * ref.U * size + ref.half_ulp(dtype) * grad.abs() + 1e-38
     lp = torch.log_softmax(z / tau, 1)
@@ -103,3 +115,13 @@ def test_in_place(dtype, V, tail):
     out = check(t)
     there = check(t, in_place=True)
     assert all(torch.equal(a, b) for a, b in zip(out, there))
+
+
+@pytest.mark.parametrize("scale", [0.125, 1.0e-3])
+def test_a_loss_in_range_of_rows_whose_sum_is_not(scale):
+    t = make(8, 900, 4, "fp32", weights=False)
+    t["ids"][:] = torch.arange(4, dtype=torch.int32, device="cuda")
+    t["z"][:, :4] = -1.5e38
+    t["scale"] = scale
+    _, rows, _ = check(t)
+    assert bool((rows > 1.0e38).all())
