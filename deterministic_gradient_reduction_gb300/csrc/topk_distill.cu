@@ -30,8 +30,9 @@
 // sums meet by ex2(fl(m k) - fl(m' k)), so the roundings of these products
 // cancel between numerator and sum. A maximum times k below -2^24 counts as -2^24
 // there, so that a thread that meets nothing but a mask's values has a sum that
-// is small and not infinite; where the row's own maximum times k is beyond 2^24
-// the row is done again with its maximum subtracted first.
+// is small and not infinite; where the maximum outside the list or in it times k
+// is beyond 2^24 the row is done again with each of the two subtracted from its
+// own elements first. Both sums are then at least 1, however far apart they lie.
 //
 // Deterministic: a row's sums go over threads, warps, CTAs of the cluster in a
 // fixed order set by V, T and the alignment; the rows' losses over one CTA in a
@@ -297,8 +298,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         const float *teacher = reinterpret_cast<const float *>(ids + K);
         copy_wait();  // each thread's own part of the list
         const float weight_2 = weight_of(item + 2 * n_clusters);
-        float a = 0.0f, c_rest = 0.0f, f = 0.0f, c_all = 0.0f, inv_mass = 0.0f, total = 1.0f, shift = 0.0f;
-        float rest_s = 0.0f, left = 0.0f;  // sum outside the list, q left for it
+        float a = 0.0f, c_rest = 0.0f, f = 0.0f, c_all = 0.0f, inv_mass = 0.0f, total = 1.0f;
+        float shift = 0.0f, base_z = 0.0f;  // subtracted before scaling: outside the list, at its entries
+        float tail = 0.0f;                  // q_r (ln q_r - ln p_r)
         bool live = false;
         if (weight != 0.0f) {
             // the list's entries in this CTA: where they lie, their bits. An
@@ -351,7 +353,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     s_list = TAIL ? make_float3(lse_t, 0.0f, sum) : make_float3(top, logf(sum), 1.0f);
                 }
             }
-            for (;;) {  // a second time only where k times the maximum is out of range; `shift` is subtracted then
+            float shift_in = 0.0f;  // subtracted in the list's sum
+            for (bool again = false;; again = true) {  // a second time only where k times a maximum is out of range
                 Running run;
                 auto pass = [&](auto shifted) {
                     const char *src = first + tid * 16;
@@ -417,10 +420,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 }
                 if (TAIL && w < list_warps) {  // the list's tokens in this CTA, each once
                     for (int k = tid; k < K; k += NT)
-                        if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.m = fmaxf(in.m, __fadd_rn(s_z[k], -shift));
+                        if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.m = fmaxf(in.m, __fadd_rn(s_z[k], -shift_in));
                     const float ci = scaled_max(in.m, p.k2);
                     for (int k = tid; k < K; k += NT)
-                        if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.s = __fadd_rn(in.s, ex2(__fmaf_rn(__fadd_rn(s_z[k], -shift), p.k2, -ci)));
+                        if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.s = __fadd_rn(in.s, ex2(__fmaf_rn(__fadd_rn(s_z[k], -shift_in), p.k2, -ci)));
                     in.over_warp(p.k2);
                 }
                 __syncwarp();
@@ -446,25 +449,44 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 }
                 rest.s = warp_sum(rest.s);
                 if (TAIL) in.s = warp_sum(in.s);
-                const float m_all = TAIL ? fmaxf(rest.m, in.m) : rest.m;
-                if (shift == 0.0f && fabsf(m_all) < INFINITY && fabsf(__fmul_rn(m_all, p.k2)) >= kFar) {
-                    shift = m_all;  // the same in every warp of the cluster
+                auto far = [&](float m) { return fabsf(m) < INFINITY && fabsf(__fmul_rn(m, p.k2)) >= kFar; };
+                if (!again && (far(rest.m) || (TAIL && far(in.m)))) {  // the same in every warp of the cluster
+                    if (far(rest.m)) shift = rest.m;
+                    if (TAIL && far(in.m)) shift_in = in.m;
                     if (size > 1) cluster_barrier();  // before the pairs are written over
                     else __syncthreads();
                     continue;
                 }
+                // the two maxima's exponents below the row's own maximum
+                float gap = 0.0f, gap_in = 0.0f;
+                if (!again) {
+                    c_all = TAIL ? scaled_max(fmaxf(rest.m, in.m), p.k2) : c_rest;
+                    gap = __fadd_rn(c_rest, -c_all);
+                    gap_in = __fadd_rn(c_in, -c_all);
+                } else {  // a maximum that was subtracted is 0 now
+                    const float m_rest = shift != 0.0f ? shift : rest.m, m_in = shift_in != 0.0f ? shift_in : in.m;
+                    base_z = TAIL ? fmaxf(m_rest, m_in) : m_rest;
+                    gap = __fmul_rn(__fadd_rn(m_rest, -base_z), p.k2);
+                    gap_in = __fmul_rn(__fadd_rn(m_in, -base_z), p.k2);
+                    c_all = 0.0f;
+                }
                 live = s_any != 0;
                 const float sum_q = s_list.z;
-                c_all = scaled_max(m_all, p.k2);
-                const float down = ex2(__fadd_rn(c_rest, -c_all));
-                total = TAIL ? __fmaf_rn(rest.s, down, __fmul_rn(in.s, ex2(__fadd_rn(c_in, -c_all)))) : rest.s;
+                const float down = ex2(gap);
+                total = TAIL ? __fmaf_rn(rest.s, down, __fmul_rn(in.s, ex2(gap_in))) : rest.s;
                 const float inv = 1.0f / total;
                 const float q_rest = TAIL && rest.m != -INFINITY ? fmaxf(__fadd_rn(1.0f, -sum_q), 0.0f) : 0.0f;
                 inv_mass = __fmul_rn(inv, !TAIL || q_rest > 0.0f ? 1.0f : sum_q);
                 f = __fmul_rn(__fmul_rn(__fmul_rn(p.scale, weight), p.inv_tau), p.dloss ? __ldg(p.dloss) : 1.0f);
                 a = __fmul_rn(TAIL ? __fadd_rn(__fmul_rn(down, inv_mass), q_rest > 0.0f ? -q_rest / rest.s : 0.0f) : inv, f);
-                rest_s = rest.s;
-                left = q_rest;
+                if (TAIL && p.row_loss && rank == 0 && w == W - 1 && q_rest > 0.0f && live) {
+                    if (!again) {
+                        tail = __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -__fadd_rn(__fmaf_rn(gap, kLn2, logf(rest.s)), -logf(total))));
+                    } else {  // times q_r before 1 / tau: the exponent alone may be out of range
+                        const float near = __fadd_rn(logf(q_rest), __fadd_rn(logf(total), -logf(rest.s)));
+                        tail = __fmaf_rn(__fmul_rn(q_rest, __fadd_rn(base_z, shift != 0.0f ? -shift : -rest.m)), p.inv_tau, __fmul_rn(q_rest, near));
+                    }
+                }
                 break;
             }
         } else {
@@ -544,9 +566,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             if (p.row_loss && rank == 0 && w == W - 1) {
                 finish_loss();
                 loss_row = row;
-                loss_tail = 0.0f;
-                if (left > 0.0f && live)
-                    loss_tail = __fmul_rn(left, __fadd_rn(logf(left), -__fadd_rn(__fmaf_rn(__fadd_rn(c_rest, -c_all), kLn2, logf(rest_s)), -logf(total))));
+                loss_tail = tail;
             }
             // the list's entries: their part of the loss, their tokens' gradient
             if (w < list_warps) {
@@ -560,8 +580,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     if (!live) continue;
                     const float lq = __fadd_rn(__fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -base.x), -base.y);
                     float q = expf(lq);
-                    const float x = __fmaf_rn(__fadd_rn(s_z[k], -shift), p.k2, -c_all);  // log2 of p times the total
-                    if (q != 0.0f) part = __fmaf_rn(q, __fadd_rn(lq, -__fmaf_rn(x, kLn2, -ln_total)), part);
+                    const float below = __fadd_rn(s_z[k], -base_z);
+                    const float x = __fmaf_rn(below, p.k2, -c_all);  // log2 of p times the total
+                    if (q != 0.0f) {
+                        if (x > -1e30f || !(fabsf(below) < INFINITY)) part = __fmaf_rn(q, __fadd_rn(lq, -__fmaf_rn(x, kLn2, -ln_total)), part);
+                        else part = __fmaf_rn(-__fmul_rn(q, below), p.inv_tau, part);  // x may be out of range; the rest is nothing beside it
+                    }
                     if (!p.dz || (s_copy[k] & kCopy)) continue;
                     const int id = ids[k];
                     if (s_twice == item + 1) {

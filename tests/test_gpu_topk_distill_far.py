@@ -1,5 +1,6 @@
 """The distillation loss and gradient of rows with logits far from zero, by value against the 64-bit
-form: finite masks over part of a row, whole rows far below or above, in place and not.
+form: finite masks over part of a row, whole rows far below or above, all that the list leaves out
+masked while the teacher has mass there, masked list entries, in place and not.
 
 Bounds as in operator_ref.distill_bounds, with the exponents that count: distances from the maximum
 outside the list and from the row's maximum, up to 200 (beyond, a probability is 0 in both)."""
@@ -101,6 +102,30 @@ def test_whole_rows(V, dtype, tail, value):
         t["z"][1] = value
         t["z"][1, ::3] = value - abs(value) / 2  # a third of it much lower
     t["z"][2, V // 2:] = value               # two levels: one of them far away
+    check(t)
+
+
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [900, 40000])
+def test_nothing_but_the_list_is_open(V, dtype, value):
+    """The gradient outside is -q_r / n each, though the student has no mass there."""
+    t = make(4, V, 8, dtype, tau=1.5, tail=True, weights=False)
+    t["lse"] += 0.4
+    t["z"][unlisted(t)] = masks(value, dtype)
+    t["z"][3, 5] = t["z"][3, 5] / 2           # one a little more open than the others
+    out = check(t)
+    assert bool((out[2][0][unlisted(t)[0]] < 0).all())
+
+
+@pytest.mark.parametrize("value", [-1.0e10, -1.0e30, "lowest", 1.0e10, 1.0e30])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_far_list_entries(dtype, tail, value):
+    t = make(4, 3000, 8, dtype, tau=1.5, tail=tail, weights=False)
+    t["ids"][:] = torch.arange(8, dtype=torch.int32, device="cuda") * 301
+    t["z"][0, 301] = masks(value, dtype)      # one entry
+    t["z"][1, ::301] = masks(value, dtype)    # the whole list
     check(t)
 
 
