@@ -493,12 +493,6 @@ NormPlan norm_plan(int64_t T, int64_t H) {
     return pl;
 }
 
-template <typename K>
-dgr_status grant(K *k, size_t smem) {
-    if (smem <= 40 * 1024) return DGR_OK;
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
-}
-
 // FB, BB: CTAs that an SM is to hold, forward and backward (registers and, by
 // the ring's depth, shared memory). Few rows streamed at a time suit the memory:
 // 16384 x 4096 bf16 forward 89.4 us with 2 CTAs an SM, 100.5 with 3, 125.8 with
@@ -520,7 +514,7 @@ dgr_status launch_norm(bool backward, NormParams &p, const NormPlan &pl, int sms
     size_t smem = row * p.depth;
     if (!backward) {
         auto *k = norm_forward<T, VEC, NV, MAXT, FB, WARP>;
-        const dgr_status st = grant(k, smem);
+        const dgr_status st = allow_smem(k, smem, room);
         if (st != DGR_OK) return st;
         const int64_t want = (p.T + teams - 1) / teams, most = static_cast<int64_t>(sms) * FB;
         k<<<sched_grid(static_cast<unsigned>(want < most ? want : most)), pl.threads, smem, s>>>(p);
@@ -529,7 +523,7 @@ dgr_status launch_norm(bool backward, NormParams &p, const NormPlan &pl, int sms
     const size_t cols = WARP ? static_cast<size_t>(kWarpTeams) * 2 * p.H * 4 : 0;  // at most 32 KB
     if (smem < cols) smem = cols;
     auto *k = norm_backward<T, VEC, NV, MAXT, BB, WARP>;
-    const dgr_status st = grant(k, smem);
+    const dgr_status st = allow_smem(k, smem, room);
     if (st != DGR_OK) return st;
     k<<<sched_grid(static_cast<unsigned>(pl.slots)), pl.threads, smem, s>>>(p);
     return launch_status();

@@ -231,6 +231,18 @@ dgr_status usable_sms(int *sms);
 // array (the no-alloc entry's scratch); looked up once per device.
 dgr_status noalloc_scratch(void **ptr);
 
+// Lets kernel k have `bytes` of dynamic shared memory, where it is not free to
+// have `most`, the largest size that any call of it asks for. The limit is the
+// kernel's and shared by all host threads, so it is always set to `most`: another
+// thread's call never finds it lowered between its own setting and its launch.
+template <typename K>
+inline dgr_status allow_smem(K *k, size_t bytes, size_t most) {
+    constexpr size_t kFree = 40 * 1024;  // 48 KB, of which the static arrays take a few
+    if (bytes <= kFree) return DGR_OK;
+    if (bytes > most) return DGR_ERR_UNSUPPORTED;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
+}
+
 inline dgr_status launch_status() {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;

@@ -642,6 +642,10 @@ BalLayout balance_layout(int64_t N, int64_t E, int64_t G) {
     return L;
 }
 
+// The forward kernel asks for at most 83,980 bytes (1024 experts and 1024
+// groups, of which the warps' columns are 67,584).
+constexpr size_t kMostSmem = 84 * 1024;
+
 size_t fold_bytes(int E, int threads) {
     const FoldShape f = E % 4 == 0 ? fold_shape<4>(E, threads) : fold_shape<1>(E, threads);
     return static_cast<size_t>(E % 4 == 0 ? 4 : 1) * f.ways * f.stride * 8;
@@ -660,8 +664,8 @@ dgr_status launch_one(bool backward, BalParams &p, unsigned grid, cudaStream_t s
         const size_t cols = static_cast<size_t>(threads / 32) * (p.E + 32) * 4, fold = fold_bytes(p.E, threads);  // the fold takes the columns' place
         const size_t smem = (p.G + 1) * 12 + p.E * 4 + (cols > fold ? cols : fold);
         auto *k = balance_forward<T, VEC, NV, LANES, SIGMOID>;
-        if (smem > 47 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-            return DGR_ERR_CUDA;
+        const dgr_status st = allow_smem(k, smem, kMostSmem);
+        if (st != DGR_OK) return st;
         k<<<grid, threads, smem, s>>>(p);
     }
     return launch_status();

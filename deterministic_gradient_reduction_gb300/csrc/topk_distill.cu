@@ -234,6 +234,9 @@ size_t distill_smem(int K, int V, int threads, int size, int es) {
     return 2 * list_bytes(K) + static_cast<size_t>(K) * 8 + static_cast<size_t>(batches(vectors(V, size, es), threads)) * threads * 4;
 }
 
+// At most 57,344 bytes: lists of 1024, and a row of 2^20 32-bit logits over 8 CTAs.
+constexpr size_t kMostSmem = 56 * 1024;
+
 template <typename T, int NT, bool TAIL>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParams p) {
     using View = RowView<T>;
@@ -651,11 +654,8 @@ dgr_status launch_rows(DistillParams &p, int cluster, int sms, cudaStream_t s) {
     const size_t smem = distill_smem(p.K, p.V, NT, cluster, sizeof(T));
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DGR_ERR_CUDA;
-    static std::atomic<int> granted[64];  // the largest size asked for so far
-    if (smem > 32 * 1024 && static_cast<int>(smem) > granted[dev].load(std::memory_order_relaxed)) {
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return DGR_ERR_CUDA;
-        granted[dev].store(static_cast<int>(smem), std::memory_order_relaxed);
-    }
+    const dgr_status st = allow_smem(k, smem, kMostSmem);
+    if (st != DGR_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(NT);
