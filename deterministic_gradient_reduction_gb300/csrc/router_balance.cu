@@ -98,7 +98,8 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
 
 // The row's probabilities in place of its logits (-inf where a lane has no
 // expert); 0 for a row that is not live, whose logits must be finite, and for
-// a row of -inf only. A NaN or +inf logit makes the row NaN, as the formula does.
+// a row of -inf only. A NaN logit makes the row NaN, and so does a +inf in the
+// softmax, as the formula does; a +inf's sigmoid is 1.
 template <int E, int LANES, bool SIGMOID>
 __device__ __forceinline__ void scores(float (&x)[E], int lanes, bool live) {
     float m = x[0];

@@ -35,8 +35,9 @@
 // own elements first. Both sums are then at least 1, however far apart they lie.
 //
 // Deterministic: a row's sums go over threads, warps, CTAs of the cluster in a
-// fixed order set by V, T and the alignment; the rows' losses over one CTA in a
-// fixed order.
+// fixed order set by the type, V, T, K, the alignment, whether there is a tail
+// and, for rows of more than 128 KB, whether there is a gradient; the rows'
+// losses over one CTA in a fixed order.
 //
 // Measured: 4096 x 131072 bf16, loss and gradient (2.15 GB) 449 us = 4.79 TB/s;
 // what a CTA does once a row (list, exchange, factors) takes about half of a
@@ -691,7 +692,11 @@ dgr_status launch_size(DistillParams &p, int sms, cudaStream_t s) {
     // the second reading finds most of it in L2: 1021 x 50001 bf16 (100 KB) 53
     // us with 1, 58 with 2. Longer rows have CTAs of 512 threads (4096 x 131072
     // bf16, 2 CTAs a row: 449 us with 512, 461 with 256), others of 256 (2048 x
-    // 32768 fp32 forward 56 us with 256, 66 with 512).
+    // 32768 fp32 forward 56 us with 256, 66 with 512). A loss alone reads its rows
+    // once and is better off with one CTA of 256 however long they are, though a
+    // loss has other bits then than with its gradient: 4096 x 131072 bf16 199 us
+    // so, 218 with one of 512, 283 as with the gradient; the gradient takes 498,
+    // 476 and 464.
     const bool is_long = p.dz && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10);
     int cluster = 1;
     while (is_long && cluster < kMaxCluster && static_cast<int64_t>(p.V) * static_cast<int64_t>(sizeof(T)) > (128 << 10) * cluster) cluster <<= 1;

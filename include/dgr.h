@@ -412,10 +412,12 @@ dgr_status dgr_dsrelu_dprob(const void *A, const void *B, const int64_t *d_offs,
  *   dl_t[e]   = *dloss * a_g * p_t[e] (counts[g][e] - sum_j counts[g][j] p_t[j])
  *               [* (1 - sigmoid(l_t[e]))], 0 for a token that is not valid.
  *
- * Sums are binary32 in a fixed order that depends on N, E and G alone: the
- * bits do not depend on the launch. Logits of -inf have probability 0 (a row
- * of them only: 0 everywhere); a NaN or +inf makes its row NaN. Masked tokens
- * are not read, whatever they hold.
+ * Sums are binary32 in a fixed order that depends on the type, on N, E, G and
+ * the offsets, and on whether E, the row stride and the address of the logits
+ * (in the backward call those of dlogits too) are whole vectors of 4 elements:
+ * the bits do not depend on the launch. Logits of -inf have probability 0 (a row
+ * of them only: 0 everywhere). A NaN makes its row NaN, and so does a +inf with
+ * score 0 (its sigmoid is 1). Masked tokens are not read, whatever they hold.
  *
  * logits:   [N, E] bf16 or fp32 (dtype), row stride ld.
  * ids:      [N, K] int32, row stride ld_ids; an id < 0 is no expert; an id >= E
@@ -471,9 +473,9 @@ dgr_status dgr_router_balance_backward(const void *logits, int32_t dtype, int64_
  * read without w_pre); x is not needed.
  *
  * Binary32 throughout, each output rounded once (u from the unrounded h). The
- * order of every sum depends on T, H and the rows' alignment alone; a row's
- * sums are its own, the sums over tokens go through a number of slots set by T
- * and H.
+ * order of every sum depends on the type, T, H and the alignment of all rows of
+ * the call (inputs and outputs) alone; a row's sums are its own, the sums over
+ * tokens go through a number of slots set by T and H.
  *
  * x, y, h, u, dh, du, dx, dy: [T, H] bf16 or fp32 (dtype), each with its row
  *           stride; w_post, gate, w_pre: bf16 or fp32 (w_dtype);
@@ -520,7 +522,11 @@ dgr_status dgr_block_norm_backward(const void *h, int64_t ld_h, const void *y, i
  * passed as they are); an id >= V is left out and records DGR_ERR_INVALID_ARG
  * in the status word. An id that comes twice adds both its q. A row of weight 0,
  * or without a valid entry, has loss 0 and gradient 0, whatever its logits hold.
- * Sums are binary32 in an order that depends on T, V, K and alignment alone.
+ * Sums are binary32 in an order that depends on the type, T, V, K, the alignment
+ * of the logits' rows and whether teacher_lse is given. For rows of more than 128
+ * KB it also depends on whether dlogits is given (a row then lies over more CTAs):
+ * a loss taken alone may differ in its last bits from the one taken with its
+ * gradient. Up to 128 KB the two are the same bits.
  *
  * logits:   [T, V] bf16 or fp32 (dtype), row stride ld; ids int32 and teacher
  *           fp32 [T, K], strides ld_ids, ld_teacher; teacher_lse, weights [T]
