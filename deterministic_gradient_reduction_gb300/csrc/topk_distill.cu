@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         bool live = false;
         if (weight != 0.0f) {
             // the list's entries in this CTA: where they lie, their bits. An
-            // entry whose bit is set already is a copy; which of the two does
-            // not matter, the other writes the sum of both.
+            // entry whose bit is set already is a copy, until behind the barrier
+            // the first one in the list is chosen.
             for (int k = tid; k < K; k += NT) {
                 const int id = ids[k];
                 int at = id >= 0 && id < p.V ? view.place(id) : -1;
@@ -328,6 +328,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             raw_t<T, 1> z_raw = 0;
             if (tid < K) load_if<false>(z_raw, z + max(ids[tid], 0), s_copy[tid] >= 0);
             __syncthreads();
+            // which of two threads set a bit first is chance, and the sum over
+            // the list's tokens would take one or the other: the first counts
+            if (s_twice == item + 1)
+                for (int k = tid; k < K; k += NT)
+                    if (s_copy[k] >= 0) {
+                        int at = s_copy[k] & ~kCopy;
+                        for (int j = 0; j < k; ++j)
+                            if (ids[j] == ids[k]) at |= kCopy;
+                        s_copy[k] = at;
+                    }
             fetch_list(item + n_clusters, n + 1, weight_next);
             if (w == W - 1) {  // the list's sums (read behind the cluster barrier)
                 float top = -INFINITY, sum = 0.0f;

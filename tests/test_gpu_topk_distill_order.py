@@ -1,9 +1,11 @@
-"""The order of the distillation's sums: with a gradient and without."""
+"""The order of the distillation's sums: with a gradient and without, and from run to run where ids come
+twice."""
 import pytest
 import torch
 
 import deterministic_gradient_reduction_gb300 as dgr
-from test_gpu_topk_distill import DT
+from gpu_util import bits
+from test_gpu_topk_distill import DT, _call
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,14 @@ def test_longer_rows_keep_their_bits_in_either_form(T, V, dtype, tail):
     reach = 1.4427 * max(2 * float(z.abs().max()), 2 * float(top), 0.0 if t["lse"] is None else float(t["lse"].max())) + 32
     size = torch.log_softmax(z, 1).abs().amax(1) + 2 * top + 16
     assert ((a[1] - b[1]).abs() <= 2 * (64 + 8 * reach) * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("V", [3000, 20000])
+@pytest.mark.parametrize("tail", [False, True])
+def test_ids_that_come_twice_give_the_same_bits_every_time(V, tail):
+    t = rows_of(600, V, 512, "fp32", tail)
+    t["ids"][:, 256:] = t["ids"][:, :256].flip(1)  # the copies lie in other warps
+    t["z"] *= 3.0
+    base = bits(_call(t))
+    for _ in range(20):
+        assert (bits(_call(t)) == base).all()
