@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
     __shared__ float s_loss[2][kMaxCluster * W];   // likewise their parts of a row's loss
     __shared__ float3 s_list;                      // ln of the list's normaliser in two parts (one sum of them
                                                    // would be rounded at its own size), sum of its q
+    __shared__ float s_base;                       // subtracted from the logits at the list's entries before scaling
     __shared__ int s_any, last;
     __shared__ uint32_t s_twice;                   // the row (item + 1) in whose list an id came twice
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -302,13 +303,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         copy_wait();  // each thread's own part of the list
         const float weight_2 = weight_of(item + 2 * n_clusters);
         float a = 0.0f, c_rest = 0.0f, f = 0.0f, c_all = 0.0f, inv_mass = 0.0f, total = 1.0f;
-        float shift = 0.0f, base_z = 0.0f;  // subtracted before scaling: outside the list, at its entries
-        float tail = 0.0f;                  // q_r (ln q_r - ln p_r)
+        float shift = 0.0f;                // subtracted before scaling outside the list
+        float rest_s = 0.0f, left = 0.0f;  // sum outside the list, q left for it
         bool live = false;
         if (weight != 0.0f) {
             // the list's entries in this CTA: where they lie, their bits. An
-            // entry whose bit is set already is a copy, until behind the barrier
-            // the first one in the list is chosen.
+            // entry whose bit is set already is a copy (without a tail it does not
+            // matter which of the two: the other writes the sum of both).
             for (int k = tid; k < K; k += NT) {
                 const int id = ids[k];
                 int at = id >= 0 && id < p.V ? view.place(id) : -1;
@@ -328,16 +329,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             raw_t<T, 1> z_raw = 0;
             if (tid < K) load_if<false>(z_raw, z + max(ids[tid], 0), s_copy[tid] >= 0);
             __syncthreads();
-            // which of two threads set a bit first is chance, and the sum over
-            // the list's tokens would take one or the other: the first counts
-            if (s_twice == item + 1)
-                for (int k = tid; k < K; k += NT)
-                    if (s_copy[k] >= 0) {
-                        int at = s_copy[k] & ~kCopy;
-                        for (int j = 0; j < k; ++j)
-                            if (ids[j] == ids[k]) at |= kCopy;
-                        s_copy[k] = at;
-                    }
             fetch_list(item + n_clusters, n + 1, weight_next);
             if (w == W - 1) {  // the list's sums (read behind the cluster barrier)
                 float top = -INFINITY, sum = 0.0f;
@@ -432,6 +423,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     s_z[tid] = one[0];
                 }
                 if (TAIL && w < list_warps) {  // the list's tokens in this CTA, each once
+                    // which of two threads set a bit first is chance, and the sum would
+                    // take the entry of one or the other: the first in the list counts
+                    if (s_twice == item + 1)
+                        for (int k = tid; k < K; k += NT)
+                            if (s_copy[k] >= 0) {
+                                int at = s_copy[k] & ~kCopy;
+                                for (int j = 0; j < k; ++j)
+                                    if (ids[j] == ids[k]) at |= kCopy;
+                                s_copy[k] = at;
+                            }
                     for (int k = tid; k < K; k += NT)
                         if (s_copy[k] >= 0 && !(s_copy[k] & kCopy)) in.m = fmaxf(in.m, __fadd_rn(s_z[k], -shift_in));
                     const float ci = scaled_max(in.m, p.k2);
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     continue;
                 }
                 // the two maxima's exponents below the row's own maximum
-                float gap = 0.0f, gap_in = 0.0f;
+                float gap = 0.0f, gap_in = 0.0f, base_z = 0.0f;
                 if (!again) {
                     c_all = TAIL ? scaled_max(fmaxf(rest.m, in.m), p.k2) : c_rest;
                     gap = __fadd_rn(c_rest, -c_all);
@@ -492,14 +493,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                 inv_mass = __fmul_rn(inv, !TAIL || q_rest > 0.0f ? 1.0f : sum_q);
                 f = __fmul_rn(__fmul_rn(__fmul_rn(p.scale, weight), p.inv_tau), p.dloss ? __ldg(p.dloss) : 1.0f);
                 a = __fmul_rn(TAIL ? __fadd_rn(__fmul_rn(down, inv_mass), q_rest > 0.0f ? -q_rest / rest.s : 0.0f) : inv, f);
-                if (TAIL && p.row_loss && rank == 0 && w == W - 1 && q_rest > 0.0f && live) {
-                    if (!again) {
-                        tail = __fmul_rn(q_rest, __fadd_rn(logf(q_rest), -__fadd_rn(__fmaf_rn(gap, kLn2, logf(rest.s)), -logf(total))));
-                    } else {  // times q_r before 1 / tau: the exponent alone may be out of range
-                        const float near = __fadd_rn(logf(q_rest), __fadd_rn(logf(total), -logf(rest.s)));
-                        tail = __fmaf_rn(__fmul_rn(q_rest, __fadd_rn(base_z, shift != 0.0f ? -shift : -rest.m)), p.inv_tau, __fmul_rn(q_rest, near));
-                    }
-                }
+                if (tid == 0) s_base = base_z;
+                rest_s = rest.s;
+                left = q_rest;
                 break;
             }
         } else {
@@ -579,13 +575,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
             if (p.row_loss && rank == 0 && w == W - 1) {
                 finish_loss();
                 loss_row = row;
-                loss_tail = tail;
+                loss_tail = 0.0f;
+                if (left > 0.0f && live) {
+                    loss_tail = __fmul_rn(left, __fadd_rn(logf(left), -__fadd_rn(__fmaf_rn(__fadd_rn(c_rest, -c_all), kLn2, logf(rest_s)), -logf(total))));
+                    // what was subtracted, times q_r before 1 / tau: the exponent alone may be out of range
+                    const float apart = __fadd_rn(s_base, -shift);
+                    if (apart != 0.0f) loss_tail = __fmaf_rn(__fmul_rn(left, apart), p.inv_tau, loss_tail);
+                }
             }
             // the list's entries: their part of the loss, their tokens' gradient
             if (w < list_warps) {
                 float part = 0.0f;
                 const float2 base = make_float2(s_list.x, s_list.y);
-                const float ln_total = logf(total);
+                const float ln_total = logf(total), base_z = s_base;
                 for (int k = tid; k < K; k += NT) {
                     const int at = s_copy[k] & ~kCopy;
                     if (s_copy[k] < 0) continue;
