@@ -2,9 +2,11 @@
 
 Each translation unit in csrc/ is compiled by nvcc for sm_103a only, in
 parallel, then linked into deterministic_gradient_reduction_gb300/libdgr.so.
-Reductions are compiled with --fmad=false (no multiply-add contraction) and
-without fast-math, so every add and multiply is one IEEE binary32 rounding;
-denormals are kept (-ftz=false).
+Everything is compiled with --fmad=false (no multiply-add contraction) and
+without fast-math, so every add and multiply that the source writes is one IEEE
+binary32 rounding; denormals are kept (-ftz=false). The router balance loss, the
+block norms and the distillation write fused multiply-adds and approximate
+exponentials out where they mean them.
 """
 from __future__ import annotations
 

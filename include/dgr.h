@@ -8,6 +8,8 @@
  * ascending tile order, and the result either written or added to the output
  * with one IEEE binary32 rounding. Results are therefore bitwise identical
  * from run to run, whatever the launch order, grid size or concurrent streams.
+ * The operators around an expert block (sections 9-11) have fixed orders of
+ * their own, given there, and the same reproducibility.
  *
  * Conventions for every entry point:
  *   - Pointers are DEVICE pointers unless stated otherwise; the caller owns
@@ -32,8 +34,13 @@
  *     workspace's status word, read with dgr_read_device_status(). After such
  *     an error the outputs of that call are unspecified and the workspace must
  *     be zeroed again before reuse.
- *   - Floating point: binary32 round-to-nearest-even, subnormals kept, no
- *     fused multiply-add anywhere in a reduction.
+ *   - Floating point, sections 1-8: binary32 round-to-nearest-even, subnormals
+ *     kept, no fused multiply-add anywhere in a reduction. Sections 9-11: sums
+ *     and statistics in binary32 with fused multiply-adds; exponentials to base
+ *     2, their quotients and reciprocal roots by the GPU's approximations of
+ *     them, a few units in the last place, with subnormal exponentials taken
+ *     as 0. Their results are held to bounds against 64 bits, not to one
+ *     sequence of roundings.
  *   - Only devices of compute capability 10.3 (sm_103a, GB300) are supported;
  *     on others every launching entry returns DGR_ERR_UNSUPPORTED.
  */
@@ -66,8 +73,9 @@ const char *dgr_status_string(dgr_status s);
 
 /* Library ABI version (major * 100 + minor). 1.01 added sections 5-8 (grouped
  * dbias, canonical top-K, aux-loss scalar, dsReLU dprob); 1.02 added
- * dgr_query_device_status; 1.03 added dgr_colsum_noalloc_read_status;
- * earlier entries unchanged. */
+ * dgr_query_device_status; 1.03 added dgr_colsum_noalloc_read_status; 1.04
+ * added sections 9-11 (router balance loss, block norms, distillation); earlier
+ * entries unchanged. */
 int32_t dgr_version(void);
 
 /* DGR_OK when `device` is a compute capability 10.3 GPU, else DGR_ERR_UNSUPPORTED. */
