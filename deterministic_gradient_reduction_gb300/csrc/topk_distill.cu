@@ -273,6 +273,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
         }
         copy_commit();
     };
+    // ln of an entry's q. The list's own maximum is subtracted before 1 / tau, as
+    // it may be out of range after it; the logsumexp is given at temperature tau.
+    auto log_q = [&](float t, float2 base) {
+        return __fadd_rn(TAIL ? __fadd_rn(__fmul_rn(t, p.inv_tau), -base.x) : __fmul_rn(__fadd_rn(t, -base.x), p.inv_tau), -base.y);
+    };
     const int list_warps = min(W, (K + 31) / 32);  // warps that hold entries
     int64_t loss_row = -1;      // CTA 0, last warp: a row whose loss waits for the other CTAs' parts
     float loss_tail = 0.0f;
@@ -338,16 +343,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     const int id = ids[k];
                     bad |= id >= p.V;
                     if (id < 0 || id >= p.V) continue;
-                    const float t = __fmul_rn(teacher[k], p.inv_tau);
-                    any |= TAIL || !(t == -INFINITY);
-                    if (TAIL) sum = __fadd_rn(sum, expf(__fadd_rn(t, -lse_t)));
-                    else top = fmaxf(top, t);
+                    any |= TAIL || !(teacher[k] == -INFINITY);
+                    if (TAIL) sum = __fadd_rn(sum, expf(__fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -lse_t)));
+                    else top = fmaxf(top, teacher[k]);
                 }
                 if (!TAIL) {
                     top = warp_max(top);
                     if (!(top > -INFINITY)) top = 0.0f;
                     for (int k = lane; k < K; k += 32)
-                        if (ids[k] >= 0 && ids[k] < p.V) sum = __fadd_rn(sum, expf(__fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -top)));
+                        if (ids[k] >= 0 && ids[k] < p.V) sum = __fadd_rn(sum, expf(__fmul_rn(__fadd_rn(teacher[k], -top), p.inv_tau)));
                 }
                 sum = warp_sum(sum);
                 any = __any_sync(0xffffffffu, any);
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     if (s_copy[k] < 0) continue;
                     if (at < View::kSingle) s_bits[at / VEC / NT / U * NT + at / VEC % NT] = 0;  // free again
                     if (!live) continue;
-                    const float lq = __fadd_rn(__fadd_rn(__fmul_rn(teacher[k], p.inv_tau), -base.x), -base.y);
+                    const float lq = log_q(teacher[k], base);
                     float q = expf(lq);
                     const float below = __fadd_rn(s_z[k], -base_z);
                     const float x = __fmaf_rn(below, p.k2, -c_all);  // log2 of p times the total
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows(const DistillParam
                     if (s_twice == item + 1) {
                         q = 0.0f;
                         for (int j = 0; j < K; ++j)
-                            if (ids[j] == id) q = __fadd_rn(q, expf(__fadd_rn(__fadd_rn(__fmul_rn(teacher[j], p.inv_tau), -base.x), -base.y)));
+                            if (ids[j] == id) q = __fadd_rn(q, expf(log_q(teacher[j], base)));
                     }
                     const float g = __fmul_rn(__fmaf_rn(ex2(x), inv_mass, -q), f);
                     *reinterpret_cast<raw_t<T, 1> *>(dz + id) = pack<T, 1>(&g);

@@ -150,3 +150,27 @@ def test_a_loss_in_range_of_rows_whose_sum_is_not(scale):
     t["scale"] = scale
     _, rows, _ = check(t)
     assert bool((rows > 1.0e38).all())
+
+
+@pytest.mark.parametrize("value", ["lowest", -3.0e38, -1.0e30, 1.0e6, 3.0e38])
+@pytest.mark.parametrize("tau", [0.3, 1.0, 1.7])
+def test_teachers_far_from_zero(tau, value):
+    """Without the teacher's logsumexp its list counts by distances from its own maximum alone."""
+    t = make(4, 900, 8, "fp32", tau=tau, weights=False)
+    t["ids"][:] = torch.arange(8, dtype=torch.int32, device="cuda") * 7
+    near = t["t"].clone()
+    t["t"][0] = masks(value, "fp32")
+    t["t"][1, 3:] = masks(value, "fp32")
+    t["t"][2] = 1.0e6 + torch.round(near[2])
+    z, ids, teacher = ref.d(t["z"]), t["ids"].cpu(), ref.d(t["t"])
+    teacher = teacher - teacher.amax(1, keepdim=True)  # 64 bits do not resolve a logsumexp's ln K beyond 1e16 either
+    loss, rows, grad = ref.distill(z, ids, teacher, tau, None, None, t["scale"])
+    dz = torch.empty_like(t["z"])
+    got, got_rows = dgr.topk_distill(t["z"], t["ids"], t["t"], tau=tau, scale=t["scale"], dlogits=dz)
+    # operator_ref.distill_bounds, with a teacher's distances (up to 200) in the place of its values
+    apart = -teacher / tau
+    apart = torch.where(apart < 200, apart, torch.zeros_like(apart))
+    rel, bound = ref.distill_bounds(z, ids, -apart * tau, tau, None, None, t["scale"], t["z"].dtype, grad)
+    size = torch.log_softmax(z / tau, 1).abs().amax(1) + 2 * apart.amax(1) + 16
+    assert ((ref.d(got_rows) - rows).abs() <= rel * size).all(), (got_rows, rows)
+    assert ((ref.d(dz) - grad).abs() <= bound + 1e-38).all()
