@@ -39,7 +39,7 @@
 // and, for rows of more than 128 KB, whether there is a gradient; the rows'
 // losses over one CTA in a fixed order.
 //
-// Measured: 4096 x 131072 bf16, loss and gradient (2.15 GB) 449 us = 4.79 TB/s;
+// Measured: 4096 x 131072 bf16, loss and gradient (2.15 GB) 452 us = 4.75 TB/s;
 // what a CTA does once a row (list, exchange, factors) takes about half of a
 // row's time and is hidden in part by the SM's other CTAs.
 #include <type_traits>
