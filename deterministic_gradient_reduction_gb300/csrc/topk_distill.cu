@@ -707,7 +707,7 @@ dgr_status launch_size(DistillParams &p, int sms, cudaStream_t s) {
     // that the CTAs of the device hold no more than about 80 MB at a time and
     // the second reading finds most of it in L2: 1021 x 50001 bf16 (100 KB) 53
     // us with 1, 58 with 2. Longer rows have CTAs of 512 threads (4096 x 131072
-    // bf16, 2 CTAs a row: 449 us with 512, 461 with 256), others of 256 (2048 x
+    // bf16, 2 CTAs a row: 464 us with 512, 486 with 256), others of 256 (2048 x
     // 32768 fp32 forward 56 us with 256, 66 with 512). A loss alone reads its rows
     // once and is better off with one CTA of 256 however long they are, though a
     // loss has other bits then than with its gradient: 4096 x 131072 bf16 199 us
