@@ -709,7 +709,8 @@ dgr_status launch_size(DistillParams &p, int sms, cudaStream_t s) {
     // us with 1, 58 with 2. Longer rows have CTAs of 512 threads (4096 x 131072
     // bf16, 2 CTAs a row: 464 us with 512, 486 with 256), others of 256 (2048 x
     // 32768 fp32 forward 56 us with 256, 66 with 512). A loss alone reads its rows
-    // once and is better off with one CTA of 256 however long they are, though a
+    // once and does best with one CTA of 256 up to 256 KB (at 640 KB 117 us, 109
+    // with one of 512: 800 x 160000 fp32), though a
     // loss has other bits then than with its gradient: 4096 x 131072 bf16 199 us
     // so, 218 with one of 512, 283 as with the gradient; the gradient takes 498,
     // 476 and 464.
