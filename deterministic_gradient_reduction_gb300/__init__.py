@@ -25,7 +25,9 @@ __all__ = [
     "ordered_colsum_noalloc", "colsum_noalloc_read_status",
     "router_balance", "router_balance_backward", "router_balance_workspace_bytes", "block_norm",
     "block_norm_backward", "block_norm_workspace_bytes", "topk_distill", "topk_distill_backward",
-    "topk_distill_workspace_bytes",
+    "topk_distill_workspace_bytes", "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_bytes", "qk_norm_rope",
+    "qk_norm_rope_backward", "qk_norm_rope_workspace_bytes", "token_logprobs", "token_logprobs_backward",
+    "token_logprobs_workspace_bytes",
 ]
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
@@ -84,6 +86,19 @@ def lib() -> ctypes.CDLL:
             "dgr_topk_distill_workspace_bytes": ([I64], SZ),
             "dgr_topk_distill": ([P, I32, I64, I64, I64, P, I64, P, I64, I32, F32, P, P, F32, P, P, P, P, I64, P, SZ,
                                   P], I32),
+            "dgr_gated_ffn_workspace_bytes": ([I64, I64, I64, I32], SZ),
+            "dgr_gated_ffn": ([P, I64, P, P, P, I32, I64, I64, I64, I32, P, I64, P, I64, P, I64, P, SZ, P], I32),
+            "dgr_gated_ffn_backward": ([P, I64, P, I64, P, I64, P, P, P, I32, I64, I64, I64, I32, P, I64, P, I64, P,
+                                        I64, P, SZ, P], I32),
+            "dgr_qk_norm_rope_workspace_bytes": ([I64, I32, I32, I32], SZ),
+            "dgr_qk_norm_rope": ([P, I64, I64, I32, P, I64, I64, I32, I32, I64, I32, P, P, I32, P, P, I32, I32, I32, P,
+                                  F32, P, I64, I64, P, I64, I64, P, SZ, P], I32),
+            "dgr_qk_norm_rope_backward": ([P, I64, I64, P, I64, I64, P, I64, I64, I32, P, I64, I64, I32, I32, I64, I32,
+                                           P, P, I32, P, P, I32, I32, I32, P, F32, P, I64, I64, P, I64, I64, P, P, I32,
+                                           P, SZ, P], I32),
+            "dgr_token_logprobs_workspace_bytes": ([I64], SZ),
+            "dgr_token_logprobs": ([P, I32, I64, I64, I64, P, F32, I32, P, P, P, P, P, P, P, P, SZ, P], I32),
+            "dgr_token_logprobs_backward": ([P, I32, I64, I64, I64, P, F32, P, P, P, P, P, I64, P], I32),
             "dgr_diag_wait_timeout": ([I32, I32, P, SZ, P], I32),
             "dgr_diag_wgrad_stall": ([P, P, P, I32, I64, I64, I64, P, P, SZ, I32, I32, I32, P], I32),
             "dgr_diag_packed_ops": ([P, P, I64, P, P, P], I32),
@@ -574,4 +589,246 @@ def topk_distill_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torc
         with _on(stream):
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     _distill(logits, ids, teacher, tau, teacher_lse, weights, scale, dloss, None, None, dlogits, ws, stream)
+    return dlogits
+
+
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def gated_ffn_workspace_bytes(T: int, H: int, F: int, E: int = 1) -> int:
+    return int(lib().dgr_gated_ffn_workspace_bytes(T, H, F, E))
+
+
+def _experts(w_gate, w_up, offs, act):
+    """(E, F, H, offs' address): weights [E, F, H], or [F, H] of a single expert."""
+    if w_gate.dim() not in (2, 3) or w_gate.shape != w_up.shape or act not in _ACTS:
+        raise ValueError("w_gate and w_up [E, F, H] and act 'silu' or 'gelu' expected")
+    if w_gate.dtype != torch.bfloat16 or w_up.dtype != torch.bfloat16:
+        raise TypeError("bf16 weights expected")
+    if not (w_gate.is_contiguous() and w_up.is_contiguous()):
+        raise ValueError("w_gate and w_up must be contiguous")
+    E = 1 if w_gate.dim() == 2 else w_gate.shape[0]
+    if offs is None and E != 1:
+        raise ValueError("offs int64 [E+1] expected for more than one expert")
+    return E, w_gate.shape[-2], w_gate.shape[-1], _vec(offs, E + 1, torch.int64, "offs")
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, offs: torch.Tensor | None = None,
+              act: str = "silu", h: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+              up: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h = act(x w_gate[e]^T) * (x w_up[e]^T) for the rows offs[e] .. offs[e+1]-1 of each expert e.
+
+    x bf16 [T, H]; w_gate and w_up bf16 [E, F, H] (or [F, H] without offs); offs int64 device [E+1].
+    gate and up, where given ([T, F]), receive the two products, which gated_ffn_backward takes."""
+    E, F, H, po = _experts(w_gate, w_up, offs, act)
+    T, bf = x.shape[0], torch.bfloat16
+    ld_x = _rows(x, (T, H), bf, "x")
+    if h is None:
+        with _on(stream):
+            h = torch.empty(T, F, dtype=bf, device=x.device)
+    if ws is None:
+        ws = workspace(gated_ffn_workspace_bytes(T, H, F, E), x.device, stream)
+    ld = lambda t, name: _rows(t, (T, F), bf, name) if t is not None else 0  # noqa: E731
+    _check("dgr_gated_ffn", lib().dgr_gated_ffn(
+        x.data_ptr(), ld_x, w_gate.data_ptr(), w_up.data_ptr(), po, E, T, H, F, _ACTS[act], h.data_ptr(), ld(h, "h"),
+        _ptr(gate), ld(gate, "gate"), _ptr(up), ld(up, "up"), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return h
+
+
+def gated_ffn_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       *, offs: torch.Tensor | None = None, act: str = "silu", dx: torch.Tensor | None = None,
+                       dgate: torch.Tensor | None = None, dup: torch.Tensor | None = None, x: torch.Tensor | None = None,
+                       dw_gate: torch.Tensor | None = None, dw_up: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of gated_ffn from that of h and the products gate and up that it stored: a dict of
+    dx, dgate and dup (gradients of the products; dgate may be gate, dup may be up).
+
+    Given x and dw_gate, dw_up (fp32 [E, F, H]; without offs [F, H]), the weights' gradients are added to them by
+    grouped_wgrad_accumulate(dgate or dup, x): its limits hold then (F a multiple of 128, H of 256; contiguous rows)."""
+    E, F, H, po = _experts(w_gate, w_up, offs, act)
+    T, bf = dh.shape[0], torch.bfloat16
+    grads = [(d, w) for d, w in ((dw_gate, "dw_gate"), (dw_up, "dw_up")) if d is not None]
+    if grads and x is None:
+        raise ValueError("x [T, H] expected for the weights' gradients")
+    for d, name in grads:
+        _vec(d, E * F * H, torch.float32, name)
+    ld = lambda t, name: _rows(t, (T, F), bf, name)  # noqa: E731
+    lds = ld(dh, "dh"), ld(gate, "gate"), ld(up, "up")
+    if grads and (_rows(x, (T, H), bf, "x") != H or any(d is not None and ld(d, n) != F for d, n in ((dgate, "dgate"), (dup, "dup")))):
+        raise ValueError("x, dgate and dup must be contiguous for the weights' gradients")
+    if grads and (F % 128 or H % 256):
+        raise ValueError("F a multiple of 128 and H of 256 expected for the weights' gradients")
+    with _on(stream):
+        dx = torch.empty(T, H, dtype=bf, device=dh.device) if dx is None else dx
+        dgate = torch.empty(T, F, dtype=bf, device=dh.device) if dgate is None else dgate
+        dup = torch.empty(T, F, dtype=bf, device=dh.device) if dup is None else dup
+        if grads and offs is None:
+            offs = torch.arange(2, device=dh.device) * T
+    if ws is None:
+        ws = workspace(gated_ffn_workspace_bytes(T, H, F, E), dh.device, stream)
+    _check("dgr_gated_ffn_backward", lib().dgr_gated_ffn_backward(
+        dh.data_ptr(), lds[0], gate.data_ptr(), lds[1], up.data_ptr(), lds[2], w_gate.data_ptr(), w_up.data_ptr(), po, E,
+        T, H, F, _ACTS[act], dgate.data_ptr(), ld(dgate, "dgate"), dup.data_ptr(), ld(dup, "dup"), dx.data_ptr(),
+        _rows(dx, (T, H), bf, "dx"), ws.data_ptr(), ws.numel(), _stream(stream)))
+    if dw_gate is not None:
+        grouped_wgrad_accumulate(dgate, x, offs, dw_gate, ws=ws, stream=stream)
+    if dw_up is not None:
+        grouped_wgrad_accumulate(dup, x, offs, dw_up, ws=ws, stream=stream)
+    return {"dx": dx, "dgate": dgate, "dup": dup}
+
+
+def qk_norm_rope_workspace_bytes(T: int, n_q: int, n_k: int, D: int) -> int:
+    return int(lib().dgr_qk_norm_rope_workspace_bytes(T, n_q, n_k, D))
+
+
+def _heads(t: torch.Tensor | None, shape, dtype, name: str):
+    """(address, token stride, head stride) of a [T, heads, D] tensor with contiguous heads."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2], shape[2]
+    if t.stride(2) != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: contiguous heads expected")
+    # the stride of a single token or head says nothing
+    head = t.stride(1) if shape[1] > 1 else shape[2]
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else head * shape[1], head
+
+
+def _qk_args(q, k, cos, sin, positions, w_q, w_k):
+    """Sizes, types and addresses that both directions share."""
+    some = q if q is not None else k
+    if some is None or any(t is not None and t.dim() != 3 for t in (q, k)) or cos.dim() != 2:
+        raise ValueError("q [T, heads, D] or k [T, heads, D] and cos [P, R/2] expected")
+    T, _, D = some.shape
+    shapes = [None if t is None else (T, t.shape[1], D) for t in (q, k)]
+    weights = [w for w in (w_q, w_k) if w is not None]
+    wdt = weights[0].dtype if weights else torch.float32
+    P, R = cos.shape[0], 2 * cos.shape[1]
+    f32 = torch.float32
+    return T, D, some, shapes, (_vec(w_q, D, wdt, "w_q"), _vec(w_k, D, wdt, "w_k"), _dtype(weights[0]) if weights else DTYPE_F32,
+                                _vec(cos, P * (R // 2), f32, "cos"), _vec(sin, P * (R // 2), f32, "sin"), P, R), \
+        _vec(positions, T, torch.int32, "positions")
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, cos: torch.Tensor, sin: torch.Tensor,
+                 positions: torch.Tensor, *, w_q: torch.Tensor | None = None, w_k: torch.Tensor | None = None,
+                 eps: float = 1e-6, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Queries and keys normed a head (weights w_q, w_k [D]) and turned by their positions: (q_out, k_out).
+
+    q bf16/fp32 [T, heads, D] and k [T, kv heads, D] (either may be None), with any token and head
+    strides; cos and sin fp32 [P, R/2] for the first R elements of a head; positions int32 [T].
+    Pairs are (m, m + R/2), or (2m, 2m + 1) when interleaved. q_out may be q, k_out may be k."""
+    T, D, some, (sq, sk), same, pos = _qk_args(q, k, cos, sin, positions, w_q, w_k)
+    dt = some.dtype
+    if (q is not None and q_out is None) or (k is not None and k_out is None):
+        with _on(stream):
+            q_out = torch.empty(sq, dtype=dt, device=some.device) if q is not None and q_out is None else q_out
+            k_out = torch.empty(sk, dtype=dt, device=some.device) if k is not None and k_out is None else k_out
+    if ws is None:
+        ws = workspace(256, some.device, stream)
+    _check("dgr_qk_norm_rope", lib().dgr_qk_norm_rope(
+        *_heads(q, sq, dt, "q"), sq[1] if sq else 0, *_heads(k, sk, dt, "k"), sk[1] if sk else 0, _dtype(some), T, D, *same,
+        int(interleaved), pos, eps, *_heads(q_out, sq, dt, "q_out"), *_heads(k_out, sk, dt, "k_out"), ws.data_ptr(),
+        ws.numel(), _stream(stream)))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None, q: torch.Tensor | None,
+                          k: torch.Tensor | None, cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor, *,
+                          w_q: torch.Tensor | None = None, w_k: torch.Tensor | None = None, eps: float = 1e-6,
+                          interleaved: bool = False, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                          dw_q: torch.Tensor | None = None, dw_k: torch.Tensor | None = None, accumulate: bool = False,
+                          ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of qk_norm_rope from those of its outputs and its inputs: a dict of dq, dk (of q's
+    type; dq may be dq_out, dk may be dk_out) and, for the weights given, fp32 dw_q, dw_k [D];
+    accumulate adds these to what dw_q and dw_k hold."""
+    T, D, some, (sq, sk), same, pos = _qk_args(q, k, cos, sin, positions, w_q, w_k)
+    dt, dev = some.dtype, some.device
+    if (q is None) != (dq_out is None) or (k is None) != (dk_out is None):
+        raise ValueError("dq_out goes with q and dk_out with k")
+    if accumulate and any(w is not None and d is None for w, d in ((w_q, dw_q), (w_k, dw_k))):
+        raise ValueError("accumulate needs dw_q and dw_k to add to")
+    with _on(stream):
+        dq = torch.empty(sq, dtype=dt, device=dev) if q is not None and dq is None else dq
+        dk = torch.empty(sk, dtype=dt, device=dev) if k is not None and dk is None else dk
+        f32 = dict(dtype=torch.float32, device=dev)
+        dw_q = torch.empty(D, **f32) if w_q is not None and q is not None and dw_q is None else dw_q
+        dw_k = torch.empty(D, **f32) if w_k is not None and k is not None and dw_k is None else dw_k
+    n_q, n_k = sq[1] if sq else 0, sk[1] if sk else 0
+    if ws is None:
+        ws = workspace(qk_norm_rope_workspace_bytes(T, n_q, n_k, D), dev, stream)
+    _check("dgr_qk_norm_rope_backward", lib().dgr_qk_norm_rope_backward(
+        *_heads(dq_out, sq, dt, "dq_out"), *_heads(dk_out, sk, dt, "dk_out"), *_heads(q, sq, dt, "q"), n_q,
+        *_heads(k, sk, dt, "k"), n_k, _dtype(some), T, D, *same, int(interleaved), pos, eps, *_heads(dq, sq, dt, "dq"),
+        *_heads(dk, sk, dt, "dk"), _vec(dw_q, D, torch.float32, "dw_q"), _vec(dw_k, D, torch.float32, "dw_k"),
+        int(accumulate), ws.data_ptr(), ws.numel(), _stream(stream)))
+    out = {"dq": dq, "dk": dk, "dw_q": dw_q, "dw_k": dw_k}
+    return {n: v for n, v in out.items() if v is not None}
+
+
+def token_logprobs_workspace_bytes(T: int) -> int:
+    return int(lib().dgr_token_logprobs_workspace_bytes(T))
+
+
+def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, *, tau: float = 1.0, top: int = 0,
+                   logp: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, stats: torch.Tensor | None = None,
+                   top_ids: torch.Tensor | None = None, top_logits: torch.Tensor | None = None,
+                   top_logp: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Log probabilities at temperature tau of the tokens ids (int32 [T]; None: no logp): a dict of logp,
+    entropy, lse (logsumexp of logits / tau), all fp32 [T], stats (fp32 [T, 2], for the gradient) and,
+    with top > 0, the top alternatives: top_ids int32, top_logits and top_logp fp32 [T, top].
+
+    logits bf16/fp32 [T, V]. A row whose id is negative is left out: zeros, an empty list (ids -1).
+    top_ids, top_logits and lse are the ids, teacher and teacher_lse of topk_distill."""
+    if logits.dim() != 2 or top < 0:
+        raise ValueError("logits [T, V] and top >= 0 expected")
+    T, V = logits.shape
+    f32, dev = torch.float32, logits.device
+    ld, pi = _rows(logits, (T, V), logits.dtype, "logits"), _vec(ids, T, torch.int32, "ids")
+    if (ids is not None and logp is None) or entropy is None or lse is None or stats is None or \
+            (top and (top_ids is None or top_logits is None or top_logp is None)):
+        with _on(stream):
+            new = lambda *s: torch.empty(*s, dtype=f32, device=dev)  # noqa: E731
+            logp = new(T) if ids is not None and logp is None else logp
+            entropy = new(T) if entropy is None else entropy
+            lse = new(T) if lse is None else lse
+            stats = new(T, 2) if stats is None else stats
+            if top:
+                top_ids = torch.empty(T, top, dtype=torch.int32, device=dev) if top_ids is None else top_ids
+                top_logits = new(T, top) if top_logits is None else top_logits
+                top_logp = new(T, top) if top_logp is None else top_logp
+    if ws is None:
+        ws = workspace(256, dev, stream)
+    _check("dgr_token_logprobs", lib().dgr_token_logprobs(
+        logits.data_ptr(), _dtype(logits), T, V, ld, pi, tau, top, _vec(logp, T, f32, "logp"),
+        _vec(entropy, T, f32, "entropy"), _vec(lse, T, f32, "lse"), _vec(stats, 2 * T, f32, "stats"),
+        _vec(top_ids, T * top, torch.int32, "top_ids"), _vec(top_logits, T * top, f32, "top_logits"),
+        _vec(top_logp, T * top, f32, "top_logp"), ws.data_ptr(), ws.numel(), _stream(stream)))
+    out = {"logp": logp, "entropy": entropy, "lse": lse, "stats": stats, "top_ids": top_ids, "top_logits": top_logits,
+           "top_logp": top_logp}
+    return {n: v for n, v in out.items() if v is not None}
+
+
+def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, stats: torch.Tensor,
+                            entropy: torch.Tensor | None = None, *, dlogp: torch.Tensor | None = None,
+                            dentropy: torch.Tensor | None = None, tau: float = 1.0, dlogits: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """Gradient to the logits from those of logp and entropy (fp32 [T] each, None: 0), with the stats and
+    the entropy that token_logprobs gave; dlogits may be logits itself."""
+    if logits.dim() != 2:
+        raise ValueError("logits [T, V] expected")
+    T, V = logits.shape
+    if dlogits is None:
+        with _on(stream):
+            dlogits = torch.empty(T, V, dtype=logits.dtype, device=logits.device)
+    f32 = torch.float32
+    _check("dgr_token_logprobs_backward", lib().dgr_token_logprobs_backward(
+        logits.data_ptr(), _dtype(logits), T, V, _rows(logits, (T, V), logits.dtype, "logits"),
+        _vec(ids, T, torch.int32, "ids"), tau, _vec(stats, 2 * T, f32, "stats"), _vec(entropy, T, f32, "entropy"),
+        _vec(dlogp, T, f32, "dlogp"), _vec(dentropy, T, f32, "dentropy"), dlogits.data_ptr(),
+        _rows(dlogits, (T, V), logits.dtype, "dlogits"), _stream(stream)))
     return dlogits

@@ -5,8 +5,9 @@ parallel, then linked into deterministic_gradient_reduction_gb300/libdgr.so.
 Everything is compiled with --fmad=false (no multiply-add contraction) and
 without fast-math, so every add and multiply that the source writes is one IEEE
 binary32 rounding; denormals are kept (-ftz=false). The router balance loss, the
-block norms and the distillation write fused multiply-adds and approximate
-exponentials out where they mean them.
+block norms, the distillation, the gated feed-forward, the norm and rotation of
+queries and keys and the token log probabilities write fused multiply-adds and
+approximate exponentials out where they mean them.
 """
 from __future__ import annotations
 

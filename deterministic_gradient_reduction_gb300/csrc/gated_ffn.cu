@@ -1,0 +1,615 @@
+// Gated feed-forward of grouped experts, forward and backward.
+//
+// The rows d_offs[e] .. d_offs[e+1]-1 of x belong to expert e:
+//   a = x Wg_e^T,  b = x Wu_e^T,  h = act(a) b            (a, b in binary32, h rounded once);
+//   da = dh b act'(a),  db = dh act(a),  dx = da Wg_e + db Wu_e.
+// Both activations are v sigmoid(s(v)): silu with s(v) = v, the tanh form of
+// gelu with s(v) = 2 sqrt(2 / pi) (v + 0.044715 v^3), as (1 + tanh u) / 2 =
+// sigmoid(2 u); written so, nothing cancels for small v.
+//
+// Forward, one launch: a persistent kernel, one CTA per SM, 12 warps. A tile is
+// 128 rows of one expert (counted from its first row) by FT columns of h, done as
+// one product of N = 2 FT columns: the FT rows of Wg_e and the FT of Wu_e lie one
+// after another in shared memory, so a and b of an element end in the same lane
+// of TMEM, and the epilogue has both. Warp 0 loads 64-deep stages by TMA (x and
+// the weights K-major as they lie, 128-byte swizzle; what is past a matrix's end
+// comes as zeros), warp 1 issues tcgen05.mma into one of two accumulators, warps
+// 4-11 (lane quarter q, column half) read one while the other fills.
+// Backward, two launches: da and db element by element (memory bound), then dx
+// by the same kernel with the two parts of its sum, da Wg_e and db Wu_e, one
+// after another along K in one accumulator (weights N-major as they lie). The
+// gradients of the weights are dgr_grouped_wgrad_accumulate's.
+//
+// Rows of a tile past the expert's end are another expert's (or zeros): a row of
+// the product depends on its own row of x alone, and they are not written.
+// Deterministic: K in ascending order into one accumulator, one writer an element.
+// Every wait is bounded; a timeout aborts the CTA, which then waits (bounded
+// again) for its copies in flight and for its MMAs before it frees its TMEM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "row_common.cuh"
+#include "tc_common.cuh"
+
+namespace dgr {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;  // rows of a tile (TMEM lanes)
+constexpr int BK = 64;   // k per stage: one 128-byte row of a swizzle atom
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (4 + kEpiWarps) * 32;
+constexpr int kMaxExperts = 1024;
+constexpr uint32_t kStageA = BM * 128;
+constexpr uint32_t kRing = 192 * 1024;  // stages, beside 4 KB of offsets and the barriers
+constexpr uint32_t kSBO = 1024;         // between 8-row groups of an atom
+constexpr uint32_t kLboK = 16;          // K-major: one atom spans the K16 step
+constexpr uint32_t kLboN = 64 * 128;    // N-major: between 64-wide atoms along n
+
+enum { kSilu = 0, kGelu = 1 };
+
+template <int BN>
+struct Shape {
+    static constexpr uint32_t kStageB = BN * 128;
+    static constexpr uint32_t kStage = kStageA + kStageB;
+    static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
+    static constexpr uint32_t kTmemCols = 2 * BN;
+    // tcgen05 instruction descriptor: fp32 D, bf16 A and B, A K-major, B K-major or (bit 16) N-major
+    static __host__ __device__ constexpr uint32_t idesc(bool n_major) {
+        return (1u << 4) | (1u << 7) | (1u << 10) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN >> 3) << 17) |
+               (static_cast<uint32_t>(BM >> 4) << 24);
+    }
+};
+
+struct Ctl {
+    uint64_t full[8];
+    uint64_t empty[8];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int BN>
+constexpr size_t kSmem = 1024 + Shape<BN>::kStages * Shape<BN>::kStage + sizeof(Ctl);
+
+struct FfnParams {
+    const int64_t *offs;  // or null: one expert with all rows
+    int32_t E, T;
+    int32_t K;            // of one part (forward: H, backward: F)
+    int32_t N;            // columns of the output (forward: F, backward: H)
+    int32_t nbs;          // column blocks
+    int32_t act;
+    uint16_t *out, *gate, *up;  // forward: h and, or null, a and b; backward: dx
+    int64_t ld_out, ld_gate, ld_up;
+    WsHeader *hdr;
+    Sched sched;  // the setting; bound to the tile count on the device
+};
+
+// mb_base[e] = first row block of expert e (mb_base[E] = all row blocks), by the
+// whole block; false when the offsets break the contract.
+__device__ bool row_blocks(const FfnParams &p, int rows, int32_t *mb_base, int32_t *wsum, int32_t *bad) {
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nw = kThreads >> 5;
+    if (!p.offs) {
+        if (tid == 0) mb_base[0] = 0, mb_base[1] = (p.T + rows - 1) / rows;
+        __syncthreads();
+        return true;
+    }
+    if (tid == 0) *bad = 0;
+    __syncthreads();
+    int32_t run = 0;
+    for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+        const int e = e0 + tid;
+        int32_t c = 0;
+        if (e < p.E) {
+            const int64_t a = p.offs[e], b = p.offs[e + 1];
+            if (a < 0 || b < a || b > p.T || (e == 0 && a != 0) || (e == p.E - 1 && b != p.T)) *bad = 1;
+            else c = static_cast<int32_t>((b - a + rows - 1) / rows);
+        }
+        int32_t incl = c;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, incl, s);
+            if (lane >= s) incl += o;
+        }
+        if (lane == 31) wsum[w] = incl;
+        __syncthreads();
+        int32_t before = run;
+        for (int v = 0; v < w; ++v) before += wsum[v];
+        if (e < p.E) mb_base[e] = before + incl - c;
+        for (int v = 0; v < nw; ++v) run += wsum[v];
+        __syncthreads();
+    }
+    if (tid == 0) mb_base[p.E] = run;
+    __syncthreads();
+    return *bad == 0;
+}
+
+struct Tile {
+    int e, nb;
+    int32_t row, end;  // first row; the expert's end
+};
+
+// tile tau: row blocks expert by expert, the column blocks of one after another
+__device__ __forceinline__ Tile tile_of(const FfnParams &p, int rows, const int32_t *mb_base, uint32_t tau) {
+    const int32_t gmb = static_cast<int32_t>(tau / static_cast<uint32_t>(p.nbs));
+    Tile t;
+    t.nb = static_cast<int>(tau - static_cast<uint32_t>(gmb) * static_cast<uint32_t>(p.nbs));
+    int lo = 0, hi = p.E - 1;
+    while (lo < hi) {  // the last expert that starts at or before gmb (empty ones start where the next does)
+        const int mid = (lo + hi + 1) >> 1;
+        if (mb_base[mid] <= gmb) lo = mid;
+        else hi = mid - 1;
+    }
+    t.e = lo;
+    t.row = (p.offs ? static_cast<int32_t>(p.offs[lo]) : 0) + (gmb - mb_base[lo]) * rows;
+    t.end = p.offs ? static_cast<int32_t>(p.offs[lo + 1]) : p.T;
+    return t;
+}
+
+// sigmoid(s(v)): 1 / (1 + 2^(-s log2 e)); an exponential beyond the range gives 0.
+__device__ __forceinline__ float gate_sigmoid(float v, int act) {
+    float s = v;
+    if (act == kGelu) s = __fmul_rn(1.5957691216057308f, __fmaf_rn(__fmul_rn(0.044715f, __fmul_rn(v, v)), v, v));
+    return __fdividef(1.0f, __fadd_rn(1.0f, row::ex2(__fmul_rn(s, -row::kLog2e))));
+}
+
+// 16 bf16 values to columns c .. c + 15 of a row, those below n (a multiple of 8).
+__device__ __forceinline__ void store16(uint16_t *to, int c, int n, const float (&v)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = row::pack2(v[2 * i], v[2 * i + 1]);
+    to += c;
+    if (c + 16 <= n && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        if (c + 8 <= n) *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c + 16 <= n) *reinterpret_cast<uint4 *>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// The wait for a load, with its registers taken through (tmem_wait_ld says why).
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
+// FWD: a, b and h; else dx. Maps: A (and A2, the second part's), B and B2
+// (forward Wg and Wu, FT rows a box; backward the same, 64 x 64 atoms).
+template <int BN, bool FWD>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+             const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2, const FfnParams p) {
+    using S = Shape<BN>;
+    constexpr int kStages = S::kStages;
+    constexpr int kCols = FWD ? BN / 2 : BN;  // columns of the output a tile
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + kStages * S::kStage);
+    __shared__ int32_t mb_base[kMaxExperts + 1];
+    __shared__ int32_t wsum[kThreads / 32];
+    __shared__ int32_t bad;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    volatile int *abort_flag = &ctl->abort;
+
+    if (!row_blocks(p, BM, mb_base, wsum, &bad)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, 400);
+        return;
+    }
+    const uint32_t n_tiles = static_cast<uint32_t>(mb_base[p.E]) * static_cast<uint32_t>(p.nbs);
+    const Sched sched = sched_over(p.sched, n_tiles);
+    const int part_k = (p.K + BK - 1) / BK;  // stages of one part
+    const int n_k = FWD ? part_k : 2 * part_k;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->tfull[b], 1);
+            mbar_init(&ctl->tempty[b], kEpiWarps);
+        }
+        ctl->abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        prefetch_tmap(&tmB2);
+        if (!FWD) prefetch_tmap(&tmA2);
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, S::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool armed[kStages] = {};
+            uint32_t armed_phase[kStages] = {};
+            bool ok = true;
+            for (uint32_t tau = blockIdx.x; ok && tau < n_tiles; tau += gridDim.x) {
+                const Tile t = tile_of(p, BM, mb_base, sched_item(sched, tau));
+                for (int kb = 0; kb < n_k; ++kb) {
+                    if (!mbar_wait(&ctl->empty[stage], phase ^ 1, abort_flag, p.hdr, 401)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sA = smem + stage * S::kStage;
+                    uint8_t *sB = sA + kStageA;
+                    uint64_t *bar = &ctl->full[stage];
+                    mbar_arrive_expect_tx(bar, S::kStage);
+                    armed[stage] = true;
+                    armed_phase[stage] = phase;
+                    if (FWD) {
+                        tma_load_3d(sA, &tmA, bar, kb * BK, t.row, 0);
+                        tma_load_3d(sB, &tmB, bar, kb * BK, t.nb * kCols, t.e);
+                        tma_load_3d(sB + kCols * 128, &tmB2, bar, kb * BK, t.nb * kCols, t.e);
+                    } else {
+                        const bool second = kb >= part_k;
+                        const int k0 = (second ? kb - part_k : kb) * BK;
+                        tma_load_3d(sA, second ? &tmA2 : &tmA, bar, k0, t.row, 0);
+#pragma unroll
+                        for (int j = 0; j < BN / 64; ++j)
+                            tma_load_3d(sB + j * kLboN, second ? &tmB2 : &tmB, bar, t.nb * BN + 64 * j, k0, t.e);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {  // aborted: let our copies in flight land (bounded) before the CTA exits
+                int dummy = 0;
+                for (int s = 0; s < kStages; ++s)
+                    if (armed[s]) mbar_wait(&ctl->full[s], armed_phase[s], &dummy, nullptr, kWaitLimitNs);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        constexpr uint32_t kIdesc = S::idesc(!FWD);
+        uint32_t stage = 0, phase = 0, g = 0;
+        uint32_t last_stage = 0, last_phase = 0;  // the latest stage-release commit
+        bool committed = false, ok = true;
+        for (uint32_t tau = blockIdx.x; ok && tau < n_tiles; tau += gridDim.x, ++g) {
+            const uint32_t buf = g & 1, tph = (g >> 1) & 1;
+            if (!mbar_wait(&ctl->tempty[buf], tph ^ 1, abort_flag, p.hdr, 402)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem + buf * BN;
+            for (int kb = 0; kb < n_k; ++kb) {
+                if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.hdr, 403)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t a0 = smem_u32(smem + stage * S::kStage), b0 = a0 + kStageA;
+                    // the stage's four K16 steps back to back, descriptors ready
+                    uint64_t ad[4], bd[4];
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        ad[kk] = smem_desc_sw128(a0 + kk * 32, kLboK, kSBO);
+                        bd[kk] = FWD ? smem_desc_sw128(b0 + kk * 32, kLboK, kSBO) : smem_desc_sw128(b0 + kk * 2048, kLboN, kSBO);
+                    }
+                    mma_bf16(d_tmem, ad[0], bd[0], kIdesc, kb > 0 ? 1u : 0u);
+                    mma_bf16(d_tmem, ad[1], bd[1], kIdesc, 1u);
+                    mma_bf16(d_tmem, ad[2], bd[2], kIdesc, 1u);
+                    mma_bf16(d_tmem, ad[3], bd[3], kIdesc, 1u);
+                    mma_commit(&ctl->empty[stage]);
+                }
+                __syncwarp();
+                committed = true;
+                last_stage = stage;
+                last_phase = phase;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) mma_commit(&ctl->tfull[buf]);
+            __syncwarp();
+        }
+        if (!ok && committed) {
+            // aborted: wait (bounded) until the MMAs issued here are done, as
+            // their latest commit says, before the CTA frees its TMEM and exits
+            int dummy = 0;
+            mbar_wait(&ctl->empty[last_stage], last_phase, &dummy, nullptr, kWaitLimitNs);
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue ----------------
+        const int q = warp & 3;         // TMEM lane quarter this warp may access
+        const int half = (warp - 4) >> 2;
+        uint32_t g = 0;
+        for (uint32_t tau = blockIdx.x; tau < n_tiles; tau += gridDim.x, ++g) {
+            const Tile t = tile_of(p, BM, mb_base, sched_item(sched, tau));
+            const int32_t row = t.row + 32 * q + lane;
+            const bool mine = row < t.end;
+            const uint32_t buf = g & 1, tph = (g >> 1) & 1;
+            if (!mbar_wait(&ctl->tfull[buf], tph, abort_flag, p.hdr, 404)) break;
+            tc_fence_after();
+            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * BN;
+            const int c_tile = t.nb * kCols;
+#pragma unroll 1
+            for (int c = half * (kCols / 2); c < (half + 1) * (kCols / 2); c += 16) {
+                uint32_t ra[16], rb[16];
+                tmem_ld16(base + c, ra);
+                if (FWD) tmem_ld16(base + kCols + c, rb);
+                tmem_wait16(ra);
+                if (FWD) tmem_wait16(rb);
+                if (mine) {
+                    float a[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) a[i] = __uint_as_float(ra[i]);
+                    if constexpr (FWD) {
+                        float b[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) b[i] = __uint_as_float(rb[i]);
+                        if (p.gate) store16(p.gate + row * p.ld_gate, c_tile + c, p.N, a);
+                        if (p.up) store16(p.up + row * p.ld_up, c_tile + c, p.N, b);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) a[i] = __fmul_rn(__fmul_rn(a[i], gate_sigmoid(a[i], p.act)), b[i]);
+                    }
+                    store16(p.out + row * p.ld_out, c_tile + c, p.N, a);
+                }
+                __syncwarp();
+            }
+            // the accumulator is read: the MMA may refill it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tempty[buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+// ---- da and db ----------------------------------------------------------------
+
+struct PreParams {
+    const uint16_t *dh, *gate, *up;
+    uint16_t *dgate, *dup;
+    int64_t ld_dh, ld_gate, ld_up, ld_dgate, ld_dup;
+    int32_t T, vecs, act;  // 8-element vectors a row
+};
+
+// da = dh b act'(a), db = dh act(a); act'(v) = g + v g (1 - g) s'(v), g = sigmoid(s(v)).
+// g (1 - g) is 0 long before s'(v) leaves the range, so their product counts as 0 then.
+__device__ __forceinline__ void pre_grad(float dh, float a, float b, int act, float &da, float &db) {
+    const float g = gate_sigmoid(a, act);
+    const float down = __fmul_rn(g, __fadd_rn(1.0f, -g));
+    float turn = down;
+    if (act == kGelu) turn = down > 0.0f ? __fmul_rn(down, __fmul_rn(1.5957691216057308f, __fmaf_rn(__fmul_rn(0.134145f, a), a, 1.0f))) : down;
+    db = __fmul_rn(dh, __fmul_rn(a, g));
+    da = __fmul_rn(__fmul_rn(dh, b), __fmaf_rn(a, turn, g));
+}
+
+__global__ void __launch_bounds__(256) ffn_pre_grad(const PreParams p) {
+    const int64_t n = static_cast<int64_t>(p.T) * p.vecs;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t t = i / p.vecs;
+        const int c = static_cast<int>(i - t * p.vecs) * 8;
+        float d[8], a[8], b[8], da[8], db[8];
+        row::unpack<row::bf16, 8>(ldg_nc_v4(p.dh + t * p.ld_dh + c), d);
+        row::unpack<row::bf16, 8>(*reinterpret_cast<const uint4 *>(p.gate + t * p.ld_gate + c), a);
+        row::unpack<row::bf16, 8>(*reinterpret_cast<const uint4 *>(p.up + t * p.ld_up + c), b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pre_grad(d[j], a[j], b[j], p.act, da[j], db[j]);
+        *reinterpret_cast<uint4 *>(p.dgate + t * p.ld_dgate + c) = row::pack<row::bf16, 8>(da);
+        *reinterpret_cast<uint4 *>(p.dup + t * p.ld_dup + c) = row::pack<row::bf16, 8>(db);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+dgr_status encode_fn(PFN_cuTensorMapEncodeTiled_v12000 *fn) {
+    std::call_once(g_encode_once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (!g_encode) return DGR_ERR_CUDA;
+    *fn = g_encode;
+    return DGR_OK;
+}
+
+// Map over `count` row-major bf16 matrices [rows, cols], one behind the other
+// (row stride ld): boxes of 64 columns by box_rows rows of one matrix, 128-byte
+// swizzle, zeros past its last row and column.
+dgr_status make_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int64_t count, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    const dgr_status st = encode_fn(&enc);
+    if (st != DGR_OK) return st;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
+}
+
+struct Operand {
+    const void *a, *a2;
+    int64_t ld_a, ld_a2;
+    const void *b, *b2;
+};
+
+template <int BN, bool FWD>
+dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
+    constexpr int kCols = FWD ? BN / 2 : BN;
+    CUtensorMap mA, mA2, mB, mB2;
+    dgr_status st;
+    if ((st = make_map(&mA, o.a, p.K, p.T, o.ld_a, 1, BM)) != DGR_OK) return st;
+    mA2 = mA;
+    if (!FWD && (st = make_map(&mA2, o.a2, p.K, p.T, o.ld_a2, 1, BM)) != DGR_OK) return st;
+    // the weights are [E, F, H]: forward N = F by K = H, backward K = F by N = H
+    const int64_t F = FWD ? p.N : p.K, H = FWD ? p.K : p.N;
+    const uint32_t box = FWD ? kCols : 64;
+    if ((st = make_map(&mB, o.b, H, F, H, p.E, box)) != DGR_OK || (st = make_map(&mB2, o.b2, H, F, H, p.E, box)) != DGR_OK) return st;
+    p.nbs = (p.N + kCols - 1) / kCols;
+    const int64_t blocks = (static_cast<int64_t>(p.T) + BM - 1) / BM + (p.offs ? p.E : 0);
+    if (blocks * p.nbs > INT32_MAX) return DGR_ERR_UNSUPPORTED;
+    auto *k = ffn_gemm<BN, FWD>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem<BN>)) != cudaSuccess) return DGR_ERR_CUDA;
+    const int64_t tiles = blocks * p.nbs;
+    k<<<sched_grid(static_cast<unsigned>(tiles < sms ? tiles : sms)), kThreads, kSmem<BN>, s>>>(mA, mA2, mB, mB2, p);
+    return launch_status();
+}
+
+// What both entries check of the rows, sizes, offsets and workspace.
+dgr_status check_sizes(int64_t T, int64_t H, int64_t F, int32_t E, int32_t act, const int64_t *offs) {
+    if (T < 0 || H < 1 || F < 1 || E < 1 || (act != kSilu && act != kGelu) || (!offs && E != 1)) return DGR_ERR_INVALID_ARG;
+    if (T > INT32_MAX - 256 || H > (1 << 20) || F > (1 << 20) || E > kMaxExperts) return DGR_ERR_UNSUPPORTED;
+    if (H % 8 != 0 || F % 8 != 0) return DGR_ERR_MISALIGNED;
+    return DGR_OK;
+}
+
+struct Rows {
+    const void *p;
+    int64_t ld, cols;
+};
+size_t extent(int64_t T, const Rows &r) { return r.p && T > 0 ? static_cast<size_t>((T - 1) * r.ld + r.cols) * 2 : 0; }
+
+}  // namespace
+}  // namespace dgr
+
+using namespace dgr;
+
+extern "C" size_t dgr_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t F, int32_t E) {
+    if (T < 0 || H < 1 || F < 1 || E < 1 || E > kMaxExperts || T > INT32_MAX - 256 || H > (1 << 20) || F > (1 << 20)) return 0;
+    return sizeof(WsHeader);
+}
+
+extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_gate, const void *w_up, const int64_t *d_offs,
+                                    int32_t E, int64_t T, int64_t H, int64_t F, int32_t act, void *h, int64_t ld_h, void *gate,
+                                    int64_t ld_gate, void *up, int64_t ld_up, void *ws, size_t ws_bytes, void *stream) {
+    dgr_status st = check_sizes(T, H, F, E, act, d_offs);
+    if (st != DGR_OK) return st;
+    const Rows in = {x, ld_x, H}, outs[] = {{h, ld_h, F}, {gate, ld_gate, F}, {up, ld_up, F}};
+    if (!ws || (T > 0 && (!x || !w_gate || !w_up || !h))) return DGR_ERR_INVALID_ARG;
+    if (ld_x < H) return DGR_ERR_INVALID_ARG;
+    for (const Rows &o : outs)
+        if (o.p && o.ld < F) return DGR_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || ld_x % 8 || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(d_offs, 8) || !aligned(ws, kAlign))
+        return DGR_ERR_MISALIGNED;
+    for (const Rows &o : outs)
+        if (o.p && (!aligned(o.p, 16) || o.ld % 8)) return DGR_ERR_MISALIGNED;
+    if (ws_bytes < sizeof(WsHeader)) return DGR_ERR_WORKSPACE_TOO_SMALL;
+    const size_t weights = static_cast<size_t>(E) * F * H * 2;
+    for (const Rows &o : outs) {
+        const size_t n = extent(T, o);
+        if (ranges_overlap(o.p, n, x, extent(T, in)) || ranges_overlap(o.p, n, w_gate, weights) || ranges_overlap(o.p, n, w_up, weights) ||
+            ranges_overlap(o.p, n, d_offs, (static_cast<size_t>(E) + 1) * 8) || ranges_overlap(o.p, n, ws, sizeof(WsHeader)))
+            return DGR_ERR_ALIAS;
+        for (const Rows &q : outs)
+            if (&q < &o && ranges_overlap(o.p, n, q.p, extent(T, q))) return DGR_ERR_ALIAS;
+    }
+    for (const Rows &i : {in, Rows{w_gate, 0, 0}, Rows{w_up, 0, 0}})
+        if (ranges_overlap(ws, sizeof(WsHeader), i.p, i.cols ? extent(T, i) : weights)) return DGR_ERR_ALIAS;
+    if ((st = check_device()) != DGR_OK) return st;
+    if (T == 0) return DGR_OK;
+    FfnParams p{};
+    p.offs = d_offs, p.E = E, p.T = static_cast<int32_t>(T);
+    p.K = static_cast<int32_t>(H), p.N = static_cast<int32_t>(F), p.act = act;
+    p.out = static_cast<uint16_t *>(h), p.gate = static_cast<uint16_t *>(gate), p.up = static_cast<uint16_t *>(up);
+    p.ld_out = ld_h, p.ld_gate = ld_gate, p.ld_up = ld_up;
+    p.hdr = static_cast<WsHeader *>(ws);
+    p.sched = sched_setting();
+    int sms = 0;
+    if ((st = usable_sms(&sms)) != DGR_OK) return st;
+    const Operand o{x, nullptr, ld_x, 0, w_gate, w_up};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launch_gemm<256, true>(p, o, sms, s);
+}
+
+extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gate, int64_t ld_gate, const void *up,
+                                             int64_t ld_up, const void *w_gate, const void *w_up, const int64_t *d_offs, int32_t E,
+                                             int64_t T, int64_t H, int64_t F, int32_t act, void *dgate, int64_t ld_dgate,
+                                             void *dup, int64_t ld_dup, void *dx, int64_t ld_dx, void *ws, size_t ws_bytes,
+                                             void *stream) {
+    dgr_status st = check_sizes(T, H, F, E, act, d_offs);
+    if (st != DGR_OK) return st;
+    const Rows ins[] = {{dh, ld_dh, F}, {gate, ld_gate, F}, {up, ld_up, F}}, outs[] = {{dgate, ld_dgate, F}, {dup, ld_dup, F}, {dx, ld_dx, H}};
+    if (!ws || (T > 0 && (!dh || !gate || !up || !dgate || !dup || (dx && (!w_gate || !w_up))))) return DGR_ERR_INVALID_ARG;
+    for (const Rows &r : ins)
+        if (r.ld < F) return DGR_ERR_INVALID_ARG;
+    for (const Rows &r : outs)
+        if (r.p && r.ld < r.cols) return DGR_ERR_INVALID_ARG;
+    for (const Rows &r : ins)
+        if (!aligned(r.p, 16) || r.ld % 8) return DGR_ERR_MISALIGNED;
+    for (const Rows &r : outs)
+        if (r.p && (!aligned(r.p, 16) || r.ld % 8)) return DGR_ERR_MISALIGNED;
+    if (!aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(d_offs, 8) || !aligned(ws, kAlign)) return DGR_ERR_MISALIGNED;
+    if (ws_bytes < sizeof(WsHeader)) return DGR_ERR_WORKSPACE_TOO_SMALL;
+    const size_t weights = static_cast<size_t>(E) * F * H * 2;
+    for (const Rows &o : outs) {
+        const size_t n = extent(T, o);
+        for (const Rows &i : ins) {
+            // dgate in gate's place, dup in up's: the same pointer and stride
+            const bool in_place = ((o.p == dgate && i.p == gate) || (o.p == dup && i.p == up)) && o.p == i.p && o.ld == i.ld;
+            if (!in_place && ranges_overlap(o.p, n, i.p, extent(T, i))) return DGR_ERR_ALIAS;
+        }
+        if (ranges_overlap(o.p, n, w_gate, weights) || ranges_overlap(o.p, n, w_up, weights) ||
+            ranges_overlap(o.p, n, d_offs, (static_cast<size_t>(E) + 1) * 8) || ranges_overlap(o.p, n, ws, sizeof(WsHeader)))
+            return DGR_ERR_ALIAS;
+        for (const Rows &q : outs)
+            if (&q < &o && ranges_overlap(o.p, n, q.p, extent(T, q))) return DGR_ERR_ALIAS;
+    }
+    for (const Rows &i : ins)
+        if (ranges_overlap(ws, sizeof(WsHeader), i.p, extent(T, i))) return DGR_ERR_ALIAS;
+    if (ranges_overlap(ws, sizeof(WsHeader), w_gate, weights) || ranges_overlap(ws, sizeof(WsHeader), w_up, weights)) return DGR_ERR_ALIAS;
+    if ((st = check_device()) != DGR_OK) return st;
+    if (T == 0) return DGR_OK;
+    int sms = 0;
+    if ((st = usable_sms(&sms)) != DGR_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PreParams g{};
+    g.dh = static_cast<const uint16_t *>(dh), g.gate = static_cast<const uint16_t *>(gate), g.up = static_cast<const uint16_t *>(up);
+    g.dgate = static_cast<uint16_t *>(dgate), g.dup = static_cast<uint16_t *>(dup);
+    g.ld_dh = ld_dh, g.ld_gate = ld_gate, g.ld_up = ld_up, g.ld_dgate = ld_dgate, g.ld_dup = ld_dup;
+    g.T = static_cast<int32_t>(T), g.vecs = static_cast<int32_t>(F / 8), g.act = act;
+    const int64_t n = T * g.vecs, ctas = (n + 255) / 256, most = static_cast<int64_t>(sms) * 8;
+    ffn_pre_grad<<<static_cast<unsigned>(ctas < most ? ctas : most), 256, 0, s>>>(g);
+    if ((st = launch_status()) != DGR_OK || !dx) return st;
+    FfnParams p{};
+    p.offs = d_offs, p.E = E, p.T = static_cast<int32_t>(T);
+    p.K = static_cast<int32_t>(F), p.N = static_cast<int32_t>(H), p.act = act;
+    p.out = static_cast<uint16_t *>(dx), p.ld_out = ld_dx;
+    p.hdr = static_cast<WsHeader *>(ws);
+    p.sched = sched_setting();
+    const Operand o{dgate, dup, ld_dgate, ld_dup, w_gate, w_up};
+    return launch_gemm<256, false>(p, o, sms, s);
+}

@@ -1,0 +1,620 @@
+// Norm of queries and keys a head, and their rotation by position, in one pass,
+// forward and backward.
+//
+// For every head v [D] of a token at position t:
+//   r = (mean(v^2) + eps)^(-1/2),  n = v r w,
+//   (y_lo, y_hi) = (n_lo c - n_hi s, n_hi c + n_lo s) for each of the R / 2 pairs,
+// c and s the table's cosine and sine of the pair's angle at t; the elements
+// behind R stay. Pairs are (i, i + R/2) or, interleaved, (2i, 2i + 1).
+// Backwards, from dy: g = dy turned back (s -> -s),
+//   dw = sum over tokens and heads of g v r,
+//   dv = r (g w) - v (r^3 / D) (g w . v).
+// All in binary32 from the stored heads; every output rounded once.
+//
+// A team of lanes has a head: lane l of it V pairs (the same places of the lower
+// and the upper half, so a rotation stays in the lane) and NV such groups; a
+// warp has several teams, which share a token, so that its cosines and sines are
+// read once for all of the token's heads.
+//
+// Deterministic: a head's sums go over its team in a fixed order; dw goes through
+// a number of slots set by the sizes alone: a slot's warps take their units in
+// ascending order, its warps and teams are added in order, and a second launch
+// adds the slots in a fixed tree.
+#include "row_common.cuh"
+
+namespace dgr {
+namespace {
+
+using namespace row;
+
+constexpr int kWarps = 8;
+constexpr int kMaxDim = 512;
+constexpr int kMaxHeads = 1024;
+constexpr int kSlots = 304;     // CTAs of the backward pass at most, two an SM
+constexpr int kFoldCols = 8, kFoldWays = 32;
+constexpr int kWherePos = 420;
+
+// Heads of one kind (queries or keys): element (t, head, d) at t * st + head * sh + d.
+struct Heads {
+    const void *v, *dy;
+    void *out;  // forward: y; backward: dv
+    int64_t st, sh, st_dy, sh_dy, st_out, sh_out;
+    int32_t n;
+    const void *w;
+    float *dw;
+};
+
+struct QkParams {
+    Heads kind[2];
+    int32_t T, D, R, w_bf16, P;
+    const float *cos, *sin;    // [P, R/2]
+    const int32_t *pos;
+    float eps;
+    int32_t team, chunks;      // lanes a head; warps a token
+    int32_t n_slots, accumulate;
+    float *slots;              // [n_slots, 2, D]
+    WsHeader *hdr;
+    Sched sched;
+};
+
+// Where this lane's pairs lie: group i of it starts at pair b = (i * team + tl) * V.
+template <int V, int NV, bool INTER>
+struct Pairs {
+    int lo[NV], hi[NV];  // element offsets of the first of V; interleaved: of 2 V neighbours, in two vectors
+    int at[NV];          // pair
+    bool has[NV];
+    __device__ __forceinline__ Pairs(const QkParams &p, int tl) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int b = (i * p.team + tl) * V;
+            has[i] = b < p.D / 2;
+            at[i] = b;
+            if (INTER) {
+                lo[i] = 2 * b, hi[i] = 2 * b + V;
+            } else if (b < p.R / 2) {
+                lo[i] = b, hi[i] = b + p.R / 2;
+            } else {
+                lo[i] = p.R / 2 + b, hi[i] = p.D / 2 + b;
+            }
+        }
+    }
+};
+
+// The first and second elements of V pairs out of their two vectors, and back.
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ void split(const raw_t<T, V> &x, const raw_t<T, V> &y, float (&a)[V], float (&b)[V]) {
+    if constexpr (!INTER) {
+        unpack<T, V>(x, a);
+        unpack<T, V>(y, b);
+    } else {
+        float f[2 * V];
+        unpack<T, V>(x, f);
+        unpack<T, V>(y, f + V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = f[2 * j], b[j] = f[2 * j + 1];
+    }
+}
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ void join(const float (&a)[V], const float (&b)[V], raw_t<T, V> &x, raw_t<T, V> &y) {
+    if constexpr (!INTER) {
+        x = pack<T, V>(a);
+        y = pack<T, V>(b);
+    } else {
+        float f[2 * V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[2 * j] = a[j], f[2 * j + 1] = b[j];
+        x = pack<T, V>(f);
+        y = pack<T, V>(f + V);
+    }
+}
+
+__device__ __forceinline__ float team_sum(float v, int team) {
+    for (int s = team >> 1; s > 0; s >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, s));
+    return v;
+}
+
+// Cosines and sines of the lane's pairs at a position (1 and 0 behind R).
+template <int V, int NV, bool INTER>
+__device__ __forceinline__ void angles(const QkParams &p, const Pairs<V, NV, INTER> &m, int32_t pos, float (&c)[NV][V], float (&s)[NV][V]) {
+    const int64_t row = static_cast<int64_t>(pos) * (p.R / 2);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const bool on = m.has[i] && m.at[i] < p.R / 2;
+#pragma unroll
+        for (int j = 0; j < V; ++j) c[i][j] = 1.0f, s[i][j] = 0.0f;
+        if (!on) continue;
+        if constexpr (V % 4 == 0) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                unpack<float, 4>(__ldg(reinterpret_cast<const uint4 *>(p.cos + row + m.at[i] + j)), &c[i][j]);
+                unpack<float, 4>(__ldg(reinterpret_cast<const uint4 *>(p.sin + row + m.at[i] + j)), &s[i][j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[i][j] = __ldg(p.cos + row + m.at[i] + j), s[i][j] = __ldg(p.sin + row + m.at[i] + j);
+        }
+    }
+}
+
+// Both weights as binary32 into shared memory (1 where there is none), in the
+// order of the pairs: first elements, then second ones.
+template <bool INTER>
+__device__ __forceinline__ void load_weights(const QkParams &p, float (*w)[kMaxDim]) {
+    for (int i = threadIdx.x; i < 2 * p.D; i += kWarps * 32) {
+        const int kind = i >= p.D, e = i - kind * p.D;
+        const void *from = p.kind[kind].w;
+        int pair, second;
+        if (INTER) pair = e >> 1, second = e & 1;
+        else if (e < p.R) second = e >= p.R / 2, pair = e - second * (p.R / 2);
+        else second = e - p.R >= (p.D - p.R) / 2, pair = p.R / 2 + (e - p.R) - second * ((p.D - p.R) / 2);
+        w[kind][second * (p.D / 2) + pair] = from ? param(from, p.w_bf16, e) : 1.0f;
+    }
+    __syncthreads();
+}
+
+template <int V, int NV, bool INTER>
+__device__ __forceinline__ void lane_weights(const QkParams &p, const Pairs<V, NV, INTER> &m, const float *w, float (&a)[NV][V], float (&b)[NV][V]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            a[i][j] = m.has[i] ? w[m.at[i] + j] : 0.0f;
+            b[i][j] = m.has[i] ? w[p.D / 2 + m.at[i] + j] : 0.0f;
+        }
+}
+
+// The position of a token; outside the table it is recorded and false is returned.
+__device__ __forceinline__ bool position(const QkParams &p, int64_t t, int32_t &pos) {
+    pos = __ldg(p.pos + t);
+    if (pos >= 0 && pos < p.P) return true;
+    if ((threadIdx.x & 31) == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWherePos);
+    return false;
+}
+
+template <typename T, int V, int NV, bool INTER, int U>
+__global__ void __launch_bounds__(kWarps * 32) qk_forward(const QkParams p) {
+    using raw = raw_t<T, V>;
+    __shared__ __align__(16) float s_w[2][kMaxDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tl = lane & (p.team - 1), mine = lane / p.team, teams = 32 / p.team;
+    const Pairs<V, NV, INTER> m(p, tl);
+    load_weights<INTER>(p, s_w);
+    const int64_t units = static_cast<int64_t>(p.T) * p.chunks;
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units; u += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int64_t i = sched_item(p.sched, static_cast<uint32_t>(u));
+        const int64_t t = i / p.chunks;
+        const int chunk = static_cast<int>(i - t * p.chunks);
+        int32_t pos;
+        const bool good = position(p, t, pos);
+        float c[NV][V], s[NV][V];
+        angles<V, NV, INTER>(p, m, good ? pos : 0, c, s);
+        int first = chunk;  // this warp's first group of heads among the kind's
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const Heads &h = p.kind[kind];
+            const int groups = (h.n + teams - 1) / teams;
+            const T *v = static_cast<const T *>(h.v) + t * h.st;
+            T *out = static_cast<T *>(h.out) + t * h.st_out;
+            float wa[NV][V], wb[NV][V];
+            if (first < groups) lane_weights<V, NV, INTER>(p, m, s_w[kind], wa, wb);
+            for (int g0 = first; g0 < groups; g0 += U * p.chunks) {
+                raw lo[U][NV] = {}, hi[U][NV] = {};
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int head = (g0 + k * p.chunks) * teams + mine;
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        const bool on = head < h.n && m.has[n];
+                        load_if<false>(lo[k][n], v + head * h.sh + m.lo[n], on);
+                        load_if<false>(hi[k][n], v + head * h.sh + m.hi[n], on);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int head = (g0 + k * p.chunks) * teams + mine;
+                    float a[NV][V], b[NV][V], ss = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        split<T, V, INTER>(lo[k][n], hi[k][n], a[n], b[n]);
+                        ss = __fadd_rn(ss, __fadd_rn(vec_dot(a[n], a[n]), vec_dot(b[n], b[n])));
+                    }
+                    const float r = rsqrtf(__fmaf_rn(team_sum(ss, p.team), inv_d, p.eps));
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        float x[V], y[V];
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float na = __fmul_rn(__fmul_rn(a[n][j], r), wa[n][j]), nb = __fmul_rn(__fmul_rn(b[n][j], r), wb[n][j]);
+                            x[j] = good ? __fmaf_rn(na, c[n][j], -__fmul_rn(nb, s[n][j])) : 0.0f;
+                            y[j] = good ? __fmaf_rn(nb, c[n][j], __fmul_rn(na, s[n][j])) : 0.0f;
+                        }
+                        raw rx, ry;
+                        join<T, V, INTER>(x, y, rx, ry);
+                        if (head < h.n && m.has[n]) {
+                            *reinterpret_cast<raw *>(out + head * h.sh_out + m.lo[n]) = rx;
+                            *reinterpret_cast<raw *>(out + head * h.sh_out + m.hi[n]) = ry;
+                        }
+                    }
+                }
+            }
+            first = (first - groups % p.chunks + p.chunks) % p.chunks;  // groups go round the chunks, over both kinds
+        }
+    }
+}
+
+template <typename T, int V, int NV, bool INTER, int U>
+__global__ void __launch_bounds__(kWarps * 32, 2) qk_backward(const QkParams p) {
+    using raw = raw_t<T, V>;
+    __shared__ __align__(16) float s_w[2][kMaxDim];
+    __shared__ float s_dw[kWarps][kMaxDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tl = lane & (p.team - 1), mine = lane / p.team, teams = 32 / p.team;
+    const Pairs<V, NV, INTER> m(p, tl);
+    load_weights<INTER>(p, s_w);
+    const int64_t units = static_cast<int64_t>(p.T) * p.chunks;
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    for (int turn = blockIdx.x; turn < p.n_slots; turn += gridDim.x) {
+        const int slot = static_cast<int>(sched_item(p.sched, static_cast<uint32_t>(turn)));
+#pragma unroll 1
+        for (int kind = 0; kind < 2; ++kind) {
+            const Heads &h = p.kind[kind];
+            const int groups = (h.n + teams - 1) / teams;
+            float acc_a[NV][V] = {}, acc_b[NV][V] = {}, wa[NV][V], wb[NV][V];
+            lane_weights<V, NV, INTER>(p, m, s_w[kind], wa, wb);
+            for (int64_t u = static_cast<int64_t>(slot) * kWarps + warp; u < units; u += static_cast<int64_t>(p.n_slots) * kWarps) {
+                const int64_t t = u / p.chunks;
+                int first = static_cast<int>(u - t * p.chunks);
+                if (kind) first = (first - (p.kind[0].n + teams - 1) / teams % p.chunks + p.chunks) % p.chunks;
+                if (first >= groups) continue;
+                int32_t pos;
+                const bool good = position(p, t, pos);
+                float c[NV][V], s[NV][V];
+                angles<V, NV, INTER>(p, m, good ? pos : 0, c, s);
+                const T *v = static_cast<const T *>(h.v) + t * h.st;
+                const T *dy = static_cast<const T *>(h.dy) + t * h.st_dy;
+                T *out = static_cast<T *>(h.out) + t * h.st_out;
+                for (int g0 = first; g0 < groups; g0 += U * p.chunks) {
+                    raw lo[U][NV] = {}, hi[U][NV] = {}, dlo[U][NV] = {}, dhi[U][NV] = {};
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        const int head = (g0 + k * p.chunks) * teams + mine;
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            const bool on = head < h.n && m.has[n] && good;
+                            load_if<false>(lo[k][n], v + head * h.sh + m.lo[n], on);
+                            load_if<false>(hi[k][n], v + head * h.sh + m.hi[n], on);
+                            load_if<false>(dlo[k][n], dy + head * h.sh_dy + m.lo[n], on);
+                            load_if<false>(dhi[k][n], dy + head * h.sh_dy + m.hi[n], on);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        const int head = (g0 + k * p.chunks) * teams + mine;
+                        float a[NV][V], b[NV][V], ga[NV][V], gb[NV][V], ss = 0.0f, dot = 0.0f;
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            float x[V], y[V];
+                            split<T, V, INTER>(lo[k][n], hi[k][n], a[n], b[n]);
+                            split<T, V, INTER>(dlo[k][n], dhi[k][n], x, y);
+                            ss = __fadd_rn(ss, __fadd_rn(vec_dot(a[n], a[n]), vec_dot(b[n], b[n])));
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                ga[n][j] = __fmaf_rn(x[j], c[n][j], __fmul_rn(y[j], s[n][j]));
+                                gb[n][j] = __fmaf_rn(y[j], c[n][j], -__fmul_rn(x[j], s[n][j]));
+                                dot = __fmaf_rn(__fmul_rn(ga[n][j], wa[n][j]), a[n][j], dot);
+                                dot = __fmaf_rn(__fmul_rn(gb[n][j], wb[n][j]), b[n][j], dot);
+                            }
+                        }
+                        for (int sh = p.team >> 1; sh > 0; sh >>= 1) {
+                            ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, sh));
+                            dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, sh));
+                        }
+                        // a place without a head, or a token without a position: nothing for dw
+                        const bool on = head < h.n && good;
+                        const float r = on ? rsqrtf(__fmaf_rn(ss, inv_d, p.eps)) : 0.0f;
+                        const float back = on ? __fmul_rn(__fmul_rn(r, r), __fmul_rn(r, __fmul_rn(dot, inv_d))) : 0.0f;
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            float x[V], y[V];
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                acc_a[n][j] = __fmaf_rn(__fmul_rn(a[n][j], r), ga[n][j], acc_a[n][j]);
+                                acc_b[n][j] = __fmaf_rn(__fmul_rn(b[n][j], r), gb[n][j], acc_b[n][j]);
+                                x[j] = __fmaf_rn(__fmul_rn(ga[n][j], wa[n][j]), r, -__fmul_rn(a[n][j], back));
+                                y[j] = __fmaf_rn(__fmul_rn(gb[n][j], wb[n][j]), r, -__fmul_rn(b[n][j], back));
+                            }
+                            raw rx, ry;
+                            join<T, V, INTER>(x, y, rx, ry);
+                            if (head < h.n && m.has[n]) {
+                                *reinterpret_cast<raw *>(out + head * h.sh_out + m.lo[n]) = rx;
+                                *reinterpret_cast<raw *>(out + head * h.sh_out + m.hi[n]) = ry;
+                            }
+                        }
+                    }
+                }
+            }
+            if (!h.dw) continue;
+            // the warp's teams, then the slot's warps
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    for (int sh = p.team; sh < 32; sh <<= 1) {
+                        acc_a[n][j] = __fadd_rn(acc_a[n][j], __shfl_xor_sync(0xffffffffu, acc_a[n][j], sh));
+                        acc_b[n][j] = __fadd_rn(acc_b[n][j], __shfl_xor_sync(0xffffffffu, acc_b[n][j], sh));
+                    }
+                    if (mine == 0 && m.has[n]) {
+                        const int first = INTER ? 2 * (m.at[n] + j) : m.lo[n] + j, second = INTER ? first + 1 : m.hi[n] + j;
+                        s_dw[warp][first] = acc_a[n][j];
+                        s_dw[warp][second] = acc_b[n][j];
+                    }
+                }
+            __syncthreads();
+            for (int d = threadIdx.x; d < p.D; d += kWarps * 32) {
+                float v = s_dw[0][d];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v = __fadd_rn(v, s_dw[w][d]);
+                p.slots[(static_cast<int64_t>(slot) * 2 + kind) * p.D + d] = v;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// dw from the slots: kFoldWays threads a column, then a tree.
+__global__ void __launch_bounds__(kFoldCols *kFoldWays) qk_fold(const QkParams p) {
+    __shared__ float part[kFoldWays][kFoldCols + 1];
+    const int col = threadIdx.x % kFoldCols, way = threadIdx.x / kFoldCols;
+    const int i = blockIdx.x * kFoldCols + col, kind = i >= p.D;
+    const bool on = i < 2 * p.D && p.kind[kind].dw;
+    float v = 0.0f;
+    if (on)
+        for (int s = way; s < p.n_slots; s += kFoldWays) v = __fadd_rn(v, __ldcg(p.slots + static_cast<int64_t>(s) * 2 * p.D + i));
+    part[way][col] = v;
+    for (int half = kFoldWays / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        if (way < half) part[way][col] = __fadd_rn(part[way][col], part[way + half][col]);
+    }
+    if (on && way == 0) {
+        float *to = p.kind[kind].dw + i - kind * p.D;
+        *to = p.accumulate ? __fadd_rn(*to, part[0][col]) : part[0][col];
+    }
+}
+
+// ---- host ---------------------------------------------------------------------
+
+// A [T, n, D] view with contiguous heads.
+struct View {
+    const void *p;
+    int64_t st, sh, n;
+};
+
+struct Layout {
+    int64_t T, D, es;
+    // from the first to behind the last element of one token's heads, of all
+    size_t footprint(const View &v) const { return static_cast<size_t>(((v.n - 1) * v.sh + D) * es); }
+    size_t extent(const View &v) const { return v.p && T > 0 && v.n > 0 ? static_cast<size_t>((T - 1) * v.st * es) + footprint(v) : 0; }
+    // Whether two views share memory. Parts of one packed row (the same token
+    // stride, each within it) do where their places in the row do.
+    bool overlap(const View &a, const View &b) const {
+        if (!ranges_overlap(a.p, extent(a), b.p, extent(b))) return false;
+        const size_t stride = static_cast<size_t>(a.st * es), fa = footprint(a), fb = footprint(b);
+        if (a.st != b.st || T == 1 || fa > stride || fb > stride) return true;
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        const size_t apart = y >= x ? (y - x) % stride : (stride - (x - y) % stride) % stride;
+        return apart < fa || apart + fb > stride;
+    }
+    // heads apart from each other: tokens outside heads, or heads outside tokens
+    bool valid(const View &v) const {
+        if (v.n == 0 || T == 0) return true;
+        if ((v.n > 1 && v.sh < D) || (T > 1 && v.st < D)) return false;
+        return T == 1 || v.n == 1 || v.st >= (v.n - 1) * v.sh + D || v.sh >= (T - 1) * v.st + D;
+    }
+};
+
+struct Call {
+    Layout lay;
+    View in[2], dy[2], out[2];
+    const void *w[2];
+    float *dw[2];
+    int32_t dtype, w_dtype, R, P, interleaved, accumulate;
+    const float *cos, *sin;
+    const int32_t *pos;
+    float eps;
+    void *ws;
+    size_t ws_bytes;
+    bool backward;
+};
+
+int32_t slots_of(int64_t T) {
+    const int64_t n = (T + kWarps - 1) / kWarps;
+    return static_cast<int32_t>(n < 1 ? 1 : n < kSlots ? n : kSlots);
+}
+
+dgr_status check(const Call &c) {
+    const Layout &l = c.lay;
+    if ((c.dtype != DGR_DTYPE_BF16 && c.dtype != DGR_DTYPE_F32) || (c.w_dtype != DGR_DTYPE_BF16 && c.w_dtype != DGR_DTYPE_F32)) return DGR_ERR_INVALID_ARG;
+    if (l.T < 0 || l.D < 2 || l.D % 2 || c.R < 2 || c.R % 2 || c.R > l.D || c.P < 1 || !(c.eps >= 0.0f) || c.in[0].n < 0 || c.in[1].n < 0 ||
+        c.in[0].n + c.in[1].n < 1)
+        return DGR_ERR_INVALID_ARG;
+    if (!c.ws) return DGR_ERR_INVALID_ARG;
+    if (l.T > (1 << 26) || l.D > kMaxDim || c.in[0].n > kMaxHeads || c.in[1].n > kMaxHeads) return DGR_ERR_UNSUPPORTED;
+    if (l.T > 0 && (!c.cos || !c.sin || !c.pos)) return DGR_ERR_INVALID_ARG;
+    const size_t es = static_cast<size_t>(l.es), wes = c.w_dtype == DGR_DTYPE_BF16 ? 2 : 4;
+    for (int k = 0; k < 2; ++k) {
+        if (c.in[k].n == 0) {
+            if (c.dw[k]) return DGR_ERR_INVALID_ARG;
+            continue;
+        }
+        if (l.T > 0 && (!c.in[k].p || !c.out[k].p || (c.backward && !c.dy[k].p))) return DGR_ERR_INVALID_ARG;
+        if (c.backward && c.dw[k] && !c.w[k]) return DGR_ERR_INVALID_ARG;
+        for (const View *v : {&c.in[k], &c.out[k], &c.dy[k]}) {
+            if (v->p && !l.valid(*v)) return DGR_ERR_INVALID_ARG;
+            if (!aligned(v->p, es)) return DGR_ERR_MISALIGNED;
+        }
+        if (!aligned(c.w[k], wes) || !aligned(c.dw[k], 4)) return DGR_ERR_MISALIGNED;
+    }
+    if (!aligned(c.cos, 4) || !aligned(c.sin, 4) || !aligned(c.pos, 4) || !aligned(c.ws, kAlign)) return DGR_ERR_MISALIGNED;
+    const size_t need = c.backward ? dgr_qk_norm_rope_workspace_bytes(l.T, static_cast<int32_t>(c.in[0].n), static_cast<int32_t>(c.in[1].n),
+                                                                      static_cast<int32_t>(l.D))
+                                   : sizeof(WsHeader);
+    if (c.ws_bytes < need) return DGR_ERR_WORKSPACE_TOO_SMALL;
+    struct Range { const void *p; size_t n; };
+    const size_t table = static_cast<size_t>(c.P) * (c.R / 2) * 4, d = static_cast<size_t>(l.D);
+    const Range flat[] = {{c.cos, table}, {c.sin, table}, {c.pos, static_cast<size_t>(l.T) * 4}, {c.w[0], d * wes}, {c.w[1], d * wes}};
+    const Range flat_out[] = {{c.ws, need}, {c.dw[0], d * 4}, {c.dw[1], d * 4}};
+    for (int k = 0; k < 2; ++k) {
+        const View &o = c.out[k];
+        const size_t n = l.extent(o);
+        for (const Range &r : flat)
+            if (ranges_overlap(o.p, n, r.p, r.n)) return DGR_ERR_ALIAS;
+        for (const Range &r : flat_out)
+            if (ranges_overlap(o.p, n, r.p, r.n)) return DGR_ERR_ALIAS;
+        for (int j = 0; j < 2; ++j) {
+            // in place: each head is read by the lanes that write it (forward over v, backward over dy)
+            const View &home = c.backward ? c.dy[j] : c.in[j];
+            const bool same = j == k && home.p == o.p && home.st == o.st && home.sh == o.sh;
+            if (!same && l.overlap(o, home)) return DGR_ERR_ALIAS;
+            if (c.backward && l.overlap(o, c.in[j])) return DGR_ERR_ALIAS;
+        }
+    }
+    if (l.overlap(c.out[0], c.out[1])) return DGR_ERR_ALIAS;
+    for (const Range &o : flat_out) {
+        for (const Range &r : flat)
+            if (ranges_overlap(o.p, o.n, r.p, r.n)) return DGR_ERR_ALIAS;
+        for (int j = 0; j < 2; ++j)
+            if (ranges_overlap(o.p, o.n, c.in[j].p, l.extent(c.in[j])) || ranges_overlap(o.p, o.n, c.dy[j].p, l.extent(c.dy[j]))) return DGR_ERR_ALIAS;
+        for (const Range &r : flat_out)
+            if (&r < &o && ranges_overlap(o.p, o.n, r.p, r.n)) return DGR_ERR_ALIAS;
+    }
+    return DGR_OK;
+}
+
+template <typename T, int V, int NV, bool INTER>
+dgr_status launch(QkParams p, bool backward, int sms, cudaStream_t s) {
+    const int vecs = (p.D / 2 + V - 1) / V;  // groups of pairs a head
+    int team = 1;
+    while (team * NV < vecs) team <<= 1;
+    p.team = team;
+    const int teams = 32 / team;
+    const int groups = (p.kind[0].n + teams - 1) / teams + (p.kind[1].n + teams - 1) / teams;
+    // few tokens: a token over several warps, down to one group of heads each
+    int64_t chunks = p.T > 0 ? (304 * kWarps + p.T - 1) / p.T : 1;
+    if (chunks > groups) chunks = groups;
+    p.chunks = static_cast<int32_t>(chunks);
+    const int64_t units = static_cast<int64_t>(p.T) * p.chunks;
+    if (units >= INT32_MAX) return DGR_ERR_UNSUPPORTED;
+    if (!backward) {
+        p.sched = sched_for(static_cast<uint32_t>(units));
+        const int64_t ctas = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 4;
+        qk_forward<T, V, NV, INTER, (V * NV >= 8 ? 4 : 2)><<<sched_grid(static_cast<unsigned>(ctas < most ? ctas : most)), kWarps * 32, 0, s>>>(p);
+        return launch_status();
+    }
+    p.n_slots = slots_of(units);
+    p.sched = sched_for(static_cast<uint32_t>(p.n_slots));
+    const int most = sms * 2;
+    qk_backward<T, V, NV, INTER, 2><<<sched_grid(static_cast<unsigned>(p.n_slots < most ? p.n_slots : most)), kWarps * 32, 0, s>>>(p);
+    dgr_status st = launch_status();
+    if (st != DGR_OK || (!p.kind[0].dw && !p.kind[1].dw)) return st;
+    qk_fold<<<static_cast<unsigned>((2 * p.D + kFoldCols - 1) / kFoldCols), kFoldCols * kFoldWays, 0, s>>>(p);
+    return launch_status();
+}
+
+template <typename T, bool INTER>
+dgr_status launch_width(const QkParams &p, int vec, bool backward, int sms, cudaStream_t s) {
+    constexpr int W = 16 / static_cast<int>(sizeof(T));
+    if (vec == W) return launch<T, W, 8 / W, INTER>(p, backward, sms, s);
+    if (vec == 2) return launch<T, 2, 4, INTER>(p, backward, sms, s);
+    return launch<T, 1, 8, INTER>(p, backward, sms, s);
+}
+
+dgr_status run(const Call &c, void *stream) {
+    dgr_status st = check(c);
+    if (st != DGR_OK) return st;
+    if ((st = check_device()) != DGR_OK) return st;
+    const Layout &l = c.lay;
+    if (l.T == 0 && (!c.backward || (!c.dw[0] && !c.dw[1]))) return DGR_OK;
+    QkParams p{};
+    // pairs in a vector: of 16 bytes, 2 or 1, as far as heads, halves and tables start at multiples of it
+    const int es = static_cast<int>(l.es);
+    int vec = 16 / es;
+    auto fits = [&](int v) {
+        if (c.R / 2 % v || l.D / 2 % v) return false;
+        if (v % 4 == 0 && (!aligned(c.cos, 16) || !aligned(c.sin, 16))) return false;
+        for (int k = 0; k < 2; ++k)
+            for (const View *w : {&c.in[k], &c.out[k], &c.dy[k]})
+                if (w->p && w->n > 0 &&
+                    (!aligned(w->p, static_cast<size_t>(v * es)) || (l.T > 1 && w->st % v) || (w->n > 1 && w->sh % v)))
+                    return false;
+        return true;
+    };
+    if (!fits(vec)) vec = fits(2) ? 2 : 1;
+    for (int k = 0; k < 2; ++k) {
+        Heads &h = p.kind[k];
+        h.n = static_cast<int32_t>(c.in[k].n);
+        h.v = c.in[k].p, h.st = c.in[k].st, h.sh = c.in[k].sh;
+        h.dy = c.dy[k].p, h.st_dy = c.dy[k].st, h.sh_dy = c.dy[k].sh;
+        h.out = const_cast<void *>(c.out[k].p), h.st_out = c.out[k].st, h.sh_out = c.out[k].sh;
+        h.w = c.w[k], h.dw = c.dw[k];
+    }
+    p.T = static_cast<int32_t>(l.T), p.D = static_cast<int32_t>(l.D), p.R = c.R, p.P = c.P;
+    p.w_bf16 = c.w_dtype == DGR_DTYPE_BF16;
+    p.cos = c.cos, p.sin = c.sin, p.pos = c.pos, p.eps = c.eps;
+    p.accumulate = c.accumulate ? 1 : 0;
+    p.hdr = static_cast<WsHeader *>(c.ws);
+    p.slots = reinterpret_cast<float *>(static_cast<char *>(c.ws) + sizeof(WsHeader));
+    int sms = 0;
+    if ((st = usable_sms(&sms)) != DGR_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (es == 2) return c.interleaved ? launch_width<bf16, true>(p, vec, c.backward, sms, s) : launch_width<bf16, false>(p, vec, c.backward, sms, s);
+    return c.interleaved ? launch_width<float, true>(p, vec, c.backward, sms, s) : launch_width<float, false>(p, vec, c.backward, sms, s);
+}
+
+}  // namespace
+}  // namespace dgr
+
+using namespace dgr;
+
+extern "C" size_t dgr_qk_norm_rope_workspace_bytes(int64_t T, int32_t n_q, int32_t n_k, int32_t D) {
+    if (T < 0 || T > (1 << 26) || n_q < 0 || n_k < 0 || n_q + n_k < 1 || n_q > kMaxHeads || n_k > kMaxHeads || D < 2 || D > kMaxDim) return 0;
+    return sizeof(WsHeader) + static_cast<size_t>(kSlots) * 2 * static_cast<size_t>(D) * 4;
+}
+
+extern "C" dgr_status dgr_qk_norm_rope(const void *q, int64_t q_token, int64_t q_head, int32_t n_q, const void *k, int64_t k_token,
+                                       int64_t k_head, int32_t n_k, int32_t dtype, int64_t T, int32_t D, const void *w_q,
+                                       const void *w_k, int32_t w_dtype, const float *cos, const float *sin, int32_t P, int32_t R,
+                                       int32_t interleaved, const int32_t *positions, float eps, void *q_out, int64_t qo_token,
+                                       int64_t qo_head, void *k_out, int64_t ko_token, int64_t ko_head, void *ws, size_t ws_bytes,
+                                       void *stream) {
+    Call c{};
+    c.lay = {T, D, dtype == DGR_DTYPE_BF16 ? 2 : 4};
+    c.in[0] = {q, q_token, q_head, n_q}, c.in[1] = {k, k_token, k_head, n_k};
+    c.out[0] = {q_out, qo_token, qo_head, n_q}, c.out[1] = {k_out, ko_token, ko_head, n_k};
+    c.w[0] = w_q, c.w[1] = w_k;
+    c.dtype = dtype, c.w_dtype = w_dtype, c.R = R, c.P = P, c.interleaved = interleaved;
+    c.cos = cos, c.sin = sin, c.pos = positions, c.eps = eps;
+    c.ws = ws, c.ws_bytes = ws_bytes;
+    return run(c, stream);
+}
+
+extern "C" dgr_status dgr_qk_norm_rope_backward(const void *dq_out, int64_t dqo_token, int64_t dqo_head, const void *dk_out,
+                                                int64_t dko_token, int64_t dko_head, const void *q, int64_t q_token, int64_t q_head,
+                                                int32_t n_q, const void *k, int64_t k_token, int64_t k_head, int32_t n_k,
+                                                int32_t dtype, int64_t T, int32_t D, const void *w_q, const void *w_k,
+                                                int32_t w_dtype, const float *cos, const float *sin, int32_t P, int32_t R,
+                                                int32_t interleaved, const int32_t *positions, float eps, void *dq, int64_t dq_token,
+                                                int64_t dq_head, void *dk, int64_t dk_token, int64_t dk_head, float *dw_q, float *dw_k,
+                                                int32_t accumulate, void *ws, size_t ws_bytes, void *stream) {
+    Call c{};
+    c.lay = {T, D, dtype == DGR_DTYPE_BF16 ? 2 : 4};
+    c.in[0] = {q, q_token, q_head, n_q}, c.in[1] = {k, k_token, k_head, n_k};
+    c.dy[0] = {dq_out, dqo_token, dqo_head, n_q}, c.dy[1] = {dk_out, dko_token, dko_head, n_k};
+    c.out[0] = {dq, dq_token, dq_head, n_q}, c.out[1] = {dk, dk_token, dk_head, n_k};
+    c.w[0] = w_q, c.w[1] = w_k, c.dw[0] = dw_q, c.dw[1] = dw_k;
+    c.dtype = dtype, c.w_dtype = w_dtype, c.R = R, c.P = P, c.interleaved = interleaved, c.accumulate = accumulate;
+    c.cos = cos, c.sin = sin, c.pos = positions, c.eps = eps;
+    c.ws = ws, c.ws_bytes = ws_bytes;
+    c.backward = true;
+    return run(c, stream);
+}

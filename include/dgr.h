@@ -8,8 +8,8 @@
  * ascending tile order, and the result either written or added to the output
  * with one IEEE binary32 rounding. Results are therefore bitwise identical
  * from run to run, whatever the launch order, grid size or concurrent streams.
- * The operators around an expert block (sections 9-11) have fixed orders of
- * their own, given there, and the same reproducibility.
+ * The operators around an expert block and of a training step (sections 9-14)
+ * have fixed orders of their own, given there, and the same reproducibility.
  *
  * Conventions for every entry point:
  *   - Pointers are DEVICE pointers unless stated otherwise; the caller owns
@@ -35,7 +35,7 @@
  *     an error the outputs of that call are unspecified and the workspace must
  *     be zeroed again before reuse.
  *   - Floating point, sections 1-8: binary32 round-to-nearest-even, subnormals
- *     kept, no fused multiply-add anywhere in a reduction. Sections 9-11: sums
+ *     kept, no fused multiply-add anywhere in a reduction. Sections 9-14: sums
  *     and statistics in binary32 with fused multiply-adds; exponentials to base
  *     2, their quotients and reciprocal roots by the GPU's approximations of
  *     them, a few units in the last place, with subnormal exponentials taken
@@ -74,8 +74,9 @@ const char *dgr_status_string(dgr_status s);
 /* Library ABI version (major * 100 + minor). 1.01 added sections 5-8 (grouped
  * dbias, canonical top-K, aux-loss scalar, dsReLU dprob); 1.02 added
  * dgr_query_device_status; 1.03 added dgr_colsum_noalloc_read_status; 1.04
- * added sections 9-11 (router balance loss, block norms, distillation); earlier
- * entries unchanged. */
+ * added sections 9-11 (router balance loss, block norms, distillation); 1.05
+ * added sections 12-14 (gated feed-forward, norm and rotation of queries and
+ * keys, token log probabilities); earlier entries unchanged. */
 int32_t dgr_version(void);
 
 /* DGR_OK when `device` is a compute capability 10.3 GPU, else DGR_ERR_UNSUPPORTED. */
@@ -554,6 +555,156 @@ dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_
                             const float *teacher_lse, const float *weights, float scale, const float *dloss,
                             float *row_loss, float *loss, void *dlogits, int64_t ld_d, void *ws, size_t ws_bytes,
                             void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* 12. Gated feed-forward of grouped experts, and its gradient               */
+/* ------------------------------------------------------------------------ */
+/*
+ * Both projections, the activation and the product of a gated feed-forward, for
+ * the tokens of expert e (rows d_offs[e] .. d_offs[e+1]-1):
+ *
+ *   a = x w_gate[e]^T,  b = x w_up[e]^T,  h = act(a) * b;
+ *   act 0: silu, a sigmoid(a);  act 1: gelu in its tanh form,
+ *          a sigmoid(2 sqrt(2/pi) (a + 0.044715 a^3)).
+ *
+ * Backward, from dh and the a and b that the forward call stored:
+ *   dgate = dh b act'(a),  dup = dh act(a),  dx = dgate w_gate[e] + dup w_up[e];
+ * the weights' gradients are dgr_grouped_wgrad_accumulate(dgate, x) and (dup, x).
+ *
+ * Products on the tensor cores (bf16 in, binary32 accumulators, K ascending);
+ * h is made from the unrounded a and b, and dx from dgate and dup as stored.
+ * Every output is rounded once and has one writer; the bits of a row depend on
+ * that row, the weights and H and F alone, not on its neighbours, the other
+ * experts, T or the launch.
+ *
+ * x: [T, H], h, gate, up, dh, dgate, dup: [T, F], dx: [T, H]: bf16, each with a
+ *           row stride; w_gate, w_up: [E, F, H] bf16, contiguous.
+ * d_offs:   [E+1] int64 DEVICE array, non-decreasing, d_offs[0] = 0, d_offs[E] = T,
+ *           or null with E = 1. Offsets outside this contract record
+ *           DGR_ERR_INVALID_ARG in the status word; h, gate, up and dx are then
+ *           not written.
+ * gate, up: forward: a and b, or null each; backward: those (not null).
+ * dx may be null (dgate and dup alone).
+ * Limits:   H and F multiples of 8 up to 2^20, 1 <= E <= 1024, T < 2^31 - 256.
+ * Alignment: pointers 16 bytes, row strides multiples of 8 elements.
+ * ws:       dgr_gated_ffn_workspace_bytes(T, H, F, E) bytes, zeroed once (status
+ *           word); it may go on to calls with other sizes as it is.
+ * dgate may be gate and dup may be up (same pointer and stride); nothing else
+ * may overlap.
+ */
+size_t dgr_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t F, int32_t E);
+dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_gate, const void *w_up, const int64_t *d_offs,
+                         int32_t E, int64_t T, int64_t H, int64_t F, int32_t act, void *h, int64_t ld_h, void *gate,
+                         int64_t ld_gate, void *up, int64_t ld_up, void *ws, size_t ws_bytes, void *stream);
+dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gate, int64_t ld_gate, const void *up,
+                                  int64_t ld_up, const void *w_gate, const void *w_up, const int64_t *d_offs,
+                                  int32_t E, int64_t T, int64_t H, int64_t F, int32_t act, void *dgate,
+                                  int64_t ld_dgate, void *dup, int64_t ld_dup, void *dx, int64_t ld_dx, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* 13. Norm of queries and keys a head with their rotation by position       */
+/* ------------------------------------------------------------------------ */
+/*
+ * For every head v [D] of every token, with the token's position pos:
+ *
+ *   n = v * r * w,                    r = (mean(v^2) + eps)^(-1/2);
+ *   (y_i, y_j) = (n_i c - n_j s, n_j c + n_i s) for each of the R/2 pairs (i, j),
+ *   c = cos[pos][pair], s = sin[pos][pair]; elements R .. D-1: y = n.
+ *
+ * Pair m is (m, m + R/2), or with interleaved != 0 (2m, 2m + 1). w null: 1.
+ *
+ * Backward, from the gradients of y: g = those turned back (s -> -s),
+ *   dw = sum over tokens and heads of g v r,
+ *   dv = r (g w) - (r^3 / D) (g w . v) v.
+ * dw_q and dw_k may be null; they are written, or added to with one rounding
+ * (accumulate != 0). T = 0: 0, or left as they are but for a -0.
+ *
+ * Binary32 throughout, each output rounded once. The order of every sum depends
+ * on the type, T, the head counts, D, R, interleaved and the alignment alone.
+ *
+ * q: [T, n_q, D], k: [T, n_k, D] bf16 or fp32 (dtype), element (t, head, d) at
+ *           t * token + head * head_stride + d; heads and tokens of one tensor
+ *           must not overlap one another, but q and k may lie in one packed row.
+ *           The same for q_out, k_out, dq_out, dk_out, dq, dk. n_q or n_k may
+ *           be 0 (its pointers are then not used).
+ * w_q, w_k: [D] bf16 or fp32 (w_dtype); dw_q, dw_k: [D] fp32.
+ * cos, sin: [P, R/2] fp32, contiguous; positions: [T] int32. A token with a
+ *           position outside [0, P) gets zeros (forward: y, backward: dv, and no
+ *           part in dw) and records DGR_ERR_INVALID_ARG in the status word.
+ * Limits:   D even, 2 <= D <= 512; R even, 2 <= R <= D; head counts up to 1024,
+ *           T <= 2^26.
+ * ws:       dgr_qk_norm_rope_workspace_bytes(T, n_q, n_k, D) bytes for the
+ *           backward call, 256 for the forward one, zeroed once; it may go on to
+ *           calls with other sizes as it is.
+ * q_out may be q, k_out may be k, dq may be dq_out and dk may be dk_out (same
+ * pointer and strides); nothing else may overlap.
+ */
+size_t dgr_qk_norm_rope_workspace_bytes(int64_t T, int32_t n_q, int32_t n_k, int32_t D);
+dgr_status dgr_qk_norm_rope(const void *q, int64_t q_token, int64_t q_head, int32_t n_q, const void *k,
+                            int64_t k_token, int64_t k_head, int32_t n_k, int32_t dtype, int64_t T, int32_t D,
+                            const void *w_q, const void *w_k, int32_t w_dtype, const float *cos, const float *sin,
+                            int32_t P, int32_t R, int32_t interleaved, const int32_t *positions, float eps,
+                            void *q_out, int64_t qo_token, int64_t qo_head, void *k_out, int64_t ko_token,
+                            int64_t ko_head, void *ws, size_t ws_bytes, void *stream);
+dgr_status dgr_qk_norm_rope_backward(const void *dq_out, int64_t dqo_token, int64_t dqo_head, const void *dk_out,
+                                     int64_t dko_token, int64_t dko_head, const void *q, int64_t q_token,
+                                     int64_t q_head, int32_t n_q, const void *k, int64_t k_token, int64_t k_head,
+                                     int32_t n_k, int32_t dtype, int64_t T, int32_t D, const void *w_q,
+                                     const void *w_k, int32_t w_dtype, const float *cos, const float *sin, int32_t P,
+                                     int32_t R, int32_t interleaved, const int32_t *positions, float eps, void *dq,
+                                     int64_t dq_token, int64_t dq_head, void *dk, int64_t dk_token, int64_t dk_head,
+                                     float *dw_q, float *dw_k, int32_t accumulate, void *ws, size_t ws_bytes,
+                                     void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* 14. Token log probabilities, entropy and top alternatives                 */
+/* ------------------------------------------------------------------------ */
+/*
+ * For each row of logits z [V] at temperature tau, with m its largest:
+ *
+ *   s = sum_j exp((z_j - m) / tau),  ln p_j = (z_j - m) / tau - ln s;
+ *   logp[t] = ln p_id,  entropy[t] = -sum_j p_j ln p_j,  lse[t] = m / tau + ln s,
+ *   stats[t] = (m, ln s);
+ *   top_ids[t][0 .. K-1]: the K largest logits above -inf, in descending order,
+ *   equal ones by the lower index; top_logits their logits as they are and
+ *   top_logp their ln p. Where there are fewer, the rest has id -1 and -inf.
+ *   top_ids, top_logits and lse are what dgr_topk_distill takes as the teacher's
+ *   ids, teacher and teacher_lse.
+ *
+ * Backward, from dlogp and dentropy (null: 0) and the row's stats and entropy:
+ *   dz_j = (dlogp (1[j = id] - p_j) - dentropy p_j (ln p_j + entropy)) / tau.
+ *
+ * A row whose id is negative is not read: its outputs are 0, its list empty and
+ * its gradient 0; an id >= V is taken alike, and the forward call records
+ * DGR_ERR_INVALID_ARG in the status word. ids null (then without logp and dlogp):
+ * every row counts. Logits of -inf have probability 0; a row of nothing else
+ * has logp and lse -inf, entropy 0 and gradient 0. A NaN, or a logit of +inf,
+ * makes its row's logp, entropy, lse, ln s, top_logp and gradient NaN; a NaN is
+ * in no list.
+ * Sums are binary32 in an order that depends on the type, T, V, the alignment of
+ * the logits' rows and whether K is 0. Each output is rounded once.
+ *
+ * logits:   [T, V] bf16 or fp32 (dtype), row stride ld; ids [T] int32 or null.
+ * logp, entropy, lse: [T] fp32; stats: [T, 2] fp32; top_ids int32, top_logits and
+ *           top_logp fp32: [T, K]. Each may be null, not all; the three lists
+ *           exactly if K = 0.
+ * dlogits:  [T, V] of dtype, row stride ld_d. One of dlogp and dentropy is given
+ *           at least; dlogp needs ids, dentropy needs entropy.
+ * Limits:   1 <= V <= 2^20, 0 <= K <= 256, T <= 2^26, 1e-6 <= tau <= 1e6.
+ * ws:       dgr_token_logprobs_workspace_bytes(T) bytes, zeroed once (status
+ *           word); it may go on to calls with other sizes. Backward needs none.
+ * dlogits may be logits (same pointer and stride); nothing else may overlap.
+ */
+size_t dgr_token_logprobs_workspace_bytes(int64_t T);
+dgr_status dgr_token_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                              const int32_t *ids, float tau, int32_t K, float *logp, float *entropy, float *lse,
+                              float *stats, int32_t *top_ids, float *top_logits, float *top_logp, void *ws,
+                              size_t ws_bytes, void *stream);
+dgr_status dgr_token_logprobs_backward(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                       const int32_t *ids, float tau, const float *stats, const float *entropy,
+                                       const float *dlogp, const float *dentropy, void *dlogits, int64_t ld_d,
+                                       void *stream);
 
 #ifdef __cplusplus
 }
