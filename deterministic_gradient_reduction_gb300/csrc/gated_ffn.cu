@@ -51,16 +51,17 @@ constexpr uint32_t kLboN = 64 * 128;    // N-major: between 64-wide atoms along 
 
 enum { kSilu = 0, kGelu = 1 };
 
-template <int BN>
+// CG CTAs share a tile of CG * 128 rows by BN columns of the product.
+template <int CG, int BN>
 struct Shape {
-    static constexpr uint32_t kStageB = BN * 128;
+    static constexpr uint32_t kStageB = BN / CG * 128;
     static constexpr uint32_t kStage = kStageA + kStageB;
     static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
     static constexpr uint32_t kTmemCols = 2 * BN;
     // tcgen05 instruction descriptor: fp32 D, bf16 A and B, A K-major, B K-major or (bit 16) N-major
     static __host__ __device__ constexpr uint32_t idesc(bool n_major) {
         return (1u << 4) | (1u << 7) | (1u << 10) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN >> 3) << 17) |
-               (static_cast<uint32_t>(BM >> 4) << 24);
+               (static_cast<uint32_t>(CG * BM >> 4) << 24);
     }
 };
 
@@ -73,8 +74,8 @@ struct Ctl {
     int abort;
 };
 
-template <int BN>
-constexpr size_t kSmem = 1024 + Shape<BN>::kStages * Shape<BN>::kStage + sizeof(Ctl);
+template <int CG, int BN>
+constexpr size_t kSmem = 1024 + Shape<CG, BN>::kStages * Shape<CG, BN>::kStage + sizeof(Ctl);
 
 struct FfnParams {
     const int64_t *offs;  // or null: one expert with all rows
@@ -187,13 +188,88 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
+// ---- pairs of CTAs (clusters of two: the even one leads) -----------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The leader's copy of a barrier.
+__device__ __forceinline__ uint32_t of_leader(const uint64_t *bar) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+    return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A copy into this CTA that reports to the leader's barrier.
+__device__ __forceinline__ void pair_load_3d(void *smem_dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (CG == 1) {
+        mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    }
+}
+// Arrive on `bar`, of both CTAs of a pair, once every MMA issued so far by this thread is done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (CG == 1) {
+        mma_commit(bar);
+    } else {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                     "h"(static_cast<uint16_t>(3))
+                     : "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void alloc_tmem(uint32_t *dst, uint32_t cols) {
+    if constexpr (CG == 1) {
+        tmem_alloc(dst, cols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void free_tmem(uint32_t taddr, uint32_t cols) {
+    if constexpr (CG == 1) tmem_dealloc(taddr, cols);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+// All threads of the CTA, or of both.
+template <int CG>
+__device__ __forceinline__ void tile_sync() {
+    if constexpr (CG == 1) __syncthreads();
+    else cluster_barrier();
+}
+
 // FWD: a, b and h; else dx. Maps: A (and A2, the second part's), B and B2
 // (forward Wg and Wu, FT rows a box; backward the same, 64 x 64 atoms).
-template <int BN, bool FWD>
+template <int CG, int BN, bool FWD>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2, const FfnParams p) {
-    using S = Shape<BN>;
+    using S = Shape<CG, BN>;
+    constexpr int kRows = CG * BM;
     constexpr int kStages = S::kStages;
     constexpr int kCols = FWD ? BN / 2 : BN;  // columns of the output a tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -204,9 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int32_t bad;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const int rank = CG == 1 ? 0 : static_cast<int>(cluster_rank());
+    const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;  // tiles of this CTA or pair
     volatile int *abort_flag = &ctl->abort;
 
-    if (!row_blocks(p, BM, mb_base, wsum, &bad)) {
+    if (!row_blocks(p, kRows, mb_base, wsum, &bad)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, 400);
         return;
     }
@@ -222,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], 1);
-            mbar_init(&ctl->tempty[b], kEpiWarps);
+            mbar_init(&ctl->tempty[b], CG * kEpiWarps);
         }
         ctl->abort = 0;
         fence_mbar_init();
@@ -232,11 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!FWD) prefetch_tmap(&tmA2);
     }
     if (warp == 1) {
-        tmem_alloc(&ctl->tmem_base, S::kTmemCols);
-        tmem_relinquish();
+        alloc_tmem<CG>(&ctl->tmem_base, S::kTmemCols);
     }
     tc_fence_before();
-    __syncthreads();
+    tile_sync<CG>();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
 
@@ -247,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool armed[kStages] = {};
             uint32_t armed_phase[kStages] = {};
             bool ok = true;
-            for (uint32_t tau = blockIdx.x; ok && tau < n_tiles; tau += gridDim.x) {
-                const Tile t = tile_of(p, BM, mb_base, sched_item(sched, tau));
+            for (uint32_t tau = first; ok && tau < n_tiles; tau += step) {
+                const Tile t = tile_of(p, kRows, mb_base, sched_item(sched, tau));
                 for (int kb = 0; kb < n_k; ++kb) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1, abort_flag, p.hdr, 401)) {
                         ok = false;
@@ -256,21 +333,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t *sA = smem + stage * S::kStage;
                     uint8_t *sB = sA + kStageA;
-                    uint64_t *bar = &ctl->full[stage];
-                    mbar_arrive_expect_tx(bar, S::kStage);
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], CG * S::kStage);
                     armed[stage] = true;
                     armed_phase[stage] = phase;
+                    auto load = [&](uint8_t *to, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+                        if (CG == 1) tma_load_3d(to, map, &ctl->full[stage], x, y, z);
+                        else pair_load_3d(to, map, of_leader(&ctl->full[stage]), x, y, z);
+                    };
+                    // a pair's CTAs have 128 of its rows each and half of its columns
                     if (FWD) {
-                        tma_load_3d(sA, &tmA, bar, kb * BK, t.row, 0);
-                        tma_load_3d(sB, &tmB, bar, kb * BK, t.nb * kCols, t.e);
-                        tma_load_3d(sB + kCols * 128, &tmB2, bar, kb * BK, t.nb * kCols, t.e);
+                        load(sA, &tmA, kb * BK, t.row + rank * BM, 0);
+                        if (CG == 1) {
+                            load(sB, &tmB, kb * BK, t.nb * kCols, t.e);
+                            load(sB + kCols * 128, &tmB2, kb * BK, t.nb * kCols, t.e);
+                        } else {
+                            load(sB, rank ? &tmB2 : &tmB, kb * BK, t.nb * kCols, t.e);
+                        }
                     } else {
                         const bool second = kb >= part_k;
                         const int k0 = (second ? kb - part_k : kb) * BK;
-                        tma_load_3d(sA, second ? &tmA2 : &tmA, bar, k0, t.row, 0);
+                        load(sA, second ? &tmA2 : &tmA, k0, t.row + rank * BM, 0);
 #pragma unroll
-                        for (int j = 0; j < BN / 64; ++j)
-                            tma_load_3d(sB + j * kLboN, second ? &tmB2 : &tmB, bar, t.nb * BN + 64 * j, k0, t.e);
+                        for (int j = 0; j < BN / CG / 64; ++j)
+                            load(sB + j * kLboN, second ? &tmB2 : &tmB, t.nb * BN + rank * (BN / CG) + 64 * j, k0, t.e);
                     }
                     if (++stage == kStages) {
                         stage = 0;
@@ -278,19 +363,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok) {  // aborted: let our copies in flight land (bounded) before the CTA exits
+            if (!ok && rank == 0) {  // aborted: let the copies in flight land (bounded) before the CTA, or the pair, exits
                 int dummy = 0;
                 for (int s = 0; s < kStages; ++s)
                     if (armed[s]) mbar_wait(&ctl->full[s], armed_phase[s], &dummy, nullptr, kWaitLimitNs);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer ----------------
         constexpr uint32_t kIdesc = S::idesc(!FWD);
         uint32_t stage = 0, phase = 0, g = 0;
         uint32_t last_stage = 0, last_phase = 0;  // the latest stage-release commit
         bool committed = false, ok = true;
-        for (uint32_t tau = blockIdx.x; ok && tau < n_tiles; tau += gridDim.x, ++g) {
+        for (uint32_t tau = first; ok && tau < n_tiles; tau += step, ++g) {
             const uint32_t buf = g & 1, tph = (g >> 1) & 1;
             if (!mbar_wait(&ctl->tempty[buf], tph ^ 1, abort_flag, p.hdr, 402)) {
                 ok = false;
@@ -313,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ad[kk] = smem_desc_sw128(a0 + kk * 32, kLboK, kSBO);
                         bd[kk] = FWD ? smem_desc_sw128(b0 + kk * 32, kLboK, kSBO) : smem_desc_sw128(b0 + kk * 2048, kLboN, kSBO);
                     }
-                    mma_bf16(d_tmem, ad[0], bd[0], kIdesc, kb > 0 ? 1u : 0u);
-                    mma_bf16(d_tmem, ad[1], bd[1], kIdesc, 1u);
-                    mma_bf16(d_tmem, ad[2], bd[2], kIdesc, 1u);
-                    mma_bf16(d_tmem, ad[3], bd[3], kIdesc, 1u);
-                    mma_commit(&ctl->empty[stage]);
+                    mma<CG>(d_tmem, ad[0], bd[0], kIdesc, kb > 0 ? 1u : 0u);
+                    mma<CG>(d_tmem, ad[1], bd[1], kIdesc, 1u);
+                    mma<CG>(d_tmem, ad[2], bd[2], kIdesc, 1u);
+                    mma<CG>(d_tmem, ad[3], bd[3], kIdesc, 1u);
+                    commit<CG>(&ctl->empty[stage]);
                 }
                 __syncwarp();
                 committed = true;
@@ -329,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            if (lane == 0) mma_commit(&ctl->tfull[buf]);
+            if (lane == 0) commit<CG>(&ctl->tfull[buf]);
             __syncwarp();
         }
         if (!ok && committed) {
@@ -343,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;         // TMEM lane quarter this warp may access
         const int half = (warp - 4) >> 2;
         uint32_t g = 0;
-        for (uint32_t tau = blockIdx.x; tau < n_tiles; tau += gridDim.x, ++g) {
-            const Tile t = tile_of(p, BM, mb_base, sched_item(sched, tau));
-            const int32_t row = t.row + 32 * q + lane;
+        for (uint32_t tau = first; tau < n_tiles; tau += step, ++g) {
+            const Tile t = tile_of(p, kRows, mb_base, sched_item(sched, tau));
+            const int32_t row = t.row + rank * BM + 32 * q + lane;
             const bool mine = row < t.end;
             const uint32_t buf = g & 1, tph = (g >> 1) & 1;
             if (!mbar_wait(&ctl->tfull[buf], tph, abort_flag, p.hdr, 404)) break;
@@ -379,14 +464,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the accumulator is read: the MMA may refill it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->tempty[buf]);
+            if (lane == 0) {
+                if (CG == 1) mbar_arrive(&ctl->tempty[buf]);
+                else arrive_at(of_leader(&ctl->tempty[buf]));
+            }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    tile_sync<CG>();  // no CTA of a pair leaves while the other reads its memory
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, S::kTmemCols);
+        free_tmem<CG>(tmem, S::kTmemCols);
     }
 }
 
@@ -467,9 +555,15 @@ struct Operand {
     const void *b, *b2;
 };
 
-template <int BN, bool FWD>
-dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
-    constexpr int kCols = FWD ? BN / 2 : BN;
+// Row blocks of `rows` rows at most: every expert may end in a ragged one.
+int64_t row_blocks_most(const FfnParams &p, int rows) {
+    const int64_t whole = (static_cast<int64_t>(p.T) + rows - 1) / rows;
+    return p.offs ? whole + (p.E < p.T ? p.E : p.T) : whole;
+}
+
+template <int CG, int BN, bool FWD>
+dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
+    constexpr int kCols = FWD ? BN / 2 : BN, kRows = CG * BM;
     CUtensorMap mA, mA2, mB, mB2;
     dgr_status st;
     if ((st = make_map(&mA, o.a, p.K, p.T, o.ld_a, 1, BM)) != DGR_OK) return st;
@@ -480,13 +574,36 @@ dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
     const uint32_t box = FWD ? kCols : 64;
     if ((st = make_map(&mB, o.b, H, F, H, p.E, box)) != DGR_OK || (st = make_map(&mB2, o.b2, H, F, H, p.E, box)) != DGR_OK) return st;
     p.nbs = (p.N + kCols - 1) / kCols;
-    const int64_t blocks = (static_cast<int64_t>(p.T) + BM - 1) / BM + (p.offs ? p.E : 0);
+    const int64_t blocks = row_blocks_most(p, kRows);
     if (blocks * p.nbs > INT32_MAX) return DGR_ERR_UNSUPPORTED;
-    auto *k = ffn_gemm<BN, FWD>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem<BN>)) != cudaSuccess) return DGR_ERR_CUDA;
-    const int64_t tiles = blocks * p.nbs;
-    k<<<sched_grid(static_cast<unsigned>(tiles < sms ? tiles : sms)), kThreads, kSmem<BN>, s>>>(mA, mA2, mB, mB2, p);
-    return launch_status();
+    auto *k = ffn_gemm<CG, BN, FWD>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem<CG, BN>)) != cudaSuccess) return DGR_ERR_CUDA;
+    const int64_t tiles = blocks * p.nbs, most = sms / CG > 0 ? sms / CG : 1;
+    cudaLaunchConfig_t cfg{};
+    const unsigned groups = sched_grid(static_cast<unsigned>((tiles < most ? tiles : most) * CG)) / CG;
+    cfg.gridDim = dim3((groups > 0 ? groups : 1) * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem<CG, BN>;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
+}
+
+// Which tile: pairs of CTAs where the experts have enough rows to fill their 256,
+// else single CTAs; there the weights' reading counts, and narrower tiles put it
+// on more SMs.
+template <bool FWD>
+dgr_status launch_gemm(const FfnParams &p, const Operand &o, int sms, cudaStream_t s) {
+    if (p.T >= 192 * static_cast<int64_t>(p.E)) return launch_tiles<2, 256, FWD>(p, o, sms, s);
+    auto tiles = [&](int cols) { return row_blocks_most(p, BM) * ((p.N + cols - 1) / cols); };
+    constexpr int kWide = FWD ? 64 : 128;  // columns of the output of a 128-wide tile
+    if (tiles(kWide) * 5 >= static_cast<int64_t>(sms) * 4) return launch_tiles<1, 128, FWD>(p, o, sms, s);
+    return launch_tiles<1, 64, FWD>(p, o, sms, s);
 }
 
 // What both entries check of the rows, sizes, offsets and workspace.
@@ -552,7 +669,7 @@ extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_g
     if ((st = usable_sms(&sms)) != DGR_OK) return st;
     const Operand o{x, nullptr, ld_x, 0, w_gate, w_up};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launch_gemm<256, true>(p, o, sms, s);
+    return launch_gemm<true>(p, o, sms, s);
 }
 
 extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gate, int64_t ld_gate, const void *up,
@@ -611,5 +728,5 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
     p.hdr = static_cast<WsHeader *>(ws);
     p.sched = sched_setting();
     const Operand o{dgate, dup, ld_dgate, ld_dup, w_gate, w_up};
-    return launch_gemm<256, false>(p, o, sms, s);
+    return launch_gemm<false>(p, o, sms, s);
 }
