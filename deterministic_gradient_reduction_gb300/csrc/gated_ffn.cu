@@ -83,6 +83,7 @@ struct FfnParams {
     int32_t K;            // of one part (forward: H, backward: F)
     int32_t N;            // columns of the output (forward: F, backward: H)
     int32_t nbs;          // column blocks
+    int32_t box;          // rows of x (or da, db) in one copy: 8, 32 or 128
     int32_t act;
     uint16_t *out, *gate, *up;  // forward: h and, or null, a and b; backward: dx
     int64_t ld_out, ld_gate, ld_up;
@@ -326,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (uint32_t tau = first; ok && tau < n_tiles; tau += step) {
                 const Tile t = tile_of(p, kRows, mb_base, sched_item(sched, tau));
+                // few rows: only the copies that hold some of the tile's (the rest of A's
+                // space keeps what it had; those rows' products are not written)
+                const int boxes = p.box == BM ? 1 : (min(t.end - t.row, BM) + p.box - 1) / p.box;
+                const uint32_t bytes = CG * (static_cast<uint32_t>(boxes * p.box) * 128u + S::kStageB);
                 for (int kb = 0; kb < n_k; ++kb) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1, abort_flag, p.hdr, 401)) {
                         ok = false;
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t *sA = smem + stage * S::kStage;
                     uint8_t *sB = sA + kStageA;
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], CG * S::kStage);
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], bytes);
                     armed[stage] = true;
                     armed_phase[stage] = phase;
                     auto load = [&](uint8_t *to, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // a pair's CTAs have 128 of its rows each and half of its columns
                     if (FWD) {
-                        load(sA, &tmA, kb * BK, t.row + rank * BM, 0);
+                        for (int b = 0; b < boxes; ++b) load(sA + b * p.box * 128, &tmA, kb * BK, t.row + rank * BM + b * p.box, 0);
                         if (CG == 1) {
                             load(sB, &tmB, kb * BK, t.nb * kCols, t.e);
                             load(sB + kCols * 128, &tmB2, kb * BK, t.nb * kCols, t.e);
@@ -352,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         const bool second = kb >= part_k;
                         const int k0 = (second ? kb - part_k : kb) * BK;
-                        load(sA, second ? &tmA2 : &tmA, k0, t.row + rank * BM, 0);
+                        for (int b = 0; b < boxes; ++b)
+                            load(sA + b * p.box * 128, second ? &tmA2 : &tmA, k0, t.row + rank * BM + b * p.box, 0);
 #pragma unroll
                         for (int j = 0; j < BN / CG / 64; ++j)
                             load(sB + j * kLboN, second ? &tmB2 : &tmB, t.nb * BN + rank * (BN / CG) + 64 * j, k0, t.e);
@@ -566,9 +572,10 @@ dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) 
     constexpr int kCols = FWD ? BN / 2 : BN, kRows = CG * BM;
     CUtensorMap mA, mA2, mB, mB2;
     dgr_status st;
-    if ((st = make_map(&mA, o.a, p.K, p.T, o.ld_a, 1, BM)) != DGR_OK) return st;
+    p.box = CG == 2 || p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
+    if ((st = make_map(&mA, o.a, p.K, p.T, o.ld_a, 1, p.box)) != DGR_OK) return st;
     mA2 = mA;
-    if (!FWD && (st = make_map(&mA2, o.a2, p.K, p.T, o.ld_a2, 1, BM)) != DGR_OK) return st;
+    if (!FWD && (st = make_map(&mA2, o.a2, p.K, p.T, o.ld_a2, 1, p.box)) != DGR_OK) return st;
     // the weights are [E, F, H]: forward N = F by K = H, backward K = F by N = H
     const int64_t F = FWD ? p.N : p.K, H = FWD ? p.K : p.N;
     const uint32_t box = FWD ? kCols : 64;
