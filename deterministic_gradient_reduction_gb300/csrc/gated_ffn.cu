@@ -51,39 +51,41 @@ constexpr uint32_t kLboN = 64 * 128;    // N-major: between 64-wide atoms along 
 
 enum { kSilu = 0, kGelu = 1 };
 
-// CG CTAs share a tile of CG * 128 rows by BN columns of the product.
-template <int CG, int BN>
-struct Shape {
-    static constexpr uint32_t kStageB = BN / CG * 128;
-    static constexpr uint32_t kStage = kStageA + kStageB;
-    static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
-    static constexpr uint32_t kTmemCols = 2 * BN;
-    // tcgen05 instruction descriptor: fp32 D, bf16 A and B, A K-major, B K-major or (bit 16) N-major
-    static __host__ __device__ constexpr uint32_t idesc(bool n_major) {
-        return (1u << 4) | (1u << 7) | (1u << 10) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN >> 3) << 17) |
-               (static_cast<uint32_t>(CG * BM >> 4) << 24);
-    }
+// CG CTAs share a tile of CG * 128 rows. Pairs have 256 columns of the product;
+// a single CTA's width goes by the call (Tiles, below).
+constexpr int kMaxStages = 8;
+constexpr int kMaxN = 256;  // columns of the product a tile: half of TMEM
+// tcgen05 instruction descriptor: fp32 D, bf16 A and B, A K-major, B K-major or (bit 16) N-major
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool n_major) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// How a call is cut into tiles and stages.
+struct Tiles {
+    int32_t cols;    // columns of the output a tile
+    int32_t nbs;     // column blocks
+    int32_t box;     // rows of x (or da, db) in one copy: 8, 32 or 128
+    int32_t stages;  // slots of the ring
 };
 
 struct Ctl {
-    uint64_t full[8];
-    uint64_t empty[8];
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint32_t tmem_base;
     int abort;
 };
 
-template <int CG, int BN>
-constexpr size_t kSmem = 1024 + Shape<CG, BN>::kStages * Shape<CG, BN>::kStage + sizeof(Ctl);
+constexpr size_t kSmem = 1024 + kRing + sizeof(Ctl);
 
 struct FfnParams {
     const int64_t *offs;  // or null: one expert with all rows
     int32_t E, T;
     int32_t K;            // of one part (forward: H, backward: F)
     int32_t N;            // columns of the output (forward: F, backward: H)
-    int32_t nbs;          // column blocks
-    int32_t box;          // rows of x (or da, db) in one copy: 8, 32 or 128
+    Tiles cut;
     int32_t act;
     uint16_t *out, *gate, *up;  // forward: h and, or null, a and b; backward: dx
     int64_t ld_out, ld_gate, ld_up;
@@ -137,9 +139,9 @@ struct Tile {
 
 // tile tau: row blocks expert by expert, the column blocks of one after another
 __device__ __forceinline__ Tile tile_of(const FfnParams &p, int rows, const int32_t *mb_base, uint32_t tau) {
-    const int32_t gmb = static_cast<int32_t>(tau / static_cast<uint32_t>(p.nbs));
+    const int32_t gmb = static_cast<int32_t>(tau / static_cast<uint32_t>(p.cut.nbs));
     Tile t;
-    t.nb = static_cast<int>(tau - static_cast<uint32_t>(gmb) * static_cast<uint32_t>(p.nbs));
+    t.nb = static_cast<int>(tau - static_cast<uint32_t>(gmb) * static_cast<uint32_t>(p.cut.nbs));
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {  // the last expert that starts at or before gmb (empty ones start where the next does)
         const int mid = (lo + hi + 1) >> 1;
@@ -265,17 +267,18 @@ __device__ __forceinline__ void tile_sync() {
 
 // FWD: a, b and h; else dx. Maps: A (and A2, the second part's), B and B2
 // (forward Wg and Wu, FT rows a box; backward the same, 64 x 64 atoms).
-template <int CG, int BN, bool FWD>
+template <int CG, bool FWD>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2, const FfnParams p) {
-    using S = Shape<CG, BN>;
     constexpr int kRows = CG * BM;
-    constexpr int kStages = S::kStages;
-    constexpr int kCols = FWD ? BN / 2 : BN;  // columns of the output a tile
+    const int cols = CG == 2 ? (FWD ? kMaxN / 2 : kMaxN) : p.cut.cols;  // columns of the output a tile
+    const int width = FWD ? 2 * cols : cols;                            // of the product
+    const uint32_t stage_b = static_cast<uint32_t>(width / CG) * 128u, stage_bytes = kStageA + stage_b;
+    const uint32_t stages = CG == 2 ? kRing / (kStageA + kMaxN / 2 * 128) : static_cast<uint32_t>(p.cut.stages);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + kStages * S::kStage);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + kRing);
     __shared__ int32_t mb_base[kMaxExperts + 1];
     __shared__ int32_t wsum[kThreads / 32];
     __shared__ int32_t bad;
@@ -289,13 +292,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.hdr, DGR_ERR_INVALID_ARG, 400);
         return;
     }
-    const uint32_t n_tiles = static_cast<uint32_t>(mb_base[p.E]) * static_cast<uint32_t>(p.nbs);
+    const uint32_t n_tiles = static_cast<uint32_t>(mb_base[p.E]) * static_cast<uint32_t>(p.cut.nbs);
     const Sched sched = sched_over(p.sched, n_tiles);
     const int part_k = (p.K + BK - 1) / BK;  // stages of one part
     const int n_k = FWD ? part_k : 2 * part_k;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
         }
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!FWD) prefetch_tmap(&tmA2);
     }
     if (warp == 1) {
-        alloc_tmem<CG>(&ctl->tmem_base, S::kTmemCols);
+        alloc_tmem<CG>(&ctl->tmem_base, 2 * kMaxN);
     }
     tc_fence_before();
     tile_sync<CG>();
@@ -322,21 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- TMA producer ----------------
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
-            bool armed[kStages] = {};
-            uint32_t armed_phase[kStages] = {};
+            bool armed[kMaxStages] = {};
+            uint32_t armed_phase[kMaxStages] = {};
             bool ok = true;
             for (uint32_t tau = first; ok && tau < n_tiles; tau += step) {
                 const Tile t = tile_of(p, kRows, mb_base, sched_item(sched, tau));
                 // few rows: only the copies that hold some of the tile's (the rest of A's
                 // space keeps what it had; those rows' products are not written)
-                const int boxes = p.box == BM ? 1 : (min(t.end - t.row, BM) + p.box - 1) / p.box;
-                const uint32_t bytes = CG * (static_cast<uint32_t>(boxes * p.box) * 128u + S::kStageB);
+                const int boxes = p.cut.box == BM ? 1 : (min(t.end - t.row, BM) + p.cut.box - 1) / p.cut.box;
+                const uint32_t bytes = CG * (static_cast<uint32_t>(boxes * p.cut.box) * 128u + stage_b);
                 for (int kb = 0; kb < n_k; ++kb) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1, abort_flag, p.hdr, 401)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sA = smem + stage * S::kStage;
+                    uint8_t *sA = smem + stage * stage_bytes;
                     uint8_t *sB = sA + kStageA;
                     if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], bytes);
                     armed[stage] = true;
@@ -347,23 +350,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // a pair's CTAs have 128 of its rows each and half of its columns
                     if (FWD) {
-                        for (int b = 0; b < boxes; ++b) load(sA + b * p.box * 128, &tmA, kb * BK, t.row + rank * BM + b * p.box, 0);
+                        for (int b = 0; b < boxes; ++b) load(sA + b * p.cut.box * 128, &tmA, kb * BK, t.row + rank * BM + b * p.cut.box, 0);
                         if (CG == 1) {
-                            load(sB, &tmB, kb * BK, t.nb * kCols, t.e);
-                            load(sB + kCols * 128, &tmB2, kb * BK, t.nb * kCols, t.e);
+                            load(sB, &tmB, kb * BK, t.nb * cols, t.e);
+                            load(sB + cols * 128, &tmB2, kb * BK, t.nb * cols, t.e);
                         } else {
-                            load(sB, rank ? &tmB2 : &tmB, kb * BK, t.nb * kCols, t.e);
+                            load(sB, rank ? &tmB2 : &tmB, kb * BK, t.nb * cols, t.e);
                         }
                     } else {
                         const bool second = kb >= part_k;
                         const int k0 = (second ? kb - part_k : kb) * BK;
                         for (int b = 0; b < boxes; ++b)
-                            load(sA + b * p.box * 128, second ? &tmA2 : &tmA, k0, t.row + rank * BM + b * p.box, 0);
-#pragma unroll
-                        for (int j = 0; j < BN / CG / 64; ++j)
-                            load(sB + j * kLboN, second ? &tmB2 : &tmB, t.nb * BN + rank * (BN / CG) + 64 * j, k0, t.e);
+                            load(sA + b * p.cut.box * 128, second ? &tmA2 : &tmA, k0, t.row + rank * BM + b * p.cut.box, 0);
+                        for (int j = 0; j < cols / CG / 64; ++j)
+                            load(sB + j * kLboN, second ? &tmB2 : &tmB, t.nb * cols + rank * (cols / CG) + 64 * j, k0, t.e);
                     }
-                    if (++stage == kStages) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -371,13 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok && rank == 0) {  // aborted: let the copies in flight land (bounded) before the CTA, or the pair, exits
                 int dummy = 0;
-                for (int s = 0; s < kStages; ++s)
+                for (int s = 0; s < kMaxStages; ++s)
                     if (armed[s]) mbar_wait(&ctl->full[s], armed_phase[s], &dummy, nullptr, kWaitLimitNs);
             }
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer ----------------
-        constexpr uint32_t kIdesc = S::idesc(!FWD);
+        const uint32_t desc = idesc(kRows, width, !FWD);
         uint32_t stage = 0, phase = 0, g = 0;
         uint32_t last_stage = 0, last_phase = 0;  // the latest stage-release commit
         bool committed = false, ok = true;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t d_tmem = tmem + buf * BN;
+            const uint32_t d_tmem = tmem + buf * kMaxN;
             for (int kb = 0; kb < n_k; ++kb) {
                 if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.hdr, 403)) {
                     ok = false;
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 if (lane == 0) {
-                    const uint32_t a0 = smem_u32(smem + stage * S::kStage), b0 = a0 + kStageA;
+                    const uint32_t a0 = smem_u32(smem + stage * stage_bytes), b0 = a0 + kStageA;
                     // the stage's four K16 steps back to back, descriptors ready
                     uint64_t ad[4], bd[4];
 #pragma unroll
@@ -404,17 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ad[kk] = smem_desc_sw128(a0 + kk * 32, kLboK, kSBO);
                         bd[kk] = FWD ? smem_desc_sw128(b0 + kk * 32, kLboK, kSBO) : smem_desc_sw128(b0 + kk * 2048, kLboN, kSBO);
                     }
-                    mma<CG>(d_tmem, ad[0], bd[0], kIdesc, kb > 0 ? 1u : 0u);
-                    mma<CG>(d_tmem, ad[1], bd[1], kIdesc, 1u);
-                    mma<CG>(d_tmem, ad[2], bd[2], kIdesc, 1u);
-                    mma<CG>(d_tmem, ad[3], bd[3], kIdesc, 1u);
+                    mma<CG>(d_tmem, ad[0], bd[0], desc, kb > 0 ? 1u : 0u);
+                    mma<CG>(d_tmem, ad[1], bd[1], desc, 1u);
+                    mma<CG>(d_tmem, ad[2], bd[2], desc, 1u);
+                    mma<CG>(d_tmem, ad[3], bd[3], desc, 1u);
                     commit<CG>(&ctl->empty[stage]);
                 }
                 __syncwarp();
                 committed = true;
                 last_stage = stage;
                 last_phase = phase;
-                if (++stage == kStages) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1;
                 }
@@ -441,13 +443,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t buf = g & 1, tph = (g >> 1) & 1;
             if (!mbar_wait(&ctl->tfull[buf], tph, abort_flag, p.hdr, 404)) break;
             tc_fence_after();
-            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * BN;
-            const int c_tile = t.nb * kCols;
+            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kMaxN;
+            // 16 columns at a time, of a tile's last ones those that are its own
+            const int c_tile = t.nb * cols, c_end = min(c_tile + cols, p.N);
 #pragma unroll 1
-            for (int c = half * (kCols / 2); c < (half + 1) * (kCols / 2); c += 16) {
+            for (int c = 16 * half; c < cols; c += 32) {
                 uint32_t ra[16], rb[16];
                 tmem_ld16(base + c, ra);
-                if (FWD) tmem_ld16(base + kCols + c, rb);
+                if (FWD) tmem_ld16(base + cols + c, rb);
                 tmem_wait16(ra);
                 if (FWD) tmem_wait16(rb);
                 if (mine) {
@@ -458,12 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float b[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) b[i] = __uint_as_float(rb[i]);
-                        if (p.gate) store16(p.gate + row * p.ld_gate, c_tile + c, p.N, a);
-                        if (p.up) store16(p.up + row * p.ld_up, c_tile + c, p.N, b);
+                        if (p.gate) store16(p.gate + row * p.ld_gate, c_tile + c, c_end, a);
+                        if (p.up) store16(p.up + row * p.ld_up, c_tile + c, c_end, b);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) a[i] = __fmul_rn(__fmul_rn(a[i], gate_sigmoid(a[i], p.act)), b[i]);
                     }
-                    store16(p.out + row * p.ld_out, c_tile + c, p.N, a);
+                    store16(p.out + row * p.ld_out, c_tile + c, c_end, a);
                 }
                 __syncwarp();
             }
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_sync<CG>();  // no CTA of a pair leaves while the other reads its memory
     if (warp == 1) {
         tc_fence_after();
-        free_tmem<CG>(tmem, S::kTmemCols);
+        free_tmem<CG>(tmem, 2 * kMaxN);
     }
 }
 
@@ -555,6 +558,8 @@ dgr_status make_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows
     return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
 }
 
+constexpr int kTileCost = 16;  // of a tile, in columns
+
 struct Operand {
     const void *a, *a2;
     int64_t ld_a, ld_a2;
@@ -567,30 +572,30 @@ int64_t row_blocks_most(const FfnParams &p, int rows) {
     return p.offs ? whole + (p.E < p.T ? p.E : p.T) : whole;
 }
 
-template <int CG, int BN, bool FWD>
+template <int CG, bool FWD>
 dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
-    constexpr int kCols = FWD ? BN / 2 : BN, kRows = CG * BM;
+    constexpr int kRows = CG * BM;
     CUtensorMap mA, mA2, mB, mB2;
     dgr_status st;
-    p.box = CG == 2 || p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
-    if ((st = make_map(&mA, o.a, p.K, p.T, o.ld_a, 1, p.box)) != DGR_OK) return st;
+    if ((st = make_map(&mA, o.a, p.K, p.T, o.ld_a, 1, p.cut.box)) != DGR_OK) return st;
     mA2 = mA;
-    if (!FWD && (st = make_map(&mA2, o.a2, p.K, p.T, o.ld_a2, 1, p.box)) != DGR_OK) return st;
+    if (!FWD && (st = make_map(&mA2, o.a2, p.K, p.T, o.ld_a2, 1, p.cut.box)) != DGR_OK) return st;
     // the weights are [E, F, H]: forward N = F by K = H, backward K = F by N = H
     const int64_t F = FWD ? p.N : p.K, H = FWD ? p.K : p.N;
-    const uint32_t box = FWD ? kCols : 64;
+    const uint32_t box = FWD ? p.cut.cols : 64;
     if ((st = make_map(&mB, o.b, H, F, H, p.E, box)) != DGR_OK || (st = make_map(&mB2, o.b2, H, F, H, p.E, box)) != DGR_OK) return st;
-    p.nbs = (p.N + kCols - 1) / kCols;
-    const int64_t blocks = row_blocks_most(p, kRows);
-    if (blocks * p.nbs > INT32_MAX) return DGR_ERR_UNSUPPORTED;
-    auto *k = ffn_gemm<CG, BN, FWD>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem<CG, BN>)) != cudaSuccess) return DGR_ERR_CUDA;
-    const int64_t tiles = blocks * p.nbs, most = sms / CG > 0 ? sms / CG : 1;
+    p.cut.nbs = (p.N + p.cut.cols - 1) / p.cut.cols;
+    p.cut.stages = static_cast<int32_t>(kRing / (kStageA + static_cast<uint32_t>(FWD ? 2 * p.cut.cols : p.cut.cols) * 128u));
+    if (p.cut.stages > kMaxStages) p.cut.stages = kMaxStages;
+    const int64_t tiles = row_blocks_most(p, kRows) * p.cut.nbs, most = sms / CG > 0 ? sms / CG : 1;
+    if (tiles > INT32_MAX) return DGR_ERR_UNSUPPORTED;
+    auto *k = ffn_gemm<CG, FWD>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess) return DGR_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     const unsigned groups = sched_grid(static_cast<unsigned>((tiles < most ? tiles : most) * CG)) / CG;
     cfg.gridDim = dim3((groups > 0 ? groups : 1) * CG);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem<CG, BN>;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -601,16 +606,27 @@ dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) 
     return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
-// Which tile: pairs of CTAs where the experts have enough rows to fill their 256,
-// else single CTAs; there the weights' reading counts, and narrower tiles put it
-// on more SMs.
+// Which tiles: pairs of CTAs where the experts have enough rows to fill their 256
+// rows, else single CTAs. There the weights' reading counts, and the SM with the
+// most of it: the width of a tile is the one with the fewest columns in all waves
+// of tiles together, and a share for what a tile costs beside its weights.
 template <bool FWD>
-dgr_status launch_gemm(const FfnParams &p, const Operand &o, int sms, cudaStream_t s) {
-    if (p.T >= 192 * static_cast<int64_t>(p.E)) return launch_tiles<2, 256, FWD>(p, o, sms, s);
-    auto tiles = [&](int cols) { return row_blocks_most(p, BM) * ((p.N + cols - 1) / cols); };
-    constexpr int kWide = FWD ? 64 : 128;  // columns of the output of a 128-wide tile
-    if (tiles(kWide) * 5 >= static_cast<int64_t>(sms) * 4) return launch_tiles<1, 128, FWD>(p, o, sms, s);
-    return launch_tiles<1, 64, FWD>(p, o, sms, s);
+dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
+    if (p.T >= 192 * static_cast<int64_t>(p.E)) {
+        p.cut.cols = FWD ? kMaxN / 2 : kMaxN, p.cut.box = BM;
+        return launch_tiles<2, FWD>(p, o, sms, s);
+    }
+    p.cut.box = p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
+    constexpr int kStep = FWD ? 8 : 64, kMost = FWD ? kMaxN / 2 : kMaxN;
+    // row blocks as they are likely to be: a ragged one for most experts
+    const int64_t some = p.E < p.T ? p.E : p.T, half = (static_cast<int64_t>(p.T) + BM - 1) / BM + some / 2;
+    const int64_t blocks = some > half ? some : half;
+    int64_t best = INT64_MAX;
+    for (int cols = kMost; cols >= kStep; cols -= kStep) {
+        const int64_t tiles = blocks * ((p.N + cols - 1) / cols), cost = (tiles + sms - 1) / sms * (cols + kTileCost);
+        if (cost < best) best = cost, p.cut.cols = cols;
+    }
+    return launch_tiles<1, FWD>(p, o, sms, s);
 }
 
 // What both entries check of the rows, sizes, offsets and workspace.
