@@ -78,7 +78,13 @@ struct Ctl {
     int abort;
 };
 
-constexpr size_t kSmem = 1024 + kRing + sizeof(Ctl);
+constexpr uint32_t kBox = 32 * 64;  // an epilogue warp's block of 32 x 32 bf16
+constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kBox + sizeof(Ctl);
+
+// Maps over the outputs, for whole blocks of 32 rows by 32 columns (h, a, b; or dx).
+struct Outputs {
+    CUtensorMap out, gate, up;
+};
 
 struct FfnParams {
     const int64_t *offs;  // or null: one expert with all rows
@@ -86,7 +92,6 @@ struct FfnParams {
     int32_t K;            // of one part (forward: H, backward: F)
     int32_t N;            // columns of the output (forward: F, backward: H)
     Tiles cut;
-    int32_t act;
     uint16_t *out, *gate, *up;  // forward: h and, or null, a and b; backward: dx
     int64_t ld_out, ld_gate, ld_up;
     WsHeader *hdr;
@@ -154,11 +159,22 @@ __device__ __forceinline__ Tile tile_of(const FfnParams &p, int rows, const int3
     return t;
 }
 
-// sigmoid(s(v)): 1 / (1 + 2^(-s log2 e)); an exponential beyond the range gives 0.
-__device__ __forceinline__ float gate_sigmoid(float v, int act) {
-    float s = v;
-    if (act == kGelu) s = __fmul_rn(1.5957691216057308f, __fmaf_rn(__fmul_rn(0.044715f, __fmul_rn(v, v)), v, v));
-    return __fdividef(1.0f, __fadd_rn(1.0f, row::ex2(__fmul_rn(s, -row::kLog2e))));
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// sigmoid(s(v)) = 1 / (1 + 2^(-s log2 e)), two at a time; an exponential beyond
+// the range gives 0. Approximations of 2^x and 1 / x are good to a unit or two.
+template <int ACT>
+__device__ __forceinline__ float2 gate_sigmoid(float2 v) {
+    constexpr float kTwice = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    float2 t;
+    if (ACT == kSilu) t = mul2(v, row::both(-row::kLog2e));
+    else t = mul2(v, row::fma2(mul2(v, v), row::both(-kTwice * 0.044715f * row::kLog2e), row::both(-kTwice * row::kLog2e)));
+    const float2 d = row::fma2(make_float2(row::ex2(t.x), row::ex2(t.y)), row::both(1.0f), row::both(1.0f));
+    return make_float2(rcp(d.x), rcp(d.y));
 }
 
 // 16 bf16 values to columns c .. c + 15 of a row, those below n (a multiple of 8).
@@ -176,6 +192,28 @@ __device__ __forceinline__ void store16(uint16_t *to, int c, int n, const float 
         if (c + 16 <= n) *reinterpret_cast<uint4 *>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
+
+// A lane's row of 16 values as 16-byte chunks i and i + 1 of its 64 bytes in a 32 x
+// 32 block, in the 64-byte swizzle of its map (chunk ^ row / 2 % 4): the lanes of
+// a store spread over the banks.
+__device__ __forceinline__ void block_row(uint32_t box, int lane, int i, const float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t to = box + lane * 64 + 16 * ((i + j) ^ (lane >> 1 & 3));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(row::pack2(v[8 * j], v[8 * j + 1])), "r"(row::pack2(v[8 * j + 2], v[8 * j + 3])),
+                     "r"(row::pack2(v[8 * j + 4], v[8 * j + 5])), "r"(row::pack2(v[8 * j + 6], v[8 * j + 7]))
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void store_2d(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The thread's committed copies have read their shared memory; are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -267,10 +305,11 @@ __device__ __forceinline__ void tile_sync() {
 
 // FWD: a, b and h; else dx. Maps: A (and A2, the second part's), B and B2
 // (forward Wg and Wu, FT rows a box; backward the same, 64 x 64 atoms).
-template <int CG, bool FWD>
+template <int CG, bool FWD, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
-             const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2, const FfnParams p) {
+             const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
+             const __grid_constant__ Outputs outs, const FfnParams p) {
     constexpr int kRows = CG * BM;
     const int cols = CG == 2 ? (FWD ? kMaxN / 2 : kMaxN) : p.cut.cols;  // columns of the output a tile
     const int width = FWD ? 2 * cols : cols;                            // of the product
@@ -278,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stages = CG == 2 ? kRing / (kStageA + kMaxN / 2 * 128) : static_cast<uint32_t>(p.cut.stages);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + kRing);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + kRing + kEpiWarps * kBox);
     __shared__ int32_t mb_base[kMaxExperts + 1];
     __shared__ int32_t wsum[kThreads / 32];
     __shared__ int32_t bad;
@@ -435,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- epilogue ----------------
         const int q = warp & 3;         // TMEM lane quarter this warp may access
         const int half = (warp - 4) >> 2;
+        const uint32_t box = smem_u32(smem + kRing) + (warp - 4) * kBox;
         uint32_t g = 0;
         for (uint32_t tau = first; tau < n_tiles; tau += step, ++g) {
             const Tile t = tile_of(p, kRows, mb_base, sched_item(sched, tau));
@@ -444,31 +484,91 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mbar_wait(&ctl->tfull[buf], tph, abort_flag, p.hdr, 404)) break;
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kMaxN;
-            // 16 columns at a time, of a tile's last ones those that are its own
             const int c_tile = t.nb * cols, c_end = min(c_tile + cols, p.N);
-#pragma unroll 1
-            for (int c = 16 * half; c < cols; c += 32) {
-                uint32_t ra[16], rb[16];
-                tmem_ld16(base + c, ra);
-                if (FWD) tmem_ld16(base + cols + c, rb);
-                tmem_wait16(ra);
-                if (FWD) tmem_wait16(rb);
-                if (mine) {
-                    float a[16];
+            // products to outputs, 16 columns from c on
+            auto finish = [&](const uint32_t (&ra)[16], const uint32_t (&rb)[16], float (&h)[16]) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) a[i] = __uint_as_float(ra[i]);
-                    if constexpr (FWD) {
-                        float b[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) b[i] = __uint_as_float(rb[i]);
-                        if (p.gate) store16(p.gate + row * p.ld_gate, c_tile + c, c_end, a);
-                        if (p.up) store16(p.up + row * p.ld_up, c_tile + c, c_end, b);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) a[i] = __fmul_rn(__fmul_rn(a[i], gate_sigmoid(a[i], p.act)), b[i]);
-                    }
-                    store16(p.out + row * p.ld_out, c_tile + c, c_end, a);
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 a = make_float2(__uint_as_float(ra[i]), __uint_as_float(ra[i + 1]));
+                    const float2 b = make_float2(__uint_as_float(rb[i]), __uint_as_float(rb[i + 1]));
+                    const float2 v = mul2(mul2(a, gate_sigmoid<ACT>(a)), b);
+                    h[i] = v.x, h[i + 1] = v.y;
                 }
-                __syncwarp();
+            };
+            auto floats = [](const uint32_t (&r)[16], float (&f)[16]) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+            };
+            if (CG == 2 && t.row + rank * BM + 32 * q + 32 <= t.end) {
+                // a whole block of rows: 32 x 32 values through shared memory and the copy
+                // engine. Stores from the lanes (32 bytes a row each) take the shared
+                // memory's port that the MMAs read their operands by (FIGURES)
+                auto send = [&](const CUtensorMap *map, const float (&v0)[16], const float (&v1)[16], int c) {
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                    block_row(box, lane, 0, v0);
+                    block_row(box, lane, 2, v1);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store_2d(map, box, c_tile + c, row - lane);
+                        bulk_commit();
+                    }
+                };
+#pragma unroll 1
+                for (int c = 32 * half; c < cols && c_tile + c < p.N; c += 64) {
+                    uint32_t a0[16], a1[16];
+                    float v0[16], v1[16];
+                    tmem_ld16(base + c, a0);
+                    tmem_ld16(base + c + 16, a1);
+                    if constexpr (FWD) {
+                        uint32_t b0[16], b1[16];
+                        tmem_ld16(base + cols + c, b0);
+                        tmem_ld16(base + cols + c + 16, b1);
+                        tmem_wait16(a0), tmem_wait16(a1), tmem_wait16(b0), tmem_wait16(b1);
+                        if (p.gate) {
+                            floats(a0, v0), floats(a1, v1);
+                            send(&outs.gate, v0, v1, c);
+                        }
+                        if (p.up) {
+                            floats(b0, v0), floats(b1, v1);
+                            send(&outs.up, v0, v1, c);
+                        }
+                        finish(a0, b0, v0), finish(a1, b1, v1);
+                    } else {
+                        tmem_wait16(a0), tmem_wait16(a1);
+                        floats(a0, v0), floats(a1, v1);
+                    }
+                    send(&outs.out, v0, v1, c);
+                }
+            } else {
+                // 16 columns at a time, of a tile's last ones those that are its own
+#pragma unroll 1
+                for (int c = 16 * half; c < cols; c += 32) {
+                    uint32_t ra[16], rb[16];
+                    tmem_ld16(base + c, ra);
+                    if (FWD) tmem_ld16(base + cols + c, rb);
+                    tmem_wait16(ra);
+                    if (FWD) tmem_wait16(rb);
+                    if (mine) {
+                        float v[16];
+                        if constexpr (FWD) {
+                            if (p.gate) {
+                                floats(ra, v);
+                                store16(p.gate + row * p.ld_gate, c_tile + c, c_end, v);
+                            }
+                            if (p.up) {
+                                floats(rb, v);
+                                store16(p.up + row * p.ld_up, c_tile + c, c_end, v);
+                            }
+                            finish(ra, rb, v);
+                        } else {
+                            floats(ra, v);
+                        }
+                        store16(p.out + row * p.ld_out, c_tile + c, c_end, v);
+                    }
+                    __syncwarp();
+                }
             }
             // the accumulator is read: the MMA may refill it
             tc_fence_before();
@@ -478,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else arrive_at(of_leader(&ctl->tempty[buf]));
             }
         }
+        if (CG == 2 && lane == 0) bulk_wait();  // this warp's last blocks are written
     }
     tc_fence_before();
     tile_sync<CG>();  // no CTA of a pair leaves while the other reads its memory
@@ -493,20 +594,24 @@ struct PreParams {
     const uint16_t *dh, *gate, *up;
     uint16_t *dgate, *dup;
     int64_t ld_dh, ld_gate, ld_up, ld_dgate, ld_dup;
-    int32_t T, vecs, act;  // 8-element vectors a row
+    int32_t T, vecs;  // 8-element vectors a row
 };
 
 // da = dh b act'(a), db = dh act(a); act'(v) = g + v g (1 - g) s'(v), g = sigmoid(s(v)).
 // g (1 - g) is 0 long before s'(v) leaves the range, so their product counts as 0 then.
-__device__ __forceinline__ void pre_grad(float dh, float a, float b, int act, float &da, float &db) {
-    const float g = gate_sigmoid(a, act);
-    const float down = __fmul_rn(g, __fadd_rn(1.0f, -g));
-    float turn = down;
-    if (act == kGelu) turn = down > 0.0f ? __fmul_rn(down, __fmul_rn(1.5957691216057308f, __fmaf_rn(__fmul_rn(0.134145f, a), a, 1.0f))) : down;
-    db = __fmul_rn(dh, __fmul_rn(a, g));
-    da = __fmul_rn(__fmul_rn(dh, b), __fmaf_rn(a, turn, g));
+template <int ACT>
+__device__ __forceinline__ void pre_grad(float2 dh, float2 a, float2 b, float2 &da, float2 &db) {
+    const float2 g = gate_sigmoid<ACT>(a), down = mul2(g, row::fma2(g, row::both(-1.0f), row::both(1.0f)));
+    float2 turn = down;
+    if (ACT == kGelu) {
+        const float2 s = row::fma2(mul2(row::both(0.21405560f), a), a, row::both(1.5957691216057308f));  // 2 sqrt(2 / pi) (1 + 3 0.044715 a^2)
+        turn = make_float2(down.x > 0.0f ? __fmul_rn(down.x, s.x) : down.x, down.y > 0.0f ? __fmul_rn(down.y, s.y) : down.y);
+    }
+    db = mul2(dh, mul2(a, g));
+    da = mul2(mul2(dh, b), row::fma2(a, turn, g));
 }
 
+template <int ACT>
 __global__ void __launch_bounds__(256) ffn_pre_grad(const PreParams p) {
     const int64_t n = static_cast<int64_t>(p.T) * p.vecs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -517,7 +622,11 @@ __global__ void __launch_bounds__(256) ffn_pre_grad(const PreParams p) {
         row::unpack<row::bf16, 8>(*reinterpret_cast<const uint4 *>(p.gate + t * p.ld_gate + c), a);
         row::unpack<row::bf16, 8>(*reinterpret_cast<const uint4 *>(p.up + t * p.ld_up + c), b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) pre_grad(d[j], a[j], b[j], p.act, da[j], db[j]);
+        for (int j = 0; j < 8; j += 2) {
+            float2 x, y;
+            pre_grad<ACT>(make_float2(d[j], d[j + 1]), make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), x, y);
+            da[j] = x.x, da[j + 1] = x.y, db[j] = y.x, db[j + 1] = y.y;
+        }
         *reinterpret_cast<uint4 *>(p.dgate + t * p.ld_dgate + c) = row::pack<row::bf16, 8>(da);
         *reinterpret_cast<uint4 *>(p.dup + t * p.ld_dup + c) = row::pack<row::bf16, 8>(db);
     }
@@ -558,6 +667,20 @@ dgr_status make_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows
     return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
 }
 
+// Map over the rows of an output, in blocks of 32 x 32, 64-byte swizzle.
+dgr_status make_block_map(CUtensorMap *m, void *base, int64_t cols, int64_t rows, int64_t ld) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    const dgr_status st = encode_fn(&enc);
+    if (st != DGR_OK) return st;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * 2)};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
+}
+
 constexpr int kTileCost = 16;  // of a tile, in columns
 
 struct Operand {
@@ -572,7 +695,7 @@ int64_t row_blocks_most(const FfnParams &p, int rows) {
     return p.offs ? whole + (p.E < p.T ? p.E : p.T) : whole;
 }
 
-template <int CG, bool FWD>
+template <int CG, bool FWD, int ACT>
 dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
     constexpr int kRows = CG * BM;
     CUtensorMap mA, mA2, mB, mB2;
@@ -584,12 +707,18 @@ dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) 
     const int64_t F = FWD ? p.N : p.K, H = FWD ? p.K : p.N;
     const uint32_t box = FWD ? p.cut.cols : 64;
     if ((st = make_map(&mB, o.b, H, F, H, p.E, box)) != DGR_OK || (st = make_map(&mB2, o.b2, H, F, H, p.E, box)) != DGR_OK) return st;
+    Outputs outs{};
+    if (CG == 2) {
+        if ((st = make_block_map(&outs.out, p.out, p.N, p.T, p.ld_out)) != DGR_OK) return st;
+        if (p.gate && (st = make_block_map(&outs.gate, p.gate, p.N, p.T, p.ld_gate)) != DGR_OK) return st;
+        if (p.up && (st = make_block_map(&outs.up, p.up, p.N, p.T, p.ld_up)) != DGR_OK) return st;
+    }
     p.cut.nbs = (p.N + p.cut.cols - 1) / p.cut.cols;
     p.cut.stages = static_cast<int32_t>(kRing / (kStageA + static_cast<uint32_t>(FWD ? 2 * p.cut.cols : p.cut.cols) * 128u));
     if (p.cut.stages > kMaxStages) p.cut.stages = kMaxStages;
     const int64_t tiles = row_blocks_most(p, kRows) * p.cut.nbs, most = sms / CG > 0 ? sms / CG : 1;
     if (tiles > INT32_MAX) return DGR_ERR_UNSUPPORTED;
-    auto *k = ffn_gemm<CG, FWD>;
+    auto *k = ffn_gemm<CG, FWD, ACT>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess) return DGR_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     const unsigned groups = sched_grid(static_cast<unsigned>((tiles < most ? tiles : most) * CG)) / CG;
@@ -603,18 +732,18 @@ dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, outs, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
 // Which tiles: pairs of CTAs where the experts have enough rows to fill their 256
 // rows, else single CTAs. There the weights' reading counts, and the SM with the
 // most of it: the width of a tile is the one with the fewest columns in all waves
 // of tiles together, and a share for what a tile costs beside its weights.
-template <bool FWD>
+template <bool FWD, int ACT>
 dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
     if (p.T >= 192 * static_cast<int64_t>(p.E)) {
         p.cut.cols = FWD ? kMaxN / 2 : kMaxN, p.cut.box = BM;
-        return launch_tiles<2, FWD>(p, o, sms, s);
+        return launch_tiles<2, FWD, ACT>(p, o, sms, s);
     }
     p.cut.box = p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
     constexpr int kStep = FWD ? 8 : 64, kMost = FWD ? kMaxN / 2 : kMaxN;
@@ -626,7 +755,7 @@ dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
         const int64_t tiles = blocks * ((p.N + cols - 1) / cols), cost = (tiles + sms - 1) / sms * (cols + kTileCost);
         if (cost < best) best = cost, p.cut.cols = cols;
     }
-    return launch_tiles<1, FWD>(p, o, sms, s);
+    return launch_tiles<1, FWD, ACT>(p, o, sms, s);
 }
 
 // What both entries check of the rows, sizes, offsets and workspace.
@@ -683,7 +812,7 @@ extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_g
     if (T == 0) return DGR_OK;
     FfnParams p{};
     p.offs = d_offs, p.E = E, p.T = static_cast<int32_t>(T);
-    p.K = static_cast<int32_t>(H), p.N = static_cast<int32_t>(F), p.act = act;
+    p.K = static_cast<int32_t>(H), p.N = static_cast<int32_t>(F);
     p.out = static_cast<uint16_t *>(h), p.gate = static_cast<uint16_t *>(gate), p.up = static_cast<uint16_t *>(up);
     p.ld_out = ld_h, p.ld_gate = ld_gate, p.ld_up = ld_up;
     p.hdr = static_cast<WsHeader *>(ws);
@@ -692,7 +821,7 @@ extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_g
     if ((st = usable_sms(&sms)) != DGR_OK) return st;
     const Operand o{x, nullptr, ld_x, 0, w_gate, w_up};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launch_gemm<true>(p, o, sms, s);
+    return act == kSilu ? launch_gemm<true, kSilu>(p, o, sms, s) : launch_gemm<true, kGelu>(p, o, sms, s);
 }
 
 extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gate, int64_t ld_gate, const void *up,
@@ -740,16 +869,18 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
     g.dh = static_cast<const uint16_t *>(dh), g.gate = static_cast<const uint16_t *>(gate), g.up = static_cast<const uint16_t *>(up);
     g.dgate = static_cast<uint16_t *>(dgate), g.dup = static_cast<uint16_t *>(dup);
     g.ld_dh = ld_dh, g.ld_gate = ld_gate, g.ld_up = ld_up, g.ld_dgate = ld_dgate, g.ld_dup = ld_dup;
-    g.T = static_cast<int32_t>(T), g.vecs = static_cast<int32_t>(F / 8), g.act = act;
+    g.T = static_cast<int32_t>(T), g.vecs = static_cast<int32_t>(F / 8);
     const int64_t n = T * g.vecs, ctas = (n + 255) / 256, most = static_cast<int64_t>(sms) * 8;
-    ffn_pre_grad<<<static_cast<unsigned>(ctas < most ? ctas : most), 256, 0, s>>>(g);
+    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
+    if (act == kSilu) ffn_pre_grad<kSilu><<<grid, 256, 0, s>>>(g);
+    else ffn_pre_grad<kGelu><<<grid, 256, 0, s>>>(g);
     if ((st = launch_status()) != DGR_OK || !dx) return st;
     FfnParams p{};
     p.offs = d_offs, p.E = E, p.T = static_cast<int32_t>(T);
-    p.K = static_cast<int32_t>(F), p.N = static_cast<int32_t>(H), p.act = act;
+    p.K = static_cast<int32_t>(F), p.N = static_cast<int32_t>(H);
     p.out = static_cast<uint16_t *>(dx), p.ld_out = ld_dx;
     p.hdr = static_cast<WsHeader *>(ws);
     p.sched = sched_setting();
     const Operand o{dgate, dup, ld_dgate, ld_dup, w_gate, w_up};
-    return launch_gemm<false>(p, o, sms, s);
+    return launch_gemm<false, kSilu>(p, o, sms, s);  // no activation in it
 }
