@@ -15,10 +15,13 @@
 // the weights K-major as they lie, 128-byte swizzle; what is past a matrix's end
 // comes as zeros), warp 1 issues tcgen05.mma into one of two accumulators, warps
 // 4-11 (lane quarter q, column half) read one while the other fills.
-// Backward, two launches: da and db element by element (memory bound), then dx
-// by the same kernel with the two parts of its sum, da Wg_e and db Wu_e, one
-// after another along K in one accumulator (weights N-major as they lie). The
-// gradients of the weights are dgr_grouped_wgrad_accumulate's.
+// Backward: da and db element by element (memory bound), and dx by the same
+// kernel with the two parts of its sum, da Wg_e and db Wu_e, one after another
+// along K in one accumulator (weights N-major as they lie). Where dx is bound by
+// its products, warps of that kernel with nothing else to do make da and db, the
+// loads of a tile wait for its rows' counters, and the elements' traffic goes on
+// under the products; else two launches. The gradients of the weights are
+// dgr_grouped_wgrad_accumulate's.
 //
 // Rows of a tile past the expert's end are another expert's (or zeros): a row of
 // the product depends on its own row of x alone, and they are not written.
@@ -42,6 +45,8 @@ constexpr int BM = 128;  // rows of a tile (TMEM lanes)
 constexpr int BK = 64;   // k per stage: one 128-byte row of a swizzle atom
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
+constexpr int kPreWarps = 6;  // of a CTA that makes da and db too: warps 2, 3 and four behind the epilogue's
+constexpr int kReadyRows = 32;  // rows of da and db that one counter stands for
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kStageA = BM * 128;
 constexpr uint32_t kRing = 192 * 1024;  // stages, beside 4 KB of offsets and the barriers
@@ -101,7 +106,7 @@ struct FfnParams {
 // mb_base[e] = first row block of expert e (mb_base[E] = all row blocks), by the
 // whole block; false when the offsets break the contract.
 __device__ bool row_blocks(const FfnParams &p, int rows, int32_t *mb_base, int32_t *wsum, int32_t *bad) {
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nw = kThreads >> 5;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nt = blockDim.x, nw = nt >> 5;
     if (!p.offs) {
         if (tid == 0) mb_base[0] = 0, mb_base[1] = (p.T + rows - 1) / rows;
         __syncthreads();
@@ -110,7 +115,7 @@ __device__ bool row_blocks(const FfnParams &p, int rows, int32_t *mb_base, int32
     if (tid == 0) *bad = 0;
     __syncthreads();
     int32_t run = 0;
-    for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    for (int e0 = 0; e0 < p.E; e0 += nt) {
         const int e = e0 + tid;
         int32_t c = 0;
         if (e < p.E) {
@@ -303,13 +308,123 @@ __device__ __forceinline__ void tile_sync() {
     else cluster_barrier();
 }
 
+// ---- da and db ----------------------------------------------------------------
+
+struct PreParams {
+    const uint16_t *dh, *gate, *up;
+    uint16_t *dgate, *dup;
+    int64_t ld_dh, ld_gate, ld_up, ld_dgate, ld_dup;
+    int32_t T, vecs;    // 8-element vectors a row
+    int32_t rows_item;  // of pre_rows
+    int32_t *ready;     // rows written, of each kReadyRows
+};
+
+// da = dh b act'(a), db = dh act(a); act'(v) = g + v g (1 - g) s'(v), g = sigmoid(s(v)).
+// g (1 - g) is 0 long before s'(v) leaves the range, so their product counts as 0 then.
+template <int ACT>
+__device__ __forceinline__ void pre_grad(float2 dh, float2 a, float2 b, float2 &da, float2 &db) {
+    const float2 g = gate_sigmoid<ACT>(a), down = mul2(g, row::fma2(g, row::both(-1.0f), row::both(1.0f)));
+    float2 turn = down;
+    if (ACT == kGelu) {
+        const float2 s = row::fma2(mul2(row::both(0.21405560f), a), a, row::both(1.5957691216057308f));  // 2 sqrt(2 / pi) (1 + 3 0.044715 a^2)
+        turn = make_float2(down.x > 0.0f ? __fmul_rn(down.x, s.x) : down.x, down.y > 0.0f ? __fmul_rn(down.y, s.y) : down.y);
+    }
+    db = mul2(dh, mul2(a, g));
+    da = mul2(mul2(dh, b), row::fma2(a, turn, g));
+}
+
+// Eight elements of da and db from vector c of row t.
+template <int ACT>
+struct PreVec {
+    uint4 d, a, b;
+    __device__ __forceinline__ void load(const PreParams &p, int64_t t, int c, bool on) {
+        d = a = b = make_uint4(0, 0, 0, 0);
+        row::load_if<false>(d, p.dh + t * p.ld_dh + c, on);
+        row::load_if<false>(a, p.gate + t * p.ld_gate + c, on);
+        row::load_if<false>(b, p.up + t * p.ld_up + c, on);
+    }
+    __device__ __forceinline__ void store(const PreParams &p, int64_t t, int c) const {
+        float x[8], y[8], z[8], da[8], db[8];
+        row::unpack<row::bf16, 8>(d, x);
+        row::unpack<row::bf16, 8>(a, y);
+        row::unpack<row::bf16, 8>(b, z);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float2 u, v;
+            pre_grad<ACT>(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]), make_float2(z[j], z[j + 1]), u, v);
+            da[j] = u.x, da[j + 1] = u.y, db[j] = v.x, db[j + 1] = v.y;
+        }
+        *reinterpret_cast<uint4 *>(p.dgate + t * p.ld_dgate + c) = row::pack<row::bf16, 8>(da);
+        *reinterpret_cast<uint4 *>(p.dup + t * p.ld_dup + c) = row::pack<row::bf16, 8>(db);
+    }
+};
+
+// da and db by the spare warps of the kernel that multiplies them: rows in
+// ascending order, a few of them (rows_item, a divisor of kReadyRows) a warp at a
+// time, over all CTAs; each adds its rows to their counter when they are written.
+template <int ACT>
+__device__ __forceinline__ void pre_rows(const PreParams &p, int worker, int workers, int lane) {
+    constexpr int U = 4;
+    const int items = (p.T + p.rows_item - 1) / p.rows_item;
+    for (int i = worker; i < items; i += workers) {
+        const int64_t t0 = static_cast<int64_t>(i) * p.rows_item;
+        const int rows = min(p.rows_item, static_cast<int>(p.T - t0)), n = rows * p.vecs;
+        for (int v = lane; v < n; v += 32 * U) {
+            PreVec<ACT> x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int w = v + 32 * u, r = w / p.vecs;
+                x[u].load(p, t0 + r, (w - r * p.vecs) * 8, w < n);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int w = v + 32 * u, r = w / p.vecs;
+                if (w < n) x[u].store(p, t0 + r, (w - r * p.vecs) * 8);
+            }
+        }
+        // seen by the copy engines of all SMs before the count is
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p.ready + t0 / kReadyRows), "r"(rows) : "memory");
+    }
+}
+
+// Until the rows [first, end) of da and db are written (bounded); by a whole warp.
+__device__ __forceinline__ bool wait_rows(const PreParams &p, int32_t first, int32_t end, int lane, volatile int *abort_flag, WsHeader *hdr) {
+    bool ok = true;
+    for (int g = first / kReadyRows + lane; g * kReadyRows < end && ok; g += 32) {
+        const int32_t want = min(kReadyRows, p.T - g * kReadyRows);
+        if (!wait_counter_geq(p.ready + g, want)) {
+            record_error(hdr, DGR_ERR_TIMEOUT, 405);
+            *abort_flag = 1;
+            ok = false;
+        }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(256) ffn_pre_grad(const PreParams p) {
+    const int64_t n = static_cast<int64_t>(p.T) * p.vecs;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t t = i / p.vecs;
+        const int c = static_cast<int>(i - t * p.vecs) * 8;
+        PreVec<ACT> x;
+        x.load(p, t, c, true);
+        x.store(p, t, c);
+    }
+}
+
 // FWD: a, b and h; else dx. Maps: A (and A2, the second part's), B and B2
 // (forward Wg and Wu, FT rows a box; backward the same, 64 x 64 atoms).
-template <int CG, bool FWD, int ACT>
-__global__ void __launch_bounds__(kThreads, 1)
+// PRE: da and db are made here too.
+template <int CG, bool FWD, int ACT, bool PRE>
+__global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1)
     ffn_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
-             const __grid_constant__ Outputs outs, const FfnParams p) {
+             const __grid_constant__ Outputs outs, const FfnParams p, const PreParams pre) {
     constexpr int kRows = CG * BM;
     const int cols = CG == 2 ? (FWD ? kMaxN / 2 : kMaxN) : p.cut.cols;  // columns of the output a tile
     const int width = FWD ? 2 * cols : cols;                            // of the product
@@ -319,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + kRing + kEpiWarps * kBox);
     __shared__ int32_t mb_base[kMaxExperts + 1];
-    __shared__ int32_t wsum[kThreads / 32];
+    __shared__ int32_t wsum[kThreads / 32 + 4];
     __shared__ int32_t bad;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -362,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
-        if (lane == 0) {
+        // one lane; where rows have to be waited for, the others help to watch them
+        if (PRE || lane == 0) {
             uint32_t stage = 0, phase = 0;
             bool armed[kMaxStages] = {};
             uint32_t armed_phase[kMaxStages] = {};
@@ -373,7 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // space keeps what it had; those rows' products are not written)
                 const int boxes = p.cut.box == BM ? 1 : (min(t.end - t.row, BM) + p.cut.box - 1) / p.cut.box;
                 const uint32_t bytes = CG * (static_cast<uint32_t>(boxes * p.cut.box) * 128u + stage_b);
-                for (int kb = 0; kb < n_k; ++kb) {
+                if (PRE) {
+                    const int32_t mine = t.row + rank * BM;
+                    ok = wait_rows(pre, mine, min(mine + BM, t.end), lane, abort_flag, p.hdr);
+                }
+                for (int kb = 0; ok && lane == 0 && kb < n_k; ++kb) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1, abort_flag, p.hdr, 401)) {
                         ok = false;
                         break;
@@ -409,8 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1;
                     }
                 }
+                if (PRE) ok = __shfl_sync(0xffffffffu, ok, 0);  // the lanes leave together
             }
-            if (!ok && rank == 0) {  // aborted: let the copies in flight land (bounded) before the CTA, or the pair, exits
+            if (!ok && rank == 0 && lane == 0) {  // aborted: let the copies in flight land (bounded) before the CTA, or the pair, exits
                 int dummy = 0;
                 for (int s = 0; s < kMaxStages; ++s)
                     if (armed[s]) mbar_wait(&ctl->full[s], armed_phase[s], &dummy, nullptr, kWaitLimitNs);
@@ -470,6 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int dummy = 0;
             mbar_wait(&ctl->empty[last_stage], last_phase, &dummy, nullptr, kWaitLimitNs);
         }
+    } else if (PRE && (warp == 2 || warp == 3 || warp >= 4 + kEpiWarps)) {
+        // ---------------- da and db ----------------
+        const int w = warp < 4 ? warp - 2 : warp - kEpiWarps - 2;
+        pre_rows<ACT>(pre, w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kPreWarps * static_cast<int>(gridDim.x), lane);
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------
         const int q = warp & 3;         // TMEM lane quarter this warp may access
@@ -588,50 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// ---- da and db ----------------------------------------------------------------
-
-struct PreParams {
-    const uint16_t *dh, *gate, *up;
-    uint16_t *dgate, *dup;
-    int64_t ld_dh, ld_gate, ld_up, ld_dgate, ld_dup;
-    int32_t T, vecs;  // 8-element vectors a row
-};
-
-// da = dh b act'(a), db = dh act(a); act'(v) = g + v g (1 - g) s'(v), g = sigmoid(s(v)).
-// g (1 - g) is 0 long before s'(v) leaves the range, so their product counts as 0 then.
-template <int ACT>
-__device__ __forceinline__ void pre_grad(float2 dh, float2 a, float2 b, float2 &da, float2 &db) {
-    const float2 g = gate_sigmoid<ACT>(a), down = mul2(g, row::fma2(g, row::both(-1.0f), row::both(1.0f)));
-    float2 turn = down;
-    if (ACT == kGelu) {
-        const float2 s = row::fma2(mul2(row::both(0.21405560f), a), a, row::both(1.5957691216057308f));  // 2 sqrt(2 / pi) (1 + 3 0.044715 a^2)
-        turn = make_float2(down.x > 0.0f ? __fmul_rn(down.x, s.x) : down.x, down.y > 0.0f ? __fmul_rn(down.y, s.y) : down.y);
-    }
-    db = mul2(dh, mul2(a, g));
-    da = mul2(mul2(dh, b), row::fma2(a, turn, g));
-}
-
-template <int ACT>
-__global__ void __launch_bounds__(256) ffn_pre_grad(const PreParams p) {
-    const int64_t n = static_cast<int64_t>(p.T) * p.vecs;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t t = i / p.vecs;
-        const int c = static_cast<int>(i - t * p.vecs) * 8;
-        float d[8], a[8], b[8], da[8], db[8];
-        row::unpack<row::bf16, 8>(ldg_nc_v4(p.dh + t * p.ld_dh + c), d);
-        row::unpack<row::bf16, 8>(*reinterpret_cast<const uint4 *>(p.gate + t * p.ld_gate + c), a);
-        row::unpack<row::bf16, 8>(*reinterpret_cast<const uint4 *>(p.up + t * p.ld_up + c), b);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            float2 x, y;
-            pre_grad<ACT>(make_float2(d[j], d[j + 1]), make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), x, y);
-            da[j] = x.x, da[j + 1] = x.y, db[j] = y.x, db[j + 1] = y.y;
-        }
-        *reinterpret_cast<uint4 *>(p.dgate + t * p.ld_dgate + c) = row::pack<row::bf16, 8>(da);
-        *reinterpret_cast<uint4 *>(p.dup + t * p.ld_dup + c) = row::pack<row::bf16, 8>(db);
-    }
-}
-
 // ---- host ---------------------------------------------------------------------
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -681,6 +762,8 @@ dgr_status make_block_map(CUtensorMap *m, void *base, int64_t cols, int64_t rows
     return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
 }
 
+size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows) * 4; }
+
 constexpr int kTileCost = 16;  // of a tile, in columns
 
 struct Operand {
@@ -695,8 +778,8 @@ int64_t row_blocks_most(const FfnParams &p, int rows) {
     return p.offs ? whole + (p.E < p.T ? p.E : p.T) : whole;
 }
 
-template <int CG, bool FWD, int ACT>
-dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
+template <int CG, bool FWD, int ACT, bool PRE>
+dgr_status launch_tiles(FfnParams p, const PreParams &pre, const Operand &o, int sms, cudaStream_t s) {
     constexpr int kRows = CG * BM;
     CUtensorMap mA, mA2, mB, mB2;
     dgr_status st;
@@ -718,12 +801,12 @@ dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) 
     if (p.cut.stages > kMaxStages) p.cut.stages = kMaxStages;
     const int64_t tiles = row_blocks_most(p, kRows) * p.cut.nbs, most = sms / CG > 0 ? sms / CG : 1;
     if (tiles > INT32_MAX) return DGR_ERR_UNSUPPORTED;
-    auto *k = ffn_gemm<CG, FWD, ACT>;
+    auto *k = ffn_gemm<CG, FWD, ACT, PRE>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess) return DGR_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     const unsigned groups = sched_grid(static_cast<unsigned>((tiles < most ? tiles : most) * CG)) / CG;
     cfg.gridDim = dim3((groups > 0 ? groups : 1) * CG);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0));
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -732,19 +815,24 @@ dgr_status launch_tiles(FfnParams p, const Operand &o, int sms, cudaStream_t s) 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, outs, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, outs, p, pre) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
-// Which tiles: pairs of CTAs where the experts have enough rows to fill their 256
-// rows, else single CTAs. There the weights' reading counts, and the SM with the
-// most of it: the width of a tile is the one with the fewest columns in all waves
-// of tiles together, and a share for what a tile costs beside its weights.
+// Whether experts have enough rows to fill the 256 of a pair of CTAs; where they
+// have fewer the weights' reading counts.
+bool takes_pairs(const FfnParams &p) { return p.T >= 192 * static_cast<int64_t>(p.E); }
+
+template <bool FWD, int ACT, bool PRE>
+dgr_status launch_pairs(FfnParams p, const PreParams &pre, const Operand &o, int sms, cudaStream_t s) {
+    p.cut.cols = FWD ? kMaxN / 2 : kMaxN, p.cut.box = BM;
+    return launch_tiles<2, FWD, ACT, PRE>(p, pre, o, sms, s);
+}
+
+// Single CTAs. What counts is the SM with the most of the weights: the width of a
+// tile is the one with the fewest columns in all waves of tiles together, and a
+// share for what a tile costs beside its weights.
 template <bool FWD, int ACT>
-dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
-    if (p.T >= 192 * static_cast<int64_t>(p.E)) {
-        p.cut.cols = FWD ? kMaxN / 2 : kMaxN, p.cut.box = BM;
-        return launch_tiles<2, FWD, ACT>(p, o, sms, s);
-    }
+dgr_status launch_singles(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
     p.cut.box = p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
     constexpr int kStep = FWD ? 8 : 64, kMost = FWD ? kMaxN / 2 : kMaxN;
     // row blocks as they are likely to be: a ragged one for most experts
@@ -755,7 +843,27 @@ dgr_status launch_gemm(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
         const int64_t tiles = blocks * ((p.N + cols - 1) / cols), cost = (tiles + sms - 1) / sms * (cols + kTileCost);
         if (cost < best) best = cost, p.cut.cols = cols;
     }
-    return launch_tiles<1, FWD, ACT>(p, o, sms, s);
+    return launch_tiles<1, FWD, ACT, false>(p, PreParams{}, o, sms, s);
+}
+
+template <int ACT>
+dgr_status launch_forward(const FfnParams &p, const Operand &o, int sms, cudaStream_t s) {
+    return takes_pairs(p) ? launch_pairs<true, ACT, false>(p, PreParams{}, o, sms, s) : launch_singles<true, ACT>(p, o, sms, s);
+}
+
+// da and db element by element, then dx; in one kernel where that is bound by its
+// products, so that the one's memory traffic goes on under the other.
+template <int ACT>
+dgr_status launch_backward(const FfnParams &p, PreParams &g, const Operand &o, int sms, cudaStream_t s) {
+    if (p.out && takes_pairs(p)) {
+        g.rows_item = g.vecs >= 256 ? 1 : g.vecs >= 128 ? 2 : g.vecs >= 64 ? 4 : 8;
+        if (cudaMemsetAsync(g.ready, 0, ready_bytes(p.T), s) != cudaSuccess) return DGR_ERR_CUDA;
+        return launch_pairs<false, ACT, true>(p, g, o, sms, s);
+    }
+    const int64_t n = static_cast<int64_t>(p.T) * g.vecs, ctas = (n + 255) / 256, most = static_cast<int64_t>(sms) * 8;
+    ffn_pre_grad<ACT><<<static_cast<unsigned>(ctas < most ? ctas : most), 256, 0, s>>>(g);
+    const dgr_status st = launch_status();
+    return st != DGR_OK || !p.out ? st : launch_singles<false, kSilu>(p, o, sms, s);  // no activation in it
 }
 
 // What both entries check of the rows, sizes, offsets and workspace.
@@ -779,7 +887,7 @@ using namespace dgr;
 
 extern "C" size_t dgr_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t F, int32_t E) {
     if (T < 0 || H < 1 || F < 1 || E < 1 || E > kMaxExperts || T > INT32_MAX - 256 || H > (1 << 20) || F > (1 << 20)) return 0;
-    return sizeof(WsHeader);
+    return sizeof(WsHeader) + align_up(ready_bytes(T));
 }
 
 extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_gate, const void *w_up, const int64_t *d_offs,
@@ -821,7 +929,7 @@ extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_g
     if ((st = usable_sms(&sms)) != DGR_OK) return st;
     const Operand o{x, nullptr, ld_x, 0, w_gate, w_up};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return act == kSilu ? launch_gemm<true, kSilu>(p, o, sms, s) : launch_gemm<true, kGelu>(p, o, sms, s);
+    return act == kSilu ? launch_forward<kSilu>(p, o, sms, s) : launch_forward<kGelu>(p, o, sms, s);
 }
 
 extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gate, int64_t ld_gate, const void *up,
@@ -842,7 +950,8 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
     for (const Rows &r : outs)
         if (r.p && (!aligned(r.p, 16) || r.ld % 8)) return DGR_ERR_MISALIGNED;
     if (!aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(d_offs, 8) || !aligned(ws, kAlign)) return DGR_ERR_MISALIGNED;
-    if (ws_bytes < sizeof(WsHeader)) return DGR_ERR_WORKSPACE_TOO_SMALL;
+    const size_t need = dgr_gated_ffn_workspace_bytes(T, H, F, E);
+    if (ws_bytes < need) return DGR_ERR_WORKSPACE_TOO_SMALL;
     const size_t weights = static_cast<size_t>(E) * F * H * 2;
     for (const Rows &o : outs) {
         const size_t n = extent(T, o);
@@ -852,14 +961,14 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
             if (!in_place && ranges_overlap(o.p, n, i.p, extent(T, i))) return DGR_ERR_ALIAS;
         }
         if (ranges_overlap(o.p, n, w_gate, weights) || ranges_overlap(o.p, n, w_up, weights) ||
-            ranges_overlap(o.p, n, d_offs, (static_cast<size_t>(E) + 1) * 8) || ranges_overlap(o.p, n, ws, sizeof(WsHeader)))
+            ranges_overlap(o.p, n, d_offs, (static_cast<size_t>(E) + 1) * 8) || ranges_overlap(o.p, n, ws, need))
             return DGR_ERR_ALIAS;
         for (const Rows &q : outs)
             if (&q < &o && ranges_overlap(o.p, n, q.p, extent(T, q))) return DGR_ERR_ALIAS;
     }
     for (const Rows &i : ins)
-        if (ranges_overlap(ws, sizeof(WsHeader), i.p, extent(T, i))) return DGR_ERR_ALIAS;
-    if (ranges_overlap(ws, sizeof(WsHeader), w_gate, weights) || ranges_overlap(ws, sizeof(WsHeader), w_up, weights)) return DGR_ERR_ALIAS;
+        if (ranges_overlap(ws, need, i.p, extent(T, i))) return DGR_ERR_ALIAS;
+    if (ranges_overlap(ws, need, w_gate, weights) || ranges_overlap(ws, need, w_up, weights)) return DGR_ERR_ALIAS;
     if ((st = check_device()) != DGR_OK) return st;
     if (T == 0) return DGR_OK;
     int sms = 0;
@@ -870,11 +979,7 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
     g.dgate = static_cast<uint16_t *>(dgate), g.dup = static_cast<uint16_t *>(dup);
     g.ld_dh = ld_dh, g.ld_gate = ld_gate, g.ld_up = ld_up, g.ld_dgate = ld_dgate, g.ld_dup = ld_dup;
     g.T = static_cast<int32_t>(T), g.vecs = static_cast<int32_t>(F / 8);
-    const int64_t n = T * g.vecs, ctas = (n + 255) / 256, most = static_cast<int64_t>(sms) * 8;
-    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-    if (act == kSilu) ffn_pre_grad<kSilu><<<grid, 256, 0, s>>>(g);
-    else ffn_pre_grad<kGelu><<<grid, 256, 0, s>>>(g);
-    if ((st = launch_status()) != DGR_OK || !dx) return st;
+    g.ready = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + sizeof(WsHeader));
     FfnParams p{};
     p.offs = d_offs, p.E = E, p.T = static_cast<int32_t>(T);
     p.K = static_cast<int32_t>(F), p.N = static_cast<int32_t>(H);
@@ -882,5 +987,5 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
     p.hdr = static_cast<WsHeader *>(ws);
     p.sched = sched_setting();
     const Operand o{dgate, dup, ld_dgate, ld_dup, w_gate, w_up};
-    return launch_gemm<false, kSilu>(p, o, sms, s);  // no activation in it
+    return act == kSilu ? launch_backward<kSilu>(p, g, o, sms, s) : launch_backward<kGelu>(p, g, o, sms, s);
 }

@@ -582,13 +582,16 @@ dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_
  * d_offs:   [E+1] int64 DEVICE array, non-decreasing, d_offs[0] = 0, d_offs[E] = T,
  *           or null with E = 1. Offsets outside this contract record
  *           DGR_ERR_INVALID_ARG in the status word; h, gate, up and dx are then
- *           not written.
+ *           not written (dgate and dup may be).
  * gate, up: forward: a and b, or null each; backward: those (not null).
  * dx may be null (dgate and dup alone).
  * Limits:   H and F multiples of 8 up to 2^20, 1 <= E <= 1024, T < 2^31 - 256.
  * Alignment: pointers 16 bytes, row strides multiples of 8 elements.
- * ws:       dgr_gated_ffn_workspace_bytes(T, H, F, E) bytes, zeroed once (status
- *           word); it may go on to calls with other sizes as it is.
+ * ws:       dgr_gated_ffn_workspace_bytes(T, H, F, E) bytes (the forward call needs
+ *           256), zeroed once; it may go on to calls with other sizes as it is.
+ * Residency: the backward call of many rows waits, bounded, for rows that other
+ * CTAs of the same launch write; it takes one CTA an SM usable at once, and the
+ * CTAs that write wait for nothing.
  * dgate may be gate and dup may be up (same pointer and stride); nothing else
  * may overlap.
  */

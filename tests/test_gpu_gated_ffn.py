@@ -55,7 +55,7 @@ def check_backward(t, act, **more):
 
 
 SIZES = [([1], 8, 8), ([5], 64, 40), ([1, 0, 2], 72, 136), ([128, 129, 0, 3], 200, 264), ([0, 0, 300], 1000, 128),
-         ([40, 41, 42, 43, 0, 1], 328, 520), ([256, 257], 64, 1040), ([700], 2048, 256), ([0, 33], 264, 8), ([513, 1, 255], 136, 392)]
+         ([40, 41, 42, 43, 0, 1], 328, 520), ([256, 257], 64, 1040), ([1000, 300], 136, 2056), ([2100], 72, 8), ([700], 2048, 256), ([0, 33], 264, 8), ([513, 1, 255], 136, 392)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -163,7 +163,7 @@ def test_weights_gradients():
 def test_offsets_out_of_order(cuts):
     """Recorded in the status word; nothing is written."""
     t = make([5, 4, 11], 64, 72)
-    ws = dgr.workspace(256)
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(20, 64, 72, 3))
     out = {k: torch.full((20, 72), 3.0, dtype=BF, device="cuda") for k in ("h", "gate", "up")}
     offs = torch.tensor(cuts, dtype=torch.int64, device="cuda")
     dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=offs, ws=ws, **out)
@@ -215,9 +215,9 @@ def test_schedules_streams_and_replays(counts, H, F):
 
 def test_two_graphs_that_share_a_workspace():
     """Captured calls of other sizes, replayed in turn with new inputs."""
-    ws = dgr.workspace(256)
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(1500, 512, 1024, 2))
     cases = []
-    for counts, H, F in (([200, 60], 136, 264), ([3], 512, 1024)):
+    for counts, H, F in (([200, 60], 136, 264), ([3], 512, 1024), ([700, 800], 264, 520)):
         t = make(counts, H, F)
         out = {"h": torch.empty(sum(counts), F, dtype=BF, device="cuda")}
         back = {k: torch.empty(sum(counts), n, dtype=BF, device="cuda") for k, n in (("dx", H), ("dgate", F), ("dup", F))}

@@ -57,7 +57,7 @@ def test_gated_ffn(L):
 
 def test_gated_ffn_backward(L):
     ok = dict(dh=P(1), lddh=32, g=P(2), ldg=32, u=P(3), ldu=32, wg=P(4), wu=P(5), offs=P(6), E=2, T=10, H=64, F=32, act=1, dg=P(7),
-              lddg=32, du=P(8), lddu=32, dx=P(9), lddx=64, ws=P(10), n=256, s=None)
+              lddg=32, du=P(8), lddu=32, dx=P(9), lddx=64, ws=P(10), n=512, s=None)
 
     def call(**kw):
         return L.dgr_gated_ffn_backward(*{**ok, **kw}.values())
@@ -67,7 +67,7 @@ def test_gated_ffn_backward(L):
         assert call(**kw) == INVALID, kw
     for kw in (dict(lddh=36), dict(dx=at(9, 8)), dict(dg=at(7, 8)), dict(wu=at(5, 8)), dict(u=at(3, 2))):
         assert call(**kw) == MISALIGNED, kw
-    assert call(n=0) == TOO_SMALL
+    assert call(n=511) == TOO_SMALL
     for kw in (dict(dx=P(1)), dict(dx=P(7)), dict(dg=P(1)), dict(dg=P(3)), dict(du=P(2)), dict(dg=P(2), lddg=64), dict(dx=P(4)), dict(du=P(6)),
                dict(dg=P(8)), dict(ws=P(1)), dict(ws=P(5)), dict(dx=P(10))):
         assert call(**kw) == ALIAS, kw
