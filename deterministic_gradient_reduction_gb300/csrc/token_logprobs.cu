@@ -18,14 +18,19 @@
 // Alternatives: the K-th largest of the threads' maxima is a lower bound of the
 // row's K-th largest element, and few elements lie above it. Each thread keeps
 // the maxima of a few parts of its share; the parts that reach the bound are
-// read again (out of L2) and their elements above it collected; each element's
-// rank among those is counted, by value and then by the lower index. Where so
-// many are equal that they do not fit, one CTA finds the K-th by its digits.
+// read again (out of L2), their elements above it collected and the lowest K of
+// those equal to it; each one's rank among them is counted, by value and then by
+// the lower index. A warp that has no share of the rows does this for a row while
+// the others read the next one. Where more elements lie above the bound than
+// there is space for, that warp finds the K-th by its digits.
 // Backward: one pass from the stored m, ln s and H, no sum over the row.
 //
 // Deterministic: sums go over threads, warps and CTAs in a fixed order set by the
 // type, T, V, the alignment and K; the collected elements' order is chance, their
 // ranks are not.
+#include <climits>
+#include <cstddef>
+
 #include "row_common.cuh"
 
 namespace dgr {
@@ -33,11 +38,12 @@ namespace {
 
 using namespace row;
 
-constexpr int kMaxTop = 256;
+constexpr int kMaxTop = 128;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxCluster = 8;
 constexpr int kParts = 16;          // parts of a thread's share with a maximum of their own
-constexpr int kCandidates = 2048;   // collected elements
+constexpr int kCandidates = 512, kCandidatesOfMany = 1536;  // collected elements of a row with one CTA, with several
+constexpr int kFew = 256;           // parts, or equal elements, that are taken as they come
 constexpr int kWhereId = 440;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kFar = 16777216.0f;
@@ -197,6 +203,13 @@ struct Triple {
     }
 };
 
+// The lowest bf16 that is not below v.
+__device__ __forceinline__ uint16_t up_to_bf16(float v) {
+    uint32_t b = __float_as_uint(v);
+    if (!(b & 0x80000000u) && b << 16) b += 0x10000u;  // (to infinity, at the end); below zero the upper bits are that
+    return static_cast<uint16_t>(b >> 16);
+}
+
 // An element by value (-0 as +0), then by the lower index, as one number.
 __device__ __forceinline__ uint64_t key_of(float v, int index) {
     uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));
@@ -211,76 +224,343 @@ __device__ __forceinline__ int key_index(uint64_t key) { return static_cast<int>
 
 // The K-th largest key of a row's elements above -inf (all of them where there
 // are fewer), by its digits of 8 bits from the top: a histogram each of the
-// elements that share the digits found so far. For rows where too many elements
-// are equal; the whole CTA, one row, every reading out of L2.
-template <typename T, int NT>
+// elements that share the digits found so far. One warp, every reading out of L2:
+// for rows whose large elements are all in a few threads' shares.
+template <typename T>
 __device__ uint64_t kth_key(const T *z, int V, int K, int *hist) {
-    __shared__ uint64_t s_prefix;
-    __shared__ int s_left;
-    const int tid = threadIdx.x;
-    if (tid == 0) s_prefix = 0, s_left = K;
-    // value digits 7..4; of the index's 32 bits the upper 8 are the same in all
+    const int lane = threadIdx.x & 31;
+    uint64_t prefix = 0;
+    int left = K;
     for (int digit = 7; digit >= 0; --digit) {
-        for (int i = tid; i < 256; i += NT) hist[i] = 0;
-        __syncthreads();
-        const uint64_t prefix = s_prefix, mask = digit == 7 ? 0 : ~uint64_t{0} << (8 * (digit + 1));
-        for (int j = tid; j < V; j += NT) {
+        for (int i = lane; i < 256; i += 32) hist[i] = 0;
+        __syncwarp();
+        const uint64_t mask = digit == 7 ? 0 : ~uint64_t{0} << (8 * (digit + 1));
+        for (int j = lane; j < V; j += 32) {
             const float v = to_f32(z[j]);
             if (!(v > -INFINITY)) continue;  // a NaN neither
             const uint64_t key = key_of(v, j);
             if ((key & mask) == prefix) atomicAdd(&hist[key >> (8 * digit) & 255], 1);
         }
-        __syncthreads();
-        if (tid == 0) {
-            int left = s_left, b = 255;
-            for (; b > 0 && hist[b] < left; --b) left -= hist[b];
-            s_left = left;
-            s_prefix = prefix | static_cast<uint64_t>(b) << (8 * digit);
-        }
-        __syncthreads();
+        __syncwarp();
+        int b = 255;
+        for (; b > 0 && hist[b] < left; --b) left -= hist[b];
+        prefix |= static_cast<uint64_t>(b) << (8 * digit);
+        __syncwarp();
     }
-    return s_prefix;
+    return prefix;
 }
 
-// The forward pass's shared memory, by name.
+// The forward pass's shared memory. MT: threads that read rows.
 template <int NT>
 struct __align__(16) Shared {
     float4 triple[2][kMaxCluster * NT / 32];  // the cluster's warps, by row parity
     float bound[2][kMaxCluster];              // lower bounds of the K-th element, likewise
 };
-template <int NT>
+// Kept small: what the four CTAs of an SM leave of it is the cache that loads in
+// flight need room in (FIGURES).
+template <int MT>
 struct __align__(16) TopShared {
-    uint64_t key[kCandidates];
-    float part[kParts][NT];   // maxima of the threads' parts
-    float top[NT];            // of the threads
-    int list[NT * kParts];    // parts to read again
-    int hist[256];
-    int n_list, n_key;
+    uint16_t part[2][kParts][MT];  // maxima of the threads' parts, rounded up to bf16, by row parity
+    float top[2][MT];              // of the threads
+    uint16_t list[kFew];           // parts to read again
+    int same[kFew];                // elements equal to the bound (and a histogram of 256)
+    int n_key;
+    alignas(16) uint64_t key[];    // candidates, and one more; read in twos
+};
+static_assert(kFew >= 256, "a histogram fits");
+static_assert(offsetof(TopShared<224>, key) % 16 == 0 && offsetof(TopShared<224>, part) % 16 == 0 && sizeof(uint16_t[kParts][224]) % 16 == 0 &&
+                  sizeof(TopShared<224>) == offsetof(TopShared<224>, key),
+              "what is read as vectors of 16 bytes starts at multiples of them");
+
+// A row's list, by one warp of each CTA of its cluster.
+template <typename T, int MT>
+struct TopOf {
+    using View = RowView<T>;
+    enum { VEC = 16 / static_cast<int>(sizeof(T)) };
+
+    const LogpParams &p;
+    TopShared<MT> &ts;
+    const T *z;
+    const View &view;
+    const char *first;
+    int par, lane, per_part, size, cap;
+    int n_key;  // candidates, where the row has one CTA
+
+    // K-th largest of the threads' maxima as a key, bit by bit from bit `from` on; what
+    // lies below bit `to` is left out, so that a lower bound comes of it
+    __device__ __forceinline__ uint32_t bound(uint32_t at, int from, int to) const {
+        uint32_t key[MT / 32];
+#pragma unroll
+        for (int i = 0; i < MT / 32; ++i) key[i] = static_cast<uint32_t>(key_of(ts.top[par][i * 32 + lane], 0) >> 32);
+        for (int bit = from; bit >= to; --bit) {
+            const uint32_t want = at | 1u << bit;
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < MT / 32; ++i) n += key[i] >= want;
+            if (static_cast<int>(__reduce_add_sync(0xffffffffu, n)) >= p.K) at = want;
+        }
+        return at;
+    }
+    // By the upper 16 bits: all that a bf16 value has (its lower ones are 0, or 1 below
+    // zero), and near enough else, as long as few parts reach it.
+    __device__ __forceinline__ float bound(uint32_t at) const {
+        if (sizeof(T) == 2 && !(at & 0x80000000u)) at |= 0xffffu;
+        // (the key of -inf is the least that counts)
+        return key_value(static_cast<uint64_t>(max(at, 0x007fffffu)) << 32);
+    }
+    // to the leader's candidates: the lanes' elements where `on`
+    __device__ __forceinline__ void push(float v, int index, bool on) {
+        const uint32_t who = __ballot_sync(0xffffffffu, on);
+        if (!who) return;
+        int at = n_key;
+        if (size > 1) {
+            if (lane == 0) at = remote_add(remote(&ts.n_key, 0), __popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0);
+        }
+        n_key = at + __popc(who);
+        at += __popc(who & ((1u << lane) - 1));
+        if (on && at < cap) {
+            if (size == 1) ts.key[at] = key_of(v, index);
+            else remote_store(remote(&ts.key[at], 0), key_of(v, index));
+        }
+    }
+    // reads the listed parts: pushes the elements above b and lists those equal to it in
+    // `same`; how many these are. Memory operations of this warp queue behind all the
+    // row loads of the SM, so few wait for one another here: values come out of registers.
+    __device__ __forceinline__ int elements(int n_list, float b, bool equal) {
+        constexpr int U = 32 / VEC;  // a bit an element
+        int n_same = 0;
+        const int n = n_list * per_part;
+        for (int i0 = 0; i0 < n; i0 += 32 * U) {
+            uint4 r[U];
+            int at[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + 32 * u + lane;
+                at[u] = i < n ? ts.list[i / per_part] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + 32 * u + lane, v = at[u] % MT + (at[u] / MT * per_part + i % per_part) * MT;
+                at[u] = i < n && v < view.count ? v : -1;
+                r[u] = make_uint4(0, 0, 0, 0);
+                load_if<true>(r[u], first + static_cast<int64_t>(v) * 16, at[u] >= 0);
+            }
+            uint32_t above = 0, same = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[VEC];
+                unpack<T, VEC>(r[u], x);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    above |= static_cast<uint32_t>(at[u] >= 0 && x[j] > b) << (u * VEC + j);
+                    same |= static_cast<uint32_t>(at[u] >= 0 && equal && x[j] == b) << (u * VEC + j);
+                }
+            }
+            auto index_of = [&](int e) {
+                int v = at[0];
+#pragma unroll
+                for (int u = 1; u < U; ++u) v = e / VEC == u ? at[u] : v;
+                return view.head + (view.first + v) * VEC + e % VEC;
+            };
+            while (__any_sync(0xffffffffu, above != 0)) {
+                const bool on = above != 0;
+                const int e = on ? __ffs(above) - 1 : 0;
+                above &= above - 1;
+                float v = 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[VEC];
+                    unpack<T, VEC>(r[u], x);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) v = e == u * VEC + j ? x[j] : v;
+                }
+                push(v, index_of(e), on);
+            }
+            while (__any_sync(0xffffffffu, same != 0) && n_same <= kFew) {
+                const bool on = same != 0;
+                const int e = on ? __ffs(same) - 1 : 0;
+                same &= same - 1;
+                const uint32_t who = __ballot_sync(0xffffffffu, on);
+                const int to = n_same + __popc(who & ((1u << lane) - 1));
+                if (on && to < kFew) ts.same[to] = index_of(e);
+                n_same += __popc(who);
+            }
+        }
+        __syncwarp();
+        return n_same;
+    }
+    // lists the parts whose maximum is above `b` (or equal to it), the first kFew; how many
+    __device__ __forceinline__ int list_parts(float b, bool equal) const {
+        constexpr int n_vec = kParts * MT / 8;
+        int n = 0;
+        const uint4 *part = reinterpret_cast<const uint4 *>(&ts.part[par][0][0]);
+        for (int i0 = 0; i0 < n_vec; i0 += 128) {
+            uint4 q[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) q[u] = i0 + 32 * u + lane < n_vec ? part[i0 + 32 * u + lane] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            uint32_t on = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float x[8];
+                unpack<bf16, 8>(q[u], x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) on |= static_cast<uint32_t>((equal ? x[j] >= b : x[j] > b) && x[j] > -INFINITY) << (8 * u + j);
+            }
+            while (__any_sync(0xffffffffu, on != 0)) {
+                const int e = __ffs(on) - 1;
+                const uint32_t who = __ballot_sync(0xffffffffu, on != 0);
+                const int to = n + __popc(who & ((1u << lane) - 1));
+                if (on != 0 && to < kFew) ts.list[to] = static_cast<uint16_t>(8 * (i0 + 32 * (e / 8) + lane) + e % 8);
+                on &= on - 1;
+                n += __popc(who);
+            }
+        }
+        __syncwarp();
+        return n;
+    }
+    // candidates of this CTA's share, each once: all above b, and the lowest K equal to
+    // it at least; n: parts that reach it, listed
+    __device__ __forceinline__ void collect(float b, int n) {
+        if (view.n_single) {
+            const int j = lane < view.n_single ? view.single(lane) : 0;
+            const float v = lane < view.n_single ? to_f32(z[j]) : -INFINITY;
+            push(v, j, v >= b && v > -INFINITY);
+        }
+        const bool some = b > -INFINITY, many = n > kFew;
+        if (some && many) n = list_parts(b, false);
+        if (n > kFew) {  // no list of them: all elements
+            walk([&](float v) { return v > b; }, INT_MAX);
+        } else {
+            const int n_same = elements(n, b, some && !many);
+            if (some && !many && n_same <= kFew) {
+                for (int i0 = 0; i0 < n_same; i0 += 32) push(b, i0 + lane < n_same ? ts.same[i0 + lane] : 0, i0 + lane < n_same);
+                __syncwarp();
+                return;
+            }
+        }
+        if (some) walk([&](float v) { return v == b; }, p.K);
+        __syncwarp();
+    }
+    // the first `most` elements of this CTA's vectors that are wanted, in order
+    template <typename F>
+    __device__ __forceinline__ void walk(F wanted, int most) {
+        int found = 0;
+        for (int v0 = 0; v0 < view.count && found < most; v0 += 32) {
+            const int v = v0 + lane;
+            uint4 r = make_uint4(0, 0, 0, 0);
+            load_if<true>(r, first + static_cast<int64_t>(v) * 16, v < view.count);
+            float x[VEC];
+            unpack<T, VEC>(r, x);
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) n += v < view.count && wanted(x[j]);
+            if (!__any_sync(0xffffffffu, n != 0)) continue;
+            int before = n;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, before, s);
+                if (lane >= s) before += o;
+            }
+            const int all = __shfl_sync(0xffffffffu, before, 31);
+            before += found - n;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const bool on = v < view.count && wanted(x[j]);
+                push(x[j], view.head + (view.first + v) * VEC + j, on && before < most);
+                before += on;
+            }
+            found += all;
+        }
+    }
+    // the leader's part: ranks and outputs
+    __device__ __forceinline__ void write(int64_t row, float m, float lns) {
+        int n = size == 1 ? n_key : ts.n_key;
+        if (n > cap) n = by_digits();
+        constexpr int R = 4;  // keys of a lane at a time
+        if (lane == 0 && n % 2) ts.key[n] = 0;  // below every key; read in twos
+        __syncwarp();
+        for (int i0 = 0; i0 < n; i0 += 32 * R) {
+            uint64_t key[R];
+            int at[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                key[r] = i0 + 32 * r + lane < n ? ts.key[i0 + 32 * r + lane] : 0;
+                at[r] = 0;
+            }
+#pragma unroll 4
+            for (int j = 0; j < n; j += 2) {
+                const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(&ts.key[j]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) at[r] += (o.x > key[r]) + (o.y > key[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (key[r] == 0 || at[r] >= p.K) continue;
+                const float v = key_value(key[r]);
+                const int64_t to = row * p.K + at[r];
+                if (p.top_ids) p.top_ids[to] = key_index(key[r]);
+                if (p.top_logits) p.top_logits[to] = v;
+                if (p.top_logp) p.top_logp[to] = __fmaf_rn(__fadd_rn(v, -m), p.inv_tau, -lns);
+            }
+        }
+        fill(row, n);
+        __syncwarp();
+        if (lane == 0) ts.n_key = 0;
+        n_key = 0;
+        __syncwarp();
+    }
+    // the row's K largest as the only candidates; how many
+    __device__ __forceinline__ int by_digits() const {
+        const uint64_t least = kth_key<T>(z, p.V, p.K, ts.same);
+        int n = 0;
+        for (int j0 = 0; j0 < p.V; j0 += 32) {
+            const int j = j0 + lane;
+            const float v = j < p.V ? to_f32(z[j]) : -INFINITY;
+            const uint64_t key = v > -INFINITY ? key_of(v, j) : 0;
+            const bool on = key >= least && key != 0;
+            const uint32_t who = __ballot_sync(0xffffffffu, on);
+            if (on) ts.key[n + __popc(who & ((1u << lane) - 1))] = key;
+            n += __popc(who);
+        }
+        __syncwarp();
+        return n;
+    }
+    __device__ __forceinline__ void fill(int64_t row, int from) const {
+        for (int k = from + lane; k < p.K; k += 32) {
+            if (p.top_ids) p.top_ids[row * p.K + k] = -1;
+            if (p.top_logits) p.top_logits[row * p.K + k] = -INFINITY;
+            if (p.top_logp) p.top_logp[row * p.K + k] = -INFINITY;
+        }
+    }
 };
 
 template <typename T, int NT, bool TOP>
 __global__ void __launch_bounds__(NT, 1024 / NT) logp_rows(const LogpParams p) {
     using View = RowView<T>;
-    constexpr int VEC = View::VEC, W = NT / 32, U = 4;
+    // warps that read rows; with lists the last one makes those
+    constexpr int VEC = View::VEC, W = NT / 32 - (TOP ? 1 : 0), MT = W * 32, U = 4;
     __shared__ Shared<NT> sh;
     extern __shared__ __align__(16) char smem[];
-    TopShared<NT> &ts = *reinterpret_cast<TopShared<NT> *>(smem);
+    TopShared<MT> &ts = *reinterpret_cast<TopShared<MT> *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     const uint32_t n_clusters = gridDim.x / size;
-    const int n_batches = (p.per + U * NT - 1) / (U * NT);       // of a thread, at most
+    const int n_batches = (p.per + U * MT - 1) / (U * MT);       // of a thread, at most
     const int part_len = (n_batches + kParts - 1) / kParts;      // batches a part
     uint32_t live = 0;  // rows worked on: the exchange's parity
-    if (TOP && tid == 0) ts.n_key = 0, ts.n_list = 0;
+    if (TOP && tid == 0) ts.n_key = 0;
     if (size > 1) cluster_barrier();  // the other CTAs have started
     else __syncthreads();
 
     for (uint32_t item = blockIdx.x / size; item < static_cast<uint32_t>(p.T); item += n_clusters) {
         const int64_t row = sched_item(p.sched, item);
         const T *z = static_cast<const T *>(p.z) + row * p.ld;
-        const int id = p.ids ? __ldg(p.ids + row) : 0;
-        const bool skip = id < 0 || id >= p.V;
-        if (skip) {  // not read: zeros, and no alternatives
+        const int id = p.ids ? __ldg(p.ids + row) : 0, par = live & 1;
+        const View view(z, p.V, rank, p.per);
+        const char *first = reinterpret_cast<const char *>(z + view.head) + static_cast<int64_t>(view.first) * 16;
+        TopOf<T, MT> top_of{p, ts, z, view, first, par, lane, part_len * U, size, size == 1 ? kCandidates : kCandidatesOfMany, 0};
+        if (id < 0 || id >= p.V) {  // not read: zeros, and no alternatives
             if (rank == 0 && tid == 0) {
                 if (id >= p.V) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereId);
                 if (p.logp) p.logp[row] = 0.0f;
@@ -288,90 +568,85 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logp_rows(const LogpParams p) {
                 if (p.lse) p.lse[row] = 0.0f;
                 if (p.stats) p.stats[2 * row] = p.stats[2 * row + 1] = 0.0f;
             }
-            if (TOP && rank == 0)
-                for (int k = tid; k < p.K; k += NT) {
-                    if (p.top_ids) p.top_ids[row * p.K + k] = -1;
-                    if (p.top_logits) p.top_logits[row * p.K + k] = -INFINITY;
-                    if (p.top_logp) p.top_logp[row * p.K + k] = -INFINITY;
-                }
+            if (TOP && rank == 0 && w == W) top_of.fill(row, 0);
             continue;
         }
-        const View view(z, p.V, rank, p.per);
-        const char *first = reinterpret_cast<const char *>(z + view.head) + static_cast<int64_t>(view.first) * 16;
+        const bool finisher = rank == 0 && w == (TOP ? W : 0);  // the warp that has the row's outputs
         float x_id = 0.0f;
-        if (p.logp && rank == 0 && w == 0) x_id = to_f32(z[id]);
-        float shift = 0.0f, c = 0.0f;
+        if (p.logp && finisher) x_id = to_f32(z[id]);
+        float shift = 0.0f;
         Triple all{-INFINITY, 0.0f, 0.0f};
         for (bool again = false;; again = true) {
-            Running run;
-            float part = -INFINITY;
-            int in_part = 0, n_part = 0;
-            for (int v = tid; v < view.count; v += U * NT) {
-                uint4 r[U];
-                constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
+            if (w < W) {
+                Running run;
+                float part = -INFINITY;
+                int in_part = 0, n_part = 0;
+                for (int v = tid; v < view.count; v += U * MT) {
+                    uint4 r[U];
+                    constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    r[u] = make_uint4(low, low, low, low);
-                    load_if<true>(r[u], first + (static_cast<int64_t>(v) + u * NT) * 16, v + u * NT < view.count);
-                }
-                const float top = max_of<T, U>(r);
-                if (TOP && !again) {
-                    part = fmaxf(part, top);
-                    if (++in_part == part_len) {
-                        ts.part[n_part++][tid] = part;
-                        part = -INFINITY, in_part = 0;
+                    for (int u = 0; u < U; ++u) {
+                        r[u] = make_uint4(low, low, low, low);
+                        load_if<true>(r[u], first + (static_cast<int64_t>(v) + u * MT) * 16, v + u * MT < view.count);
                     }
-                }
-                run.raise(__fadd_rn(top, -shift), p.k2);
+                    const float top = max_of<T, U>(r);
+                    if (TOP && !again) {
+                        part = fmaxf(part, top);
+                        if (++in_part == part_len) {
+                            ts.part[par][n_part++][tid] = up_to_bf16(part);
+                            part = -INFINITY, in_part = 0;
+                        }
+                    }
+                    run.raise(__fadd_rn(top, -shift), p.k2);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float x[VEC];
-                    if constexpr (sizeof(T) == 2) {
-                        if (!again) r[u] = make_uint4(at_least_masked2(r[u].x), at_least_masked2(r[u].y), at_least_masked2(r[u].z), at_least_masked2(r[u].w));
-                        unpack<T, VEC>(r[u], x);
-                        if (again)
+                    for (int u = 0; u < U; ++u) {
+                        float x[VEC];
+                        if constexpr (sizeof(T) == 2) {
+                            if (!again) r[u] = make_uint4(at_least_masked2(r[u].x), at_least_masked2(r[u].y), at_least_masked2(r[u].z), at_least_masked2(r[u].w));
+                            unpack<T, VEC>(r[u], x);
+                            if (again)
+#pragma unroll
+                                for (int i = 0; i < VEC; ++i) x[i] = at_least_masked(__fadd_rn(x[i], -shift));
+                        } else {
+                            unpack<T, VEC>(r[u], x);
 #pragma unroll
                             for (int i = 0; i < VEC; ++i) x[i] = at_least_masked(__fadd_rn(x[i], -shift));
-                    } else {
-                        unpack<T, VEC>(r[u], x);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) x[i] = at_least_masked(__fadd_rn(x[i], -shift));
+                        }
+                        run.add(x, p.k2);
                     }
-                    run.add(x, p.k2);
                 }
-            }
-            if (TOP && !again)
-                for (; n_part < kParts; ++n_part) {
-                    ts.part[n_part][tid] = part;
-                    part = -INFINITY;
+                if (TOP && !again)
+                    for (; n_part < kParts; ++n_part) {
+                        ts.part[par][n_part][tid] = up_to_bf16(part);
+                        part = -INFINITY;
+                    }
+                if (tid < view.n_single) {
+                    const float x = __fadd_rn(to_f32(z[view.single(tid)]), -shift);
+                    run.raise(x, p.k2);
+                    run.add_one(at_least_masked(x), p.k2);
                 }
-            if (tid < view.n_single) {
-                const float x = __fadd_rn(to_f32(z[view.single(tid)]), -shift);
-                run.raise(x, p.k2);
-                run.add_one(at_least_masked(x), p.k2);
+                if (TOP && !again) ts.top[par][tid] = run.m;
+                Triple mine{run.m, across(run.s), across(run.a)};
+                mine.over_warp(p.k2);
+                if (lane < size) remote_store(remote(&sh.triple[par][rank * W + w], lane), make_float4(mine.m, mine.s, mine.a, 0.0f));
+                __syncwarp();
             }
-            if (TOP && !again) ts.top[tid] = run.m;
-            Triple mine{run.m, across(run.s), across(run.a)};
-            mine.over_warp(p.k2);
-            if (lane < size) remote_store(remote(&sh.triple[live & 1][rank * W + w], lane), make_float4(mine.m, mine.s, mine.a, 0.0f));
-            __syncwarp();
             if (size > 1) cluster_barrier();
             else __syncthreads();
             all = Triple{-INFINITY, 0.0f, 0.0f};
-            for (int j = lane; j < size * W; j += 32) all.m = fmaxf(all.m, sh.triple[live & 1][j].x);
+            for (int j = lane; j < size * W; j += 32) all.m = fmaxf(all.m, sh.triple[par][j].x);
             all.m = warp_max(all.m);
             if (again || !(fabsf(all.m) < INFINITY) || fabsf(__fmul_rn(all.m, p.k2)) < kFar) break;
             shift = all.m;  // the same in every warp of the cluster
             if (size > 1) cluster_barrier();  // before the triples are written over
             else __syncthreads();
         }
-        // the row's sums and outputs: the first warp of the first CTA
         const float m = shift != 0.0f ? shift : all.m;
         float lns = 0.0f;
-        if (rank == 0 && (w == 0 || TOP)) {
-            c = scaled_max(all.m, p.k2);
+        if (finisher) {
+            const float c = scaled_max(all.m, p.k2);
             for (int j = lane; j < size * W; j += 32) {
-                const float4 got = sh.triple[live & 1][j];
+                const float4 got = sh.triple[par][j];
                 Triple t{got.x, got.y, got.z};
                 t.to(all.m, p.k2);
                 all.s = __fadd_rn(all.s, t.s);
@@ -383,7 +658,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logp_rows(const LogpParams p) {
             const float ln_s = logf(all.s);
             // ln s for the maximum itself: without the rounding of c
             lns = none ? 0.0f : __fmaf_rn(__fmaf_rn(all.m, p.k2, -c), -kLn2, ln_s);
-            if (w == 0 && lane == 0) {
+            if (lane == 0) {
                 if (p.logp) p.logp[row] = none ? -INFINITY : __fmaf_rn(__fadd_rn(x_id, -m), p.inv_tau, -lns);
                 if (p.entropy) p.entropy[row] = none ? 0.0f : __fmaf_rn(-kLn2, all.a / all.s, ln_s);
                 if (p.lse) p.lse[row] = __fmaf_rn(m, p.inv_tau, lns);
@@ -391,85 +666,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logp_rows(const LogpParams p) {
             }
         }
         if constexpr (TOP) {
-            // the K-th largest of the threads' maxima: the one that K - 1 come before
-            const float top = ts.top[tid];
-            int before = 0;
-            for (int j = 0; j < NT; j += 4) {
-                const float4 o = *reinterpret_cast<const float4 *>(&ts.top[j]);
-                before += (o.x > top || (o.x == top && j < tid)) + (o.y > top || (o.y == top && j + 1 < tid)) +
-                          (o.z > top || (o.z == top && j + 2 < tid)) + (o.w > top || (o.w == top && j + 3 < tid));
+            // the last warp makes the list while the others go on to the next row
+            // (where a row has several CTAs, they meet at the barriers)
+            float bound = 0.0f;
+            int reach = 0;
+            uint32_t key = 0;
+            if (w == W) {
+                key = top_of.bound(0, 31, 16);
+                bound = top_of.bound(key);
+                reach = top_of.list_parts(bound, true);
+                if (sizeof(T) == 4 && reach > kFew) {
+                    bound = top_of.bound(top_of.bound(key, 15, 0));
+                    if (size == 1) reach = top_of.list_parts(bound, true);
+                }
+                if (size > 1 && lane < size) remote_store(remote(&sh.bound[par][rank], lane), bound);
             }
-            if (before == p.K - 1)
-                for (int r = 0; r < size; ++r) remote_store(remote(&sh.bound[live & 1][rank], r), top);
+            if (size > 1) {
+                cluster_barrier();
+                for (int r = 0; r < size; ++r) bound = fmaxf(r ? bound : -INFINITY, sh.bound[par][r]);
+                if (w == W) reach = top_of.list_parts(bound, true);
+            }
+            if (w == W) top_of.collect(bound, reach);
             if (size > 1) cluster_barrier();
-            else __syncthreads();
-            float bound = sh.bound[live & 1][0];
-            for (int r = 1; r < size; ++r) bound = fmaxf(bound, sh.bound[live & 1][r]);
-            auto collect = [&](float v, int index) {
-                if (v >= bound && v > -INFINITY) {
-                    const int at = remote_add(remote(&ts.n_key, 0), 1);
-                    if (at < kCandidates) remote_store(remote(&ts.key[at], 0), key_of(v, index));
-                }
-            };
-            if (top >= bound && top > -INFINITY) {
-                for (int i = 0; i < kParts; ++i) {
-                    const float part = ts.part[i][tid];
-                    if (part >= bound && part > -INFINITY) ts.list[atomicAdd(&ts.n_list, 1)] = i * NT + tid;
-                }
-                if (tid < view.n_single) {
-                    const int j = view.single(tid);
-                    collect(to_f32(z[j]), j);
-                }
-            }
-            __syncthreads();
-            const int per_part = part_len * U;
-            for (int i = tid; i < ts.n_list * per_part; i += NT) {
-                const int which = ts.list[i / per_part], of = i % per_part;
-                const int v = which % NT + (which / NT * per_part + of) * NT;
-                if (v >= view.count) continue;
-                const uint4 r = __ldg(reinterpret_cast<const uint4 *>(first) + v);
-                float x[VEC];
-                unpack<T, VEC>(r, x);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) collect(x[j], view.head + (view.first + v) * VEC + j);
-            }
-            if (size > 1) cluster_barrier();
-            else __syncthreads();
-            if (tid == 0) ts.n_list = 0;
-            if (rank == 0) {
-                int n = ts.n_key;
-                if (n > kCandidates) {
-                    const uint64_t least = kth_key<T, NT>(z, p.V, p.K, ts.hist);
-                    if (tid == 0) ts.n_key = 0;
-                    __syncthreads();
-                    for (int j = tid; j < p.V; j += NT) {
-                        const float v = to_f32(z[j]);
-                        if (!(v > -INFINITY)) continue;
-                        const uint64_t key = key_of(v, j);
-                        if (key >= least) ts.key[atomicAdd(&ts.n_key, 1)] = key;
-                    }
-                    __syncthreads();
-                    n = ts.n_key;
-                }
-                for (int i = tid; i < n; i += NT) {
-                    const uint64_t key = ts.key[i];
-                    int at = 0;
-                    for (int j = 0; j < n; ++j) at += ts.key[j] > key;
-                    if (at >= p.K) continue;
-                    const float v = key_value(key);
-                    if (p.top_ids) p.top_ids[row * p.K + at] = key_index(key);
-                    if (p.top_logits) p.top_logits[row * p.K + at] = v;
-                    if (p.top_logp) p.top_logp[row * p.K + at] = __fmaf_rn(__fadd_rn(v, -m), p.inv_tau, -lns);
-                }
-                for (int k = n + tid; k < p.K; k += NT) {
-                    if (p.top_ids) p.top_ids[row * p.K + k] = -1;
-                    if (p.top_logits) p.top_logits[row * p.K + k] = -INFINITY;
-                    if (p.top_logp) p.top_logp[row * p.K + k] = -INFINITY;
-                }
-                __syncthreads();
-                if (tid == 0) ts.n_key = 0;  // read by the others behind the next row's barrier
-            }
-            __syncthreads();
+            if (w == W && rank == 0) top_of.write(row, m, lns);
         }
         ++live;
     }
@@ -609,8 +828,9 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
     const int vecs = p.V / (16 / static_cast<int>(sizeof(T)));
     p.per = (vecs + cluster - 1) / cluster;
     if (p.per < 1) p.per = 1;
-    const size_t smem = TOP ? sizeof(TopShared<NT>) : 0;
-    dgr_status st = allow_smem(k, smem, sizeof(TopShared<NT>));
+    constexpr size_t kTop = sizeof(TopShared<NT - 32>);
+    const size_t smem = TOP ? kTop + static_cast<size_t>((cluster == 1 ? kCandidates : kCandidatesOfMany) + 1) * 8 : 0;
+    dgr_status st = allow_smem(k, smem, kTop + (kCandidatesOfMany + 1) * 8);
     if (st != DGR_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(cluster);

@@ -694,7 +694,7 @@ dgr_status dgr_qk_norm_rope_backward(const void *dq_out, int64_t dqo_token, int6
  *           exactly if K = 0.
  * dlogits:  [T, V] of dtype, row stride ld_d. One of dlogp and dentropy is given
  *           at least; dlogp needs ids, dentropy needs entropy.
- * Limits:   1 <= V <= 2^20, 0 <= K <= 256, T <= 2^26, 1e-6 <= tau <= 1e6.
+ * Limits:   1 <= V <= 2^20, 0 <= K <= 128, T <= 2^26, 1e-6 <= tau <= 1e6.
  * ws:       dgr_token_logprobs_workspace_bytes(T) bytes, zeroed once (status
  *           word); it may go on to calls with other sizes. Backward needs none.
  * dlogits may be logits (same pointer and stride); nothing else may overlap.

@@ -108,8 +108,8 @@ def test_rows_that_start_anywhere(pad, lead, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("T,V,K", [(1, 1, 1), (3, 5, 8), (2, 300, 256), (4, 4096, 256), (3, 65536, 20), (1, 131072, 64), (700, 2000, 5),
-                                   (2, 262144, 256), (5, 50001, 1), (200, 9001, 100), (1, 1 << 20, 33)])
+@pytest.mark.parametrize("T,V,K", [(1, 1, 1), (3, 5, 8), (2, 300, 128), (4, 4096, 128), (3, 65536, 20), (1, 131072, 64), (700, 2000, 5),
+                                   (2, 262144, 128), (5, 50001, 1), (200, 9001, 100), (1, 1 << 20, 33)])
 def test_top(T, V, K, dtype):
     z, ids = make(T, V, dtype)
     check_forward(z, ids, 1.3, K)
@@ -128,12 +128,12 @@ def test_equal_logits(dtype):
     z[5] = -7.0
     z[5, 39999] = -6.0
     ids = torch.arange(6, dtype=torch.int32, device="cuda")
-    for K in (1, 7, 256):
+    for K in (1, 7, 128):
         got = check_forward(z, ids, top=K)
     check_backward(z, ids, got)
     z, ids = make(4, 3000, dtype, scale=1.0)
     z.copy_((z * 4).round() / 4)  # few values
-    check_forward(z, ids, top=200)
+    check_forward(z, ids, top=120)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -272,7 +272,7 @@ def test_no_rows():
     assert dgr.token_logprobs_backward(z, ids, got["stats"], got["entropy"], dlogp=got["logp"]).shape == (0, 100)
 
 
-@pytest.mark.parametrize("T,V,K,dtype", [(400, 3000, 0, "bf16"), (3, 70000, 40, "fp32"), (60, 9001, 200, "bf16")])
+@pytest.mark.parametrize("T,V,K,dtype", [(400, 3000, 0, "bf16"), (3, 70000, 40, "fp32"), (60, 9001, 100, "bf16")])
 def test_schedules_streams_and_replays(T, V, K, dtype):
     z, ids = make(T, V, dtype)
     one = torch.ones(T, device="cuda")

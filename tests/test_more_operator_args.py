@@ -125,7 +125,7 @@ def test_token_logprobs(L):
                dict(z=None), dict(ids=None), dict(K=-1), dict(K=0), dict(ti=None, tz=None, tp=None), dict(ws=None),
                dict(K=0, logp=None, H=None, lse=None, st=None, ti=None, tz=None, tp=None)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(K=257), dict(V=(1 << 20) + 1, ld=BIG), dict(T=(1 << 26) + 1), dict(tau=1e-7), dict(tau=1e7)):
+    for kw in (dict(K=129), dict(V=(1 << 20) + 1, ld=BIG), dict(T=(1 << 26) + 1), dict(tau=1e-7), dict(tau=1e7)):
         assert call(**kw) == UNSUPPORTED, kw
     for kw in (dict(z=at(1, 1)), dict(ids=at(2, 2)), dict(tp=at(9, 2)), dict(ws=at(10, 8))):
         assert call(**kw) == MISALIGNED, kw
