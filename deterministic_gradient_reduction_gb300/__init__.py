@@ -593,6 +593,7 @@ def topk_distill_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torc
 
 
 _ACTS = {"silu": 0, "gelu": 1}
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
 def gated_ffn_workspace_bytes(T: int, H: int, F: int, E: int = 1) -> int:
@@ -601,16 +602,17 @@ def gated_ffn_workspace_bytes(T: int, H: int, F: int, E: int = 1) -> int:
 
 def _experts(w_gate, w_up, offs, act):
     """(E, F, H, offs' address): weights [E, F, H], or [F, H] of a single expert."""
-    if w_gate.dim() not in (2, 3) or w_gate.shape != w_up.shape or act not in _ACTS:
+    shape = w_gate.shape
+    if len(shape) not in (2, 3) or w_up.shape != shape or act not in _ACTS:
         raise ValueError("w_gate and w_up [E, F, H] and act 'silu' or 'gelu' expected")
-    if w_gate.dtype != torch.bfloat16 or w_up.dtype != torch.bfloat16:
+    if w_gate.dtype is not torch.bfloat16 or w_up.dtype is not torch.bfloat16:
         raise TypeError("bf16 weights expected")
     if not (w_gate.is_contiguous() and w_up.is_contiguous()):
         raise ValueError("w_gate and w_up must be contiguous")
-    E = 1 if w_gate.dim() == 2 else w_gate.shape[0]
+    E = 1 if len(shape) == 2 else shape[0]
     if offs is None and E != 1:
         raise ValueError("offs int64 [E+1] expected for more than one expert")
-    return E, w_gate.shape[-2], w_gate.shape[-1], _vec(offs, E + 1, torch.int64, "offs")
+    return E, shape[-2], shape[-1], _vec(offs, E + 1, torch.int64, "offs")
 
 
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, offs: torch.Tensor | None = None,
@@ -681,34 +683,33 @@ def qk_norm_rope_workspace_bytes(T: int, n_q: int, n_k: int, D: int) -> int:
     return int(lib().dgr_qk_norm_rope_workspace_bytes(T, n_q, n_k, D))
 
 
-def _heads(t: torch.Tensor | None, shape, dtype, name: str):
-    """(address, token stride, head stride) of a [T, heads, D] tensor with contiguous heads."""
-    if t is None:
-        return None, 0, 0
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} {list(shape)} expected, got {t.dtype} {list(t.shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1] * shape[2], shape[2]
-    if t.stride(2) != 1 and shape[2] > 1:
+def _heads(t: torch.Tensor, T: int, n: int, D: int, dtype, name: str):
+    """(address, token stride, head stride) of a [T, n, D] tensor with contiguous heads."""
+    if t.shape != (T, n, D) or t.dtype is not dtype:
+        raise ValueError(f"{name}: {dtype} {[T, n, D]} expected, got {t.dtype} {list(t.shape)}")
+    token, head, one = t.stride()
+    if one != 1 and D > 1 and T and n:
         raise ValueError(f"{name}: contiguous heads expected")
-    # the stride of a single token or head says nothing
-    head = t.stride(1) if shape[1] > 1 else shape[2]
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else head * shape[1], head
+    if n <= 1:  # the stride of a single head or token says nothing
+        head = D
+    return t.data_ptr(), token if T > 1 else head * n, head
+
+
+_NONE = (None, 0, 0)  # queries or keys that a call does not have
 
 
 def _qk_args(q, k, cos, sin, positions, w_q, w_k):
-    """Sizes, types and addresses that both directions share."""
-    some = q if q is not None else k
-    if some is None or any(t is not None and t.dim() != 3 for t in (q, k)) or cos.dim() != 2:
+    """(T, heads of q and of k, D, one of the two, what both directions pass on alike, positions' address)."""
+    some = k if q is None else q
+    if some is None or some.dim() != 3 or (q is not None and k is not None and k.dim() != 3) or cos.dim() != 2:
         raise ValueError("q [T, heads, D] or k [T, heads, D] and cos [P, R/2] expected")
-    T, _, D = some.shape
-    shapes = [None if t is None else (T, t.shape[1], D) for t in (q, k)]
-    weights = [w for w in (w_q, w_k) if w is not None]
-    wdt = weights[0].dtype if weights else torch.float32
-    P, R = cos.shape[0], 2 * cos.shape[1]
+    T, n, D = some.shape
+    n_q, n_k = (0, n) if q is None else (n, 0 if k is None else k.shape[1])
+    P, half = cos.shape
+    wdt = w_q.dtype if w_q is not None else w_k.dtype if w_k is not None else torch.float32
     f32 = torch.float32
-    return T, D, some, shapes, (_vec(w_q, D, wdt, "w_q"), _vec(w_k, D, wdt, "w_k"), _dtype(weights[0]) if weights else DTYPE_F32,
-                                _vec(cos, P * (R // 2), f32, "cos"), _vec(sin, P * (R // 2), f32, "sin"), P, R), \
+    return T, n_q, n_k, D, some, (_vec(w_q, D, wdt, "w_q"), _vec(w_k, D, wdt, "w_k"), _DTYPES[wdt] if wdt in _DTYPES else _dtype(w_q),
+                                  _vec(cos, P * half, f32, "cos"), _vec(sin, P * half, f32, "sin"), P, 2 * half), \
         _vec(positions, T, torch.int32, "positions")
 
 
@@ -721,17 +722,20 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, cos: torch.Tens
     q bf16/fp32 [T, heads, D] and k [T, kv heads, D] (either may be None), with any token and head
     strides; cos and sin fp32 [P, R/2] for the first R elements of a head; positions int32 [T].
     Pairs are (m, m + R/2), or (2m, 2m + 1) when interleaved. q_out may be q, k_out may be k."""
-    T, D, some, (sq, sk), same, pos = _qk_args(q, k, cos, sin, positions, w_q, w_k)
+    T, n_q, n_k, D, some, same, pos = _qk_args(q, k, cos, sin, positions, w_q, w_k)
     dt = some.dtype
     if (q is not None and q_out is None) or (k is not None and k_out is None):
         with _on(stream):
-            q_out = torch.empty(sq, dtype=dt, device=some.device) if q is not None and q_out is None else q_out
-            k_out = torch.empty(sk, dtype=dt, device=some.device) if k is not None and k_out is None else k_out
+            q_out = torch.empty(T, n_q, D, dtype=dt, device=some.device) if q is not None and q_out is None else q_out
+            k_out = torch.empty(T, n_k, D, dtype=dt, device=some.device) if k is not None and k_out is None else k_out
     if ws is None:
         ws = workspace(256, some.device, stream)
+    hq = _NONE if q is None else _heads(q, T, n_q, D, dt, "q")
+    hk = _NONE if k is None else _heads(k, T, n_k, D, dt, "k")
+    oq = _NONE if q is None else _heads(q_out, T, n_q, D, dt, "q_out")
+    ok = _NONE if k is None else _heads(k_out, T, n_k, D, dt, "k_out")
     _check("dgr_qk_norm_rope", lib().dgr_qk_norm_rope(
-        *_heads(q, sq, dt, "q"), sq[1] if sq else 0, *_heads(k, sk, dt, "k"), sk[1] if sk else 0, _dtype(some), T, D, *same,
-        int(interleaved), pos, eps, *_heads(q_out, sq, dt, "q_out"), *_heads(k_out, sk, dt, "k_out"), ws.data_ptr(),
+        *hq, n_q, *hk, n_k, _dtype(some), T, D, *same, 1 if interleaved else 0, pos, eps, *oq, *ok, ws.data_ptr(),
         ws.numel(), _stream(stream)))
     return q_out, k_out
 
@@ -745,26 +749,31 @@ def qk_norm_rope_backward(dq_out: torch.Tensor | None, dk_out: torch.Tensor | No
     """Gradients of qk_norm_rope from those of its outputs and its inputs: a dict of dq, dk (of q's
     type; dq may be dq_out, dk may be dk_out) and, for the weights given, fp32 dw_q, dw_k [D];
     accumulate adds these to what dw_q and dw_k hold."""
-    T, D, some, (sq, sk), same, pos = _qk_args(q, k, cos, sin, positions, w_q, w_k)
-    dt, dev = some.dtype, some.device
+    T, n_q, n_k, D, some, same, pos = _qk_args(q, k, cos, sin, positions, w_q, w_k)
+    dt = some.dtype
     if (q is None) != (dq_out is None) or (k is None) != (dk_out is None):
         raise ValueError("dq_out goes with q and dk_out with k")
-    if accumulate and any(w is not None and d is None for w, d in ((w_q, dw_q), (w_k, dw_k))):
+    if accumulate and ((w_q is not None and dw_q is None) or (w_k is not None and dw_k is None)):
         raise ValueError("accumulate needs dw_q and dw_k to add to")
-    with _on(stream):
-        dq = torch.empty(sq, dtype=dt, device=dev) if q is not None and dq is None else dq
-        dk = torch.empty(sk, dtype=dt, device=dev) if k is not None and dk is None else dk
-        f32 = dict(dtype=torch.float32, device=dev)
-        dw_q = torch.empty(D, **f32) if w_q is not None and q is not None and dw_q is None else dw_q
-        dw_k = torch.empty(D, **f32) if w_k is not None and k is not None and dw_k is None else dw_k
-    n_q, n_k = sq[1] if sq else 0, sk[1] if sk else 0
+    if (q is not None and (dq is None or (w_q is not None and dw_q is None))) or \
+            (k is not None and (dk is None or (w_k is not None and dw_k is None))):
+        with _on(stream):
+            dev, f32 = some.device, dict(dtype=torch.float32, device=some.device)
+            dq = torch.empty(T, n_q, D, dtype=dt, device=dev) if q is not None and dq is None else dq
+            dk = torch.empty(T, n_k, D, dtype=dt, device=dev) if k is not None and dk is None else dk
+            dw_q = torch.empty(D, **f32) if w_q is not None and q is not None and dw_q is None else dw_q
+            dw_k = torch.empty(D, **f32) if w_k is not None and k is not None and dw_k is None else dw_k
     if ws is None:
-        ws = workspace(qk_norm_rope_workspace_bytes(T, n_q, n_k, D), dev, stream)
+        ws = workspace(qk_norm_rope_workspace_bytes(T, n_q, n_k, D), some.device, stream)
+    gq = vq = oq = gk = vk = ok = _NONE
+    if q is not None:
+        gq, vq, oq = _heads(dq_out, T, n_q, D, dt, "dq_out"), _heads(q, T, n_q, D, dt, "q"), _heads(dq, T, n_q, D, dt, "dq")
+    if k is not None:
+        gk, vk, ok = _heads(dk_out, T, n_k, D, dt, "dk_out"), _heads(k, T, n_k, D, dt, "k"), _heads(dk, T, n_k, D, dt, "dk")
     _check("dgr_qk_norm_rope_backward", lib().dgr_qk_norm_rope_backward(
-        *_heads(dq_out, sq, dt, "dq_out"), *_heads(dk_out, sk, dt, "dk_out"), *_heads(q, sq, dt, "q"), n_q,
-        *_heads(k, sk, dt, "k"), n_k, _dtype(some), T, D, *same, int(interleaved), pos, eps, *_heads(dq, sq, dt, "dq"),
-        *_heads(dk, sk, dt, "dk"), _vec(dw_q, D, torch.float32, "dw_q"), _vec(dw_k, D, torch.float32, "dw_k"),
-        int(accumulate), ws.data_ptr(), ws.numel(), _stream(stream)))
+        *gq, *gk, *vq, n_q, *vk, n_k, _dtype(some), T, D, *same, 1 if interleaved else 0, pos, eps, *oq, *ok,
+        _vec(dw_q, D, torch.float32, "dw_q"), _vec(dw_k, D, torch.float32, "dw_k"), 1 if accumulate else 0, ws.data_ptr(),
+        ws.numel(), _stream(stream)))
     out = {"dq": dq, "dk": dk, "dw_q": dw_q, "dw_k": dw_k}
     return {n: v for n, v in out.items() if v is not None}
 
