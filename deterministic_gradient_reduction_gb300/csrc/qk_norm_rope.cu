@@ -31,6 +31,7 @@ constexpr int kWarps = 8;
 constexpr int kMaxDim = 512;
 constexpr int kMaxHeads = 1024;
 constexpr int kSlots = 304;     // CTAs of the backward pass at most, two an SM
+constexpr int kUnitsWarp = 2;   // units a warp at least, where tokens have the groups of heads for it
 constexpr int kFoldCols = 8, kFoldWays = 32;
 constexpr int kWherePos = 420;
 
@@ -147,9 +148,16 @@ __device__ __forceinline__ void load_weights(const QkParams &p, float (*w)[kMaxD
         if (INTER) pair = e >> 1, second = e & 1;
         else if (e < p.R) second = e >= p.R / 2, pair = e - second * (p.R / 2);
         else second = e - p.R >= (p.D - p.R) / 2, pair = p.R / 2 + (e - p.R) - second * ((p.D - p.R) / 2);
-        w[kind][second * (p.D / 2) + pair] = from ? param(from, p.w_bf16, e) : 1.0f;
+        w[kind][second * (kMaxDim / 2) + pair] = from ? param(from, p.w_bf16, e) : 1.0f;
     }
     __syncthreads();
+}
+
+// V floats from a multiple of 4 on, out of shared memory.
+template <int V>
+__device__ __forceinline__ void four_by_four(const float *w, float *f) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) unpack<float, 4>(*reinterpret_cast<const uint4 *>(w + j), f + j);
 }
 
 template <int V, int NV, bool INTER>
@@ -159,7 +167,7 @@ __device__ __forceinline__ void lane_weights(const QkParams &p, const Pairs<V, N
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             a[i][j] = m.has[i] ? w[m.at[i] + j] : 0.0f;
-            b[i][j] = m.has[i] ? w[p.D / 2 + m.at[i] + j] : 0.0f;
+            b[i][j] = m.has[i] ? w[kMaxDim / 2 + m.at[i] + j] : 0.0f;
         }
 }
 
@@ -243,11 +251,39 @@ __global__ void __launch_bounds__(kWarps * 32) qk_forward(const QkParams p) {
     }
 }
 
+// The sums of a warp's lanes for dw: its teams, then the slot's warps, into the slot.
+template <int V, int NV, bool INTER>
+__device__ __forceinline__ void slot_sums(const QkParams &p, const Pairs<V, NV, INTER> &m, float (&acc_a)[NV][V], float (&acc_b)[NV][V], float *s_dw,
+                                          int slot, int kind, int warp, int mine) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            for (int sh = p.team; sh < 32; sh <<= 1) {
+                acc_a[n][j] = __fadd_rn(acc_a[n][j], __shfl_xor_sync(0xffffffffu, acc_a[n][j], sh));
+                acc_b[n][j] = __fadd_rn(acc_b[n][j], __shfl_xor_sync(0xffffffffu, acc_b[n][j], sh));
+            }
+            if (mine == 0 && m.has[n]) {
+                const int first = INTER ? 2 * (m.at[n] + j) : m.lo[n] + j, second = INTER ? first + 1 : m.hi[n] + j;
+                s_dw[warp * p.D + first] = acc_a[n][j];
+                s_dw[warp * p.D + second] = acc_b[n][j];
+            }
+        }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.D; d += kWarps * 32) {
+        float v = s_dw[d];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = __fadd_rn(v, s_dw[w * p.D + d]);
+        p.slots[(static_cast<int64_t>(slot) * 2 + kind) * p.D + d] = v;
+    }
+    __syncthreads();
+}
+
 template <typename T, int V, int NV, bool INTER, int U>
 __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward(const QkParams p) {
     using raw = raw_t<T, V>;
     __shared__ __align__(16) float s_w[2][kMaxDim];
-    __shared__ float s_dw[kWarps][kMaxDim];
+    __shared__ float s_dw[kWarps * kMaxDim];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tl = lane & (p.team - 1), mine = lane / p.team, teams = 32 / p.team;
     const Pairs<V, NV, INTER> m(p, tl);
@@ -335,29 +371,347 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward(const QkParams p) 
                 }
             }
             if (!h.dw) continue;
-            // the warp's teams, then the slot's warps
+            slot_sums<V, NV, INTER>(p, m, acc_a, acc_b, s_dw, slot, kind, warp, mine);
+        }
+    }
+}
+
+// ---- heads on their way in shared memory ----------------------------------------
+//
+// For heads in vectors of 16 bytes: each lane has the next DEPTH groups of heads of
+// its warp on their way in shared memory (it reads what it fetched itself, so
+// nothing has to meet for it), a unit's cosines and sines with its first group,
+// the position one unit earlier still.
+
+// The groups of heads that a warp takes, one after another: of its units (a token,
+// or a part of a token's groups) those of the queries, then of the keys; or, with
+// only >= 0, those of one kind. N addresses of the lane's head go along: of p's
+// inputs, or of its output (one a group: the step from a group to the next is an
+// addition each).
+enum Along { kInputs, kInputAndGradient, kOutput };
+template <typename T, Along WHAT>
+struct Walk {
+    static constexpr int N = WHAT == kInputAndGradient ? 2 : 1;
+    const QkParams &p;
+    int teams, mine, only;
+    bool scheduled;
+    int32_t u, stride, units, G0;
+    int32_t t = 0;  // the unit's token
+    int chunk = 0, kind = 0;
+    int head = 0;   // the group's first
+    int n = 0;      // heads of the kind
+    T *at[N];
+    int64_t step[N];
+    __device__ __forceinline__ Walk(const QkParams &p_, int teams_, int mine_, int only_, bool scheduled_, int32_t u_, int32_t stride_)
+        : p(p_), teams(teams_), mine(mine_), only(only_), scheduled(scheduled_), u(u_), stride(stride_), units(p_.T * p_.chunks) {
+        G0 = (p.kind[0].n + teams - 1) / teams;
+        enter();
+    }
+    __device__ __forceinline__ bool done() const { return u >= units; }
+    __device__ __forceinline__ int32_t token(int32_t unit, int &part) const {
+        const int32_t i = scheduled ? static_cast<int32_t>(sched_item(p.sched, static_cast<uint32_t>(unit))) : unit;
+        part = 0;
+        if (p.chunks == 1) return i;
+        const int32_t to = i / p.chunks;
+        part = i - to * p.chunks;
+        return to;
+    }
+    // to the unit's first group of a kind, if it has one; a token's groups go round its units, over both kinds
+    __device__ __forceinline__ bool begin(int k) {
+        const Heads &h = p.kind[k];
+        kind = k, n = h.n;
+        head = (k == 0 || p.chunks == 1 ? chunk : (chunk - G0 % p.chunks + p.chunks) % p.chunks) * teams;
+        if (head >= n) return false;
+        auto set = [&](int i, const void *base, int64_t st, int64_t sh) {
+            at[i] = const_cast<T *>(static_cast<const T *>(base)) + t * st + (head + mine) * sh;
+            step[i] = static_cast<int64_t>(p.chunks * teams) * sh;
+        };
+        if (WHAT == kOutput) set(0, h.out, h.st_out, h.sh_out);
+        else set(0, h.v, h.st, h.sh);
+        if (WHAT == kInputAndGradient) set(N - 1, h.dy, h.st_dy, h.sh_dy);
+        return true;
+    }
+    __device__ __forceinline__ void enter() {
+        for (; u < units; u += stride) {
+            t = token(u, chunk);
+            if (only <= 0 && begin(0)) return;
+            if (only != 0 && begin(1)) return;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        head += p.chunks * teams;
+#pragma unroll
+        for (int i = 0; i < N; ++i) at[i] += step[i];
+        if (head < n) return;
+        if (only < 0 && kind == 0 && begin(1)) return;
+        u += stride;
+        enter();
+    }
+    __device__ __forceinline__ bool has_head() const { return head + mine < n; }
+};
+
+// A warp's ring. Of a slot: PARTS vectors of each lane's group of heads and, with
+// a unit's first group, its cosines and sines, fetched by one team for all, and
+// whether its position lies in the table.
+template <int V, int NV, bool INTER, int DEPTH, int PARTS>
+struct Ring {
+    static constexpr int kTurns = 2 * NV * V / 4;  // vectors of a lane's cosines and sines
+    const QkParams &p;
+    const Pairs<V, NV, INTER> &m;
+    int tl, mine;
+    uint4 *heads, *turns;
+    int32_t *good_;
+    float c[NV][V], s[NV][V];  // of the unit that is worked on
+    bool good = false;
+    int32_t in = -1, out = -1, pos_next = 0;  // units
+    // bytes of all warps, behind `teams` lanes' worth of cosines and sines
+    static size_t bytes(int team) { return static_cast<size_t>(kWarps) * DEPTH * (PARTS * 32 * 16 + kTurns * team * 16 + 16); }
+    __device__ __forceinline__ Ring(const QkParams &p_, const Pairs<V, NV, INTER> &m_, uint4 *smem, int warp, int lane, int tl_, int mine_)
+        : p(p_), m(m_), tl(tl_), mine(mine_) {
+        heads = smem + warp * DEPTH * PARTS * 32 + lane;
+        smem += kWarps * DEPTH * PARTS * 32;
+        turns = smem + warp * DEPTH * kTurns * p.team;
+        smem += kWarps * DEPTH * kTurns * p.team;
+        good_ = reinterpret_cast<int32_t *>(smem + warp * DEPTH);
+    }
+    __device__ __forceinline__ uint4 *at(int slot, int i) const { return heads + (slot * PARTS + i) * 32; }
+    __device__ __forceinline__ uint4 *turn(int slot, int i) const { return turns + (slot * kTurns + i) * p.team + tl; }
+    // with a unit's first group
+    template <typename W>
+    __device__ __forceinline__ void put_angles(const W &w, int slot) {
+        if (w.u == in) return;
+        int part;
+        const int32_t pos = in >= 0 && w.u - in == w.stride ? pos_next : __ldg(p.pos + w.t);
+        in = w.u;
+        pos_next = w.units - w.u > w.stride ? __ldg(p.pos + w.token(w.u + w.stride, part)) : 0;
+        const bool ok = pos >= 0 && pos < p.P;
+        if (mine == 0) {
+            const int64_t row = static_cast<int64_t>(ok ? pos : 0) * (p.R / 2);
 #pragma unroll
             for (int n = 0; n < NV; ++n)
+                if (m.has[n] && m.at[n] < p.R / 2)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    for (int sh = p.team; sh < 32; sh <<= 1) {
-                        acc_a[n][j] = __fadd_rn(acc_a[n][j], __shfl_xor_sync(0xffffffffu, acc_a[n][j], sh));
-                        acc_b[n][j] = __fadd_rn(acc_b[n][j], __shfl_xor_sync(0xffffffffu, acc_b[n][j], sh));
+                    for (int j = 0; j < V; j += 4) {
+                        copy_async<16>(turn(slot, (n * V + j) / 2), p.cos + row + m.at[n] + j);
+                        copy_async<16>(turn(slot, (n * V + j) / 2 + 1), p.sin + row + m.at[n] + j);
                     }
-                    if (mine == 0 && m.has[n]) {
-                        const int first = INTER ? 2 * (m.at[n] + j) : m.lo[n] + j, second = INTER ? first + 1 : m.hi[n] + j;
-                        s_dw[warp][first] = acc_a[n][j];
-                        s_dw[warp][second] = acc_b[n][j];
+            if (tl == 0) {
+                good_[slot * 4] = ok;
+                if (!ok) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWherePos);
+            }
+        }
+    }
+    // when the slot's copies have come
+    template <typename W>
+    __device__ __forceinline__ void take_angles(const W &w, int slot) {
+        if (w.u == out) return;
+        out = w.u;
+        __syncwarp();
+        good = good_[slot * 4] != 0;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const bool turned = m.has[n] && m.at[n] < p.R / 2;
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                float x[4], y[4];
+                unpack<float, 4>(*turn(slot, (n * V + j) / 2), x);
+                unpack<float, 4>(*turn(slot, (n * V + j) / 2 + 1), y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[n][j + i] = turned ? x[i] : 1.0f, s[n][j + i] = turned ? y[i] : 0.0f;
+            }
+        }
+        __syncwarp();  // before the next copies into this slot
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void copy_wait_newest() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kDepthForward = 4;
+template <typename T>
+constexpr int kDepthBackward = sizeof(T) == 2 ? 4 : 2;
+
+template <typename T, int NV, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, 2) qk_forward_ring(const QkParams p) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T)), DEPTH = kDepthForward, PARTS = 2 * NV;
+    extern __shared__ __align__(16) uint4 smem[];
+    __shared__ __align__(16) float s_w[2][kMaxDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tl = lane & (p.team - 1), mine = lane / p.team, teams = 32 / p.team;
+    const Pairs<V, NV, INTER> m(p, tl);
+    Ring<V, NV, INTER, DEPTH, PARTS> ring(p, m, smem, warp, lane, tl, mine);
+    const int32_t u0 = static_cast<int32_t>(blockIdx.x) * kWarps + warp, stride = static_cast<int32_t>(gridDim.x) * kWarps;
+    Walk<T, kInputs> put(p, teams, mine, -1, true, u0, stride);
+    Walk<T, kOutput> get(p, teams, mine, -1, true, u0, stride);
+    auto issue = [&](int slot) {
+        if (!put.done()) {
+            ring.put_angles(put, slot);
+            if (put.has_head())
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+                    if (m.has[n]) {
+                        copy_async<16>(ring.at(slot, 2 * n), put.at[0] + m.lo[n]);
+                        copy_async<16>(ring.at(slot, 2 * n + 1), put.at[0] + m.hi[n]);
+                    }
+            put.next();
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) issue(d);
+    load_weights<INTER>(p, s_w);
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    for (int slot = 0; !get.done(); slot = slot + 1 == DEPTH ? 0 : slot + 1, get.next()) {
+        copy_wait_newest<DEPTH - 1>();
+        ring.take_angles(get, slot);
+        const bool on = get.has_head();
+        float a[NV][V], b[NV][V], ss = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            split<T, V, INTER>(*ring.at(slot, 2 * n), *ring.at(slot, 2 * n + 1), a[n], b[n]);
+            if (!(on && m.has[n]))  // never fetched
+#pragma unroll
+                for (int j = 0; j < V; ++j) a[n][j] = b[n][j] = 0.0f;
+            ss = __fadd_rn(ss, __fadd_rn(vec_dot(a[n], a[n]), vec_dot(b[n], b[n])));
+        }
+        issue(slot);
+        const float r = rsqrtf(__fmaf_rn(team_sum(ss, p.team), inv_d, p.eps));
+        const float *w = s_w[get.kind];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            if (!m.has[n]) continue;
+            float x[V], y[V], wa[V], wb[V];
+            four_by_four<V>(w + m.at[n], wa);
+            four_by_four<V>(w + kMaxDim / 2 + m.at[n], wb);
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                const float2 na = mul2(mul2(make_float2(a[n][j], a[n][j + 1]), both(r)), make_float2(wa[j], wa[j + 1]));
+                const float2 nb = mul2(mul2(make_float2(b[n][j], b[n][j + 1]), both(r)), make_float2(wb[j], wb[j + 1]));
+                const float2 c = make_float2(ring.c[n][j], ring.c[n][j + 1]), s = make_float2(ring.s[n][j], ring.s[n][j + 1]);
+                const float2 xx = fma2(mul2(nb, both(-1.0f)), s, mul2(na, c)), yy = fma2(na, s, mul2(nb, c));
+                x[j] = xx.x, x[j + 1] = xx.y, y[j] = yy.x, y[j + 1] = yy.y;
+            }
+            if (!ring.good)
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[j] = y[j] = 0.0f;
+            uint4 rx, ry;
+            join<T, V, INTER>(x, y, rx, ry);
+            if (on) {
+                *reinterpret_cast<uint4 *>(get.at[0] + m.lo[n]) = rx;
+                *reinterpret_cast<uint4 *>(get.at[0] + m.hi[n]) = ry;
+            }
+        }
+    }
+    copy_wait();
+}
+
+template <typename T, int NV, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParams p) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T)), DEPTH = kDepthBackward<T>, PARTS = 4 * NV;
+    extern __shared__ __align__(16) uint4 smem[];
+    __shared__ __align__(16) float s_w[2][kMaxDim];
+    float *s_dw = reinterpret_cast<float *>(smem);  // [kWarps][D]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tl = lane & (p.team - 1), mine = lane / p.team, teams = 32 / p.team;
+    const Pairs<V, NV, INTER> m(p, tl);
+    load_weights<INTER>(p, s_w);
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    for (int turn = blockIdx.x; turn < p.n_slots; turn += gridDim.x) {
+        const int out_slot = static_cast<int>(sched_item(p.sched, static_cast<uint32_t>(turn)));
+#pragma unroll 1
+        for (int kind = 0; kind < 2; ++kind) {
+            const Heads &h = p.kind[kind];
+            const int32_t u0 = out_slot * kWarps + warp, stride = p.n_slots * kWarps;
+            Walk<T, kInputAndGradient> put(p, teams, mine, kind, false, u0, stride);
+            Walk<T, kOutput> get(p, teams, mine, kind, false, u0, stride);
+            Ring<V, NV, INTER, DEPTH, PARTS> ring(p, m, smem + kWarps * p.D / 4, warp, lane, tl, mine);
+            auto issue = [&](int slot) {
+                if (!put.done()) {
+                    ring.put_angles(put, slot);
+                    if (put.has_head())
+#pragma unroll
+                        for (int n = 0; n < NV; ++n)
+                            if (m.has[n]) {
+                                copy_async<16>(ring.at(slot, 4 * n), put.at[0] + m.lo[n]);
+                                copy_async<16>(ring.at(slot, 4 * n + 1), put.at[0] + m.hi[n]);
+                                copy_async<16>(ring.at(slot, 4 * n + 2), put.at[1] + m.lo[n]);
+                                copy_async<16>(ring.at(slot, 4 * n + 3), put.at[1] + m.hi[n]);
+                            }
+                    put.next();
+                }
+                copy_commit();
+            };
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) issue(d);
+            float acc_a[NV][V] = {}, acc_b[NV][V] = {};
+            const float *w = s_w[kind];
+#pragma unroll 1
+            for (int slot = 0; !get.done(); slot = slot + 1 == DEPTH ? 0 : slot + 1, get.next()) {
+                copy_wait_newest<DEPTH - 1>();
+                ring.take_angles(get, slot);
+                const bool here = get.has_head(), on = here && ring.good;
+                float2 a[NV][V / 2], b[NV][V / 2], ga[NV][V / 2], gb[NV][V / 2], wa[NV][V / 2], wb[NV][V / 2], ss = both(0.0f), dot = both(0.0f);
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    float fa[V], fb[V], x[V], y[V];
+                    split<T, V, INTER>(*ring.at(slot, 4 * n), *ring.at(slot, 4 * n + 1), fa, fb);
+                    split<T, V, INTER>(*ring.at(slot, 4 * n + 2), *ring.at(slot, 4 * n + 3), x, y);
+                    if (!(on && m.has[n]))  // never fetched, or without a position
+#pragma unroll
+                        for (int j = 0; j < V; ++j) fa[j] = fb[j] = x[j] = y[j] = 0.0f;
+                    // places that the lane does not have read a weight of another (of no weight)
+                    const int at = m.has[n] ? m.at[n] : 0;
+                    float fw[V], gw[V];
+                    four_by_four<V>(w + at, fw);
+                    four_by_four<V>(w + kMaxDim / 2 + at, gw);
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        const float2 c = make_float2(ring.c[n][j], ring.c[n][j + 1]), s = make_float2(ring.s[n][j], ring.s[n][j + 1]);
+                        const float2 dx = make_float2(x[j], x[j + 1]), dy = make_float2(y[j], y[j + 1]);
+                        const int i = j / 2;
+                        a[n][i] = make_float2(fa[j], fa[j + 1]), b[n][i] = make_float2(fb[j], fb[j + 1]);
+                        ga[n][i] = fma2(dx, c, mul2(dy, s));
+                        gb[n][i] = fma2(mul2(dx, both(-1.0f)), s, mul2(dy, c));
+                        ss = fma2(a[n][i], a[n][i], ss);
+                        ss = fma2(b[n][i], b[n][i], ss);
+                        // g w is all that is needed of the weights later on too
+                        wa[n][i] = mul2(ga[n][i], make_float2(fw[j], fw[j + 1])), wb[n][i] = mul2(gb[n][i], make_float2(gw[j], gw[j + 1]));
+                        dot = fma2(wa[n][i], a[n][i], dot);
+                        dot = fma2(wb[n][i], b[n][i], dot);
                     }
                 }
-            __syncthreads();
-            for (int d = threadIdx.x; d < p.D; d += kWarps * 32) {
-                float v = s_dw[0][d];
+                issue(slot);
+                float sum = across(ss), inner = across(dot);
+                for (int sh = p.team >> 1; sh > 0; sh >>= 1) {
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, sh));
+                    inner = __fadd_rn(inner, __shfl_xor_sync(0xffffffffu, inner, sh));
+                }
+                // a place without a head, or a token without a position: nothing for dw
+                const float r = on ? rsqrtf(__fmaf_rn(sum, inv_d, p.eps)) : 0.0f;
+                const float back = on ? -__fmul_rn(__fmul_rn(r, r), __fmul_rn(r, __fmul_rn(inner, inv_d))) : 0.0f;
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) v = __fadd_rn(v, s_dw[w][d]);
-                p.slots[(static_cast<int64_t>(slot) * 2 + kind) * p.D + d] = v;
+                for (int n = 0; n < NV; ++n) {
+                    float x[V], y[V];
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float2 sa = fma2(mul2(a[n][i], both(r)), ga[n][i], make_float2(acc_a[n][2 * i], acc_a[n][2 * i + 1]));
+                        const float2 sb = fma2(mul2(b[n][i], both(r)), gb[n][i], make_float2(acc_b[n][2 * i], acc_b[n][2 * i + 1]));
+                        acc_a[n][2 * i] = sa.x, acc_a[n][2 * i + 1] = sa.y, acc_b[n][2 * i] = sb.x, acc_b[n][2 * i + 1] = sb.y;
+                        const float2 da = fma2(wa[n][i], both(r), mul2(a[n][i], both(back))), db = fma2(wb[n][i], both(r), mul2(b[n][i], both(back)));
+                        x[2 * i] = da.x, x[2 * i + 1] = da.y, y[2 * i] = db.x, y[2 * i + 1] = db.y;
+                    }
+                    uint4 rx, ry;
+                    join<T, V, INTER>(x, y, rx, ry);
+                    if (here && m.has[n]) {
+                        *reinterpret_cast<uint4 *>(get.at[0] + m.lo[n]) = rx;
+                        *reinterpret_cast<uint4 *>(get.at[0] + m.hi[n]) = ry;
+                    }
+                }
             }
-            __syncthreads();
+            copy_wait();
+            if (h.dw) slot_sums<V, NV, INTER>(p, m, acc_a, acc_b, s_dw, out_slot, kind, warp, mine);
         }
     }
 }
@@ -491,7 +845,8 @@ dgr_status check(const Call &c) {
     return DGR_OK;
 }
 
-template <typename T, int V, int NV, bool INTER>
+// RING: heads in vectors of 16 bytes.
+template <typename T, int V, int NV, bool INTER, bool RING>
 dgr_status launch(QkParams p, bool backward, int sms, cudaStream_t s) {
     const int vecs = (p.D / 2 + V - 1) / V;  // groups of pairs a head
     int team = 1;
@@ -500,22 +855,40 @@ dgr_status launch(QkParams p, bool backward, int sms, cudaStream_t s) {
     const int teams = 32 / team;
     const int groups = (p.kind[0].n + teams - 1) / teams + (p.kind[1].n + teams - 1) / teams;
     // few tokens: a token over several warps, down to one group of heads each
-    int64_t chunks = p.T > 0 ? (304 * kWarps + p.T - 1) / p.T : 1;
+    int64_t chunks = p.T > 0 ? (kSlots * kWarps * kUnitsWarp + p.T - 1) / p.T : 1;
     if (chunks > groups) chunks = groups;
     p.chunks = static_cast<int32_t>(chunks);
     const int64_t units = static_cast<int64_t>(p.T) * p.chunks;
-    if (units >= INT32_MAX) return DGR_ERR_UNSUPPORTED;
+    if (units > (1 << 30)) return DGR_ERR_UNSUPPORTED;
     if (!backward) {
         p.sched = sched_for(static_cast<uint32_t>(units));
-        const int64_t ctas = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 4;
-        qk_forward<T, V, NV, INTER, (V * NV >= 8 ? 4 : 2)><<<sched_grid(static_cast<unsigned>(ctas < most ? ctas : most)), kWarps * 32, 0, s>>>(p);
+        const int64_t ctas = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 2;
+        const unsigned grid = sched_grid(static_cast<unsigned>(ctas < most ? ctas : most));
+        if constexpr (RING) {
+            using R = Ring<V, NV, INTER, kDepthForward, 2 * NV>;
+            const size_t smem = R::bytes(team);
+            const dgr_status st = allow_smem(qk_forward_ring<T, NV, INTER>, smem, R::bytes(32));
+            if (st != DGR_OK) return st;
+            qk_forward_ring<T, NV, INTER><<<grid, kWarps * 32, smem, s>>>(p);
+        } else {
+            qk_forward<T, V, NV, INTER, 2><<<grid, kWarps * 32, 0, s>>>(p);
+        }
         return launch_status();
     }
     p.n_slots = slots_of(units);
     p.sched = sched_for(static_cast<uint32_t>(p.n_slots));
     const int most = sms * 2;
-    qk_backward<T, V, NV, INTER, 2><<<sched_grid(static_cast<unsigned>(p.n_slots < most ? p.n_slots : most)), kWarps * 32, 0, s>>>(p);
-    dgr_status st = launch_status();
+    const unsigned grid = sched_grid(static_cast<unsigned>(p.n_slots < most ? p.n_slots : most));
+    dgr_status st;
+    if constexpr (RING) {
+        using R = Ring<V, NV, INTER, kDepthBackward<T>, 4 * NV>;
+        const size_t smem = R::bytes(team) + sizeof(float) * kWarps * p.D;
+        if ((st = allow_smem(qk_backward_ring<T, NV, INTER>, smem, R::bytes(32) + sizeof(float) * kWarps * kMaxDim)) != DGR_OK) return st;
+        qk_backward_ring<T, NV, INTER><<<grid, kWarps * 32, smem, s>>>(p);
+    } else {
+        qk_backward<T, V, NV, INTER, 1><<<grid, kWarps * 32, 0, s>>>(p);
+    }
+    st = launch_status();
     if (st != DGR_OK || (!p.kind[0].dw && !p.kind[1].dw)) return st;
     qk_fold<<<static_cast<unsigned>((2 * p.D + kFoldCols - 1) / kFoldCols), kFoldCols * kFoldWays, 0, s>>>(p);
     return launch_status();
@@ -524,9 +897,9 @@ dgr_status launch(QkParams p, bool backward, int sms, cudaStream_t s) {
 template <typename T, bool INTER>
 dgr_status launch_width(const QkParams &p, int vec, bool backward, int sms, cudaStream_t s) {
     constexpr int W = 16 / static_cast<int>(sizeof(T));
-    if (vec == W) return launch<T, W, 8 / W, INTER>(p, backward, sms, s);
-    if (vec == 2) return launch<T, 2, 4, INTER>(p, backward, sms, s);
-    return launch<T, 1, 8, INTER>(p, backward, sms, s);
+    if (vec == W) return launch<T, W, 8 / W, INTER, true>(p, backward, sms, s);
+    if (vec == 2) return launch<T, 2, 4, INTER, false>(p, backward, sms, s);
+    return launch<T, 1, 8, INTER, false>(p, backward, sms, s);
 }
 
 dgr_status run(const Call &c, void *stream) {
