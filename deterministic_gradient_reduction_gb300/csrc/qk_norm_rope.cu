@@ -31,7 +31,6 @@ constexpr int kWarps = 8;
 constexpr int kMaxDim = 512;
 constexpr int kMaxHeads = 1024;
 constexpr int kSlots = 304;     // CTAs of the backward pass at most, two an SM
-constexpr int kUnitsWarp = 2;   // units a warp at least, where tokens have the groups of heads for it
 constexpr int kFoldCols = 8, kFoldWays = 32;
 constexpr int kWherePos = 420;
 
@@ -52,8 +51,9 @@ struct QkParams {
     const int32_t *pos;
     float eps;
     int32_t team, chunks;      // lanes a head; warps a token
-    int32_t n_slots, accumulate;
-    float *slots;              // [n_slots, 2, D]
+    // slots of dw_q and of dw_k; turns: what CTAs take, one slot of each, or (split) one
+    int32_t count[2], turns, split, accumulate;
+    float *slots;              // [count[0] + count[1], D]
     WsHeader *hdr;
     Sched sched;
 };
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_forward(const QkParams p) {
 // The sums of a warp's lanes for dw: its teams, then the slot's warps, into the slot.
 template <int V, int NV, bool INTER>
 __device__ __forceinline__ void slot_sums(const QkParams &p, const Pairs<V, NV, INTER> &m, float (&acc_a)[NV][V], float (&acc_b)[NV][V], float *s_dw,
-                                          int slot, int kind, int warp, int mine) {
+                                          int slot, int warp, int mine) {
 #pragma unroll
     for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -274,7 +274,7 @@ __device__ __forceinline__ void slot_sums(const QkParams &p, const Pairs<V, NV, 
         float v = s_dw[d];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) v = __fadd_rn(v, s_dw[w * p.D + d]);
-        p.slots[(static_cast<int64_t>(slot) * 2 + kind) * p.D + d] = v;
+        p.slots[static_cast<int64_t>(slot) * p.D + d] = v;
     }
     __syncthreads();
 }
@@ -290,18 +290,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward(const QkParams p) 
     load_weights<INTER>(p, s_w);
     const int64_t units = static_cast<int64_t>(p.T) * p.chunks;
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    for (int turn = blockIdx.x; turn < p.n_slots; turn += gridDim.x) {
-        const int slot = static_cast<int>(sched_item(p.sched, static_cast<uint32_t>(turn)));
+    for (int i = blockIdx.x; i < p.turns; i += gridDim.x) {
+        const int turn = static_cast<int>(sched_item(p.sched, static_cast<uint32_t>(i)));
 #pragma unroll 1
         for (int kind = 0; kind < 2; ++kind) {
+            const int mine_of = p.split && kind ? turn - p.count[0] : turn;  // which of the kind's slots
+            if (mine_of < 0 || mine_of >= p.count[kind]) continue;
+            const int slot_out = mine_of + (kind ? p.count[0] : 0);
             const Heads &h = p.kind[kind];
             const int groups = (h.n + teams - 1) / teams;
             float acc_a[NV][V] = {}, acc_b[NV][V] = {}, wa[NV][V], wb[NV][V];
             lane_weights<V, NV, INTER>(p, m, s_w[kind], wa, wb);
-            for (int64_t u = static_cast<int64_t>(slot) * kWarps + warp; u < units; u += static_cast<int64_t>(p.n_slots) * kWarps) {
+            for (int64_t u = static_cast<int64_t>(mine_of) * kWarps + warp; u < units; u += static_cast<int64_t>(p.count[kind]) * kWarps) {
                 const int64_t t = u / p.chunks;
-                int first = static_cast<int>(u - t * p.chunks);
-                if (kind) first = (first - (p.kind[0].n + teams - 1) / teams % p.chunks + p.chunks) % p.chunks;
+                const int first = static_cast<int>(u - t * p.chunks);
                 if (first >= groups) continue;
                 int32_t pos;
                 const bool good = position(p, t, pos);
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward(const QkParams p) 
                 }
             }
             if (!h.dw) continue;
-            slot_sums<V, NV, INTER>(p, m, acc_a, acc_b, s_dw, slot, kind, warp, mine);
+            slot_sums<V, NV, INTER>(p, m, acc_a, acc_b, s_dw, slot_out, warp, mine);
         }
     }
 }
@@ -420,7 +422,7 @@ struct Walk {
     __device__ __forceinline__ bool begin(int k) {
         const Heads &h = p.kind[k];
         kind = k, n = h.n;
-        head = (k == 0 || p.chunks == 1 ? chunk : (chunk - G0 % p.chunks + p.chunks) % p.chunks) * teams;
+        head = (k == 0 || only >= 0 || p.chunks == 1 ? chunk : (chunk - G0 % p.chunks + p.chunks) % p.chunks) * teams;
         if (head >= n) return false;
         auto set = [&](int i, const void *base, int64_t st, int64_t sh) {
             at[i] = const_cast<T *>(static_cast<const T *>(base)) + t * st + (head + mine) * sh;
@@ -566,12 +568,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_forward_ring(const QkParams
     for (int slot = 0; !get.done(); slot = slot + 1 == DEPTH ? 0 : slot + 1, get.next()) {
         copy_wait_newest<DEPTH - 1>();
         ring.take_angles(get, slot);
-        const bool on = get.has_head();
+        const bool on = get.has_head(), whole = __all_sync(0xffffffffu, on && m.has[NV - 1]);  // every lane has all its places
         float a[NV][V], b[NV][V], ss = 0.0f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             split<T, V, INTER>(*ring.at(slot, 2 * n), *ring.at(slot, 2 * n + 1), a[n], b[n]);
-            if (!(on && m.has[n]))  // never fetched
+            if (!whole && !(on && m.has[n]))  // never fetched
 #pragma unroll
                 for (int j = 0; j < V; ++j) a[n][j] = b[n][j] = 0.0f;
             ss = __fadd_rn(ss, __fadd_rn(vec_dot(a[n], a[n]), vec_dot(b[n], b[n])));
@@ -618,12 +620,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParam
     const Pairs<V, NV, INTER> m(p, tl);
     load_weights<INTER>(p, s_w);
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    for (int turn = blockIdx.x; turn < p.n_slots; turn += gridDim.x) {
-        const int out_slot = static_cast<int>(sched_item(p.sched, static_cast<uint32_t>(turn)));
+    for (int i = blockIdx.x; i < p.turns; i += gridDim.x) {
+        const int turn = static_cast<int>(sched_item(p.sched, static_cast<uint32_t>(i)));
 #pragma unroll 1
         for (int kind = 0; kind < 2; ++kind) {
+            const int mine_of = p.split && kind ? turn - p.count[0] : turn;  // which of the kind's slots
+            if (mine_of < 0 || mine_of >= p.count[kind]) continue;
+            const int slot_out = mine_of + (kind ? p.count[0] : 0);
             const Heads &h = p.kind[kind];
-            const int32_t u0 = out_slot * kWarps + warp, stride = p.n_slots * kWarps;
+            const int32_t u0 = mine_of * kWarps + warp, stride = p.count[kind] * kWarps;
             Walk<T, kInputAndGradient> put(p, teams, mine, kind, false, u0, stride);
             Walk<T, kOutput> get(p, teams, mine, kind, false, u0, stride);
             Ring<V, NV, INTER, DEPTH, PARTS> ring(p, m, smem + kWarps * p.D / 4, warp, lane, tl, mine);
@@ -651,14 +656,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParam
             for (int slot = 0; !get.done(); slot = slot + 1 == DEPTH ? 0 : slot + 1, get.next()) {
                 copy_wait_newest<DEPTH - 1>();
                 ring.take_angles(get, slot);
-                const bool here = get.has_head(), on = here && ring.good;
+                const bool here = get.has_head(), on = here && ring.good, whole = __all_sync(0xffffffffu, on && m.has[NV - 1]);
                 float2 a[NV][V / 2], b[NV][V / 2], ga[NV][V / 2], gb[NV][V / 2], wa[NV][V / 2], wb[NV][V / 2], ss = both(0.0f), dot = both(0.0f);
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     float fa[V], fb[V], x[V], y[V];
                     split<T, V, INTER>(*ring.at(slot, 4 * n), *ring.at(slot, 4 * n + 1), fa, fb);
                     split<T, V, INTER>(*ring.at(slot, 4 * n + 2), *ring.at(slot, 4 * n + 3), x, y);
-                    if (!(on && m.has[n]))  // never fetched, or without a position
+                    if (!whole && !(on && m.has[n]))  // never fetched, or without a position
 #pragma unroll
                         for (int j = 0; j < V; ++j) fa[j] = fb[j] = x[j] = y[j] = 0.0f;
                     // places that the lane does not have read a weight of another (of no weight)
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParam
                 }
             }
             copy_wait();
-            if (h.dw) slot_sums<V, NV, INTER>(p, m, acc_a, acc_b, s_dw, out_slot, kind, warp, mine);
+            if (h.dw) slot_sums<V, NV, INTER>(p, m, acc_a, acc_b, s_dw, slot_out, warp, mine);
         }
     }
 }
@@ -722,9 +727,15 @@ __global__ void __launch_bounds__(kFoldCols *kFoldWays) qk_fold(const QkParams p
     const int col = threadIdx.x % kFoldCols, way = threadIdx.x / kFoldCols;
     const int i = blockIdx.x * kFoldCols + col, kind = i >= p.D;
     const bool on = i < 2 * p.D && p.kind[kind].dw;
-    float v = 0.0f;
-    if (on)
-        for (int s = way; s < p.n_slots; s += kFoldWays) v = __fadd_rn(v, __ldcg(p.slots + static_cast<int64_t>(s) * 2 * p.D + i));
+    // all of a way's slots on their way at once
+    constexpr int kMost = (kSlots + kFoldWays - 1) / kFoldWays;
+    float x[kMost], v = 0.0f;
+    const int first = kind ? p.count[0] : 0, n = p.count[kind];
+    const float *from = p.slots + static_cast<int64_t>(first) * p.D + (i - kind * p.D);
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) x[k] = on && way + k * kFoldWays < n ? __ldcg(from + static_cast<int64_t>(way + k * kFoldWays) * p.D) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) v = __fadd_rn(v, x[k]);
     part[way][col] = v;
     for (int half = kFoldWays / 2; half > 0; half >>= 1) {
         __syncthreads();
@@ -781,9 +792,20 @@ struct Call {
     bool backward;
 };
 
-int32_t slots_of(int64_t T) {
-    const int64_t n = (T + kWarps - 1) / kWarps;
-    return static_cast<int32_t>(n < 1 ? 1 : n < kSlots ? n : kSlots);
+// Slots for the queries and for the keys. Few units: a CTA has one of either, as
+// many of each as its heads are (every CTA starts its copies once; 4096 x 32+8 x 64
+// bf16 29 -> 23 us). Many: each CTA has one of both, so that all have the same to do
+// (16384 x 32+8 x 128 bf16 102 us, 112 with the split).
+void slots_of(QkParams &p, int64_t units) {
+    const int64_t heads = p.kind[0].n + p.kind[1].n, most = (units + kWarps - 1) / kWarps;
+    p.split = units < static_cast<int64_t>(kSlots) * kWarps * 3;
+    for (int k = 0; k < 2; ++k) {
+        const int64_t n = p.kind[k].n;
+        int64_t s = !p.split ? kSlots : (kSlots - 1) * n / heads;  // together at most kSlots - 1, and one for who has none
+        if (s < 1) s = 1;
+        p.count[k] = static_cast<int32_t>(n == 0 ? 0 : s < most ? s : most);
+    }
+    p.turns = p.split ? p.count[0] + p.count[1] : p.count[0] > p.count[1] ? p.count[0] : p.count[1];
 }
 
 dgr_status check(const Call &c) {
@@ -855,7 +877,7 @@ dgr_status launch(QkParams p, bool backward, int sms, cudaStream_t s) {
     const int teams = 32 / team;
     const int groups = (p.kind[0].n + teams - 1) / teams + (p.kind[1].n + teams - 1) / teams;
     // few tokens: a token over several warps, down to one group of heads each
-    int64_t chunks = p.T > 0 ? (kSlots * kWarps * kUnitsWarp + p.T - 1) / p.T : 1;
+    int64_t chunks = p.T > 0 ? (kSlots * kWarps + p.T - 1) / p.T : 1;
     if (chunks > groups) chunks = groups;
     p.chunks = static_cast<int32_t>(chunks);
     const int64_t units = static_cast<int64_t>(p.T) * p.chunks;
@@ -875,12 +897,13 @@ dgr_status launch(QkParams p, bool backward, int sms, cudaStream_t s) {
         }
         return launch_status();
     }
-    p.n_slots = slots_of(units);
-    p.sched = sched_for(static_cast<uint32_t>(p.n_slots));
+    slots_of(p, units);
+    p.sched = sched_for(static_cast<uint32_t>(p.turns));
     const int most = sms * 2;
-    const unsigned grid = sched_grid(static_cast<unsigned>(p.n_slots < most ? p.n_slots : most));
-    dgr_status st;
-    if constexpr (RING) {
+    const unsigned grid = sched_grid(static_cast<unsigned>(p.turns < most ? p.turns : most));
+    dgr_status st = DGR_OK;
+    if (p.turns == 0) {  // no tokens: dw is 0
+    } else if constexpr (RING) {
         using R = Ring<V, NV, INTER, kDepthBackward<T>, 4 * NV>;
         const size_t smem = R::bytes(team) + sizeof(float) * kWarps * p.D;
         if ((st = allow_smem(qk_backward_ring<T, NV, INTER>, smem, R::bytes(32) + sizeof(float) * kWarps * kMaxDim)) != DGR_OK) return st;
