@@ -28,6 +28,7 @@
 // Deterministic: sums go over threads, warps and CTAs in a fixed order set by the
 // type, T, V, the alignment and K; the collected elements' order is chance, their
 // ranks are not.
+#include <cfloat>
 #include <climits>
 #include <cstddef>
 
@@ -286,18 +287,21 @@ struct TopOf {
     int par, lane, per_part, size, cap;
     int n_key;  // candidates, where the row has one CTA
 
-    // K-th largest of the threads' maxima as a key, bit by bit from bit `from` on; what
+    // K-th largest of the threads' maxima as a key, two bits at a time from bit `from` on; what
     // lies below bit `to` is left out, so that a lower bound comes of it
     __device__ __forceinline__ uint32_t bound(uint32_t at, int from, int to) const {
         uint32_t key[MT / 32];
 #pragma unroll
         for (int i = 0; i < MT / 32; ++i) key[i] = static_cast<uint32_t>(key_of(ts.top[par][i * 32 + lane], 0) >> 32);
-        for (int bit = from; bit >= to; --bit) {
-            const uint32_t want = at | 1u << bit;
-            int n = 0;
+        for (int bit = from - 1; bit >= to; bit -= 2) {
+            int n[3] = {0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < MT / 32; ++i) n += key[i] >= want;
-            if (static_cast<int>(__reduce_add_sync(0xffffffffu, n)) >= p.K) at = want;
+            for (int i = 0; i < MT / 32; ++i)
+#pragma unroll
+                for (uint32_t d = 1; d < 4; ++d) n[d - 1] += key[i] >= (at | d << bit);
+#pragma unroll
+            for (int d = 0; d < 3; ++d) n[d] = static_cast<int>(__reduce_add_sync(0xffffffffu, n[d]));
+            at |= static_cast<uint32_t>((n[0] >= p.K) + (n[1] >= p.K) + (n[2] >= p.K)) << bit;
         }
         return at;
     }
@@ -325,66 +329,53 @@ struct TopOf {
         }
     }
     // reads the listed parts: pushes the elements above b and lists those equal to it in
-    // `same`; how many these are. Memory operations of this warp queue behind all the
-    // row loads of the SM, so few wait for one another here: values come out of registers.
+    // `same`; how many these are. A lane has a part, four vectors of it at a time. One
+    // warp does this, at four or five cycles an instruction, so they are few: a mask of
+    // the elements that reach b, and a word of it by a tree of selections.
     __device__ __forceinline__ int elements(int n_list, float b, bool equal) {
-        constexpr int U = 32 / VEC;  // a bit an element
+        constexpr int U = 4, PER = 4 / static_cast<int>(sizeof(T));  // elements a word
+        const float least = b > -INFINITY ? b : -FLT_MAX;           // -inf reaches nothing
         int n_same = 0;
-        const int n = n_list * per_part;
-        for (int i0 = 0; i0 < n; i0 += 32 * U) {
-            uint4 r[U];
-            int at[U];
+        for (int i0 = 0; i0 < n_list; i0 += 32) {
+            const int which = i0 + lane < n_list ? ts.list[i0 + lane] : -1;
+            const int v0 = which < 0 ? 0 : which % MT + which / MT * per_part * MT;
+            for (int k = 0; k < per_part; k += U) {
+                uint4 r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + 32 * u + lane;
-                at[u] = i < n ? ts.list[i / per_part] : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + 32 * u + lane, v = at[u] % MT + (at[u] / MT * per_part + i % per_part) * MT;
-                at[u] = i < n && v < view.count ? v : -1;
-                r[u] = make_uint4(0, 0, 0, 0);
-                load_if<true>(r[u], first + static_cast<int64_t>(v) * 16, at[u] >= 0);
-            }
-            uint32_t above = 0, same = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float x[VEC];
-                unpack<T, VEC>(r[u], x);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    above |= static_cast<uint32_t>(at[u] >= 0 && x[j] > b) << (u * VEC + j);
-                    same |= static_cast<uint32_t>(at[u] >= 0 && equal && x[j] == b) << (u * VEC + j);
+                for (int u = 0; u < U; ++u) {
+                    const int v = v0 + (k + u) * MT;
+                    constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
+                    r[u] = make_uint4(low, low, low, low);
+                    load_if<true>(r[u], first + static_cast<int64_t>(v) * 16, which >= 0 && v < view.count);
                 }
-            }
-            auto index_of = [&](int e) {
-                int v = at[0];
-#pragma unroll
-                for (int u = 1; u < U; ++u) v = e / VEC == u ? at[u] : v;
-                return view.head + (view.first + v) * VEC + e % VEC;
-            };
-            while (__any_sync(0xffffffffu, above != 0)) {
-                const bool on = above != 0;
-                const int e = on ? __ffs(above) - 1 : 0;
-                above &= above - 1;
-                float v = 0.0f;
+                uint32_t reach = 0;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     float x[VEC];
                     unpack<T, VEC>(r[u], x);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) v = e == u * VEC + j ? x[j] : v;
+                    for (int j = 0; j < VEC; ++j)
+                        if (x[j] >= least) reach |= 1u << (u * VEC + j);
                 }
-                push(v, index_of(e), on);
-            }
-            while (__any_sync(0xffffffffu, same != 0) && n_same <= kFew) {
-                const bool on = same != 0;
-                const int e = on ? __ffs(same) - 1 : 0;
-                same &= same - 1;
-                const uint32_t who = __ballot_sync(0xffffffffu, on);
-                const int to = n_same + __popc(who & ((1u << lane) - 1));
-                if (on && to < kFew) ts.same[to] = index_of(e);
-                n_same += __popc(who);
+                while (__any_sync(0xffffffffu, reach != 0)) {
+                    const int e = __ffs(reach) - 1, word = e / PER;  // (where there is none: of nothing)
+                    uint32_t q[16] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w, r[2].x, r[2].y, r[2].z, r[2].w, r[3].x, r[3].y, r[3].z, r[3].w};
+#pragma unroll
+                    for (int half = 8; half > 0; half >>= 1)
+#pragma unroll
+                        for (int i = 0; i < half; ++i) q[i] = word & half ? q[i + half] : q[i];
+                    const float v = sizeof(T) == 4 ? __uint_as_float(q[0]) : __uint_as_float(e & 1 ? q[0] & 0xffff0000u : q[0] << 16);
+                    const int index = view.head + (view.first + v0 + (k + e / VEC) * MT) * VEC + e % VEC;
+                    const bool on = reach != 0, above = on && v > b;
+                    push(v, index, above);
+                    if (equal) {
+                        const uint32_t who = __ballot_sync(0xffffffffu, on && v == b);
+                        const int to = n_same + __popc(who & ((1u << lane) - 1));
+                        if (on && v == b && to < kFew) ts.same[to] = index;
+                        n_same += __popc(who);
+                    }
+                    reach &= reach - 1;
+                }
             }
         }
         __syncwarp();
@@ -392,26 +383,34 @@ struct TopOf {
     }
     // lists the parts whose maximum is above `b` (or equal to it), the first kFew; how many
     __device__ __forceinline__ int list_parts(float b, bool equal) const {
-        constexpr int n_vec = kParts * MT / 8;
-        int n = 0;
+        constexpr int n_vec = kParts * MT / 8, per = (n_vec + 31) / 32;
+        static_assert(per <= 32, "a bit a vector");
         const uint4 *part = reinterpret_cast<const uint4 *>(&ts.part[par][0][0]);
-        for (int i0 = 0; i0 < n_vec; i0 += 128) {
-            uint4 q[4];
+        auto reaches = [&](float x) { return equal ? x >= b : x > b; };
+        // which of a lane's vectors of eight reach it
+        uint32_t some = 0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) q[u] = i0 + 32 * u + lane < n_vec ? part[i0 + 32 * u + lane] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        for (int i = 0; i < per; ++i) {
+            const uint4 q = i * 32 + lane < n_vec ? part[i * 32 + lane] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            auto h = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+            const __nv_bfloat162 top = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
+            if (reaches(fmaxf(__low2float(top), __high2float(top)))) some |= 1u << i;
+        }
+        int n = 0;
+        while (__any_sync(0xffffffffu, some != 0)) {
+            const int i = some ? __ffs(some) - 1 : 0;
+            float x[8];
+            unpack<bf16, 8>(part[i * 32 + lane < n_vec ? i * 32 + lane : 0], x);
             uint32_t on = 0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float x[8];
-                unpack<bf16, 8>(q[u], x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) on |= static_cast<uint32_t>((equal ? x[j] >= b : x[j] > b) && x[j] > -INFINITY) << (8 * u + j);
-            }
+            for (int j = 0; j < 8; ++j)
+                if (reaches(x[j]) && x[j] > -INFINITY) on |= 1u << j;
+            if (!some) on = 0;
+            some &= some - 1;
             while (__any_sync(0xffffffffu, on != 0)) {
-                const int e = __ffs(on) - 1;
                 const uint32_t who = __ballot_sync(0xffffffffu, on != 0);
                 const int to = n + __popc(who & ((1u << lane) - 1));
-                if (on != 0 && to < kFew) ts.list[to] = static_cast<uint16_t>(8 * (i0 + 32 * (e / 8) + lane) + e % 8);
+                if (on != 0 && to < kFew) ts.list[to] = static_cast<uint16_t>(8 * (i * 32 + lane) + __ffs(on) - 1);
                 on &= on - 1;
                 n += __popc(who);
             }
