@@ -269,8 +269,8 @@ struct __align__(16) TopShared {
     alignas(16) uint64_t key[];    // candidates, and one more; read in twos
 };
 static_assert(kFew >= 256, "a histogram fits");
-static_assert(offsetof(TopShared<224>, key) % 16 == 0 && offsetof(TopShared<224>, part) % 16 == 0 && sizeof(uint16_t[kParts][224]) % 16 == 0 &&
-                  sizeof(TopShared<224>) == offsetof(TopShared<224>, key),
+static_assert(offsetof(TopShared<256>, key) % 16 == 0 && offsetof(TopShared<256>, part) % 16 == 0 && sizeof(uint16_t[kParts][256]) % 16 == 0 &&
+                  sizeof(TopShared<256>) == offsetof(TopShared<256>, key),
               "what is read as vectors of 16 bytes starts at multiples of them");
 
 // A row's list, by one warp of each CTA of its cluster.
@@ -535,7 +535,7 @@ struct TopOf {
 };
 
 template <typename T, int NT, bool TOP>
-__global__ void __launch_bounds__(NT, 1024 / NT) logp_rows(const LogpParams p) {
+__global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
     using View = RowView<T>;
     // warps that read rows; with lists the last one makes those
     constexpr int VEC = View::VEC, W = NT / 32 - (TOP ? 1 : 0), MT = W * 32, U = 4;
@@ -844,7 +844,7 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
     cfg.numAttrs = 1;
     int clusters = p.T;
     if (static_cast<int64_t>(p.T) * cluster > sms && (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) != cudaSuccess || clusters < 1)) return DGR_ERR_CUDA;
-    const int within = sms * (1024 / NT) / cluster;  // a green context's, or the test's cap
+    const int within = sms * 4 / cluster;  // a green context's, or the test's cap
     if (clusters > within) clusters = within > 0 ? within : 1;
     if (clusters > p.T) clusters = p.T;
     const unsigned capped = sched_grid(static_cast<unsigned>(clusters * cluster)) / cluster;
@@ -857,7 +857,7 @@ dgr_status launch_forward(LogpParams &p, int sms, cudaStream_t s) {
     // few rows: a row over more CTAs, down to 4096 elements each
     int cluster = 1;
     while (cluster < kMaxCluster && static_cast<int64_t>(p.T) * cluster * 2 <= 304 && p.V >= 4096 * cluster * 2) cluster <<= 1;
-    return p.K ? launch_rows<T, 256, true>(p, cluster, sms, s) : launch_rows<T, 256, false>(p, cluster, sms, s);
+    return p.K ? launch_rows<T, 288, true>(p, cluster, sms, s) : launch_rows<T, 256, false>(p, cluster, sms, s);
 }
 
 size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? static_cast<size_t>(((T - 1) * ld + W) * es) : 0; }
