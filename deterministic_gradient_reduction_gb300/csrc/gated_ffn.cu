@@ -317,6 +317,8 @@ struct PreParams {
     int32_t T, vecs;    // 8-element vectors a row
     int32_t rows_item;  // of pre_rows
     int32_t *ready;     // rows written, of each kReadyRows
+    int32_t *begun;     // tiles begun
+    int32_t nbs, lead;  // tiles a row block; rows of da and db ahead of the tiles (0: any)
 };
 
 // da = dh b act'(a), db = dh act(a); act'(v) = g + v g (1 - g) s'(v), g = sigmoid(s(v)).
@@ -366,8 +368,16 @@ template <int ACT>
 __device__ __forceinline__ void pre_rows(const PreParams &p, int worker, int workers, int lane) {
     constexpr int U = 4;
     const int items = (p.T + p.rows_item - 1) / p.rows_item;
+    int64_t limit = p.lead ? p.lead : INT64_MAX;  // rows that may be made by now
     for (int i = worker; i < items; i += workers) {
         const int64_t t0 = static_cast<int64_t>(i) * p.rows_item;
+        // no further ahead of the tiles than L2 holds (bounded: to be early is no error)
+        if (t0 >= limit) {
+            const int64_t blocks = (t0 - p.lead) / (2 * BM) + 1;
+            if (lane == 0) wait_counter_geq(p.begun, static_cast<int32_t>(blocks * p.nbs < INT32_MAX ? blocks * p.nbs : INT32_MAX));
+            __syncwarp();
+            limit = blocks * (2 * BM) + p.lead;
+        }
         const int rows = min(p.rows_item, static_cast<int>(p.T - t0)), n = rows * p.vecs;
         for (int v = lane; v < n; v += 32 * U) {
             PreVec<ACT> x[U];
@@ -491,6 +501,7 @@ __global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1
                 const uint32_t bytes = CG * (static_cast<uint32_t>(boxes * p.cut.box) * 128u + stage_b);
                 if (PRE) {
                     const int32_t mine = t.row + rank * BM;
+                    if (rank == 0 && lane == 0) atomicAdd(pre.begun, 1);
                     ok = wait_rows(pre, mine, min(mine + BM, t.end), lane, abort_flag, p.hdr);
                 }
                 for (int kb = 0; ok && lane == 0 && kb < n_k; ++kb) {
@@ -739,7 +750,8 @@ dgr_status make_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows
     const dgr_status st = encode_fn(&enc);
     if (st != DGR_OK) return st;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
+    // (of a single matrix the distance to the next one says nothing, and might be out of a map's range)
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>((count > 1 ? rows : 1) * ld * 2)};
     const cuuint32_t box[3] = {64, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
@@ -762,7 +774,9 @@ dgr_status make_block_map(CUtensorMap *m, void *base, int64_t cols, int64_t rows
     return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
 }
 
-size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows) * 4; }
+// The counters of rows, and one of tiles.
+size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows + 1) * 4; }
+constexpr int kLeadBlocks = 4;
 
 constexpr int kTileCost = 16;  // of a tile, in columns
 
@@ -857,6 +871,11 @@ template <int ACT>
 dgr_status launch_backward(const FfnParams &p, PreParams &g, const Operand &o, int sms, cudaStream_t s) {
     if (p.out && takes_pairs(p)) {
         g.rows_item = g.vecs >= 256 ? 1 : g.vecs >= 128 ? 2 : g.vecs >= 64 ? 4 : 8;
+        g.begun = g.ready + ready_bytes(p.T) / 4 - 1;
+        g.nbs = (p.N + kMaxN - 1) / kMaxN;
+        // the row blocks that all pairs are at, and a few; in another order than the
+        // rows' the tiles may want any
+        g.lead = p.sched.order == 0 ? (sms / 2 / g.nbs + 1 + kLeadBlocks) * 2 * BM : 0;
         if (cudaMemsetAsync(g.ready, 0, ready_bytes(p.T), s) != cudaSuccess) return DGR_ERR_CUDA;
         return launch_pairs<false, ACT, true>(p, g, o, sms, s);
     }
@@ -870,6 +889,7 @@ dgr_status launch_backward(const FfnParams &p, PreParams &g, const Operand &o, i
 dgr_status check_sizes(int64_t T, int64_t H, int64_t F, int32_t E, int32_t act, const int64_t *offs) {
     if (T < 0 || H < 1 || F < 1 || E < 1 || (act != kSilu && act != kGelu) || (!offs && E != 1)) return DGR_ERR_INVALID_ARG;
     if (T > INT32_MAX - 256 || H > (1 << 20) || F > (1 << 20) || E > kMaxExperts) return DGR_ERR_UNSUPPORTED;
+    if (H * F >= (int64_t{1} << 39)) return DGR_ERR_UNSUPPORTED;  // bytes from one expert's weights to the next
     if (H % 8 != 0 || F % 8 != 0) return DGR_ERR_MISALIGNED;
     return DGR_OK;
 }

@@ -585,7 +585,8 @@ dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_
  *           not written (dgate and dup may be).
  * gate, up: forward: a and b, or null each; backward: those (not null).
  * dx may be null (dgate and dup alone).
- * Limits:   H and F multiples of 8 up to 2^20, 1 <= E <= 1024, T < 2^31 - 256.
+ * Limits:   H and F multiples of 8 up to 2^20, H * F < 2^39, 1 <= E <= 1024,
+ *           T < 2^31 - 256.
  * Alignment: pointers 16 bytes, row strides multiples of 8 elements.
  * ws:       dgr_gated_ffn_workspace_bytes(T, H, F, E) bytes (the forward call needs
  *           256), zeroed once; it may go on to calls with other sizes as it is.

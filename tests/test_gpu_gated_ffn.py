@@ -82,9 +82,10 @@ def test_few_tokens_of_one_expert(T, H, F):
     check_backward(t, "silu")
 
 
-def test_strided_rows_and_what_lies_around_the_outputs():
-    t = make([130, 7, 0, 64], 264, 200, pad=24)
-    T, F, H = 201, 200, 264
+@pytest.mark.parametrize("counts", [[130, 7, 0, 64], [430, 7, 0, 564]])
+def test_strided_rows_and_what_lies_around_the_outputs(counts):
+    t = make(counts, 264, 200, pad=24)
+    T, F, H = sum(counts), 200, 264
     outs = {k: torch.full((T + 3, n + 40), 7.0, dtype=BF, device="cuda") for k, n in (("h", F), ("gate", F), ("up", F), ("dx", H), ("dgate", F), ("dup", F))}
     view = {k: v[:T, :H if k == "dx" else F] for k, v in outs.items()}
     check_forward(t, "silu", **{k: view[k] for k in ("h", "gate", "up")})
@@ -94,9 +95,10 @@ def test_strided_rows_and_what_lies_around_the_outputs():
         assert (v[T:] == 7).all() and (v[:, n:] == 7).all(), k
 
 
-def test_neighbours_with_nan():
+@pytest.mark.parametrize("tail", [90, 500])
+def test_neighbours_with_nan(tail):
     """A row of NaN, or an expert of NaN, stays with itself."""
-    t = make([100, 60, 90], 136, 264)
+    t = make([100, 60, tail], 136, 264)
     clean = check_forward(t, "silu")
     back = check_backward(t, "silu")
     for k in ("x", "dh", "gate"):
@@ -105,7 +107,7 @@ def test_neighbours_with_nan():
     t["w_up"][1] = float("inf")
     h = dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=t["offs"])
     got = dgr.gated_ffn_backward(t["dh"], t["gate"], t["up"], t["w_gate"], t["w_up"], offs=t["offs"])
-    keep = torch.ones(250, dtype=torch.bool, device="cuda")
+    keep = torch.ones(160 + tail, dtype=torch.bool, device="cuda")
     keep[100:160] = keep[7] = False
     assert torch.equal(h[keep], clean[keep]) and h[~keep].isnan().all()
     for k in back:
@@ -128,8 +130,9 @@ def test_far_values(act):
     near(got["dgate"][10::2], (dh * ref.d(t["up"]))[10::2], 2.0 ** -8 * (dh * ref.d(t["up"])).abs()[10::2] * 1.001, "dgate")
 
 
-def test_in_place_gradients():
-    t = make([90, 50], 128, 264)
+@pytest.mark.parametrize("counts", [[90, 50], [900, 50]])
+def test_in_place_gradients(counts):
+    t = make(counts, 128, 264)
     want = check_backward(t, "silu")
     gate, up = t["gate"].clone(), t["up"].clone()
     got = dgr.gated_ffn_backward(t["dh"], gate, up, t["w_gate"], t["w_up"], offs=t["offs"], dgate=gate, dup=up)
@@ -163,7 +166,7 @@ def test_weights_gradients():
 def test_offsets_out_of_order(cuts):
     """Recorded in the status word; nothing is written."""
     t = make([5, 4, 11], 64, 72)
-    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(20, 64, 72, 3))
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(1020, 64, 72, 3))
     out = {k: torch.full((20, 72), 3.0, dtype=BF, device="cuda") for k in ("h", "gate", "up")}
     offs = torch.tensor(cuts, dtype=torch.int64, device="cuda")
     dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=offs, ws=ws, **out)
@@ -171,6 +174,12 @@ def test_offsets_out_of_order(cuts):
     assert all((v == 3).all() for v in out.values())
     dx = torch.full((20, 64), 3.0, dtype=BF, device="cuda")
     dgr.gated_ffn_backward(t["dh"], t["gate"], t["up"], t["w_gate"], t["w_up"], offs=offs, ws=ws, dx=dx)
+    assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
+    many = make([5, 4, 1011], 64, 72)  # the form for many rows
+    cuts[3] += 1000
+    offs = torch.tensor(cuts, dtype=torch.int64, device="cuda")
+    dx = torch.full((1020, 64), 3.0, dtype=BF, device="cuda")
+    dgr.gated_ffn_backward(many["dh"], many["gate"], many["up"], many["w_gate"], many["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
     h = dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=t["offs"], ws=ws)  # the workspace goes on
     assert dgr.read_device_status(ws) == 0 and torch.equal(h, check_forward(t, "silu"))
@@ -193,7 +202,7 @@ def test_rows_do_not_depend_on_their_company():
         assert torch.equal(dgr.gated_ffn_backward(*one, t["w_gate"][e], t["w_up"][e])["dx"][0], dx[r])
 
 
-@pytest.mark.parametrize("counts,H,F", [([300, 1, 500, 0, 224], 264, 520), ([2, 0, 3], 512, 2048)])
+@pytest.mark.parametrize("counts,H,F", [([300, 1, 500, 0, 224], 264, 520), ([2, 0, 3], 512, 2048), ([4000, 1500], 520, 264)])
 def test_schedules_streams_and_replays(counts, H, F):
     t = make(counts, H, F)
 

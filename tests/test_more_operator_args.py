@@ -45,7 +45,8 @@ def test_gated_ffn(L):
     for kw in (dict(T=-1), dict(H=0), dict(F=0), dict(E=0), dict(act=2), dict(act=-1), dict(offs=None), dict(x=None), dict(wg=None),
                dict(wu=None), dict(h=None), dict(ws=None), dict(ldx=63), dict(ldh=31), dict(ldg=24), dict(ldu=24)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(T=(1 << 31) - 1), dict(E=1025), dict(H=(1 << 20) + 8, ldx=BIG), dict(F=(1 << 20) + 8)):
+    for kw in (dict(T=(1 << 31) - 1), dict(E=1025), dict(H=(1 << 20) + 8, ldx=BIG), dict(F=(1 << 20) + 8),
+               dict(H=1 << 20, ldx=BIG, F=1 << 19, ldh=BIG, ldg=BIG, ldu=BIG)):
         assert call(**kw) == UNSUPPORTED, kw
     for kw in (dict(H=60), dict(F=28), dict(ldx=68), dict(ldh=36), dict(x=at(1, 8)), dict(wg=at(2, 2)), dict(wu=at(3, 8)), dict(h=at(5, 8)),
                dict(g=at(6, 4)), dict(offs=at(4, 4)), dict(ws=at(8, 128))):
