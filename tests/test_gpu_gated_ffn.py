@@ -176,8 +176,9 @@ def test_offsets_out_of_order(cuts):
     dgr.gated_ffn_backward(t["dh"], t["gate"], t["up"], t["w_gate"], t["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
     many = make([5, 4, 1011], 64, 72)  # the form for many rows
-    cuts[3] += 1000
-    offs = torch.tensor(cuts, dtype=torch.int64, device="cuda")
+    # 1000 rows more in the last expert; where the third offset lies beyond the end it goes along (0, 5, 30, 1020 are in order)
+    moved = cuts[:2] + [cuts[2] + (1000 if cuts[2] > cuts[3] else 0), cuts[3] + 1000]
+    offs = torch.tensor(moved, dtype=torch.int64, device="cuda")
     dx = torch.full((1020, 64), 3.0, dtype=BF, device="cuda")
     dgr.gated_ffn_backward(many["dh"], many["gate"], many["up"], many["w_gate"], many["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
