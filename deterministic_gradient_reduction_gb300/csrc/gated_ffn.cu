@@ -778,8 +778,6 @@ dgr_status make_block_map(CUtensorMap *m, void *base, int64_t cols, int64_t rows
 size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows + 1) * 4; }
 constexpr int kLeadBlocks = 4;
 
-constexpr int kTileCost = 16;  // of a tile, in columns
-
 struct Operand {
     const void *a, *a2;
     int64_t ld_a, ld_a2;
@@ -832,9 +830,33 @@ dgr_status launch_tiles(FfnParams p, const PreParams &pre, const Operand &o, int
     return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, outs, p, pre) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
-// Whether experts have enough rows to fill the 256 of a pair of CTAs; where they
-// have fewer the weights' reading counts.
-bool takes_pairs(const FfnParams &p) { return p.T >= 192 * static_cast<int64_t>(p.E); }
+// How a call is cut: in pairs of CTAs (cut.cols 0), or in single ones whose tiles
+// are so many columns wide. The cost of a cut is that of the SM with the most to
+// do, waves of tiles times a stage of one: 0.39 us of a pair (256 x 256); of a
+// single CTA 0.10 us and 0.37 us for 256 columns of the product (0.47 us at 128 x
+// 256, 0.2 us at 64, as measured: what a stage costs however narrow, its weights'
+// reading and its MMAs). So large batches come in pairs, few rows in as many
+// narrow tiles as there are SMs, and batches in between as their last wave and
+// their experts' ragged ends make it.
+template <bool FWD>
+Tiles choose(const FfnParams &p, int sms) {
+    constexpr int kStep = FWD ? 8 : 64, kMost = FWD ? kMaxN / 2 : kMaxN, kPerCol = FWD ? 2 : 1;
+    // row blocks as they are likely to be: a ragged one for most experts
+    const int64_t some = p.E < p.T ? p.E : p.T;
+    auto blocks = [&](int rows) {
+        const int64_t half = (static_cast<int64_t>(p.T) + rows - 1) / rows + (some > 1 ? some / 2 : 0);
+        return some > half ? some : half;
+    };
+    auto waves = [&](int rows, int cols, int64_t at_once) { return (blocks(rows) * ((p.N + cols - 1) / cols) + at_once - 1) / at_once; };
+    Tiles best{};
+    double least = static_cast<double>(waves(2 * BM, kMost, sms / 2 > 0 ? sms / 2 : 1)) * 0.39;
+    for (int cols = kMost; cols >= kStep; cols -= kStep) {
+        const double cost = static_cast<double>(waves(BM, cols, sms)) * (0.10 + 0.37 / kMaxN * kPerCol * cols);
+        if (cost < least) least = cost, best.cols = cols;
+    }
+    best.box = p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
+    return best;
+}
 
 template <bool FWD, int ACT, bool PRE>
 dgr_status launch_pairs(FfnParams p, const PreParams &pre, const Operand &o, int sms, cudaStream_t s) {
@@ -842,34 +864,21 @@ dgr_status launch_pairs(FfnParams p, const PreParams &pre, const Operand &o, int
     return launch_tiles<2, FWD, ACT, PRE>(p, pre, o, sms, s);
 }
 
-// Single CTAs. What counts is the SM with the most of the weights: the width of a
-// tile is the one with the fewest columns in all waves of tiles together, and a
-// share for what a tile costs beside its weights.
-template <bool FWD, int ACT>
-dgr_status launch_singles(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
-    p.cut.box = p.T >= 128 * static_cast<int64_t>(p.E) ? BM : p.T <= 8 ? 8 : 32;
-    constexpr int kStep = FWD ? 8 : 64, kMost = FWD ? kMaxN / 2 : kMaxN;
-    // row blocks as they are likely to be: a ragged one for most experts
-    const int64_t some = p.E < p.T ? p.E : p.T, half = (static_cast<int64_t>(p.T) + BM - 1) / BM + some / 2;
-    const int64_t blocks = some > half ? some : half;
-    int64_t best = INT64_MAX;
-    for (int cols = kMost; cols >= kStep; cols -= kStep) {
-        const int64_t tiles = blocks * ((p.N + cols - 1) / cols), cost = (tiles + sms - 1) / sms * (cols + kTileCost);
-        if (cost < best) best = cost, p.cut.cols = cols;
-    }
-    return launch_tiles<1, FWD, ACT, false>(p, PreParams{}, o, sms, s);
+template <int ACT>
+dgr_status launch_forward(FfnParams p, const Operand &o, int sms, cudaStream_t s) {
+    p.cut = choose<true>(p, sms);
+    return p.cut.cols ? launch_tiles<1, true, ACT, false>(p, PreParams{}, o, sms, s) : launch_pairs<true, ACT, false>(p, PreParams{}, o, sms, s);
 }
 
-template <int ACT>
-dgr_status launch_forward(const FfnParams &p, const Operand &o, int sms, cudaStream_t s) {
-    return takes_pairs(p) ? launch_pairs<true, ACT, false>(p, PreParams{}, o, sms, s) : launch_singles<true, ACT>(p, o, sms, s);
-}
+// da and db element by element, then dx; in one kernel where its products take
+// longer than the elements' 10 bytes (4 H operations each at 1.9 PFLOP/s, 6.8 TB/s:
+// from H = 700 on), so that the one's memory traffic goes on under the other.
+constexpr int kFusedWidth = 768;
 
-// da and db element by element, then dx; in one kernel where that is bound by its
-// products, so that the one's memory traffic goes on under the other.
 template <int ACT>
-dgr_status launch_backward(const FfnParams &p, PreParams &g, const Operand &o, int sms, cudaStream_t s) {
-    if (p.out && takes_pairs(p)) {
+dgr_status launch_backward(FfnParams p, PreParams &g, const Operand &o, int sms, cudaStream_t s) {
+    if (p.out) p.cut = choose<false>(p, sms);
+    if (p.out && p.cut.cols == 0 && p.N >= kFusedWidth) {
         g.rows_item = g.vecs >= 256 ? 1 : g.vecs >= 128 ? 2 : g.vecs >= 64 ? 4 : 8;
         g.begun = g.ready + ready_bytes(p.T) / 4 - 1;
         g.nbs = (p.N + kMaxN - 1) / kMaxN;
@@ -882,7 +891,9 @@ dgr_status launch_backward(const FfnParams &p, PreParams &g, const Operand &o, i
     const int64_t n = static_cast<int64_t>(p.T) * g.vecs, ctas = (n + 255) / 256, most = static_cast<int64_t>(sms) * 8;
     ffn_pre_grad<ACT><<<static_cast<unsigned>(ctas < most ? ctas : most), 256, 0, s>>>(g);
     const dgr_status st = launch_status();
-    return st != DGR_OK || !p.out ? st : launch_singles<false, kSilu>(p, o, sms, s);  // no activation in it
+    if (st != DGR_OK || !p.out) return st;
+    // (no activation in these)
+    return p.cut.cols ? launch_tiles<1, false, kSilu, false>(p, PreParams{}, o, sms, s) : launch_pairs<false, kSilu, false>(p, PreParams{}, o, sms, s);
 }
 
 // What both entries check of the rows, sizes, offsets and workspace.

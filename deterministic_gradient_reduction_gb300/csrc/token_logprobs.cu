@@ -43,7 +43,7 @@ constexpr int kMaxTop = 128;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxCluster = 8;
 constexpr int kParts = 16;          // parts of a thread's share with a maximum of their own
-constexpr int kCandidates = 512, kCandidatesOfMany = 1536;  // collected elements of a row with one CTA, with several
+constexpr int kCandidates = 512, kCandidatesOfMany = 1536;  // collected elements of a CTA, of a row with several
 constexpr int kFew = 256;           // parts, or equal elements, that are taken as they come
 constexpr int kWhereId = 440;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -265,8 +265,8 @@ struct __align__(16) TopShared {
     float top[2][MT];              // of the threads
     uint16_t list[kFew];           // parts to read again
     int same[kFew];                // elements equal to the bound (and a histogram of 256)
-    int n_key;
-    alignas(16) uint64_t key[];    // candidates, and one more; read in twos
+    int n_all;
+    alignas(16) uint64_t key[];    // this CTA's candidates and two more, then a cluster's; read in twos
 };
 static_assert(kFew >= 256, "a histogram fits");
 static_assert(offsetof(TopShared<256>, key) % 16 == 0 && offsetof(TopShared<256>, part) % 16 == 0 && sizeof(uint16_t[kParts][256]) % 16 == 0 &&
@@ -284,8 +284,8 @@ struct TopOf {
     const T *z;
     const View &view;
     const char *first;
-    int par, lane, per_part, size, cap;
-    int n_key;  // candidates, where the row has one CTA
+    int par, lane, per_part, size;
+    int n_key;  // candidates
 
     // K-th largest of the threads' maxima as a key, two bits at a time from bit `from` on; what
     // lies below bit `to` is left out, so that a lower bound comes of it
@@ -312,21 +312,22 @@ struct TopOf {
         // (the key of -inf is the least that counts)
         return key_value(static_cast<uint64_t>(max(at, 0x007fffffu)) << 32);
     }
-    // to the leader's candidates: the lanes' elements where `on`
+    // to this CTA's candidates: the lanes' elements where `on`
     __device__ __forceinline__ void push(float v, int index, bool on) {
         const uint32_t who = __ballot_sync(0xffffffffu, on);
-        if (!who) return;
-        int at = n_key;
-        if (size > 1) {
-            if (lane == 0) at = remote_add(remote(&ts.n_key, 0), __popc(who));
-            at = __shfl_sync(0xffffffffu, at, 0);
-        }
-        n_key = at + __popc(who);
-        at += __popc(who & ((1u << lane) - 1));
-        if (on && at < cap) {
-            if (size == 1) ts.key[at] = key_of(v, index);
-            else remote_store(remote(&ts.key[at], 0), key_of(v, index));
-        }
+        const int at = n_key + __popc(who & ((1u << lane) - 1));
+        if (on && at < kCandidates) ts.key[at] = key_of(v, index);
+        n_key += __popc(who);
+    }
+    // a cluster's candidates together in the leader, behind its own; too many show in their number
+    __device__ __forceinline__ void gather() {
+        __syncwarp();
+        int at = 0;
+        if (lane == 0) at = remote_add(remote(&ts.n_all, 0), n_key);
+        at = __shfl_sync(0xffffffffu, at, 0);
+        for (int i = lane; i < n_key && i < kCandidates; i += 32)
+            if (at + i < kCandidatesOfMany) remote_store(remote(&ts.key[kCandidates + 2 + at + i], 0), ts.key[i]);
+        n_key = 0;
     }
     // reads the listed parts: pushes the elements above b and lists those equal to it in
     // `same`; how many these are. A lane has a part, four vectors of it at a time. One
@@ -474,22 +475,23 @@ struct TopOf {
     }
     // the leader's part: ranks and outputs
     __device__ __forceinline__ void write(int64_t row, float m, float lns) {
-        int n = size == 1 ? n_key : ts.n_key;
-        if (n > cap) n = by_digits();
+        uint64_t *keys = size == 1 ? ts.key : ts.key + kCandidates + 2;
+        int n = size == 1 ? n_key : ts.n_all;
+        if (n > (size == 1 ? kCandidates : kCandidatesOfMany)) n = by_digits(keys);
         constexpr int R = 4;  // keys of a lane at a time
-        if (lane == 0 && n % 2) ts.key[n] = 0;  // below every key; read in twos
+        if (lane == 0 && n % 2) keys[n] = 0;  // below every key; read in twos
         __syncwarp();
         for (int i0 = 0; i0 < n; i0 += 32 * R) {
             uint64_t key[R];
             int at[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                key[r] = i0 + 32 * r + lane < n ? ts.key[i0 + 32 * r + lane] : 0;
+                key[r] = i0 + 32 * r + lane < n ? keys[i0 + 32 * r + lane] : 0;
                 at[r] = 0;
             }
 #pragma unroll 4
             for (int j = 0; j < n; j += 2) {
-                const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(&ts.key[j]);
+                const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(&keys[j]);
 #pragma unroll
                 for (int r = 0; r < R; ++r) at[r] += (o.x > key[r]) + (o.y > key[r]);
             }
@@ -505,12 +507,12 @@ struct TopOf {
         }
         fill(row, n);
         __syncwarp();
-        if (lane == 0) ts.n_key = 0;
+        if (lane == 0) ts.n_all = 0;
         n_key = 0;
         __syncwarp();
     }
     // the row's K largest as the only candidates; how many
-    __device__ __forceinline__ int by_digits() const {
+    __device__ __forceinline__ int by_digits(uint64_t *keys) const {
         const uint64_t least = kth_key<T>(z, p.V, p.K, ts.same);
         int n = 0;
         for (int j0 = 0; j0 < p.V; j0 += 32) {
@@ -519,7 +521,7 @@ struct TopOf {
             const uint64_t key = v > -INFINITY ? key_of(v, j) : 0;
             const bool on = key >= least && key != 0;
             const uint32_t who = __ballot_sync(0xffffffffu, on);
-            if (on) ts.key[n + __popc(who & ((1u << lane) - 1))] = key;
+            if (on) keys[n + __popc(who & ((1u << lane) - 1))] = key;
             n += __popc(who);
         }
         __syncwarp();
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
     const int n_batches = (p.per + U * MT - 1) / (U * MT);       // of a thread, at most
     const int part_len = (n_batches + kParts - 1) / kParts;      // batches a part
     uint32_t live = 0;  // rows worked on: the exchange's parity
-    if (TOP && tid == 0) ts.n_key = 0;
+    if (TOP && tid == 0) ts.n_all = 0;
     if (size > 1) cluster_barrier();  // the other CTAs have started
     else __syncthreads();
 
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
         const int id = p.ids ? __ldg(p.ids + row) : 0, par = live & 1;
         const View view(z, p.V, rank, p.per);
         const char *first = reinterpret_cast<const char *>(z + view.head) + static_cast<int64_t>(view.first) * 16;
-        TopOf<T, MT> top_of{p, ts, z, view, first, par, lane, part_len * U, size, size == 1 ? kCandidates : kCandidatesOfMany, 0};
+        TopOf<T, MT> top_of{p, ts, z, view, first, par, lane, part_len * U, size, 0};
         if (id < 0 || id >= p.V) {  // not read: zeros, and no alternatives
             if (rank == 0 && tid == 0) {
                 if (id >= p.V) record_error(p.hdr, DGR_ERR_INVALID_ARG, kWhereId);
@@ -685,7 +687,10 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
                 for (int r = 0; r < size; ++r) bound = fmaxf(r ? bound : -INFINITY, sh.bound[par][r]);
                 if (w == W) reach = top_of.list_parts(bound, true);
             }
-            if (w == W) top_of.collect(bound, reach);
+            if (w == W) {
+                top_of.collect(bound, reach);
+                if (size > 1) top_of.gather();
+            }
             if (size > 1) cluster_barrier();
             if (w == W && rank == 0) top_of.write(row, m, lns);
         }
@@ -828,8 +833,8 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
     p.per = (vecs + cluster - 1) / cluster;
     if (p.per < 1) p.per = 1;
     constexpr size_t kTop = sizeof(TopShared<NT - 32>);
-    const size_t smem = TOP ? kTop + static_cast<size_t>((cluster == 1 ? kCandidates : kCandidatesOfMany) + 1) * 8 : 0;
-    dgr_status st = allow_smem(k, smem, kTop + (kCandidatesOfMany + 1) * 8);
+    const size_t smem = TOP ? kTop + static_cast<size_t>(kCandidates + 2 + (cluster == 1 ? 0 : kCandidatesOfMany + 2)) * 8 : 0;
+    dgr_status st = allow_smem(k, smem, kTop + (kCandidates + 2 + kCandidatesOfMany + 2) * 8);
     if (st != DGR_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(cluster);

@@ -55,7 +55,8 @@ def check_backward(t, act, **more):
 
 
 SIZES = [([1], 8, 8), ([5], 64, 40), ([1, 0, 2], 72, 136), ([128, 129, 0, 3], 200, 264), ([0, 0, 300], 1000, 128),
-         ([40, 41, 42, 43, 0, 1], 328, 520), ([256, 257], 64, 1040), ([1000, 300], 136, 2056), ([2100], 72, 8), ([700], 2048, 256), ([0, 33], 264, 8), ([513, 1, 255], 136, 392)]
+         ([40, 41, 42, 43, 0, 1], 328, 520), ([256, 257], 64, 1040), ([1000, 300], 136, 2056), ([2100], 72, 8), ([1800, 0, 1300], 1000, 136),
+         ([3000], 1032, 520), ([700], 2048, 256), ([0, 33], 264, 8), ([513, 1, 255], 136, 392)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -82,10 +83,10 @@ def test_few_tokens_of_one_expert(T, H, F):
     check_backward(t, "silu")
 
 
-@pytest.mark.parametrize("counts", [[130, 7, 0, 64], [430, 7, 0, 564]])
-def test_strided_rows_and_what_lies_around_the_outputs(counts):
-    t = make(counts, 264, 200, pad=24)
-    T, F, H = sum(counts), 200, 264
+@pytest.mark.parametrize("counts,H", [([130, 7, 0, 64], 264), ([1430, 7, 0, 1564], 1000)])
+def test_strided_rows_and_what_lies_around_the_outputs(counts, H):
+    t = make(counts, H, 200, pad=24)
+    T, F = sum(counts), 200
     outs = {k: torch.full((T + 3, n + 40), 7.0, dtype=BF, device="cuda") for k, n in (("h", F), ("gate", F), ("up", F), ("dx", H), ("dgate", F), ("dup", F))}
     view = {k: v[:T, :H if k == "dx" else F] for k, v in outs.items()}
     check_forward(t, "silu", **{k: view[k] for k in ("h", "gate", "up")})
@@ -95,10 +96,10 @@ def test_strided_rows_and_what_lies_around_the_outputs(counts):
         assert (v[T:] == 7).all() and (v[:, n:] == 7).all(), k
 
 
-@pytest.mark.parametrize("tail", [90, 500])
-def test_neighbours_with_nan(tail):
+@pytest.mark.parametrize("tail,H", [(90, 136), (3000, 1000)])
+def test_neighbours_with_nan(tail, H):
     """A row of NaN, or an expert of NaN, stays with itself."""
-    t = make([100, 60, tail], 136, 264)
+    t = make([100, 60, tail], H, 264)
     clean = check_forward(t, "silu")
     back = check_backward(t, "silu")
     for k in ("x", "dh", "gate"):
@@ -130,9 +131,9 @@ def test_far_values(act):
     near(got["dgate"][10::2], (dh * ref.d(t["up"]))[10::2], 2.0 ** -8 * (dh * ref.d(t["up"])).abs()[10::2] * 1.001, "dgate")
 
 
-@pytest.mark.parametrize("counts", [[90, 50], [900, 50]])
-def test_in_place_gradients(counts):
-    t = make(counts, 128, 264)
+@pytest.mark.parametrize("counts,H", [([90, 50], 128), ([2900, 50], 1000)])
+def test_in_place_gradients(counts, H):
+    t = make(counts, H, 264)
     want = check_backward(t, "silu")
     gate, up = t["gate"].clone(), t["up"].clone()
     got = dgr.gated_ffn_backward(t["dh"], gate, up, t["w_gate"], t["w_up"], offs=t["offs"], dgate=gate, dup=up)
@@ -166,7 +167,7 @@ def test_weights_gradients():
 def test_offsets_out_of_order(cuts):
     """Recorded in the status word; nothing is written."""
     t = make([5, 4, 11], 64, 72)
-    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(1020, 64, 72, 3))
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(3020, 1000, 72, 3))
     out = {k: torch.full((20, 72), 3.0, dtype=BF, device="cuda") for k in ("h", "gate", "up")}
     offs = torch.tensor(cuts, dtype=torch.int64, device="cuda")
     dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=offs, ws=ws, **out)
@@ -175,11 +176,11 @@ def test_offsets_out_of_order(cuts):
     dx = torch.full((20, 64), 3.0, dtype=BF, device="cuda")
     dgr.gated_ffn_backward(t["dh"], t["gate"], t["up"], t["w_gate"], t["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
-    many = make([5, 4, 1011], 64, 72)  # the form for many rows
-    # 1000 rows more in the last expert; where the third offset lies beyond the end it goes along (0, 5, 30, 1020 are in order)
-    moved = cuts[:2] + [cuts[2] + (1000 if cuts[2] > cuts[3] else 0), cuts[3] + 1000]
+    many = make([5, 4, 3011], 1000, 72)  # the form for many rows
+    # 3000 rows more in the last expert; where the third offset lies beyond the end it goes along (0, 5, 30, 3020 are in order)
+    moved = cuts[:2] + [cuts[2] + (3000 if cuts[2] > cuts[3] else 0), cuts[3] + 3000]
     offs = torch.tensor(moved, dtype=torch.int64, device="cuda")
-    dx = torch.full((1020, 64), 3.0, dtype=BF, device="cuda")
+    dx = torch.full((3020, 1000), 3.0, dtype=BF, device="cuda")
     dgr.gated_ffn_backward(many["dh"], many["gate"], many["up"], many["w_gate"], many["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
     h = dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=t["offs"], ws=ws)  # the workspace goes on
@@ -203,7 +204,7 @@ def test_rows_do_not_depend_on_their_company():
         assert torch.equal(dgr.gated_ffn_backward(*one, t["w_gate"][e], t["w_up"][e])["dx"][0], dx[r])
 
 
-@pytest.mark.parametrize("counts,H,F", [([300, 1, 500, 0, 224], 264, 520), ([2, 0, 3], 512, 2048), ([4000, 1500], 520, 264)])
+@pytest.mark.parametrize("counts,H,F", [([300, 1, 500, 0, 224], 264, 520), ([2, 0, 3], 512, 2048), ([2500, 1500], 1000, 264)])
 def test_schedules_streams_and_replays(counts, H, F):
     t = make(counts, H, F)
 
@@ -225,9 +226,9 @@ def test_schedules_streams_and_replays(counts, H, F):
 
 def test_two_graphs_that_share_a_workspace():
     """Captured calls of other sizes, replayed in turn with new inputs."""
-    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(1500, 512, 1024, 2))
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(3500, 512, 1024, 2))
     cases = []
-    for counts, H, F in (([200, 60], 136, 264), ([3], 512, 1024), ([700, 800], 264, 520)):
+    for counts, H, F in (([200, 60], 136, 264), ([3], 512, 1024), ([2700, 800], 1000, 520)):
         t = make(counts, H, F)
         out = {"h": torch.empty(sum(counts), F, dtype=BF, device="cuda")}
         back = {k: torch.empty(sum(counts), n, dtype=BF, device="cuda") for k, n in (("dx", H), ("dgate", F), ("dup", F))}
