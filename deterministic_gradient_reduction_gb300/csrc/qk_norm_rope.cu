@@ -452,6 +452,17 @@ struct Walk {
     __device__ __forceinline__ bool has_head() const { return head + mine < n; }
 };
 
+// Shared memory by its 32-bit addresses.
+__device__ __forceinline__ uint32_t shared_address(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint4 load_shared(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void copy_to(uint32_t a, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(src) : "memory");
+}
+
 // A warp's ring. Of a slot: PARTS vectors of each lane's group of heads and, with
 // a unit's first group, its cosines and sines, fetched by one team for all, and
 // whether its position lies in the table.
@@ -461,7 +472,7 @@ struct Ring {
     const QkParams &p;
     const Pairs<V, NV, INTER> &m;
     int tl, mine;
-    uint4 *heads, *turns;
+    uint32_t heads, turns;  // addresses
     int32_t *good_;
     float c[NV][V], s[NV][V];  // of the unit that is worked on
     bool good = false;
@@ -470,14 +481,14 @@ struct Ring {
     static size_t bytes(int team) { return static_cast<size_t>(kWarps) * DEPTH * (PARTS * 32 * 16 + kTurns * team * 16 + 16); }
     __device__ __forceinline__ Ring(const QkParams &p_, const Pairs<V, NV, INTER> &m_, uint4 *smem, int warp, int lane, int tl_, int mine_)
         : p(p_), m(m_), tl(tl_), mine(mine_) {
-        heads = smem + warp * DEPTH * PARTS * 32 + lane;
+        heads = shared_address(smem + warp * DEPTH * PARTS * 32 + lane);
         smem += kWarps * DEPTH * PARTS * 32;
-        turns = smem + warp * DEPTH * kTurns * p.team;
+        turns = shared_address(smem + warp * DEPTH * kTurns * p.team + tl);
         smem += kWarps * DEPTH * kTurns * p.team;
         good_ = reinterpret_cast<int32_t *>(smem + warp * DEPTH);
     }
-    __device__ __forceinline__ uint4 *at(int slot, int i) const { return heads + (slot * PARTS + i) * 32; }
-    __device__ __forceinline__ uint4 *turn(int slot, int i) const { return turns + (slot * kTurns + i) * p.team + tl; }
+    __device__ __forceinline__ uint32_t at(int slot, int i) const { return heads + static_cast<uint32_t>(slot * PARTS + i) * 512u; }
+    __device__ __forceinline__ uint32_t turn(int slot, int i) const { return turns + static_cast<uint32_t>((slot * kTurns + i) * p.team) * 16u; }
     // with a unit's first group
     template <typename W>
     __device__ __forceinline__ void put_angles(const W &w, int slot) {
@@ -494,8 +505,8 @@ struct Ring {
                 if (m.has[n] && m.at[n] < p.R / 2)
 #pragma unroll
                     for (int j = 0; j < V; j += 4) {
-                        copy_async<16>(turn(slot, (n * V + j) / 2), p.cos + row + m.at[n] + j);
-                        copy_async<16>(turn(slot, (n * V + j) / 2 + 1), p.sin + row + m.at[n] + j);
+                        copy_to(turn(slot, (n * V + j) / 2), p.cos + row + m.at[n] + j);
+                        copy_to(turn(slot, (n * V + j) / 2 + 1), p.sin + row + m.at[n] + j);
                     }
             if (tl == 0) {
                 good_[slot * 4] = ok;
@@ -516,8 +527,8 @@ struct Ring {
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
                 float x[4], y[4];
-                unpack<float, 4>(*turn(slot, (n * V + j) / 2), x);
-                unpack<float, 4>(*turn(slot, (n * V + j) / 2 + 1), y);
+                unpack<float, 4>(load_shared(turn(slot, (n * V + j) / 2)), x);
+                unpack<float, 4>(load_shared(turn(slot, (n * V + j) / 2 + 1)), y);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) c[n][j + i] = turned ? x[i] : 1.0f, s[n][j + i] = turned ? y[i] : 0.0f;
             }
@@ -554,8 +565,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_forward_ring(const QkParams
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
                     if (m.has[n]) {
-                        copy_async<16>(ring.at(slot, 2 * n), put.at[0] + m.lo[n]);
-                        copy_async<16>(ring.at(slot, 2 * n + 1), put.at[0] + m.hi[n]);
+                        copy_to(ring.at(slot, 2 * n), put.at[0] + m.lo[n]);
+                        copy_to(ring.at(slot, 2 * n + 1), put.at[0] + m.hi[n]);
                     }
             put.next();
         }
@@ -572,7 +583,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_forward_ring(const QkParams
         float a[NV][V], b[NV][V], ss = 0.0f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            split<T, V, INTER>(*ring.at(slot, 2 * n), *ring.at(slot, 2 * n + 1), a[n], b[n]);
+            split<T, V, INTER>(load_shared(ring.at(slot, 2 * n)), load_shared(ring.at(slot, 2 * n + 1)), a[n], b[n]);
             if (!whole && !(on && m.has[n]))  // never fetched
 #pragma unroll
                 for (int j = 0; j < V; ++j) a[n][j] = b[n][j] = 0.0f;
@@ -639,10 +650,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParam
 #pragma unroll
                         for (int n = 0; n < NV; ++n)
                             if (m.has[n]) {
-                                copy_async<16>(ring.at(slot, 4 * n), put.at[0] + m.lo[n]);
-                                copy_async<16>(ring.at(slot, 4 * n + 1), put.at[0] + m.hi[n]);
-                                copy_async<16>(ring.at(slot, 4 * n + 2), put.at[1] + m.lo[n]);
-                                copy_async<16>(ring.at(slot, 4 * n + 3), put.at[1] + m.hi[n]);
+                                copy_to(ring.at(slot, 4 * n), put.at[0] + m.lo[n]);
+                                copy_to(ring.at(slot, 4 * n + 1), put.at[0] + m.hi[n]);
+                                copy_to(ring.at(slot, 4 * n + 2), put.at[1] + m.lo[n]);
+                                copy_to(ring.at(slot, 4 * n + 3), put.at[1] + m.hi[n]);
                             }
                     put.next();
                 }
@@ -661,8 +672,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParam
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     float fa[V], fb[V], x[V], y[V];
-                    split<T, V, INTER>(*ring.at(slot, 4 * n), *ring.at(slot, 4 * n + 1), fa, fb);
-                    split<T, V, INTER>(*ring.at(slot, 4 * n + 2), *ring.at(slot, 4 * n + 3), x, y);
+                    split<T, V, INTER>(load_shared(ring.at(slot, 4 * n)), load_shared(ring.at(slot, 4 * n + 1)), fa, fb);
+                    split<T, V, INTER>(load_shared(ring.at(slot, 4 * n + 2)), load_shared(ring.at(slot, 4 * n + 3)), x, y);
                     if (!whole && !(on && m.has[n]))  // never fetched, or without a position
 #pragma unroll
                         for (int j = 0; j < V; ++j) fa[j] = fb[j] = x[j] = y[j] = 0.0f;

@@ -479,6 +479,7 @@ struct TopOf {
         int n = size == 1 ? n_key : ts.n_all;
         if (n > (size == 1 ? kCandidates : kCandidatesOfMany)) n = by_digits(keys);
         constexpr int R = 4;  // keys of a lane at a time
+        if (n > 32 * R) n = largest(keys, n);
         if (lane == 0 && n % 2) keys[n] = 0;  // below every key; read in twos
         __syncwarp();
         for (int i0 = 0; i0 < n; i0 += 32 * R) {
@@ -510,6 +511,35 @@ struct TopOf {
         if (lane == 0) ts.n_all = 0;
         n_key = 0;
         __syncwarp();
+    }
+    // the candidates whose value is at least that of the K-th, in the place of all (ranks
+    // take n^2 steps: 500 candidates of a cluster 120,000 cycles); how many
+    __device__ __forceinline__ int largest(uint64_t *keys, int n) const {
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(keys);
+        uint32_t at = 0;
+        __syncwarp();
+        for (int bit = 30; bit >= 0; bit -= 2) {
+            int c[3] = {0, 0, 0};
+#pragma unroll 4
+            for (int i = lane; i < n; i += 32) {
+                const uint32_t v = words[2 * i + 1];
+#pragma unroll
+                for (uint32_t d = 1; d < 4; ++d) c[d - 1] += v >= (at | d << bit);
+            }
+#pragma unroll
+            for (int d = 0; d < 3; ++d) c[d] = static_cast<int>(__reduce_add_sync(0xffffffffu, c[d]));
+            at |= static_cast<uint32_t>((c[0] >= p.K) + (c[1] >= p.K) + (c[2] >= p.K)) << bit;
+        }
+        int m = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const uint64_t key = i0 + lane < n ? keys[i0 + lane] : 0;
+            const bool on = i0 + lane < n && static_cast<uint32_t>(key >> 32) >= at;
+            const uint32_t who = __ballot_sync(0xffffffffu, on);  // all have read
+            if (on) keys[m + __popc(who & ((1u << lane) - 1))] = key;
+            m += __popc(who);
+        }
+        __syncwarp();
+        return m;
     }
     // the row's K largest as the only candidates; how many
     __device__ __forceinline__ int by_digits(uint64_t *keys) const {
