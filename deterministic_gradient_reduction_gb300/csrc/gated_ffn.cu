@@ -328,7 +328,8 @@ __device__ __forceinline__ void pre_grad(float2 dh, float2 a, float2 b, float2 &
     const float2 g = gate_sigmoid<ACT>(a), down = mul2(g, row::fma2(g, row::both(-1.0f), row::both(1.0f)));
     float2 turn = down;
     if (ACT == kGelu) {
-        const float2 s = row::fma2(mul2(row::both(0.21405560f), a), a, row::both(1.5957691216057308f));  // 2 sqrt(2 / pi) (1 + 3 0.044715 a^2)
+        constexpr double kTwice = 1.5957691216057308;  // s'(a) = 2 sqrt(2 / pi) (1 + 3 0.044715 a^2)
+        const float2 s = row::fma2(mul2(row::both(static_cast<float>(kTwice * 3 * 0.044715)), a), a, row::both(static_cast<float>(kTwice)));
         turn = make_float2(down.x > 0.0f ? __fmul_rn(down.x, s.x) : down.x, down.y > 0.0f ? __fmul_rn(down.y, s.y) : down.y);
     }
     db = mul2(dh, mul2(a, g));
@@ -870,15 +871,18 @@ dgr_status launch_forward(FfnParams p, const Operand &o, int sms, cudaStream_t s
     return p.cut.cols ? launch_tiles<1, true, ACT, false>(p, PreParams{}, o, sms, s) : launch_pairs<true, ACT, false>(p, PreParams{}, o, sms, s);
 }
 
-// da and db element by element, then dx; in one kernel where its products take
-// longer than the elements' 10 bytes (4 H operations each at 1.9 PFLOP/s, 6.8 TB/s:
-// from H = 700 on), so that the one's memory traffic goes on under the other.
-constexpr int kFusedWidth = 768;
+// da and db element by element, then dx; in one kernel where its products take far
+// longer than the elements' 10 bytes, so that the one's memory traffic goes on
+// under the other: back to back, one kernel and two, 16384 rows of 2048 x 4096 in 8
+// experts 401 and 453 us, 8192 218 and 229, 4096 147 and 148, 8192 of 1024 x 4096
+// 160 and 144, 5723 of 1024 x 2048 in 16 experts 85 and 72.
+constexpr int kFusedWidth = 1536, kFusedWaves = 3;
 
 template <int ACT>
 dgr_status launch_backward(FfnParams p, PreParams &g, const Operand &o, int sms, cudaStream_t s) {
     if (p.out) p.cut = choose<false>(p, sms);
-    if (p.out && p.cut.cols == 0 && p.N >= kFusedWidth) {
+    const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1, pair_tiles = row_blocks_most(p, 2 * BM) * ((p.N + kMaxN - 1) / kMaxN);
+    if (p.out && p.cut.cols == 0 && p.N >= kFusedWidth && pair_tiles >= kFusedWaves * pairs) {
         g.rows_item = g.vecs >= 256 ? 1 : g.vecs >= 128 ? 2 : g.vecs >= 64 ? 4 : 8;
         g.begun = g.ready + ready_bytes(p.T) / 4 - 1;
         g.nbs = (p.N + kMaxN - 1) / kMaxN;

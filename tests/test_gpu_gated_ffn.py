@@ -56,7 +56,7 @@ def check_backward(t, act, **more):
 
 SIZES = [([1], 8, 8), ([5], 64, 40), ([1, 0, 2], 72, 136), ([128, 129, 0, 3], 200, 264), ([0, 0, 300], 1000, 128),
          ([40, 41, 42, 43, 0, 1], 328, 520), ([256, 257], 64, 1040), ([1000, 300], 136, 2056), ([2100], 72, 8), ([1800, 0, 1300], 1000, 136),
-         ([3000], 1032, 520), ([700], 2048, 256), ([0, 33], 264, 8), ([513, 1, 255], 136, 392)]
+         ([5000, 0, 4400], 1544, 72), ([700], 2048, 256), ([0, 33], 264, 8), ([513, 1, 255], 136, 392)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -83,7 +83,7 @@ def test_few_tokens_of_one_expert(T, H, F):
     check_backward(t, "silu")
 
 
-@pytest.mark.parametrize("counts,H", [([130, 7, 0, 64], 264), ([1430, 7, 0, 1564], 1000)])
+@pytest.mark.parametrize("counts,H", [([130, 7, 0, 64], 264), ([5430, 7, 0, 4564], 1544)])
 def test_strided_rows_and_what_lies_around_the_outputs(counts, H):
     t = make(counts, H, 200, pad=24)
     T, F = sum(counts), 200
@@ -96,7 +96,7 @@ def test_strided_rows_and_what_lies_around_the_outputs(counts, H):
         assert (v[T:] == 7).all() and (v[:, n:] == 7).all(), k
 
 
-@pytest.mark.parametrize("tail,H", [(90, 136), (3000, 1000)])
+@pytest.mark.parametrize("tail,H", [(90, 136), (9900, 1544)])
 def test_neighbours_with_nan(tail, H):
     """A row of NaN, or an expert of NaN, stays with itself."""
     t = make([100, 60, tail], H, 264)
@@ -131,7 +131,7 @@ def test_far_values(act):
     near(got["dgate"][10::2], (dh * ref.d(t["up"]))[10::2], 2.0 ** -8 * (dh * ref.d(t["up"])).abs()[10::2] * 1.001, "dgate")
 
 
-@pytest.mark.parametrize("counts,H", [([90, 50], 128), ([2900, 50], 1000)])
+@pytest.mark.parametrize("counts,H", [([90, 50], 128), ([9900, 50], 1544)])
 def test_in_place_gradients(counts, H):
     t = make(counts, H, 264)
     want = check_backward(t, "silu")
@@ -167,7 +167,7 @@ def test_weights_gradients():
 def test_offsets_out_of_order(cuts):
     """Recorded in the status word; nothing is written."""
     t = make([5, 4, 11], 64, 72)
-    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(3020, 1000, 72, 3))
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(10000, 1544, 72, 3))
     out = {k: torch.full((20, 72), 3.0, dtype=BF, device="cuda") for k in ("h", "gate", "up")}
     offs = torch.tensor(cuts, dtype=torch.int64, device="cuda")
     dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=offs, ws=ws, **out)
@@ -176,11 +176,11 @@ def test_offsets_out_of_order(cuts):
     dx = torch.full((20, 64), 3.0, dtype=BF, device="cuda")
     dgr.gated_ffn_backward(t["dh"], t["gate"], t["up"], t["w_gate"], t["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
-    many = make([5, 4, 3011], 1000, 72)  # the form for many rows
-    # 3000 rows more in the last expert; where the third offset lies beyond the end it goes along (0, 5, 30, 3020 are in order)
-    moved = cuts[:2] + [cuts[2] + (3000 if cuts[2] > cuts[3] else 0), cuts[3] + 3000]
+    many = make([5, 4, 9991], 1544, 72)  # the form for many rows
+    # 9980 rows more in the last expert; where the third offset lies beyond the end it goes along (0, 5, 30, 10000 are in order)
+    moved = cuts[:2] + [cuts[2] + (9980 if cuts[2] > cuts[3] else 0), cuts[3] + 9980]
     offs = torch.tensor(moved, dtype=torch.int64, device="cuda")
-    dx = torch.full((3020, 1000), 3.0, dtype=BF, device="cuda")
+    dx = torch.full((10000, 1544), 3.0, dtype=BF, device="cuda")
     dgr.gated_ffn_backward(many["dh"], many["gate"], many["up"], many["w_gate"], many["w_up"], offs=offs, ws=ws, dx=dx)
     assert dgr.read_device_status(ws, clear=True) == 1 and (dx == 3).all()
     h = dgr.gated_ffn(t["x"], t["w_gate"], t["w_up"], offs=t["offs"], ws=ws)  # the workspace goes on
@@ -204,7 +204,7 @@ def test_rows_do_not_depend_on_their_company():
         assert torch.equal(dgr.gated_ffn_backward(*one, t["w_gate"][e], t["w_up"][e])["dx"][0], dx[r])
 
 
-@pytest.mark.parametrize("counts,H,F", [([300, 1, 500, 0, 224], 264, 520), ([2, 0, 3], 512, 2048), ([2500, 1500], 1000, 264)])
+@pytest.mark.parametrize("counts,H,F", [([300, 1, 500, 0, 224], 264, 520), ([2, 0, 3], 512, 2048), ([5500, 4500], 1544, 264)])
 def test_schedules_streams_and_replays(counts, H, F):
     t = make(counts, H, F)
 
@@ -226,9 +226,9 @@ def test_schedules_streams_and_replays(counts, H, F):
 
 def test_two_graphs_that_share_a_workspace():
     """Captured calls of other sizes, replayed in turn with new inputs."""
-    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(3500, 512, 1024, 2))
+    ws = dgr.workspace(dgr.gated_ffn_workspace_bytes(10500, 1544, 72, 2))
     cases = []
-    for counts, H, F in (([200, 60], 136, 264), ([3], 512, 1024), ([2700, 800], 1000, 520)):
+    for counts, H, F in (([200, 60], 136, 264), ([3], 512, 1024), ([5700, 4800], 1544, 72)):
         t = make(counts, H, F)
         out = {"h": torch.empty(sum(counts), F, dtype=BF, device="cuda")}
         back = {k: torch.empty(sum(counts), n, dtype=BF, device="cuda") for k, n in (("dx", H), ("dgate", F), ("dup", F))}
