@@ -42,7 +42,6 @@ using namespace row;
 constexpr int kMaxTop = 128;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxCluster = 8;
-constexpr int kParts = 16;          // parts of a thread's share with a maximum of their own
 constexpr int kCandidates = 512, kCandidatesOfMany = 1536;  // collected elements of a CTA, of a row with several
 constexpr int kFew = 256;           // parts, or equal elements, that are taken as they come
 constexpr int kWhereId = 440;
@@ -76,6 +75,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();  // .aligned: the warp's lanes together
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
@@ -83,8 +83,8 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void remote_store(uint32_t a, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+__device__ __forceinline__ void remote_store(uint32_t a, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 __device__ __forceinline__ void remote_store(uint32_t a, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
@@ -255,23 +255,29 @@ __device__ uint64_t kth_key(const T *z, int V, int K, int *hist) {
 template <int NT>
 struct __align__(16) Shared {
     float4 triple[2][kMaxCluster * NT / 32];  // the cluster's warps, by row parity
-    float bound[2][kMaxCluster];              // lower bounds of the K-th element, likewise
+    float2 bound[2][kMaxCluster];             // lower bounds of the CTAs' K-th element and of their K / CTAs-th, likewise
 };
 // Kept small: what the four CTAs of an SM leave of it is the cache that loads in
-// flight need room in (FIGURES).
+// flight need room in.
 template <int MT>
 struct __align__(16) TopShared {
+    static constexpr bool kFewThreads = MT < kMaxTop;
+    static constexpr int kParts = kFewThreads ? 4 : 16;  // parts of a thread's share with a maximum of their own
+    static constexpr int kTops = kFewThreads ? kParts * MT : MT;
     uint16_t part[2][kParts][MT];  // maxima of the threads' parts, rounded up to bf16, by row parity
-    float top[2][MT];              // of the threads
+    float top[2][kTops];           // of the threads, or of the parts where threads are few
     uint16_t list[kFew];           // parts to read again
     int same[kFew];                // elements equal to the bound (and a histogram of 256)
     int n_all;
     alignas(16) uint64_t key[];    // this CTA's candidates and two more, then a cluster's; read in twos
 };
 static_assert(kFew >= 256, "a histogram fits");
-static_assert(offsetof(TopShared<256>, key) % 16 == 0 && offsetof(TopShared<256>, part) % 16 == 0 && sizeof(uint16_t[kParts][256]) % 16 == 0 &&
-                  sizeof(TopShared<256>) == offsetof(TopShared<256>, key),
-              "what is read as vectors of 16 bytes starts at multiples of them");
+template <int MT>
+constexpr bool vectors_aligned = offsetof(TopShared<MT>, key) % 16 == 0 && offsetof(TopShared<MT>, part) % 16 == 0 &&
+                                 sizeof(uint16_t[TopShared<MT>::kParts][MT]) % 16 == 0 && sizeof(TopShared<MT>) == offsetof(TopShared<MT>, key);
+static_assert(vectors_aligned<256> && vectors_aligned<64>, "what is read as vectors of 16 bytes starts at multiples of them");
+
+constexpr int kBatch = 4;  // vectors that a thread reads at a time
 
 // A row's list, by one warp of each CTA of its cluster.
 template <typename T, int MT>
@@ -287,30 +293,41 @@ struct TopOf {
     int par, lane, per_part, size;
     int n_key;  // candidates
 
-    // K-th largest of the threads' maxima as a key, two bits at a time from bit `from` on; what
-    // lies below bit `to` is left out, so that a lower bound comes of it
-    __device__ __forceinline__ uint32_t bound(uint32_t at, int from, int to) const {
-        uint32_t key[MT / 32];
+    // K-th largest of the threads' maxima as a key, two bits at a time; what lies below bit
+    // `to` is left out, so that a lower bound comes of it
+    __device__ __forceinline__ uint32_t bound(int K, int to) const {
+        constexpr int N = TopShared<MT>::kTops / 32;
+        uint32_t key[N], at = 0;
 #pragma unroll
-        for (int i = 0; i < MT / 32; ++i) key[i] = static_cast<uint32_t>(key_of(ts.top[par][i * 32 + lane], 0) >> 32);
-        for (int bit = from - 1; bit >= to; bit -= 2) {
+        for (int i = 0; i < N; ++i) key[i] = static_cast<uint32_t>(key_of(ts.top[par][i * 32 + lane], 0) >> 32);
+        for (int bit = 30; bit >= to; bit -= 2) {
             int n[3] = {0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < MT / 32; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (uint32_t d = 1; d < 4; ++d) n[d - 1] += key[i] >= (at | d << bit);
 #pragma unroll
             for (int d = 0; d < 3; ++d) n[d] = static_cast<int>(__reduce_add_sync(0xffffffffu, n[d]));
-            at |= static_cast<uint32_t>((n[0] >= p.K) + (n[1] >= p.K) + (n[2] >= p.K)) << bit;
+            at |= static_cast<uint32_t>((n[0] >= K) + (n[1] >= K) + (n[2] >= K)) << bit;
         }
         return at;
     }
     // By the upper 16 bits: all that a bf16 value has (its lower ones are 0, or 1 below
     // zero), and near enough else, as long as few parts reach it.
-    __device__ __forceinline__ float bound(uint32_t at) const {
+    __device__ __forceinline__ float value_of(uint32_t at) const {
         if (sizeof(T) == 2 && !(at & 0x80000000u)) at |= 0xffffu;
         // (the key of -inf is the least that counts)
         return key_value(static_cast<uint64_t>(max(at, 0x007fffffu)) << 32);
+    }
+    // by all bits where many more than K threads reach it
+    __device__ __forceinline__ float near_bound(int K) const {
+        const uint32_t at = bound(K, 16);
+        if (sizeof(T) == 4) {
+            int n = 0;
+            for (int i = lane; i < TopShared<MT>::kTops; i += 32) n += static_cast<uint32_t>(key_of(ts.top[par][i], 0) >> 32) >= at;
+            if (static_cast<int>(__reduce_add_sync(0xffffffffu, n)) > K + 32) return value_of(bound(K, 0));
+        }
+        return value_of(at);
     }
     // to this CTA's candidates: the lanes' elements where `on`
     __device__ __forceinline__ void push(float v, int index, bool on) {
@@ -334,7 +351,7 @@ struct TopOf {
     // warp does this, at four or five cycles an instruction, so they are few: a mask of
     // the elements that reach b, and a word of it by a tree of selections.
     __device__ __forceinline__ int elements(int n_list, float b, bool equal) {
-        constexpr int U = 4, PER = 4 / static_cast<int>(sizeof(T));  // elements a word
+        constexpr int U = kBatch, PER = 4 / static_cast<int>(sizeof(T));  // elements a word
         const float least = b > -INFINITY ? b : -FLT_MAX;           // -inf reaches nothing
         int n_same = 0;
         for (int i0 = 0; i0 < n_list; i0 += 32) {
@@ -360,9 +377,11 @@ struct TopOf {
                 }
                 while (__any_sync(0xffffffffu, reach != 0)) {
                     const int e = __ffs(reach) - 1, word = e / PER;  // (where there is none: of nothing)
-                    uint32_t q[16] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w, r[2].x, r[2].y, r[2].z, r[2].w, r[3].x, r[3].y, r[3].z, r[3].w};
+                    uint32_t q[4 * U];
 #pragma unroll
-                    for (int half = 8; half > 0; half >>= 1)
+                    for (int u = 0; u < U; ++u) q[4 * u] = r[u].x, q[4 * u + 1] = r[u].y, q[4 * u + 2] = r[u].z, q[4 * u + 3] = r[u].w;
+#pragma unroll
+                    for (int half = 2 * U; half > 0; half >>= 1)
 #pragma unroll
                         for (int i = 0; i < half; ++i) q[i] = word & half ? q[i + half] : q[i];
                     const float v = sizeof(T) == 4 ? __uint_as_float(q[0]) : __uint_as_float(e & 1 ? q[0] & 0xffff0000u : q[0] << 16);
@@ -384,7 +403,7 @@ struct TopOf {
     }
     // lists the parts whose maximum is above `b` (or equal to it), the first kFew; how many
     __device__ __forceinline__ int list_parts(float b, bool equal) const {
-        constexpr int n_vec = kParts * MT / 8, per = (n_vec + 31) / 32;
+        constexpr int n_vec = TopShared<MT>::kParts * MT / 8, per = (n_vec + 31) / 32;
         static_assert(per <= 32, "a bit a vector");
         const uint4 *part = reinterpret_cast<const uint4 *>(&ts.part[par][0][0]);
         auto reaches = [&](float x) { return equal ? x >= b : x > b; };
@@ -473,15 +492,9 @@ struct TopOf {
             found += all;
         }
     }
-    // the leader's part: ranks and outputs
-    __device__ __forceinline__ void write(int64_t row, float m, float lns) {
-        uint64_t *keys = size == 1 ? ts.key : ts.key + kCandidates + 2;
-        int n = size == 1 ? n_key : ts.n_all;
-        if (n > (size == 1 ? kCandidates : kCandidatesOfMany)) n = by_digits(keys);
-        constexpr int R = 4;  // keys of a lane at a time
-        if (n > 32 * R) n = largest(keys, n);
-        if (lane == 0 && n % 2) keys[n] = 0;  // below every key; read in twos
-        __syncwarp();
+    // ranks and outputs, R keys of a lane at a time
+    template <int R>
+    __device__ __forceinline__ void ranks(const uint64_t *keys, int n, int64_t row, float m, float lns) const {
         for (int i0 = 0; i0 < n; i0 += 32 * R) {
             uint64_t key[R];
             int at[R];
@@ -506,6 +519,18 @@ struct TopOf {
                 if (p.top_logp) p.top_logp[to] = __fmaf_rn(__fadd_rn(v, -m), p.inv_tau, -lns);
             }
         }
+    }
+    // the leader's part: ranks and outputs
+    __device__ __forceinline__ void write(int64_t row, float m, float lns) {
+        uint64_t *keys = size == 1 ? ts.key : ts.key + kCandidates + 2;
+        int n = size == 1 ? n_key : ts.n_all;
+        if (n > (size == 1 ? kCandidates : kCandidatesOfMany)) n = by_digits(keys);
+        if (n > 128) n = largest(keys, n);
+        if (lane == 0 && n % 2) keys[n] = 0;  // below every key; read in twos
+        __syncwarp();
+        if (n <= 32) ranks<1>(keys, n, row, m, lns);
+        else if (n <= 64) ranks<2>(keys, n, row, m, lns);
+        else ranks<4>(keys, n, row, m, lns);
         fill(row, n);
         __syncwarp();
         if (lane == 0) ts.n_all = 0;
@@ -566,19 +591,28 @@ struct TopOf {
     }
 };
 
+// A list takes its warp 10,000 cycles (2,200 of them the bound's, 3,500 to 8,000 what
+// is collected and ranked), whatever the row's length: short rows want more such warps
+// on an SM, so small CTAs. 8192 rows of 4096 bf16, the best 20: 91 us with 4 CTAs of
+// 288 threads on an SM, 52 with 10 of 96.
+constexpr int kThreads = 288, kFewThreads = 96;
+template <int NT>
+constexpr int kCtas = NT == kFewThreads ? 10 : 4;
+
 template <typename T, int NT, bool TOP>
-__global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
+__global__ void __launch_bounds__(NT, kCtas<NT>) logp_rows(const LogpParams p) {
     using View = RowView<T>;
     // warps that read rows; with lists the last one makes those
-    constexpr int VEC = View::VEC, W = NT / 32 - (TOP ? 1 : 0), MT = W * 32, U = 4;
+    constexpr int VEC = View::VEC, W = NT / 32 - (TOP ? 1 : 0), MT = W * 32, U = kBatch;
     __shared__ Shared<NT> sh;
     extern __shared__ __align__(16) char smem[];
-    TopShared<MT> &ts = *reinterpret_cast<TopShared<MT> *>(smem);
+    using Top = TopShared<MT>;
+    Top &ts = *reinterpret_cast<Top *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     const uint32_t n_clusters = gridDim.x / size;
     const int n_batches = (p.per + U * MT - 1) / (U * MT);       // of a thread, at most
-    const int part_len = (n_batches + kParts - 1) / kParts;      // batches a part
+    const int part_len = (n_batches + Top::kParts - 1) / Top::kParts;      // batches a part
     uint32_t live = 0;  // rows worked on: the exchange's parity
     if (TOP && tid == 0) ts.n_all = 0;
     if (size > 1) cluster_barrier();  // the other CTAs have started
@@ -624,6 +658,7 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
                     if (TOP && !again) {
                         part = fmaxf(part, top);
                         if (++in_part == part_len) {
+                            if (Top::kFewThreads) ts.top[par][n_part * MT + tid] = part;
                             ts.part[par][n_part++][tid] = up_to_bf16(part);
                             part = -INFINITY, in_part = 0;
                         }
@@ -647,7 +682,8 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
                     }
                 }
                 if (TOP && !again)
-                    for (; n_part < kParts; ++n_part) {
+                    for (; n_part < Top::kParts; ++n_part) {
+                        if (Top::kFewThreads) ts.top[par][n_part * MT + tid] = part;
                         ts.part[par][n_part][tid] = up_to_bf16(part);
                         part = -INFINITY;
                     }
@@ -656,7 +692,7 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
                     run.raise(x, p.k2);
                     run.add_one(at_least_masked(x), p.k2);
                 }
-                if (TOP && !again) ts.top[par][tid] = run.m;
+                if (TOP && !Top::kFewThreads && !again) ts.top[par][tid] = run.m;
                 Triple mine{run.m, across(run.s), across(run.a)};
                 mine.over_warp(p.k2);
                 if (lane < size) remote_store(remote(&sh.triple[par][rank * W + w], lane), make_float4(mine.m, mine.s, mine.a, 0.0f));
@@ -701,20 +737,25 @@ __global__ void __launch_bounds__(NT, 4) logp_rows(const LogpParams p) {
             // (where a row has several CTAs, they meet at the barriers)
             float bound = 0.0f;
             int reach = 0;
-            uint32_t key = 0;
-            if (w == W) {
-                key = top_of.bound(0, 31, 16);
-                bound = top_of.bound(key);
+            if (w == W && size == 1) {
+                bound = top_of.value_of(top_of.bound(p.K, 16));
                 reach = top_of.list_parts(bound, true);
                 if (sizeof(T) == 4 && reach > kFew) {
-                    bound = top_of.bound(top_of.bound(key, 15, 0));
-                    if (size == 1) reach = top_of.list_parts(bound, true);
+                    bound = top_of.value_of(top_of.bound(p.K, 0));
+                    reach = top_of.list_parts(bound, true);
                 }
-                if (size > 1 && lane < size) remote_store(remote(&sh.bound[par][rank], lane), bound);
             }
             if (size > 1) {
+                // the row has K elements from any CTA's K-th on, and from the least of
+                // their K / CTAs-th on, which is nearer where the large ones are spread
+                if (w == W) {
+                    const float2 mine = make_float2(top_of.near_bound(p.K), top_of.near_bound((p.K + size - 1) / size));
+                    if (lane < size) remote_store(remote(&sh.bound[par][rank], lane), mine);
+                }
                 cluster_barrier();
-                for (int r = 0; r < size; ++r) bound = fmaxf(r ? bound : -INFINITY, sh.bound[par][r]);
+                float one = -INFINITY, each = INFINITY;
+                for (int r = 0; r < size; ++r) one = fmaxf(one, sh.bound[par][r].x), each = fminf(each, sh.bound[par][r].y);
+                bound = fmaxf(one, each);
                 if (w == W) reach = top_of.list_parts(bound, true);
             }
             if (w == W) {
@@ -879,7 +920,7 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
     cfg.numAttrs = 1;
     int clusters = p.T;
     if (static_cast<int64_t>(p.T) * cluster > sms && (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) != cudaSuccess || clusters < 1)) return DGR_ERR_CUDA;
-    const int within = sms * 4 / cluster;  // a green context's, or the test's cap
+    const int within = sms * kCtas<NT> / cluster;  // a green context's, or the test's cap
     if (clusters > within) clusters = within > 0 ? within : 1;
     if (clusters > p.T) clusters = p.T;
     const unsigned capped = sched_grid(static_cast<unsigned>(clusters * cluster)) / cluster;
@@ -887,12 +928,26 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? DGR_OK : DGR_ERR_CUDA;
 }
 
+// Rows for the small CTAs: short, as two warps have too few loads in flight for long
+// ones (2048 vectors, the best 20 of 8192 fp32 rows: 77 us, with large CTAs 93; 4096
+// vectors: 129 and 115); with maxima of parts enough for a bound that leaves few (2 K);
+// and so many that the large CTAs' list warps would be behind (300 rows of 8192 bf16,
+// the best 20: 15.5 us with the small ones, 14.5 with the large; 700, the best 64: 19.5
+// and 24.7). The device's SMs
+// have no say: a row's sums are in the same order on a part of it.
+constexpr int kShort = 2048, kMany = 608;
+
 template <typename T>
 dgr_status launch_forward(LogpParams &p, int sms, cudaStream_t s) {
     // few rows: a row over more CTAs, down to 4096 elements each
     int cluster = 1;
     while (cluster < kMaxCluster && static_cast<int64_t>(p.T) * cluster * 2 <= 304 && p.V >= 4096 * cluster * 2) cluster <<= 1;
-    return p.K ? launch_rows<T, 288, true>(p, cluster, sms, s) : launch_rows<T, 256, false>(p, cluster, sms, s);
+    if (!p.K) return launch_rows<T, 256, false>(p, cluster, sms, s);
+    constexpr int kReaders = kFewThreads - 32, kRound = kReaders * kBatch;
+    const int64_t vecs = p.V / (16 / static_cast<int>(sizeof(T))), last = vecs % kRound;
+    const int64_t maxima = vecs / kRound * kReaders + (last < kReaders ? last : kReaders);
+    const bool small = vecs <= kShort && maxima >= 2 * p.K && p.T > kMany;
+    return small ? launch_rows<T, kFewThreads, true>(p, 1, sms, s) : launch_rows<T, kThreads, true>(p, cluster, sms, s);
 }
 
 size_t extent(int64_t T, int64_t W, int64_t ld, int64_t es) { return T > 0 ? static_cast<size_t>(((T - 1) * ld + W) * es) : 0; }

@@ -316,3 +316,33 @@ def test_captured_twice_with_one_workspace():
             got = [v.clone() for v in (*out.values(), dz)]
             call()
             assert all(torch.equal(a, b) for a, b in zip(got, (*out.values(), dz)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V,K,pad,lead", [(1, 1, 0, 0), (300, 1, 3, 1), (1000, 5, 0, 0), (4099, 60, 5, 3), (8150, 128, 2, 0), (16380, 20, 0, 0)])
+def test_many_short_rows(V, K, pad, lead, dtype):
+    """Rows beyond what the list warps of large CTAs hold at once: ties, masks, NaN, rows left out, far values among them."""
+    T = 1300
+    z, ids = make(T, V, dtype, pad=pad, lead=lead)
+    z[::9] = 0.25
+    z[1::9, ::2] = -INF
+    z[2::9] = -INF
+    z[3::9] = (z[3::9] * 2).round() / 2  # few values
+    z[4::9, V // 2:] = torch.finfo(DT[dtype]).min
+    z[5::9, : V // 3] = 40.0
+    ids[6::9] = -1
+    z[6::9] = float("nan")
+    keep = torch.arange(T) % 9 != 6
+    got = dgr.token_logprobs(z, ids, top=K, tau=1.3)
+    some = check_forward(z[keep].contiguous(), ids[keep].contiguous(), 1.3, K)
+    assert (got["top_ids"][~keep] == -1).all() and not got["logp"][~keep].any()
+    for k in ("top_ids", "top_logits"):
+        assert torch.equal(got[k][keep], some[k]), k
+    assert_replays_identical(lambda: torch.cat([v.reshape(-1).float() for v in dgr.token_logprobs(z, ids, top=K, tau=1.3).values()]), n=3)
+    # one far above the others, NaN in another row: neither reaches a third
+    z, ids = make(T, max(V, 8), dtype)
+    clean = dgr.token_logprobs(z, ids, top=1)
+    z[5, 3], z[700, 7] = INF, float("nan")
+    got = dgr.token_logprobs(z, ids, top=1)
+    rest = [t for t in range(T) if t not in (5, 700)]
+    assert all(torch.equal(got[k][rest], clean[k][rest]) for k in got) and int(got["top_ids"][5]) == 3
