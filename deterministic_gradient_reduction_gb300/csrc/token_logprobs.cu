@@ -594,10 +594,10 @@ struct TopOf {
 // A list takes its warp 10,000 cycles (2,200 of them the bound's, 3,500 to 8,000 what
 // is collected and ranked), whatever the row's length: short rows want more such warps
 // on an SM, so small CTAs. 8192 rows of 4096 bf16, the best 20: 91 us with 4 CTAs of
-// 288 threads on an SM, 52 with 10 of 96.
+// 288 threads on an SM, 46 with 12 of 96.
 constexpr int kThreads = 288, kFewThreads = 96;
 template <int NT>
-constexpr int kCtas = NT == kFewThreads ? 10 : 4;
+constexpr int kCtas = NT == kFewThreads ? 12 : 4;
 
 template <typename T, int NT, bool TOP>
 __global__ void __launch_bounds__(NT, kCtas<NT>) logp_rows(const LogpParams p) {
@@ -917,9 +917,9 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
     at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = NT != kFewThreads;  // (an SM has 8 CTAs of clusters at most, of one CTA too)
     int clusters = p.T;
-    if (static_cast<int64_t>(p.T) * cluster > sms && (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) != cudaSuccess || clusters < 1)) return DGR_ERR_CUDA;
+    if (cluster > 1 && static_cast<int64_t>(p.T) * cluster > sms && (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) != cudaSuccess || clusters < 1)) return DGR_ERR_CUDA;
     const int within = sms * kCtas<NT> / cluster;  // a green context's, or the test's cap
     if (clusters > within) clusters = within > 0 ? within : 1;
     if (clusters > p.T) clusters = p.T;
@@ -929,8 +929,8 @@ dgr_status launch_rows(LogpParams &p, int cluster, int sms, cudaStream_t s) {
 }
 
 // Rows for the small CTAs: short, as two warps have too few loads in flight for long
-// ones (2048 vectors, the best 20 of 8192 fp32 rows: 77 us, with large CTAs 93; 4096
-// vectors: 129 and 115); with maxima of parts enough for a bound that leaves few (2 K);
+// ones (2048 vectors, the best 20 of 8192 fp32 rows: 71 us, with large CTAs 93; 4096
+// vectors: 126 and 116); with maxima of parts enough for a bound that leaves few (2 K);
 // and so many that the large CTAs' list warps would be behind (300 rows of 8192 bf16,
 // the best 20: 15.5 us with the small ones, 14.5 with the large; 700, the best 64: 19.5
 // and 24.7). The device's SMs
