@@ -7,12 +7,14 @@
 // gelu with s(v) = 2 sqrt(2 / pi) (v + 0.044715 v^3), as (1 + tanh u) / 2 =
 // sigmoid(2 u); written so, nothing cancels for small v.
 //
-// Forward, one launch: a persistent kernel, one CTA per SM, 12 warps. A tile is
-// 128 rows of one expert (counted from its first row) by FT columns of h, done as
-// one product of N = 2 FT columns: the FT rows of Wg_e and the FT of Wu_e lie one
-// after another in shared memory, so a and b of an element end in the same lane
-// of TMEM, and the epilogue has both. Warp 0 loads 64-deep stages by TMA (x and
-// the weights K-major as they lie, 128-byte swizzle; what is past a matrix's end
+// Forward, one launch: a persistent kernel, 12 warps a CTA, one CTA per SM. A tile
+// is, for calls with many rows, 256 rows of one expert (counted from its first row)
+// by 256 columns of the product, shared by a pair of CTAs (cta_group::2: each loads
+// half of either operand); for few rows 128 rows and a single CTA, as many columns as
+// waste least of the last wave (choose). The columns are half rows of Wg_e, half rows
+// of Wu_e, one after another in shared memory, so a and b of an element end in the
+// same lane of TMEM, and the epilogue has both. Warp 0 loads 64-deep stages by TMA (x
+// and the weights K-major as they lie, 128-byte swizzle; what is past a matrix's end
 // comes as zeros), warp 1 issues tcgen05.mma into one of two accumulators, warps
 // 4-11 (lane quarter q, column half) read one while the other fills.
 // Backward: da and db element by element (memory bound), and dx by the same
@@ -22,6 +24,13 @@
 // loads of a tile wait for its rows' counters, and the elements' traffic goes on
 // under the products; else two launches. The gradients of the weights are
 // dgr_grouped_wgrad_accumulate's.
+//
+// Bound by the tensor cores, and over seconds by the power that these take: 32768 rows,
+// 2048 x 4096, 8 experts, forward with a and b kept 632 us in a burst (1.74 PFLOP/s,
+// 0.90 of the measured rate; the products without any epilogue 565 us), 720-732 over
+// seconds (1.51, 0.87 of the sustained rate). Backward 735 in a burst, 855 over
+// seconds; as two launches 884. Few rows are bound by reading the weights: 1 x 4096 x
+// 8192 in 28.7 us (4.7 TB/s; a kernel that only reads them 27).
 //
 // Rows of a tile past the expert's end are another expert's (or zeros): a row of
 // the product depends on its own row of x alone, and they are not written.
@@ -638,8 +647,8 @@ __global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1
             };
             if (CG == 2 && t.row + rank * BM + 32 * q + 32 <= t.end) {
                 // a whole block of rows: 32 x 32 values through shared memory and the copy
-                // engine. Stores from the lanes (32 bytes a row each) take the shared
-                // memory's port that the MMAs read their operands by (FIGURES)
+                // engine. Stores from the lanes (32 bytes a row each) are many more requests
+                // beside the loads: 32768 rows of 2048 x 4096 741 us, so 725
                 auto send = [&](const CUtensorMap *map, const float (&v0)[16], const float (&v1)[16], int c) {
                     if (lane == 0) bulk_wait_read();
                     __syncwarp();
