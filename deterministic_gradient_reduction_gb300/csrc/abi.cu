@@ -12,12 +12,6 @@
 
 namespace dgr {
 
-dgr_status check_device() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return DGR_ERR_CUDA;
-    return dgr_device_supported(dev);
-}
-
 namespace {
 
 std::atomic<int32_t> g_order{0};
@@ -43,7 +37,27 @@ void *driver_entry(const char *name, int version) {
     return f;
 }
 
+void driver_entries() {
+    std::call_once(g_driver_once, [] {
+        g_get_cur = reinterpret_cast<CtxGetCurrent>(driver_entry("cuCtxGetCurrent", 12000));
+        g_get_res = reinterpret_cast<CtxGetDevResource>(driver_entry("cuCtxGetDevResource", 12040));
+    });
+}
+
 }  // namespace
+
+dgr_status check_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DGR_ERR_CUDA;
+    const dgr_status st = dgr_device_supported(dev);
+    if (st != DGR_OK) return st;
+    // a host thread whose first call this is: the device's context for it, which tensor
+    // maps need (one that is current, a green one too, stays)
+    driver_entries();
+    CUcontext ctx = nullptr;
+    if (g_get_cur && g_get_cur(&ctx) == CUDA_SUCCESS && !ctx && cudaSetDevice(dev) != cudaSuccess) return DGR_ERR_CUDA;
+    return DGR_OK;
+}
 
 Sched sched_setting() {
     Sched s{};
@@ -67,10 +81,7 @@ dgr_status usable_sms(int *sms) {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return DGR_ERR_CUDA;
-    std::call_once(g_driver_once, [] {
-        g_get_cur = reinterpret_cast<CtxGetCurrent>(driver_entry("cuCtxGetCurrent", 12000));
-        g_get_res = reinterpret_cast<CtxGetDevResource>(driver_entry("cuCtxGetDevResource", 12040));
-    });
+    driver_entries();
     CUcontext ctx = nullptr;
     CUdevResource r{};
     // a green context's SM partition, when the current context is one
