@@ -56,6 +56,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
 constexpr int kPreWarps = 6;  // of a CTA that makes da and db too: warps 2, 3 and four behind the epilogue's
 constexpr int kReadyRows = 32;  // rows of da and db that one counter stands for
+constexpr uint64_t kLeadWaitNs = 5000000;  // that da and db wait for the tiles, many times a tile's 0.1 ms
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kStageA = BM * 128;
 constexpr uint32_t kRing = 192 * 1024;  // stages, beside 4 KB of offsets and the barriers
@@ -327,6 +328,7 @@ struct PreParams {
     int32_t rows_item;  // of pre_rows
     int32_t *ready;     // rows written, of each kReadyRows
     int32_t *begun;     // tiles begun
+    int32_t *taken;     // shares of pre_rows taken
     int32_t nbs, lead;  // tiles a row block; rows of da and db ahead of the tiles (0: any)
 };
 
@@ -373,40 +375,53 @@ struct PreVec {
 
 // da and db by the spare warps of the kernel that multiplies them: rows in
 // ascending order, a few of them (rows_item, a divisor of kReadyRows) a warp at a
-// time, over all CTAs; each adds its rows to their counter when they are written.
+// time, over all CTAs; each adds its rows to their counter when they are written. A
+// share of the rows belongs to the warp that takes it, and who is done takes another:
+// no tile waits for a CTA that has no SM yet (another call's CTAs may have the other
+// SMs, and wait for theirs).
+__device__ __forceinline__ int take(int32_t *from, int lane) {
+    const int n = lane == 0 ? atomicAdd(from, 1) : 0;
+    return __shfl_sync(0xffffffffu, n, 0);
+}
 template <int ACT>
-__device__ __forceinline__ void pre_rows(const PreParams &p, int worker, int workers, int lane) {
+__device__ __forceinline__ void pre_rows(const PreParams &p, int lane) {
     constexpr int U = 4;
     const int items = (p.T + p.rows_item - 1) / p.rows_item;
     int64_t limit = p.lead ? p.lead : INT64_MAX;  // rows that may be made by now
-    for (int i = worker; i < items; i += workers) {
-        const int64_t t0 = static_cast<int64_t>(i) * p.rows_item;
-        // no further ahead of the tiles than L2 holds (bounded: to be early is no error)
-        if (t0 >= limit) {
-            const int64_t blocks = (t0 - p.lead) / (2 * BM) + 1;
-            if (lane == 0) wait_counter_geq(p.begun, static_cast<int32_t>(blocks * p.nbs < INT32_MAX ? blocks * p.nbs : INT32_MAX));
+    const int shares = kPreWarps * static_cast<int>(gridDim.x);
+    for (int share = take(p.taken, lane); share < shares; share = take(p.taken, lane)) {
+        for (int i = share; i < items; i += shares) {
+            const int64_t t0 = static_cast<int64_t>(i) * p.rows_item;
+            // no further ahead of the tiles than L2 holds; as CTAs without an SM begin no
+            // tiles, not for long, and then never again (to be early is no error)
+            if (t0 >= limit) {
+                const int64_t blocks = (t0 - p.lead) / (2 * BM) + 1;
+                int there = 1;
+                const int32_t tiles = static_cast<int32_t>(blocks * p.nbs < INT32_MAX ? blocks * p.nbs : INT32_MAX);
+                if (lane == 0) there = wait_counter_geq(p.begun, tiles, kLeadWaitNs);
+                there = __shfl_sync(0xffffffffu, there, 0);
+                limit = there ? blocks * (2 * BM) + p.lead : INT64_MAX;
+            }
+            const int rows = min(p.rows_item, static_cast<int>(p.T - t0)), n = rows * p.vecs;
+            for (int v = lane; v < n; v += 32 * U) {
+                PreVec<ACT> x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int w = v + 32 * u, r = w / p.vecs;
+                    x[u].load(p, t0 + r, (w - r * p.vecs) * 8, w < n);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int w = v + 32 * u, r = w / p.vecs;
+                    if (w < n) x[u].store(p, t0 + r, (w - r * p.vecs) * 8);
+                }
+            }
+            // seen by the copy engines of all SMs before the count is
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __threadfence();
             __syncwarp();
-            limit = blocks * (2 * BM) + p.lead;
+            if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p.ready + t0 / kReadyRows), "r"(rows) : "memory");
         }
-        const int rows = min(p.rows_item, static_cast<int>(p.T - t0)), n = rows * p.vecs;
-        for (int v = lane; v < n; v += 32 * U) {
-            PreVec<ACT> x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int w = v + 32 * u, r = w / p.vecs;
-                x[u].load(p, t0 + r, (w - r * p.vecs) * 8, w < n);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int w = v + 32 * u, r = w / p.vecs;
-                if (w < n) x[u].store(p, t0 + r, (w - r * p.vecs) * 8);
-            }
-        }
-        // seen by the copy engines of all SMs before the count is
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p.ready + t0 / kReadyRows), "r"(rows) : "memory");
     }
 }
 
@@ -614,8 +629,7 @@ __global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1
         }
     } else if (PRE && (warp == 2 || warp == 3 || warp >= 4 + kEpiWarps)) {
         // ---------------- da and db ----------------
-        const int w = warp < 4 ? warp - 2 : warp - kEpiWarps - 2;
-        pre_rows<ACT>(pre, w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kPreWarps * static_cast<int>(gridDim.x), lane);
+        pre_rows<ACT>(pre, lane);
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------
         const int q = warp & 3;         // TMEM lane quarter this warp may access
@@ -784,8 +798,8 @@ dgr_status make_block_map(CUtensorMap *m, void *base, int64_t cols, int64_t rows
     return r == CUDA_SUCCESS ? DGR_OK : DGR_ERR_CUDA;
 }
 
-// The counters of rows, and one of tiles.
-size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows + 1) * 4; }
+// The counters of rows, one of tiles and one of shares.
+size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows + 2) * 4; }
 constexpr int kLeadBlocks = 4;
 
 struct Operand {
@@ -893,7 +907,7 @@ dgr_status launch_backward(FfnParams p, PreParams &g, const Operand &o, int sms,
     const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1, pair_tiles = row_blocks_most(p, 2 * BM) * ((p.N + kMaxN - 1) / kMaxN);
     if (p.out && p.cut.cols == 0 && p.N >= kFusedWidth && pair_tiles >= kFusedWaves * pairs) {
         g.rows_item = g.vecs >= 256 ? 1 : g.vecs >= 128 ? 2 : g.vecs >= 64 ? 4 : 8;
-        g.begun = g.ready + ready_bytes(p.T) / 4 - 1;
+        g.taken = g.ready + ready_bytes(p.T) / 4 - 1, g.begun = g.taken - 1;
         g.nbs = (p.N + kMaxN - 1) / kMaxN;
         // the row blocks that all pairs are at, and a few; in another order than the
         // rows' the tiles may want any
