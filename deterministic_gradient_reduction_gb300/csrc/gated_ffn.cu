@@ -26,11 +26,11 @@
 // dgr_grouped_wgrad_accumulate's.
 //
 // Bound by the tensor cores, and over seconds by the power that these take: 32768 rows,
-// 2048 x 4096, 8 experts, forward with a and b kept 632 us in a burst (1.74 PFLOP/s,
-// 0.90 of the measured rate; the products without any epilogue 565 us), 720-732 over
-// seconds (1.51, 0.87 of the sustained rate). Backward 735 in a burst, 855 over
-// seconds; as two launches 884. Few rows are bound by reading the weights: 1 x 4096 x
-// 8192 in 28.7 us (4.7 TB/s; a kernel that only reads them 27).
+// 2048 x 4096, 8 experts, forward 587 us in a burst (1.87 PFLOP/s, 0.97 of the measured
+// rate), with a and b kept and over seconds 718 (1.53, 0.88 of the sustained rate).
+// Backward 730 in a burst, 834 over seconds; as two launches 884. Few rows are bound by
+// reading the weights: 1 x 4096 x 8192 in 28.5 us (4.7 TB/s; a kernel that only reads
+// them 27).
 //
 // Rows of a tile past the expert's end are another expert's (or zeros): a row of
 // the product depends on its own row of x alone, and they are not written.
@@ -68,7 +68,7 @@ enum { kSilu = 0, kGelu = 1 };
 
 // CG CTAs share a tile of CG * 128 rows. Pairs have 256 columns of the product;
 // a single CTA's width goes by the call (Tiles, below).
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 24;
 constexpr int kMaxN = 256;  // columns of the product a tile: half of TMEM
 // tcgen05 instruction descriptor: fp32 D, bf16 A and B, A K-major, B K-major or (bit 16) N-major
 __host__ __device__ constexpr uint32_t idesc(int m, int n, bool n_major) {
@@ -81,6 +81,7 @@ struct Tiles {
     int32_t cols;    // columns of the output a tile
     int32_t nbs;     // column blocks
     int32_t box;     // rows of x (or da, db) in one copy: 8, 32 or 128
+    int32_t room;    // rows of x that a stage has room for
     int32_t stages;  // slots of the ring
 };
 
@@ -263,13 +264,22 @@ __device__ __forceinline__ uint32_t of_leader(const uint64_t *bar) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// A copy into this CTA that reports to the leader's barrier.
-__device__ __forceinline__ void pair_load_3d(void *smem_dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
+// A copy into this CTA; a pair's reports to the leader's barrier.
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t to, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    if constexpr (CG == 1) {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(to),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(to),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    }
 }
 
 template <int CG>
@@ -463,7 +473,11 @@ __global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1
     constexpr int kRows = CG * BM;
     const int cols = CG == 2 ? (FWD ? kMaxN / 2 : kMaxN) : p.cut.cols;  // columns of the output a tile
     const int width = FWD ? 2 * cols : cols;                            // of the product
-    const uint32_t stage_b = static_cast<uint32_t>(width / CG) * 128u, stage_bytes = kStageA + stage_b;
+    const uint32_t stage_b = static_cast<uint32_t>(width / CG) * 128u;
+    // a call of few rows: a stage has room for those, so there are more stages (1 x 4096 x
+    // 8192 cold 40 -> 38 us); what the MMAs read as the others are bytes of the ring behind
+    // them, and those rows' products are not written
+    const uint32_t stage_a = CG == 2 ? kStageA : static_cast<uint32_t>(p.cut.room) * 128u, stage_bytes = stage_a + stage_b;
     const uint32_t stages = CG == 2 ? kRing / (kStageA + kMaxN / 2 * 128) : static_cast<uint32_t>(p.cut.stages);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -514,54 +528,50 @@ __global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1
         // ---------------- TMA producer ----------------
         // one lane; where rows have to be waited for, the others help to watch them
         if (PRE || lane == 0) {
-            uint32_t stage = 0, phase = 0;
-            bool armed[kMaxStages] = {};
-            uint32_t armed_phase[kMaxStages] = {};
+            uint32_t stage = 0, phase = 0, issued = 0;
+            uint32_t at = smem_u32(smem);  // the stage's
             bool ok = true;
             for (uint32_t tau = first; ok && tau < n_tiles; tau += step) {
                 const Tile t = tile_of(p, kRows, mb_base, sched_item(sched, tau));
-                // few rows: only the copies that hold some of the tile's (the rest of A's
-                // space keeps what it had; those rows' products are not written)
+                // few rows: only the copies that hold some of the tile's
                 const int boxes = p.cut.box == BM ? 1 : (min(t.end - t.row, BM) + p.cut.box - 1) / p.cut.box;
                 const uint32_t bytes = CG * (static_cast<uint32_t>(boxes * p.cut.box) * 128u + stage_b);
+                const int32_t row0 = t.row + rank * BM, col0 = t.nb * cols + (FWD ? 0 : rank * (cols / CG));
                 if (PRE) {
-                    const int32_t mine = t.row + rank * BM;
                     if (rank == 0 && lane == 0) atomicAdd(pre.begun, 1);
-                    ok = wait_rows(pre, mine, min(mine + BM, t.end), lane, abort_flag, p.hdr);
+                    ok = wait_rows(pre, row0, min(row0 + BM, t.end), lane, abort_flag, p.hdr);
                 }
                 for (int kb = 0; ok && lane == 0 && kb < n_k; ++kb) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1, abort_flag, p.hdr, 401)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sA = smem + stage * stage_bytes;
-                    uint8_t *sB = sA + kStageA;
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], bytes);
-                    armed[stage] = true;
-                    armed_phase[stage] = phase;
-                    auto load = [&](uint8_t *to, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
-                        if (CG == 1) tma_load_3d(to, map, &ctl->full[stage], x, y, z);
-                        else pair_load_3d(to, map, of_leader(&ctl->full[stage]), x, y, z);
-                    };
+                    uint64_t *full = &ctl->full[stage];
+                    if (rank == 0) mbar_arrive_expect_tx(full, bytes);
+                    ++issued;
+                    const uint32_t bar = CG == 1 ? smem_u32(full) : of_leader(full), sB = at + stage_a;
+                    auto load = [&](uint32_t to, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) { load_3d<CG>(to, map, bar, x, y, z); };
                     // a pair's CTAs have 128 of its rows each and half of its columns
                     if (FWD) {
-                        for (int b = 0; b < boxes; ++b) load(sA + b * p.cut.box * 128, &tmA, kb * BK, t.row + rank * BM + b * p.cut.box, 0);
+                        load(at, &tmA, kb * BK, row0, 0);
+                        for (int b = 1; b < boxes; ++b) load(at + b * p.cut.box * 128, &tmA, kb * BK, row0 + b * p.cut.box, 0);
                         if (CG == 1) {
-                            load(sB, &tmB, kb * BK, t.nb * cols, t.e);
-                            load(sB + cols * 128, &tmB2, kb * BK, t.nb * cols, t.e);
+                            load(sB, &tmB, kb * BK, col0, t.e);
+                            load(sB + cols * 128, &tmB2, kb * BK, col0, t.e);
                         } else {
-                            load(sB, rank ? &tmB2 : &tmB, kb * BK, t.nb * cols, t.e);
+                            load(sB, rank ? &tmB2 : &tmB, kb * BK, col0, t.e);
                         }
                     } else {
                         const bool second = kb >= part_k;
                         const int k0 = (second ? kb - part_k : kb) * BK;
-                        for (int b = 0; b < boxes; ++b)
-                            load(sA + b * p.cut.box * 128, second ? &tmA2 : &tmA, k0, t.row + rank * BM + b * p.cut.box, 0);
-                        for (int j = 0; j < cols / CG / 64; ++j)
-                            load(sB + j * kLboN, second ? &tmB2 : &tmB, t.nb * cols + rank * (cols / CG) + 64 * j, k0, t.e);
+                        load(at, second ? &tmA2 : &tmA, k0, row0, 0);
+                        for (int b = 1; b < boxes; ++b) load(at + b * p.cut.box * 128, second ? &tmA2 : &tmA, k0, row0 + b * p.cut.box, 0);
+                        for (int j = 0; j < cols / CG / 64; ++j) load(sB + j * kLboN, second ? &tmB2 : &tmB, col0 + 64 * j, k0, t.e);
                     }
+                    at += stage_bytes;
                     if (++stage == stages) {
                         stage = 0;
+                        at = smem_u32(smem);
                         phase ^= 1;
                     }
                 }
@@ -569,63 +579,63 @@ __global__ void __launch_bounds__(kThreads + (PRE ? (kPreWarps - 2) * 32 : 0), 1
             }
             if (!ok && rank == 0 && lane == 0) {  // aborted: let the copies in flight land (bounded) before the CTA, or the pair, exits
                 int dummy = 0;
-                for (int s = 0; s < kMaxStages; ++s)
-                    if (armed[s]) mbar_wait(&ctl->full[s], armed_phase[s], &dummy, nullptr, kWaitLimitNs);
+                for (uint32_t i = 0; i < stages && i < issued; ++i) {  // the latest use of each stage, backwards
+                    phase ^= stage == 0;
+                    stage = (stage == 0 ? stages : stage) - 1;
+                    mbar_wait(&ctl->full[stage], phase, &dummy, nullptr, kWaitLimitNs);
+                }
             }
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer ----------------
-        const uint32_t desc = idesc(kRows, width, !FWD);
-        uint32_t stage = 0, phase = 0, g = 0;
-        uint32_t last_stage = 0, last_phase = 0;  // the latest stage-release commit
-        bool committed = false, ok = true;
-        for (uint32_t tau = first; ok && tau < n_tiles; tau += step, ++g) {
-            const uint32_t buf = g & 1, tph = (g >> 1) & 1;
-            if (!mbar_wait(&ctl->tempty[buf], tph ^ 1, abort_flag, p.hdr, 402)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d_tmem = tmem + buf * kMaxN;
-            for (int kb = 0; kb < n_k; ++kb) {
-                if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.hdr, 403)) {
+        // one lane, descriptors by addition: a stage's instructions, at four or five cycles
+        // each, were near to what its MMAs take (32768 rows of 2048 x 4096 598 us, so 587)
+        if (lane == 0) {
+            const uint32_t desc = idesc(kRows, width, !FWD);
+            const uint64_t a_desc = smem_desc_sw128(smem_u32(smem), kLboK, kSBO);
+            const uint64_t b_desc = smem_desc_sw128(smem_u32(smem) + stage_a, FWD ? kLboK : kLboN, kSBO);
+            constexpr uint32_t kStepA = 32 >> 4, kStepB = (FWD ? 32 : 2048) >> 4;  // a K16 step in a descriptor's address
+            uint32_t stage = 0, phase = 0, g = 0, at = 0;  // at: the stage's, likewise
+            uint32_t last_stage = 0, last_phase = 0;       // the latest stage-release commit
+            bool committed = false, ok = true;
+            for (uint32_t tau = first; ok && tau < n_tiles; tau += step, ++g) {
+                const uint32_t buf = g & 1, tph = (g >> 1) & 1;
+                if (!mbar_wait(&ctl->tempty[buf], tph ^ 1, abort_flag, p.hdr, 402)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t a0 = smem_u32(smem + stage * stage_bytes), b0 = a0 + kStageA;
-                    // the stage's four K16 steps back to back, descriptors ready
-                    uint64_t ad[4], bd[4];
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        ad[kk] = smem_desc_sw128(a0 + kk * 32, kLboK, kSBO);
-                        bd[kk] = FWD ? smem_desc_sw128(b0 + kk * 32, kLboK, kSBO) : smem_desc_sw128(b0 + kk * 2048, kLboN, kSBO);
+                const uint32_t d_tmem = tmem + buf * kMaxN;
+                for (int kb = 0; kb < n_k; ++kb) {
+                    if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.hdr, 403)) {
+                        ok = false;
+                        break;
                     }
-                    mma<CG>(d_tmem, ad[0], bd[0], desc, kb > 0 ? 1u : 0u);
-                    mma<CG>(d_tmem, ad[1], bd[1], desc, 1u);
-                    mma<CG>(d_tmem, ad[2], bd[2], desc, 1u);
-                    mma<CG>(d_tmem, ad[3], bd[3], desc, 1u);
+                    tc_fence_after();
+                    const uint64_t ad = a_desc + at, bd = b_desc + at;
+                    mma<CG>(d_tmem, ad, bd, desc, kb > 0 ? 1u : 0u);
+                    mma<CG>(d_tmem, ad + kStepA, bd + kStepB, desc, 1u);
+                    mma<CG>(d_tmem, ad + 2 * kStepA, bd + 2 * kStepB, desc, 1u);
+                    mma<CG>(d_tmem, ad + 3 * kStepA, bd + 3 * kStepB, desc, 1u);
                     commit<CG>(&ctl->empty[stage]);
+                    committed = true;
+                    last_stage = stage;
+                    last_phase = phase;
+                    at += stage_bytes >> 4;
+                    if (++stage == stages) {
+                        stage = at = 0;
+                        phase ^= 1;
+                    }
                 }
-                __syncwarp();
-                committed = true;
-                last_stage = stage;
-                last_phase = phase;
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
+                if (!ok) break;
+                commit<CG>(&ctl->tfull[buf]);
             }
-            if (!ok) break;
-            if (lane == 0) commit<CG>(&ctl->tfull[buf]);
-            __syncwarp();
-        }
-        if (!ok && committed) {
-            // aborted: wait (bounded) until the MMAs issued here are done, as
-            // their latest commit says, before the CTA frees its TMEM and exits
-            int dummy = 0;
-            mbar_wait(&ctl->empty[last_stage], last_phase, &dummy, nullptr, kWaitLimitNs);
+            if (!ok && committed) {
+                // aborted: wait (bounded) until the MMAs issued here are done, as
+                // their latest commit says, before the CTA frees its TMEM and exits
+                int dummy = 0;
+                mbar_wait(&ctl->empty[last_stage], last_phase, &dummy, nullptr, kWaitLimitNs);
+            }
         }
     } else if (PRE && (warp == 2 || warp == 3 || warp >= 4 + kEpiWarps)) {
         // ---------------- da and db ----------------
@@ -833,7 +843,11 @@ dgr_status launch_tiles(FfnParams p, const PreParams &pre, const Operand &o, int
         if (p.up && (st = make_block_map(&outs.up, p.up, p.N, p.T, p.ld_up)) != DGR_OK) return st;
     }
     p.cut.nbs = (p.N + p.cut.cols - 1) / p.cut.cols;
-    p.cut.stages = static_cast<int32_t>(kRing / (kStageA + static_cast<uint32_t>(FWD ? 2 * p.cut.cols : p.cut.cols) * 128u));
+    // as many stages as fit, the last one's A read as 128 rows too
+    p.cut.room = p.T < BM ? (p.T + p.cut.box - 1) / p.cut.box * p.cut.box : BM;
+    const uint32_t stage_a = static_cast<uint32_t>(p.cut.room) * 128u, stage = stage_a + static_cast<uint32_t>(FWD ? 2 * p.cut.cols : p.cut.cols) * 128u;
+    const uint32_t by_end = kRing / stage, by_last = 1 + (kRing - kStageA) / stage;
+    p.cut.stages = static_cast<int32_t>(by_end < by_last ? by_end : by_last);
     if (p.cut.stages > kMaxStages) p.cut.stages = kMaxStages;
     const int64_t tiles = row_blocks_most(p, kRows) * p.cut.nbs, most = sms / CG > 0 ? sms / CG : 1;
     if (tiles > INT32_MAX) return DGR_ERR_UNSUPPORTED;
