@@ -590,9 +590,9 @@ dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_
  * Alignment: pointers 16 bytes, row strides multiples of 8 elements.
  * ws:       dgr_gated_ffn_workspace_bytes(T, H, F, E) bytes (the forward call needs
  *           256), zeroed once; it may go on to calls with other sizes as it is.
- * Residency: the backward call of many rows waits, bounded, for rows that other
- * CTAs of the same launch write; it takes one CTA an SM usable at once, and the
- * CTAs that write wait for nothing.
+ * Residency: none is needed. The backward call of many rows waits, bounded, for
+ * rows that other CTAs of the same launch write, but those that run write all of
+ * them, however few they are.
  * dgate may be gate and dup may be up (same pointer and stride); nothing else
  * may overlap.
  */
