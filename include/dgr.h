@@ -687,7 +687,7 @@ dgr_status dgr_qk_norm_rope_backward(const void *dq_out, int64_t dqo_token, int6
  * makes its row's logp, entropy, lse, ln s, top_logp and gradient NaN; a NaN is
  * in no list.
  * Sums are binary32 in an order that depends on the type, T, V, the alignment of
- * the logits' rows and whether K is 0. Each output is rounded once.
+ * the logits' rows and K. Each output is rounded once.
  *
  * logits:   [T, V] bf16 or fp32 (dtype), row stride ld; ids [T] int32 or null.
  * logp, entropy, lse: [T] fp32; stats: [T, 2] fp32; top_ids int32, top_logits and
