@@ -341,11 +341,13 @@ struct TopOf {
         if (on && at < kCandidates) ts.key[at] = key_of(v, index);
         n_key += __popc(who);
     }
-    // a cluster's candidates together in the leader, behind its own; too many show in their number
+    // a cluster's candidates together in the leader, behind its own; too many show in their
+    // number, of a CTA as of all: one that had no space for all of its own (a run of large
+    // elements side by side) counts as more than a row's space
     __device__ __forceinline__ void gather() {
         __syncwarp();
         int at = 0;
-        if (lane == 0) at = remote_add(remote(&ts.n_all, 0), n_key);
+        if (lane == 0) at = remote_add(remote(&ts.n_all, 0), n_key > kCandidates ? kCandidatesOfMany + 1 : n_key);
         at = __shfl_sync(0xffffffffu, at, 0);
         for (int i = lane; i < n_key && i < kCandidates; i += 32)
             if (at + i < kCandidatesOfMany) remote_store(remote(&ts.key[kCandidates + 2 + at + i], 0), ts.key[i]);
