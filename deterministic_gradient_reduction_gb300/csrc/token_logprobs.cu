@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(NT, kCtas<NT>) logp_rows(const LogpParams p) {
             }
             all.s = warp_sum(all.s);
             all.a = warp_sum(all.a);
-            const bool none = m == -INFINITY;  // nothing is left of the row
+            const bool none = m == -INFINITY && all.s == 0.0f;  // nothing is left of the row (a sum of NaN: it holds NaN)
             const float ln_s = logf(all.s);
             // ln s for the maximum itself: without the rounding of c
             lns = none ? 0.0f : __fmaf_rn(__fmaf_rn(all.m, p.k2, -c), -kLn2, ln_s);
@@ -807,7 +807,8 @@ struct RowGrad {
         A = -__fmaf_rn(b, p.entropy ? __ldg(p.entropy + row) : 0.0f, a);
         B = __fmul_rn(-kLn2, b);
         at_id = a;
-        on = (!p.ids || (id >= 0 && id < p.V)) && m != -INFINITY;
+        // (no maximum and a logarithm of the sum that is a number: a row of nothing but -inf)
+        on = (!p.ids || (id >= 0 && id < p.V)) && !(m == -INFINITY && l == l);
     }
     template <int N>
     __device__ __forceinline__ void of(float (&x)[N]) const {
