@@ -446,8 +446,12 @@ __device__ __forceinline__ bool wait_rows(const PreParams &p, int32_t first, int
             ok = false;
         }
     }
+    ok = __all_sync(0xffffffffu, ok);
+    // the lanes' readings of the counters come before lane 0's copies: the warp's barrier
+    // orders memory between lanes (a vote does not), the fence behind it the copy engine
+    __syncwarp();
     asm volatile("fence.proxy.async;" ::: "memory");
-    return __all_sync(0xffffffffu, ok);
+    return ok;
 }
 
 template <int ACT>
