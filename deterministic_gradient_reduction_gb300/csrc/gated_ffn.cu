@@ -56,7 +56,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
 constexpr int kPreWarps = 6;  // of a CTA that makes da and db too: warps 2, 3 and four behind the epilogue's
 constexpr int kReadyRows = 32;  // rows of da and db that one counter stands for
-constexpr uint64_t kLeadWaitNs = 5000000;  // that da and db wait for the tiles, many times a tile's 0.1 ms
+constexpr uint64_t kStageNs = 390;  // of a pair's tile, as measured (choose)
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kStageA = BM * 128;
 constexpr uint32_t kRing = 192 * 1024;  // stages, beside 4 KB of offsets and the barriers
@@ -340,6 +340,7 @@ struct PreParams {
     int32_t *begun;     // tiles begun
     int32_t *taken;     // shares of pre_rows taken
     int32_t nbs, lead;  // tiles a row block; rows of da and db ahead of the tiles (0: any)
+    uint64_t lead_ns;   // that they wait for the tiles at most
 };
 
 // da = dh b act'(a), db = dh act(a); act'(v) = g + v g (1 - g) s'(v), g = sigmoid(s(v)).
@@ -402,13 +403,15 @@ __device__ __forceinline__ void pre_rows(const PreParams &p, int lane) {
     for (int share = take(p.taken, lane); share < shares; share = take(p.taken, lane)) {
         for (int i = share; i < items; i += shares) {
             const int64_t t0 = static_cast<int64_t>(i) * p.rows_item;
-            // no further ahead of the tiles than L2 holds; as CTAs without an SM begin no
-            // tiles, not for long, and then never again (to be early is no error)
+            // no further ahead of the tiles than L2 holds. All pairs begin their tiles a tile's
+            // time apart at most; CTAs without an SM (another stream's kernel has it) begin none,
+            // so the wait ends, and then there is none again: to be early is no error (on 120 of
+            // 152 SMs 32768 rows of 2048 x 4096 took 5.1 ms with a limit of 5 ms)
             if (t0 >= limit) {
                 const int64_t blocks = (t0 - p.lead) / (2 * BM) + 1;
                 int there = 1;
                 const int32_t tiles = static_cast<int32_t>(blocks * p.nbs < INT32_MAX ? blocks * p.nbs : INT32_MAX);
-                if (lane == 0) there = wait_counter_geq(p.begun, tiles, kLeadWaitNs);
+                if (lane == 0) there = wait_counter_geq(p.begun, tiles, p.lead_ns);
                 there = __shfl_sync(0xffffffffu, there, 0);
                 limit = there ? blocks * (2 * BM) + p.lead : INT64_MAX;
             }
@@ -815,6 +818,7 @@ dgr_status make_block_map(CUtensorMap *m, void *base, int64_t cols, int64_t rows
 // The counters of rows, one of tiles and one of shares.
 size_t ready_bytes(int64_t T) { return static_cast<size_t>((T + kReadyRows - 1) / kReadyRows + 2) * 4; }
 constexpr int kLeadBlocks = 4;
+constexpr uint64_t kTileLeastNs = 10000;  // a tile of few stages takes its epilogue's time
 
 struct Operand {
     const void *a, *a2;
@@ -930,6 +934,9 @@ dgr_status launch_backward(FfnParams p, PreParams &g, const Operand &o, int sms,
         // the row blocks that all pairs are at, and a few; in another order than the
         // rows' the tiles may want any
         g.lead = p.sched.order == 0 ? (sms / 2 / g.nbs + 1 + kLeadBlocks) * 2 * BM : 0;
+        // twice the time of a tile's stages (0.1 ms at F = 4096): clocks may be down by a quarter
+        const uint64_t tile_ns = 2 * static_cast<uint64_t>((p.K + BK - 1) / BK) * kStageNs;
+        g.lead_ns = 2 * (tile_ns > kTileLeastNs ? tile_ns : kTileLeastNs);
         if (cudaMemsetAsync(g.ready, 0, ready_bytes(p.T), s) != cudaSuccess) return DGR_ERR_CUDA;
         return launch_pairs<false, ACT, true>(p, g, o, sms, s);
     }
