@@ -205,6 +205,39 @@ inline bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb) {
     return a0 < b0 + nb && b0 < a0 + na;
 }
 
+// Runs of `width` bytes from p on, `inner` bytes apart, n_inner of them, and the
+// whole again every `outer` bytes, n_outer times: the rows of a strided matrix, the
+// heads of a tensor of tokens. A count of 1 makes its distance irrelevant.
+struct Runs {
+    const void *p;
+    int64_t outer, n_outer, inner, n_inner, width;
+    int64_t span() const { return (n_inner - 1) * inner + width; }
+    size_t extent() const { return p && n_outer > 0 && n_inner > 0 && width > 0 ? static_cast<size_t>((n_outer - 1) * outer + span()) : 0; }
+};
+
+// Whether two sets of runs share memory. Runs between one another's are told apart
+// where the sets have the same distances; ranges that meet at different ones count
+// as overlapping.
+inline bool runs_overlap(const Runs &a, const Runs &b) {
+    if (!ranges_overlap(a.p, a.extent(), b.p, b.extent())) return false;
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p));
+    auto behind = [](int64_t v, int64_t step) { return v % step < 0 ? v % step + step : v % step; };
+    // b's inner runs, `shift` bytes from a's
+    auto meet = [&](int64_t shift) {
+        if (shift >= a.span() || shift + b.span() <= 0) return false;
+        if (a.n_inner == 1 && b.n_inner == 1) return true;
+        if (a.n_inner > 1 && b.n_inner > 1 && a.inner != b.inner) return true;
+        const int64_t step = a.n_inner > 1 ? a.inner : b.inner, r = behind(shift, step);
+        return r < a.width || r + b.width > step;
+    };
+    if (a.n_outer == 1 && b.n_outer == 1) return meet(d);
+    if (a.n_outer > 1 && b.n_outer > 1 && a.outer != b.outer) return true;
+    const int64_t outer = a.n_outer > 1 ? a.outer : b.outer;
+    if (a.span() > outer || b.span() > outer) return true;
+    const int64_t r = behind(d, outer);
+    return meet(r) || meet(r - outer);
+}
+
 inline bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

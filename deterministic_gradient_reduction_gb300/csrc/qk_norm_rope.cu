@@ -774,19 +774,14 @@ struct View {
 
 struct Layout {
     int64_t T, D, es;
-    // from the first to behind the last element of one token's heads, of all
-    size_t footprint(const View &v) const { return static_cast<size_t>(((v.n - 1) * v.sh + D) * es); }
-    size_t extent(const View &v) const { return v.p && T > 0 && v.n > 0 ? static_cast<size_t>((T - 1) * v.st * es) + footprint(v) : 0; }
-    // Whether two views share memory. Parts of one packed row (the same token
-    // stride, each within it) do where their places in the row do.
-    bool overlap(const View &a, const View &b) const {
-        if (!ranges_overlap(a.p, extent(a), b.p, extent(b))) return false;
-        const size_t stride = static_cast<size_t>(a.st * es), fa = footprint(a), fb = footprint(b);
-        if (a.st != b.st || T == 1 || fa > stride || fb > stride) return true;
-        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-        const size_t apart = y >= x ? (y - x) % stride : (stride - (x - y) % stride) % stride;
-        return apart < fa || apart + fb > stride;
+    // its heads, token by token or (where these lie further apart) head by head
+    Runs runs(const View &v) const {
+        const bool heads_outside = v.n > 1 && T > 1 && v.sh >= (T - 1) * v.st + D;
+        if (heads_outside) return {v.p, v.sh * es, v.n, v.st * es, T, D * es};
+        return {v.p, v.st * es, T, v.sh * es, v.n, D * es};
     }
+    size_t extent(const View &v) const { return runs(v).extent(); }
+    bool overlap(const View &a, const View &b) const { return runs_overlap(runs(a), runs(b)); }
     // heads apart from each other: tokens outside heads, or heads outside tokens
     bool valid(const View &v) const {
         if (v.n == 0 || T == 0) return true;

@@ -629,7 +629,8 @@ dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gat
  *
  * q: [T, n_q, D], k: [T, n_k, D] bf16 or fp32 (dtype), element (t, head, d) at
  *           t * token + head * head_stride + d; heads and tokens of one tensor
- *           must not overlap one another, but q and k may lie in one packed row.
+ *           must not overlap one another, but q and k may lie in one packed row,
+ *           one behind the other or, with the same strides, head by head in turn.
  *           The same for q_out, k_out, dq_out, dk_out, dq, dk. n_q or n_k may
  *           be 0 (its pointers are then not used).
  * w_q, w_k: [D] bf16 or fp32 (w_dtype); dw_q, dw_k: [D] fp32.
