@@ -961,7 +961,9 @@ struct Rows {
     const void *p;
     int64_t ld, cols;
 };
-size_t extent(int64_t T, const Rows &r) { return r.p && T > 0 ? static_cast<size_t>((T - 1) * r.ld + r.cols) * 2 : 0; }
+Runs runs(int64_t T, const Rows &r) { return {r.p, r.ld * 2, T, 0, 1, r.cols * 2}; }
+size_t extent(int64_t T, const Rows &r) { return runs(T, r).extent(); }
+bool overlap(int64_t T, const Rows &a, const Rows &b) { return runs_overlap(runs(T, a), runs(T, b)); }  // parts of one row do not
 
 }  // namespace
 }  // namespace dgr
@@ -991,11 +993,11 @@ extern "C" dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_g
     const size_t weights = static_cast<size_t>(E) * F * H * 2;
     for (const Rows &o : outs) {
         const size_t n = extent(T, o);
-        if (ranges_overlap(o.p, n, x, extent(T, in)) || ranges_overlap(o.p, n, w_gate, weights) || ranges_overlap(o.p, n, w_up, weights) ||
+        if (overlap(T, o, in) || ranges_overlap(o.p, n, w_gate, weights) || ranges_overlap(o.p, n, w_up, weights) ||
             ranges_overlap(o.p, n, d_offs, (static_cast<size_t>(E) + 1) * 8) || ranges_overlap(o.p, n, ws, sizeof(WsHeader)))
             return DGR_ERR_ALIAS;
         for (const Rows &q : outs)
-            if (&q < &o && ranges_overlap(o.p, n, q.p, extent(T, q))) return DGR_ERR_ALIAS;
+            if (&q < &o && overlap(T, o, q)) return DGR_ERR_ALIAS;
     }
     for (const Rows &i : {in, Rows{w_gate, 0, 0}, Rows{w_up, 0, 0}})
         if (ranges_overlap(ws, sizeof(WsHeader), i.p, i.cols ? extent(T, i) : weights)) return DGR_ERR_ALIAS;
@@ -1041,13 +1043,13 @@ extern "C" dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, cons
         for (const Rows &i : ins) {
             // dgate in gate's place, dup in up's: the same pointer and stride
             const bool in_place = ((o.p == dgate && i.p == gate) || (o.p == dup && i.p == up)) && o.p == i.p && o.ld == i.ld;
-            if (!in_place && ranges_overlap(o.p, n, i.p, extent(T, i))) return DGR_ERR_ALIAS;
+            if (!in_place && overlap(T, o, i)) return DGR_ERR_ALIAS;
         }
         if (ranges_overlap(o.p, n, w_gate, weights) || ranges_overlap(o.p, n, w_up, weights) ||
             ranges_overlap(o.p, n, d_offs, (static_cast<size_t>(E) + 1) * 8) || ranges_overlap(o.p, n, ws, need))
             return DGR_ERR_ALIAS;
         for (const Rows &q : outs)
-            if (&q < &o && ranges_overlap(o.p, n, q.p, extent(T, q))) return DGR_ERR_ALIAS;
+            if (&q < &o && overlap(T, o, q)) return DGR_ERR_ALIAS;
     }
     for (const Rows &i : ins)
         if (ranges_overlap(ws, need, i.p, extent(T, i))) return DGR_ERR_ALIAS;

@@ -1036,7 +1036,7 @@ extern "C" dgr_status dgr_token_logprobs_backward(const void *logits, int32_t dt
         if (!aligned(i.q, 4)) return DGR_ERR_MISALIGNED;
         if (ranges_overlap(dlogits, n, i.q, i.n)) return DGR_ERR_ALIAS;
     }
-    if (!(dlogits == logits && ld == ld_d) && ranges_overlap(dlogits, n, logits, extent(T, V, ld, es))) return DGR_ERR_ALIAS;
+    if (!(dlogits == logits && ld == ld_d) && runs_overlap({dlogits, ld_d * es, T, 0, 1, V * es}, {logits, ld * es, T, 0, 1, V * es})) return DGR_ERR_ALIAS;
     if ((st = check_device()) != DGR_OK) return st;
     if (T == 0) return DGR_OK;
     LogpBackParams p{};

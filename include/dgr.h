@@ -594,7 +594,7 @@ dgr_status dgr_topk_distill(const void *logits, int32_t dtype, int64_t T, int64_
  * rows that other CTAs of the same launch write, but those that run write all of
  * them, however few they are.
  * dgate may be gate and dup may be up (same pointer and stride); nothing else
- * may overlap.
+ * may overlap. Parts of one row ([T, 2 F] with gate and up side by side, say) do not.
  */
 size_t dgr_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t F, int32_t E);
 dgr_status dgr_gated_ffn(const void *x, int64_t ld_x, const void *w_gate, const void *w_up, const int64_t *d_offs,
@@ -699,7 +699,8 @@ dgr_status dgr_qk_norm_rope_backward(const void *dq_out, int64_t dqo_token, int6
  * Limits:   1 <= V <= 2^20, 0 <= K <= 128, T <= 2^26, 1e-6 <= tau <= 1e6.
  * ws:       dgr_token_logprobs_workspace_bytes(T) bytes, zeroed once (status
  *           word); it may go on to calls with other sizes. Backward needs none.
- * dlogits may be logits (same pointer and stride); nothing else may overlap.
+ * dlogits may be logits (same pointer and stride), or lie beside them in one row;
+ * nothing else may overlap.
  */
 size_t dgr_token_logprobs_workspace_bytes(int64_t T);
 dgr_status dgr_token_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,

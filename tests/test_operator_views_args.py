@@ -34,3 +34,28 @@ def test_heads(L):
             # [heads, 2, tokens, 64] with the tokens' runs of 1280 bytes shifted into one another
             dict(qt=64, qh=1280, k=P(2), kt=64, kh=64 * 10, qo=at(1, 1152), qot=64, qoh=1280)):
         assert call(**kw) == ALIAS, kw
+
+
+def test_rows(L):
+    """Rows of 40 bf16 (80 bytes) side by side in rows of 160: what reaches into its neighbour's."""
+    ok = dict(x=P(1), ldx=64, wg=P(2), wu=P(3), offs=P(4), E=2, T=10, H=64, F=40, act=0, h=P(5), ldh=80, g=P(6), ldg=80,
+              u=at(6, 80), ldu=80, ws=P(8), n=256, s=None)
+
+    def forward(**kw):
+        return L.dgr_gated_ffn(*{**ok, **kw}.values())
+
+    for kw in (dict(u=at(6, 64)), dict(u=at(6, 96)), dict(u=at(6, 160 * 5 + 64)), dict(u=P(6)), dict(u=at(6, 80), ldu=88), dict(h=at(6, 160)),
+               dict(h=at(6, 32)), dict(h=at(1, 80), ldh=64), dict(T=1, u=at(6, 64)), dict(h=at(6, 160 * 9 + 64), ldh=400)):
+        assert forward(**kw) == ALIAS, kw
+    ok_back = dict(dh=P(1), lddh=40, g=P(2), ldg=80, u=at(2, 80), ldu=80, wg=P(4), wu=P(5), offs=P(6), E=2, T=10, H=64, F=40, act=1, dg=P(7),
+                   lddg=80, du=at(7, 80), lddu=80, dx=P(9), lddx=64, ws=P(10), n=512, s=None)
+
+    def backward(**kw):
+        return L.dgr_gated_ffn_backward(*{**ok_back, **kw}.values())
+
+    for kw in (dict(du=at(7, 64)), dict(du=at(7, 96)), dict(dg=at(2, 80)), dict(dg=at(2, 16)), dict(dx=at(7, 160), lddx=80), dict(dx=at(2, 80), lddx=80),
+               dict(dg=P(2), lddg=88)):
+        assert backward(**kw) == ALIAS, kw
+    back = dict(z=P(1), dt=0, T=10, V=100, ld=208, ids=P(2), tau=1.0, st=P(3), H=P(4), dl=P(5), dH=P(6), dz=at(1, 400), ldd=208, s=None)
+    for kw in (dict(dz=at(1, 396)), dict(dz=at(1, 436)), dict(dz=at(1, 400 + 3 * 832 + 36)), dict(ldd=209)):
+        assert L.dgr_token_logprobs_backward(*{**back, **kw}.values()) == ALIAS, kw
