@@ -8,7 +8,8 @@
 // behind R stay. Pairs are (i, i + R/2) or, interleaved, (2i, 2i + 1).
 // Backwards, from dy: g = dy turned back (s -> -s),
 //   dw = sum over tokens and heads of g v r,
-//   dv = r (g w) - v (r^3 / D) (g w . v).
+//   dv = r (g w) - (v r) (r (r (g w . v) / D)): no factor is larger than what comes
+//        of it, so that heads close to 0, whose r^2 or r^3 is out of range, have theirs.
 // All in binary32 from the stored heads; every output rounded once.
 //
 // A team of lanes has a head: lane l of it V pairs (the same places of the lower
@@ -357,16 +358,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward(const QkParams p) 
                         // a place without a head, or a token without a position: nothing for dw
                         const bool on = head < h.n && good;
                         const float r = on ? rsqrtf(__fmaf_rn(ss, inv_d, p.eps)) : 0.0f;
-                        const float back = on ? __fmul_rn(__fmul_rn(r, r), __fmul_rn(r, __fmul_rn(dot, inv_d))) : 0.0f;
+                        const float back = on ? __fmul_rn(r, __fmul_rn(r, __fmul_rn(dot, inv_d))) : 0.0f;  // (times v r)
 #pragma unroll
                         for (int n = 0; n < NV; ++n) {
                             float x[V], y[V];
 #pragma unroll
                             for (int j = 0; j < V; ++j) {
-                                acc_a[n][j] = __fmaf_rn(__fmul_rn(a[n][j], r), ga[n][j], acc_a[n][j]);
-                                acc_b[n][j] = __fmaf_rn(__fmul_rn(b[n][j], r), gb[n][j], acc_b[n][j]);
-                                x[j] = __fmaf_rn(__fmul_rn(ga[n][j], wa[n][j]), r, -__fmul_rn(a[n][j], back));
-                                y[j] = __fmaf_rn(__fmul_rn(gb[n][j], wb[n][j]), r, -__fmul_rn(b[n][j], back));
+                                const float na = __fmul_rn(a[n][j], r), nb = __fmul_rn(b[n][j], r);
+                                acc_a[n][j] = __fmaf_rn(na, ga[n][j], acc_a[n][j]);
+                                acc_b[n][j] = __fmaf_rn(nb, gb[n][j], acc_b[n][j]);
+                                x[j] = __fmaf_rn(__fmul_rn(ga[n][j], wa[n][j]), r, -__fmul_rn(na, back));
+                                y[j] = __fmaf_rn(__fmul_rn(gb[n][j], wb[n][j]), r, -__fmul_rn(nb, back));
                             }
                             raw rx, ry;
                             join<T, V, INTER>(x, y, rx, ry);
@@ -712,16 +714,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_backward_ring(const QkParam
                 }
                 // a place without a head, or a token without a position: nothing for dw
                 const float r = on ? rsqrtf(__fmaf_rn(sum, inv_d, p.eps)) : 0.0f;
-                const float back = on ? -__fmul_rn(__fmul_rn(r, r), __fmul_rn(r, __fmul_rn(inner, inv_d))) : 0.0f;
+                const float back = on ? -__fmul_rn(r, __fmul_rn(r, __fmul_rn(inner, inv_d))) : 0.0f;  // (times v r)
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     float x[V], y[V];
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        const float2 sa = fma2(mul2(a[n][i], both(r)), ga[n][i], make_float2(acc_a[n][2 * i], acc_a[n][2 * i + 1]));
-                        const float2 sb = fma2(mul2(b[n][i], both(r)), gb[n][i], make_float2(acc_b[n][2 * i], acc_b[n][2 * i + 1]));
+                        const float2 na = mul2(a[n][i], both(r)), nb = mul2(b[n][i], both(r));
+                        const float2 sa = fma2(na, ga[n][i], make_float2(acc_a[n][2 * i], acc_a[n][2 * i + 1]));
+                        const float2 sb = fma2(nb, gb[n][i], make_float2(acc_b[n][2 * i], acc_b[n][2 * i + 1]));
                         acc_a[n][2 * i] = sa.x, acc_a[n][2 * i + 1] = sa.y, acc_b[n][2 * i] = sb.x, acc_b[n][2 * i + 1] = sb.y;
-                        const float2 da = fma2(wa[n][i], both(r), mul2(a[n][i], both(back))), db = fma2(wb[n][i], both(r), mul2(b[n][i], both(back)));
+                        const float2 da = fma2(wa[n][i], both(r), mul2(na, both(back))), db = fma2(wb[n][i], both(r), mul2(nb, both(back)));
                         x[2 * i] = da.x, x[2 * i + 1] = da.y, y[2 * i] = db.x, y[2 * i + 1] = db.y;
                     }
                     uint4 rx, ry;
