@@ -27,10 +27,15 @@
 //
 // Bound by the tensor cores, and over seconds by the power that these take: 32768 rows,
 // 2048 x 4096, 8 experts, forward 587 us in a burst (1.87 PFLOP/s, 0.97 of the measured
-// rate), with a and b kept and over seconds 718 (1.53, 0.88 of the sustained rate).
-// Backward 730 in a burst, 834 over seconds; as two launches 884. Few rows are bound by
-// reading the weights: 1 x 4096 x 8192 in 28.5 us (4.7 TB/s; a kernel that only reads
-// them 27).
+// rate), with a and b kept and over seconds 710 (1.55, 0.89 of the sustained rate).
+// Backward 720 in a burst, 823 over seconds; as two launches 884. Few rows are bound by
+// reading the weights: 1 x 4096 x 8192 in 28 us (4.8 TB/s), 38 with cold caches; a
+// kernel that only reads them takes 23, and 28 with cold caches.
+//
+// da and db are rounded to bf16 before they are multiplied, as they are stored: beside
+// bf16 weights a tensor-core operand has no wider form, and two bf16 terms for each
+// would be twice the products. dx is 0.0023 of its size off 64 bits for it; with da and
+// db in 32 bits its own rounding alone would leave 0.0017.
 //
 // Rows of a tile past the expert's end are another expert's (or zeros): a row of
 // the product depends on its own row of x alone, and they are not written.

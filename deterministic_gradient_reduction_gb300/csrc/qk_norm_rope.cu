@@ -18,10 +18,11 @@
 // read once for all of the token's heads.
 //
 // Bound by memory, each head read and written once: 16384 tokens of 32 + 8 heads of
-// 128 bf16 forward 58 us (5.9 TB/s, 0.88 of the measured copy rate), backward 89 us
-// (5.75 TB/s, 0.85; 344 instructions a warp and group of heads, half of the issue
+// 128 bf16 forward 58 us (5.9 TB/s, 0.87 of the measured copy rate), backward 91 us
+// (5.6 TB/s, 0.83; 344 instructions a warp and group of heads, half of the issue
 // slots, and 128 registers, so 16 warps on an SM). Few tokens: the launches, 3 us
-// forward and, with the fold, 7 backward.
+// forward and, with the fold, 7 backward; 3001 x (12 + 4) x 80 fp32 backward 26 us
+// in a graph too: the device's, not the host's.
 //
 // Deterministic: a head's sums go over its team in a fixed order; dw goes through
 // a number of slots set by the sizes alone: a slot's warps take their units in

@@ -624,8 +624,10 @@ dgr_status dgr_gated_ffn_backward(const void *dh, int64_t ld_dh, const void *gat
  * dw_q and dw_k may be null; they are written, or added to with one rounding
  * (accumulate != 0). T = 0: 0, or left as they are but for a -0.
  *
- * Binary32 throughout, each output rounded once. The order of every sum depends
- * on the type, T, the head counts, D, R, interleaved and the alignment alone.
+ * Binary32 throughout, each output rounded once; a head's sum of squares has to
+ * lie in binary32's range (below 3.4e38: elements up to 8e17 always do). The order
+ * of every sum depends on the type, T, the head counts, D, R, interleaved and the
+ * alignment alone.
  *
  * q: [T, n_q, D], k: [T, n_k, D] bf16 or fp32 (dtype), element (t, head, d) at
  *           t * token + head * head_stride + d; heads and tokens of one tensor
@@ -672,7 +674,7 @@ dgr_status dgr_qk_norm_rope_backward(const void *dq_out, int64_t dqo_token, int6
  *   logp[t] = ln p_id,  entropy[t] = -sum_j p_j ln p_j,  lse[t] = m / tau + ln s,
  *   stats[t] = (m, ln s);
  *   top_ids[t][0 .. K-1]: the K largest logits above -inf, in descending order,
- *   equal ones by the lower index; top_logits their logits as they are and
+ *   equal ones by the lower index; top_logits their logits (-0 as 0) and
  *   top_logp their ln p. Where there are fewer, the rest has id -1 and -inf.
  *   top_ids, top_logits and lse are what dgr_topk_distill takes as the teacher's
  *   ids, teacher and teacher_lse.
